@@ -18,13 +18,20 @@ Entry points (same names as the C ABI):
   fwd_varlen(q, k, v, cu_q, cu_k, scale=None)   -> (o, lse)      packed sequences
   fwd_fp8(q8, k8, vt8, q_scale, k_scale, v_scale, scale=None) -> (o, lse)   e4m3, d = 128
   bwd_varlen(q, k, v, o, do, lse, cu_q, cu_k, scale=None) -> (dq, dk, dv)
+  rope_fwd(q, k, positions, plan), rope_bwd(dq, dk, positions, plan) -> (q, k)   rotary positions
+  rope(q, k, positions, plan)                   -> (q, k)   (autograd-aware)
+  cache_append(cache, k, v, page_table, seq_lens, cu_new=None, rope=None, positions=None)
+  decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None) -> (o, lse)
+with the handles Rope (a rotation: axes, frequencies, pairs) and PagedCache (key and value pages).
 Tensors are CUDA, contiguous, [B, H, L, d] with d in {64, 128}; q, k, v, o,
 do are bfloat16, lse and partials float32. The default scale is 1/sqrt(d).
 fwd, bwd and attention also take k, v with fewer heads H_kv dividing H
 (grouped-query attention: query head h reads K/V head h // (H // H_kv);
 attn_fwd_gqa / attn_bwd_gqa).
 Packed sequences are token-major [T, H, d] with lse [H, Tq]; cu_q, cu_k are
-host-side cumulative lengths (n_seqs + 1 ints, first 0).
+host-side cumulative lengths (n_seqs + 1 ints, first 0). The rotation and the
+cache calls also take views whose heads are contiguous rows on 16-byte
+boundaries; their positions, page tables and lengths are int32 device tensors.
 """
 from __future__ import annotations
 
@@ -40,13 +47,31 @@ __all__ = [
     "AttnError", "lib", "fwd", "bwd", "bwd_noalloc", "partial_fwd", "split_fwd", "merge", "attention",
     "bwd_workspace_size", "poll_device_status", "set_wait_limit_ns", "status_string",
     "MAX_CHUNKS", "MAX_SEQS", "fwd_varlen", "bwd_varlen", "bwd_varlen_workspace_size", "fwd_fp8",
-    "attention_varlen",
+    "attention_varlen", "Rope", "rope_fwd", "rope_bwd", "rope", "PagedCache", "cache_append",
+    "decode", "decode_workspace_size",
 ]
 
 ATTN_OK = 0
 MAX_CHUNKS = 64
 MAX_SEQS = 1024
+MAX_AXES = 4
+MAX_PAIRS = 64
 _LIB = None
+
+
+class _RopeStruct(ctypes.Structure):
+    """attn_rope_t"""
+    _fields_ = [("n_pairs", ctypes.c_int), ("n_axes", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("axis", ctypes.c_ubyte * MAX_PAIRS), ("turns", ctypes.c_ulonglong * MAX_PAIRS)]
+
+
+class _CacheStruct(ctypes.Structure):
+    """attn_cache_t"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_strides", ctypes.c_longlong * 3), ("v_strides", ctypes.c_longlong * 3),
+                ("n_pages", ctypes.c_longlong), ("page_size", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("d", ctypes.c_int), ("type", ctypes.c_int),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
 class AttnError(RuntimeError):
@@ -92,6 +117,16 @@ def _declare(L):
     L.attn_fwd_varlen_gqa.argtypes = [vp, vp, vp, vp, vp, ip, ip, i, i, i, i, f, vp]
     L.attn_bwd_varlen_gqa.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, ip, ip, i, i, i, i, f,
                                       vp, sz, vp]
+    ll, rp, cp = ctypes.c_longlong, ctypes.POINTER(_RopeStruct), ctypes.POINTER(_CacheStruct)
+    lp = ctypes.POINTER(ll)
+    L.attn_rope_init.argtypes = [rp, i, i, ip, ctypes.POINTER(ctypes.c_double), i]
+    L.attn_rope.argtypes = [rp, vp, lp, vp, lp, vp, lp, vp, lp, vp, lp, i, i, i, i, i, i, vp]
+    L.attn_cache_append.argtypes = [cp, vp, lp, vp, lp, vp, ll, i, vp, i, vp, i, rp, vp, ll, vp]
+    L.attn_decode_workspace_size.argtypes = [i, i, i, i]
+    L.attn_decode_workspace_size.restype = sz
+    L.attn_decode.argtypes = [cp, vp, lp, vp, ll, i, vp, i, i, f, rp, vp, ll, vp, vp, vp, sz, vp]
+    for name in ("attn_rope_init", "attn_rope", "attn_cache_append", "attn_decode"):
+        getattr(L, name).restype = ctypes.c_int
     for name in ("attn_fwd", "attn_bwd", "attn_partial_fwd", "attn_split_fwd", "attn_merge",
                  "attn_poll_device_status", "attn_fwd_varlen", "attn_bwd_varlen", "attn_fwd_gqa",
                  "attn_bwd_gqa", "attn_fwd_fp8", "attn_fwd_varlen_gqa", "attn_bwd_varlen_gqa"):
@@ -382,7 +417,8 @@ def bwd_varlen(q, k, v, o, do, lse, cu_q, cu_k, scale=None, workspace=None):
 
 
 def poll_device_status() -> int:
-    """Synchronise the current stream; return the status word (0 ok, 5 a wait timed out)."""
+    """Synchronise the current stream; return the status word (0 ok, 5 a wait timed
+    out, 7 a cached length or page was out of range)."""
     return int(lib().attn_poll_device_status(_stream()))
 
 
@@ -430,3 +466,353 @@ def attention_varlen(q, k, v, cu_q, cu_k, scale=None):
     """Autograd-aware exact attention over packed sequences (token-major
     [T, H, d]; cu_q, cu_k host cumulative lengths)."""
     return _AttentionVarlen.apply(q, k, v, cu_q, cu_k, scale)
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------
+
+_Strides2, _Strides3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
+
+
+def _rows(t, name, ndim, device_type="cuda"):
+    """Checks a bf16 tensor of rows (the last dimension contiguous, every row on
+    a 16-byte boundary) and returns the strides of its other dimensions, 0 for
+    those of size 1."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    if t.device.type != device_type:
+        raise ValueError(f"{name} must be a {device_type.upper()} tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {len(shape)}")
+    if shape[-1] not in (64, 128):
+        raise ValueError(f"{name}'s head dimension must be 64 or 128, got {shape[-1]}")
+    strides = t.stride()
+    if strides[-1] != 1:
+        raise ValueError(f"{name}'s heads must be contiguous rows")
+    out = [s if n != 1 else 0 for s, n in zip(strides[:-1], shape)]
+    if any(s & 7 for s in out) or t.data_ptr() & 15:
+        raise ValueError(f"{name}'s rows must start on 16-byte boundaries")
+    return out
+
+
+def _int32(t, name, device, ndim=None):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise ValueError(f"{name} must be an int32 tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if ndim is not None and t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+class Rope:
+    """A rotation by position over one or several axes (attn_rope_t).
+
+    axis_pairs   pairs of a head's elements that each axis turns, e.g. (8, 12, 12)
+                 for time, height and width of a 64-element head, or (64,) for
+                 text positions of a 128-element one; together a multiple of 8.
+                 The first 2 * sum(axis_pairs) elements of a head are rotated.
+    theta        pair i of an axis with n pairs turns by theta ** (-i / n) radians
+                 a position
+    pairing      "half": pair i is elements (i, i + sum(axis_pairs));
+                 "interleaved": elements (2 i, 2 i + 1)
+    frequencies  the pairs' radians a position instead of theta's (scaled long
+                 contexts, one spectrum over all axes, 0 for a pair that stays)
+    """
+
+    def __init__(self, axis_pairs, theta=10000.0, pairing="half", frequencies=None):
+        axis_pairs = [int(n) for n in axis_pairs]
+        if not axis_pairs or min(axis_pairs) < 1 or len(axis_pairs) > MAX_AXES:
+            raise ValueError(f"axis_pairs must hold 1 to {MAX_AXES} positive numbers")
+        n = sum(axis_pairs)
+        if n % 8 or n > MAX_PAIRS:
+            raise ValueError(f"axis_pairs must add up to a multiple of 8, at most {MAX_PAIRS}, got {n}")
+        if pairing not in ("half", "interleaved"):
+            raise ValueError(f"pairing must be 'half' or 'interleaved', got {pairing!r}")
+        if frequencies is None:
+            theta = float(theta)
+            if not (math.isfinite(theta) and theta > 0):
+                raise ValueError("theta must be finite and positive")
+            frequencies = [theta ** (-i / m) for m in axis_pairs for i in range(m)]
+        frequencies = [float(x) for x in frequencies]
+        if len(frequencies) != n or not all(map(math.isfinite, frequencies)):
+            raise ValueError(f"frequencies must be {n} finite numbers")
+        axes = [a for a, m in enumerate(axis_pairs) for _ in range(m)]
+        self.axis_pairs, self.n_axes, self.n_pairs = tuple(axis_pairs), len(axis_pairs), n
+        self.pairing, self.frequencies = pairing, tuple(frequencies)
+        self._struct = _RopeStruct()
+        _check("attn_rope_init", lib().attn_rope_init(
+            self._struct, n, self.n_axes, (ctypes.c_int * n)(*axes),
+            (ctypes.c_double * n)(*frequencies), int(pairing == "interleaved")))
+
+    def _positions(self, t, device, tokens):
+        """Positions [n_axes, *tokens] (one axis: tokens alone); returns the axis' stride."""
+        _int32(t, "positions", device)
+        shape = tuple(t.shape)
+        if self.n_axes == 1 and shape == tokens:
+            return 0
+        if shape != (self.n_axes, *tokens):
+            raise ValueError(f"positions must be {(self.n_axes, *tokens)}, got {shape}")
+        return t.stride(0)
+
+
+def _launch(device, fn, *args):
+    """Call an entry point on the current stream of ``device``."""
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream())
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream())
+    if st != ATTN_OK:
+        raise AttnError(fn.__name__, st)
+
+
+def _rope(q, k, positions, plan, inverse):
+    if not isinstance(plan, Rope):
+        raise ValueError("plan must be a Rope")
+    nd = q.dim() if isinstance(q, torch.Tensor) else 0
+    if nd not in (3, 4):
+        raise ValueError("q must be a [B, H, L, d] or [T, H, d] tensor")
+    sq = _rows(q, "q", nd)
+    d = q.shape[-1]
+    if 2 * plan.n_pairs > d:
+        raise ValueError(f"the plan rotates {2 * plan.n_pairs} elements of a head of {d}")
+    packed = nd == 3
+    B, H, L = (1, q.shape[1], q.shape[0]) if packed else q.shape[:3]
+    sk, Hk = None, 0
+    if k is not None:
+        sk, Hk = _rows(k, "k", nd), k.shape[1]
+        like = (L, Hk, d) if packed else (B, Hk, L, d)
+        if tuple(k.shape) != like or k.device != q.device:
+            raise ValueError(f"k must be {like} on {q.device}, got {tuple(k.shape)} on {k.device}")
+    dev = q.device
+    if not packed and isinstance(positions, torch.Tensor) and positions.dim() == (
+            3 if plan.n_axes > 1 or positions.dim() == 3 else 2) and positions.shape[-2:] == (B, L):
+        axis, batch = plan._positions(positions, dev, (B, L)), positions.stride(-2)
+    else:
+        axis, batch = plan._positions(positions, dev, (L,)), 0
+
+    def order(s):  # batch, head, token
+        return _Strides3(0, s[1], s[0]) if packed else _Strides3(*s)
+
+    def fresh(t):
+        o = torch.empty(t.shape, device=dev, dtype=torch.bfloat16)
+        return o, order(o.stride()[:-1])
+
+    qo, sqo = fresh(q)
+    ko, sko = (None, None) if k is None else fresh(k)
+    _launch(dev, lib().attn_rope, plan._struct, q.data_ptr(), order(sq), qo.data_ptr(), sqo,
+            None if k is None else k.data_ptr(), None if k is None else order(sk),
+            None if k is None else ko.data_ptr(), sko, positions.data_ptr(),
+            _Strides2(axis, batch), B, H, Hk, L, d, int(inverse))
+    return qo, ko
+
+
+def rope_fwd(q, k, positions, plan):
+    """q and k (or None) rotated by their tokens' positions: new contiguous tensors.
+
+    q [B, H, L, d] with k [B, H_k, L, d], or token-major q [T, H, d] with k
+    [T, H_k, d]; positions int32 on the device, [n_axes, L] (shared by the batch),
+    [n_axes, B, L] or [n_axes, T]; with one axis its dimension may be left out."""
+    return _rope(q, k, positions, plan, False)
+
+
+def rope_bwd(dq, dk, positions, plan):
+    """Gradients of rope_fwd's inputs from those of its outputs (the rotation back)."""
+    return _rope(dq, dk, positions, plan, True)
+
+
+def _rotatable(g):
+    """A gradient as the kernel reads it: autograd also hands over expanded or transposed ones."""
+    ok = g is None or (g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and
+                       all(s % 8 == 0 for s, n in zip(g.stride()[:-1], g.shape) if n != 1))
+    return g if ok else g.contiguous()
+
+
+class _Rotation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, plan, inverse):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions)
+        ctx.plan, ctx.inverse = plan, inverse
+        return _rope(q, k, positions, plan, inverse)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        (positions,) = ctx.saved_tensors
+        dq, dk = _rotatable(dq), _rotatable(dk)
+        if dq is None and dk is not None:
+            dk, dq = _Rotation.apply(dk, None, positions, ctx.plan, not ctx.inverse)
+        elif dq is not None:
+            dq, dk = _Rotation.apply(dq, dk, positions, ctx.plan, not ctx.inverse)
+        return dq, dk, None, None, None
+
+
+def rope(q, k, positions, plan):
+    """Autograd-aware rope_fwd; only the positions are saved for backward."""
+    return _Rotation.apply(q, k, positions, plan, False)
+
+
+# ---------------------------------------------------------------------------
+# The paged key-value cache
+# ---------------------------------------------------------------------------
+
+_CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+
+
+class PagedCache:
+    """Pages of keys and values, [n_pages, page_size, H_kv, d] each, bf16 or
+    float8_e4m3fn (a stored value then stands for itself times k_scale or
+    v_scale). The dimensions before d may be strided, so pages laid out
+    [n_pages, H_kv, page_size, d] are passed as a transposed view. The tensors
+    stay the caller's; the handle keeps their layout and the scales."""
+
+    def __init__(self, k, v, k_scale=1.0, v_scale=1.0):
+        s = _CacheStruct()
+        for name, t in (("k", k), ("v", v)):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4:
+                raise ValueError(f"{name} must be a [n_pages, page_size, H_kv, d] tensor")
+            if t.dtype not in _CACHE_TYPES:
+                raise ValueError(f"{name} must be bfloat16 or float8_e4m3fn, got {t.dtype}")
+            if t.shape != k.shape or t.dtype != k.dtype or t.device != k.device:
+                raise ValueError("k and v must have the same shape, type and device")
+            if t.numel() == 0 or t.shape[3] not in (64, 128):
+                raise ValueError(f"{name} must hold pages of heads of 64 or 128, got {tuple(t.shape)}")
+            if t.stride(3) != 1:
+                raise ValueError(f"{name}'s heads must be contiguous rows")
+            strides = [st if n != 1 else 0 for st, n in zip(t.stride()[:3], t.shape)]
+            if any(st * t.element_size() % 16 for st in strides) or t.data_ptr() % 16:
+                raise ValueError(f"{name}'s rows must start on 16-byte boundaries")
+            reach = t.shape[3]  # rows must not overlap: each is written by itself
+            for st, n in sorted((st, n) for st, n in zip(strides, t.shape) if n != 1):
+                if st < reach:
+                    raise ValueError(f"{name}'s rows must not overlap")
+                reach += st * (n - 1)
+            getattr(s, name + "_strides")[:] = strides
+        if k.data_ptr() == v.data_ptr():
+            raise ValueError("k and v must be different tensors")
+        for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if not (math.isfinite(x) and x > 0):
+                raise ValueError(f"{name} must be finite and positive")
+            if k.dtype == torch.bfloat16 and x != 1:
+                raise ValueError(f"{name} must be 1 for a bfloat16 cache")
+        s.n_pages, s.page_size, s.H_kv, s.d = k.shape
+        s.type, s.k_scale, s.v_scale = _CACHE_TYPES[k.dtype], float(k_scale), float(v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
+        self.n_pages, self.page_size, self.H_kv, self.d = k.shape
+        self.device = k.device
+        self._struct = s
+
+    def _at(self):
+        if self.device.type != "cuda":
+            raise ValueError("the cache must be on a CUDA device")
+        self._struct.k, self._struct.v = self.k.data_ptr(), self.v.data_ptr()
+        return self._struct
+
+    def _batch(self, page_table, seq_lens):
+        """Checks a batch's page table and lengths; returns the number of sequences."""
+        _int32(page_table, "page_table", self.device, 2)
+        _int32(seq_lens, "seq_lens", self.device, 1)
+        n = seq_lens.shape[0]
+        if page_table.shape[0] != n or n < 1 or page_table.shape[1] < 1:
+            raise ValueError(f"page_table must be [n_seqs, max_pages] for {n} sequences, "
+                             f"got {tuple(page_table.shape)}")
+        return n
+
+    def _turn(self, rope, positions, tokens):
+        """The rotation's arguments: its struct, the positions' address and axis stride."""
+        if rope is None:
+            if positions is not None:
+                raise ValueError("positions are used with a rope only")
+            return None, None, 0
+        if not isinstance(rope, Rope):
+            raise ValueError("rope must be a Rope")
+        if 2 * rope.n_pairs > self.d:
+            raise ValueError(f"the rope rotates {2 * rope.n_pairs} elements of a head of {self.d}")
+        if positions is None:
+            if rope.n_axes != 1:
+                raise ValueError("positions are needed for a rope with several axes")
+            return rope._struct, None, 0
+        return rope._struct, positions.data_ptr(), rope._positions(positions, self.device, (tokens,))
+
+
+def cache_append(cache, k, v, page_table, seq_lens, cu_new=None, rope=None, positions=None):
+    """Write new keys (rotated by ``rope``) and values, [T, H_kv, d] bf16, into the
+    cache's pages.
+
+    page_table int32 [n_seqs, max_pages] and seq_lens int32 [n_seqs] on the
+    device; seq_lens counts the new tokens, the last ones of their sequences.
+    cu_new int32 [n_seqs + 1] on the device: sequence b's new tokens are rows
+    cu_new[b] .. cu_new[b + 1]; without it each sequence has one. Rows outside
+    cu_new and those of a sequence of length 0 are left out. positions int32
+    [n_axes, T]; without them (one axis) a token's place in its sequence. The
+    pages written must not be shared. Lengths and pages out of range write
+    nothing and are reported by poll_device_status."""
+    if not isinstance(cache, PagedCache):
+        raise ValueError("cache must be a PagedCache")
+    sk, sv = _rows(k, "k", 3), _rows(v, "v", 3)
+    T = k.shape[0]
+    if k.shape != v.shape or k.shape[1] != cache.H_kv or k.shape[2] != cache.d:
+        raise ValueError(f"k and v must be [T, {cache.H_kv}, {cache.d}], got {tuple(k.shape)} "
+                         f"and {tuple(v.shape)}")
+    if k.device != cache.device or v.device != cache.device:
+        raise ValueError(f"k and v must be on {cache.device}")
+    n = cache._batch(page_table, seq_lens)
+    if cu_new is not None:
+        _int32(cu_new, "cu_new", cache.device, 1)
+        if cu_new.shape[0] != n + 1:
+            raise ValueError(f"cu_new must have {n + 1} entries, got {cu_new.shape[0]}")
+    elif T != n:
+        raise ValueError(f"without cu_new there is one new token per sequence: {n}, got {T}")
+    r, pos, stride = cache._turn(rope, positions, T)
+    _launch(cache.device, lib().attn_cache_append, cache._at(), k.data_ptr(), _Strides2(*sk),
+            v.data_ptr(), _Strides2(*sv), page_table.data_ptr(), page_table.stride(0),
+            page_table.shape[1], seq_lens.data_ptr(), n,
+            None if cu_new is None else cu_new.data_ptr(), T, r, pos, stride)
+
+
+def decode_workspace_size(B, H, H_kv, d) -> int:
+    return int(lib().attn_decode_workspace_size(B, H, H_kv, d))
+
+
+def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None, workspace=None):
+    """Attention of one new token per sequence, q [B, H, d] bf16, over the
+    seq_lens[b] keys and values its sequence has in the cache: (o bf16 [B, H, d],
+    lse fp32 [B, H]); a sequence of length 0 gives o = 0 and lse = -inf.
+
+    H is a multiple of the cache's heads (grouped-query attention). With ``rope``
+    q is rotated on the way (and rounded to bf16, as rope_fwd gives it) by
+    positions, int32 [n_axes, B], or, with one axis and none given, by
+    seq_lens - 1. page_table and seq_lens as for cache_append; the GPU reads
+    them, so a captured call follows their contents."""
+    if not isinstance(cache, PagedCache):
+        raise ValueError("cache must be a PagedCache")
+    sq = _rows(q, "q", 3)
+    B, H, d = q.shape
+    if d != cache.d or H < 1 or H % cache.H_kv:
+        raise ValueError(f"q must be [B, a multiple of {cache.H_kv}, {cache.d}], got {tuple(q.shape)}")
+    dev = cache.device
+    if q.device != dev:
+        raise ValueError(f"q must be on {dev}")
+    n = cache._batch(page_table, seq_lens)
+    if n != B:
+        raise ValueError(f"q holds {B} sequences, seq_lens {n}")
+    r, pos, stride = cache._turn(rope, positions, B)
+    L = lib()
+    need = L.attn_decode_workspace_size(B, H, cache.H_kv, d)
+    if workspace is None:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    elif workspace.numel() * workspace.element_size() < need or workspace.device != dev or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {dev}")
+    o = torch.empty((B, H, d), device=dev, dtype=torch.bfloat16)
+    lse = torch.empty((B, H), device=dev, dtype=torch.float32)
+    _launch(dev, L.attn_decode, cache._at(), q.data_ptr(), _Strides2(*sq), page_table.data_ptr(),
+            page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(), B, H, _scale(scale, d),
+            r, pos, stride, o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), need)
+    return o, lse

@@ -276,6 +276,63 @@ int check_ptrs(std::initializer_list<const void*> ps) {
   return ATTN_OK;
 }
 
+// Strides that keep every row 16-byte aligned.
+int check_strides(const long long* s, int n, int multiple) {
+  for (int i = 0; i < n; ++i) {
+    if (s[i] < 0) return ATTN_ERR_INVALID_ARG;
+    if (s[i] % multiple != 0) return ATTN_ERR_MISALIGNED;
+  }
+  return ATTN_OK;
+}
+
+int check_rope(const attn_rope_t& r, int d) {
+  if (r.n_pairs < 8 || r.n_pairs % 8 != 0 || r.n_pairs > d / 2 || r.n_axes < 1 ||
+      r.n_axes > ATTN_MAX_AXES)
+    return ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < r.n_pairs; ++i)
+    if (r.axis[i] >= r.n_axes) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+// Grid limits of the per-row kernels (a thread per 16 elements, heads in y).
+bool rows_fit(long long tokens, int d, long long heads) {
+  return tokens * (d / 16) < (1ll << 37) && heads <= 65535;
+}
+
+int check_cache(const attn_cache_t* c) {
+  if (!c) return ATTN_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->n_pages >= (1ll << 31) || c->page_size < 1 || c->H_kv < 1 ||
+      c->H_kv > 65535)
+    return ATTN_ERR_INVALID_ARG;
+  for (float f : {c->k_scale, c->v_scale})
+    if (!std::isfinite(f) || !(f > 0.0f) || !std::isfinite(1.f / f)) return ATTN_ERR_INVALID_ARG;
+  if ((c->d != 64 && c->d != 128) || (c->type != ATTN_CACHE_BF16 && c->type != ATTN_CACHE_E4M3))
+    return ATTN_ERR_UNSUPPORTED;
+  if (c->type == ATTN_CACHE_BF16 && (c->k_scale != 1.f || c->v_scale != 1.f))
+    return ATTN_ERR_INVALID_ARG;
+  int s = check_ptrs({c->k, c->v});
+  const int multiple = c->type == ATTN_CACHE_E4M3 ? 16 : 8;
+  if (s == ATTN_OK) s = check_strides(c->k_strides, 3, multiple);
+  if (s == ATTN_OK) s = check_strides(c->v_strides, 3, multiple);
+  return s;
+}
+
+int check_table(const int* table, long long stride, int max_pages, const int* lens, int n_seqs) {
+  if (!table || !lens || max_pages < 1 || n_seqs < 1 || stride < 0) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+// Query heads of one K/V head that a decode CTA holds, and blocks of them: the
+// matrix instruction has 8 columns, so groups of up to 8 take one set and
+// larger groups two at a time.
+struct DecodeShape {
+  int rows, blocks;
+};
+DecodeShape decode_shape(int group) {
+  const int rows = group <= 8 ? 8 : 16;
+  return {rows, (group + rows - 1) / rows};
+}
+
 // Short sequences (at most 64 queries and keys) are packed several to a
 // 128-row tile; returns the number per tile, or 0 for the per-head tiling.
 int packing(int Lq, int Lk) {
@@ -729,6 +786,196 @@ int attn_merge(const float* o_parts, const float* lse_parts, int n_chunks, void*
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
+int attn_rope_init(attn_rope_t* r, int n_pairs, int n_axes, const int* axis, const double* freq,
+                   int interleaved) {
+  if (!r || !axis || !freq) return ATTN_ERR_INVALID_ARG;
+  if (n_pairs < 8 || n_pairs % 8 != 0 || n_axes < 1) return ATTN_ERR_INVALID_ARG;
+  if (n_pairs > ATTN_MAX_PAIRS || n_axes > ATTN_MAX_AXES) return ATTN_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_pairs; ++i)
+    if (axis[i] < 0 || axis[i] >= n_axes || !std::isfinite(freq[i])) return ATTN_ERR_INVALID_ARG;
+  *r = attn_rope_t{};
+  r->n_pairs = n_pairs;
+  r->n_axes = n_axes;
+  r->interleaved = interleaved != 0;
+  for (int i = 0; i < n_pairs; ++i) {
+    constexpr double kTwoPi = 6.283185307179586476925;
+    double x = freq[i] / kTwoPi;
+    x -= std::floor(x);  // [0, 1], 1 by rounding of a tiny negative number
+    r->axis[i] = static_cast<unsigned char>(axis[i]);
+    r->turns[i] = x < 1.0 ? static_cast<unsigned long long>(std::ldexp(x, 64)) : 0ull;
+  }
+  return ATTN_OK;
+}
+
+int attn_rope(const attn_rope_t* r, const void* q, const long long* q_strides, void* q_out,
+              const long long* q_out_strides, const void* k, const long long* k_strides,
+              void* k_out, const long long* k_out_strides, const int* pos,
+              const long long* pos_strides, int B, int H_q, int H_k, int L, int d, int inverse,
+              void* stream) {
+  if (!r || !q_strides || !q_out_strides || !pos || !pos_strides) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || H_q < 1 || H_k < 0 || L < 1) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  int s = check_rope(*r, d);
+  if (s != ATTN_OK) return s;
+  if ((s = check_ptrs({q, q_out})) != ATTN_OK) return s;
+  if ((s = check_strides(q_strides, 3, 8)) != ATTN_OK) return s;
+  if ((s = check_strides(q_out_strides, 3, 8)) != ATTN_OK) return s;
+  if (H_k > 0) {
+    if (!k_strides || !k_out_strides) return ATTN_ERR_INVALID_ARG;
+    if ((s = check_ptrs({k, k_out})) != ATTN_OK) return s;
+    if ((s = check_strides(k_strides, 3, 8)) != ATTN_OK) return s;
+    if ((s = check_strides(k_out_strides, 3, 8)) != ATTN_OK) return s;
+  }
+  const long long tokens = static_cast<long long>(B) * L;
+  if (!rows_fit(tokens, d, static_cast<long long>(H_q) + H_k)) return ATTN_ERR_INVALID_ARG;
+  if (bind_device() < 0) return ATTN_ERR_CUDA;
+  eba::RopeArgs a{};
+  a.in[0] = q;
+  a.out[0] = q_out;
+  a.in[1] = k;
+  a.out[1] = k_out;
+  for (int i = 0; i < 3; ++i) {
+    a.si[0][i] = q_strides[i];
+    a.so[0][i] = q_out_strides[i];
+    a.si[1][i] = H_k > 0 ? k_strides[i] : 0;
+    a.so[1][i] = H_k > 0 ? k_out_strides[i] : 0;
+  }
+  a.H[0] = H_q;
+  a.H[1] = H_k;
+  a.pos = pos;
+  a.pos_axis = pos_strides[0];
+  a.pos_batch = pos_strides[1];
+  a.tokens = tokens;
+  a.L = L;
+  a.sign = inverse ? -1.f : 1.f;
+  a.rope = *r;
+  cudaError_t e = eba::launch_rope(a, d, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+int attn_cache_append(const attn_cache_t* cache, const void* k, const long long* k_strides,
+                      const void* v, const long long* v_strides, const int* page_table,
+                      long long table_stride, int max_pages, const int* seq_lens, int n_seqs,
+                      const int* cu_new, int T, const attn_rope_t* rope, const int* pos,
+                      long long pos_stride, void* stream) {
+  int s = check_cache(cache);
+  if (s != ATTN_OK) return s;
+  if (!k_strides || !v_strides) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_table(page_table, table_stride, max_pages, seq_lens, n_seqs)) != ATTN_OK) return s;
+  if (T < 1 || (!cu_new && T != n_seqs)) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_ptrs({k, v})) != ATTN_OK) return s;
+  if ((s = check_strides(k_strides, 2, 8)) != ATTN_OK) return s;
+  if ((s = check_strides(v_strides, 2, 8)) != ATTN_OK) return s;
+  if (rope) {
+    if ((s = check_rope(*rope, cache->d)) != ATTN_OK) return s;
+    if (!pos && rope->n_axes != 1) return ATTN_ERR_INVALID_ARG;
+  }
+  if (!rows_fit(T, cache->d, cache->H_kv)) return ATTN_ERR_INVALID_ARG;
+  int* status = status_word_ptr();
+  if (!status) return ATTN_ERR_CUDA;
+  eba::AppendArgs a{};
+  a.k = k;
+  a.v = v;
+  a.k_token = k_strides[0];
+  a.k_head = k_strides[1];
+  a.v_token = v_strides[0];
+  a.v_head = v_strides[1];
+  a.cache = *cache;
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.lens = seq_lens;
+  a.cu_new = cu_new;
+  a.n_seqs = n_seqs;
+  a.tokens = T;
+  a.pos = pos;
+  a.pos_axis = pos_stride;
+  a.k_inv = 1.f / cache->k_scale;
+  a.v_inv = 1.f / cache->v_scale;
+  a.status = status;
+  if (rope) a.rope = *rope;
+  cudaError_t e = eba::launch_append(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+size_t attn_decode_workspace_size(int B, int H, int H_kv, int d) {
+  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
+  const DecodeShape p = decode_shape(H / H_kv);
+  const size_t items = static_cast<size_t>(B) * H_kv * p.blocks;
+  const size_t slots = 2 * static_cast<size_t>(eba::kDecodeCtas) * p.rows;
+  return (items * sizeof(int) + 15) / 16 * 16 + slots * (d + 2) * sizeof(float);
+}
+
+int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_strides,
+                const int* page_table, long long table_stride, int max_pages, const int* seq_lens,
+                int B, int H, float scale, const attn_rope_t* rope, const int* pos,
+                long long pos_stride, void* o, float* lse, void* workspace,
+                size_t workspace_bytes, void* stream) {
+  int s = check_cache(cache);
+  if (s != ATTN_OK) return s;
+  if (!q_strides) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_table(page_table, table_stride, max_pages, seq_lens, B)) != ATTN_OK) return s;
+  if (H < 1 || H % cache->H_kv != 0) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * H >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_ptrs({q, o, lse})) != ATTN_OK) return s;
+  if ((s = check_strides(q_strides, 2, 8)) != ATTN_OK) return s;
+  if (rope) {
+    if ((s = check_rope(*rope, cache->d)) != ATTN_OK) return s;
+    if (!pos && rope->n_axes != 1) return ATTN_ERR_INVALID_ARG;
+  }
+  const DecodeShape p = decode_shape(H / cache->H_kv);
+  if (!workspace || workspace_bytes < attn_decode_workspace_size(B, H, cache->H_kv, cache->d))
+    return ATTN_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  eba::DecodeArgs a{};
+  const long long capacity = static_cast<long long>(max_pages) * cache->page_size;
+  a.max_len = static_cast<int>(std::min(capacity, (1ll << 31) - 1 - eba::kDecodeTileKeys));
+  a.heads = cache->H_kv * p.blocks;
+  const long long item_tiles = (a.max_len + eba::kDecodeTileKeys - 1) / eba::kDecodeTileKeys;
+  const long long seq_tiles = item_tiles * a.heads;  // < 2^57
+  if (seq_tiles >= (1ll << 31) || seq_tiles * B >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  int* status = status_word_ptr();
+  if (!status) return ATTN_ERR_CUDA;
+  const int esz = cache->type == ATTN_CACHE_E4M3 ? 1 : 2;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_seq = q_strides[0];
+  a.q_head = q_strides[1];
+  a.k = static_cast<const unsigned char*>(cache->k);
+  a.v = static_cast<const unsigned char*>(cache->v);
+  for (int i = 0; i < 3; ++i) {
+    a.k_strides[i] = cache->k_strides[i] * esz;
+    a.v_strides[i] = cache->v_strides[i] * esz;
+  }
+  a.cache = *cache;
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.lens = seq_lens;
+  a.B = B;
+  a.H = H;
+  a.group = H / cache->H_kv;
+  a.rows = p.rows;
+  a.blocks = p.blocks;
+  a.scale_log2 = scale * kLog2e * cache->k_scale;
+  a.o_scale = cache->v_scale;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  const size_t items = static_cast<size_t>(B) * a.heads;
+  const size_t slots = 2 * static_cast<size_t>(eba::kDecodeCtas) * p.rows;
+  a.item = static_cast<int*>(workspace);
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                      (items * sizeof(int) + 15) / 16 * 16);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * cache->d);
+  a.pos = pos;
+  a.pos_axis = pos_stride;
+  a.status = status;
+  if (rope) a.rope = *rope;
+  // no more CTAs than tiles the tables can hold; a single-tile item is never cut
+  const int ctas = static_cast<int>(std::min<long long>(eba::kDecodeCtas, seq_tiles * B));
+  cudaError_t e = eba::launch_decode(a, ctas, item_tiles > 1, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
 const char* attn_status_string(int status) {
   switch (status) {
     case ATTN_OK: return "ok";
@@ -738,6 +985,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_CUDA: return "CUDA call failed";
     case ATTN_ERR_TIMEOUT: return "an in-kernel wait timed out";
     case ATTN_ERR_WORKSPACE: return "workspace missing or too small";
+    case ATTN_ERR_PAGE: return "a cached length or page is out of range";
     default: return "unknown status";
   }
 }
@@ -754,7 +1002,8 @@ int attn_poll_device_status(void* stream) {
     if ((e = cudaMemcpyToSymbol(g_status_word, &zero, sizeof(int))) != cudaSuccess)
       return cuda_fail(e);
   }
-  return value == 0 ? ATTN_OK : (value == ATTN_ERR_TIMEOUT ? ATTN_ERR_TIMEOUT : ATTN_ERR_CUDA);
+  if (value == ATTN_OK || value == ATTN_ERR_TIMEOUT || value == ATTN_ERR_PAGE) return value;
+  return ATTN_ERR_CUDA;
 }
 
 int attn_last_cuda_error(void) { return t_last_cuda_error; }

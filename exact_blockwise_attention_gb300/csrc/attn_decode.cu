@@ -1,0 +1,730 @@
+// Attention of one new token per sequence over a paged key-value cache, split
+// over the cache's length and joined.
+//
+// For each sequence b and query head h (K/V head g = h / G, n = lens[b] keys):
+//   s_j = scale q . k_j,  M = max_j s_j,  O = sum_j e^(s_j - M) v_j / L,
+//   L = sum_j e^(s_j - M),  lse = M + ln L;
+// over parts c of the keys the same sums join exactly:
+//   M = max_c M_c,  L = sum_c e^(M_c - M) L_c,  O = sum_c e^(M_c - M) O_c / L.
+//
+// Every cached element is read once for its G query heads: 2 G flops per
+// element, far below what the card computes per byte, so the kernel is bound
+// by HBM reads. What it is built around:
+//  - The work is the list of all 64-key tiles of all (sequence, K/V head)
+//    items, cut into equal runs, one per CTA (two CTAs per SM): long and short
+//    sequences balance without the host knowing the lengths, and a call can be
+//    captured and replayed with other lengths. An item cut between CTAs leaves
+//    fp32 partials, which the join kernel adds up in the order of the keys.
+//  - A warp owns 16 keys of each tile and walks the CTA's run on its own, with
+//    its own running maximum and sums: its loads (cp.async, 16 bytes a lane,
+//    rows of whole cache lines) run several tiles ahead, across item borders,
+//    and the four warps meet only at an item's end.
+//  - The products use the 16x8x16 warp matrix instruction with the keys as its
+//    16 rows and the G query heads as its 8 columns: S^T = K Q^T, then
+//    O^T += V^T P^T, with K and V read from shared memory as they lie there
+//    (V transposed by ldmatrix) and P^T made from S^T by an 8x8 register
+//    transpose. A 128-row tensor-core tile would be almost empty at these
+//    heights, and the matrix pipe is not what bounds the kernel.
+//  - bf16 caches: P is split into two bf16 terms (P = hi + lo to 2^-15), so
+//    that its rounding stays far below that of the bf16 output; e4m3 caches:
+//    K and V widen exactly to fp16, q is scaled per head by a power of two
+//    into fp16's range (exact above 2^-28 of the head's largest element) and P
+//    is held as fp16, 2^15 at the running maximum (2^-12 relative down to
+//    2^-29 of the largest weight).
+// Scores, maxima, sums and outputs are fp32 throughout.
+#include <cuda_fp16.h>
+
+#include "rope.cuh"
+
+namespace eba {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStepKeys = 16;                     // keys of a warp's step
+constexpr int kTileKeys = kWarps * kStepKeys;     // 64
+constexpr int kRingBytes = 24 * 1024;             // of each warp
+constexpr int kPassCols = 64;                     // columns of O summed over the warps at a time
+constexpr int kPassRow = kPassCols + 4;           // floats; +4: conflict-free column writes
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kF16Shift = 15.f;                 // e4m3 caches: P's largest value is 2^15
+static_assert(kTileKeys == kDecodeTileKeys, "");
+
+template <int D, int NB, bool F8>
+struct Layout {
+  static constexpr int N = 8 * NB;                    // query heads of a CTA
+  static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a cached row
+  static constexpr int kTile = kStepKeys * kRow;      // of a warp's K (or V) step
+  static constexpr int kStages = kRingBytes / (2 * kTile);
+  static constexpr int kQRow = D + 8;                 // 16-bit elements of a staged query row
+  static constexpr int kRing = kWarps * kRingBytes;
+  static constexpr int kSum = kWarps * 8 * kPassRow * 4;
+  static constexpr int kQ = N * kQRow * 2;
+  static constexpr int kOffSum = kRing;
+  static constexpr int kOffQ = kOffSum + kSum;
+  static constexpr int kOffMl = kOffQ + kQ;           // per warp and row: reference, sum
+  static constexpr int kOffQs = kOffMl + kWarps * N * 8;  // per row: score factor
+  static constexpr int kOffMask = kOffQs + N * 4;     // per warp and stage: keys that count
+  static constexpr int kBytes = kOffMask + kWarps * kStages * 4;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// An 8x8 matrix of 16-bit elements, one 32-bit register a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool F8>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (F8) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+// Two e4m3 bytes -> two fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// The largest bf16 strictly below p > 0 (0 for 0), as fp32 bits: what is left of
+// p is then positive, and both terms of a weight give an infinite value its sign.
+__device__ __forceinline__ uint32_t below(float p) {
+  return (max(__float_as_uint(p), 1u) - 1u) & 0xFFFF0000u;
+}
+
+// Where 16-byte chunk c of row r lies in a tile of kRow-byte rows, so that the
+// 8 rows of a matrix load fall into 8 different bank groups.
+template <int kRow>
+__device__ __forceinline__ uint32_t tile_offset(int r, int c) {
+  if constexpr (kRow >= 128) return static_cast<uint32_t>(r * kRow + ((c ^ (r & 7)) << 4));
+  return static_cast<uint32_t>(r * kRow + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// A place in the list of tiles: tile t of nt of sequence b (len keys), head hh
+// (K/V head and block of query heads).
+struct Cursor {
+  int b, hh, t, nt, len;
+};
+
+__device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
+  const int len = __ldg(a.lens + b);
+  return min(max(len, 0), a.max_len);
+}
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
+
+__device__ __forceinline__ void advance(Cursor& c, const DecodeArgs& a) {
+  if (++c.t < c.nt) return;
+  c.t = 0;
+  if (++c.hh < a.heads) return;
+  c.hh = 0;
+  c.nt = 0;
+  while (c.nt == 0 && ++c.b < a.B) {
+    c.len = clamp_len(a, c.b);
+    c.nt = tiles_of(c.len);
+  }
+}
+
+// The first tile of CTA i: an equal share of all tiles.
+__device__ __forceinline__ int first_tile(int i, int tiles, int ctas) {
+  return static_cast<int>(static_cast<long long>(i) * tiles / ctas);
+}
+
+template <int D, int NB, bool F8>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_kernel(const __grid_constant__ DecodeArgs a) {
+  using L = Layout<D, NB, F8>;
+  constexpr int N = L::N;
+  constexpr int kStages = L::kStages;
+  constexpr int kKSteps = D / 16;  // 16-element steps of a product over d; 16-row tiles of V^T
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int s_scan[kWarps];
+  __shared__ Cursor s_first;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int j4 = lane & 3, u8 = lane >> 2;
+  const int cta = blockIdx.x;
+
+  // ---- the list of tiles: each thread counts a run of sequences ----
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int raw = __ldg(a.lens + b);
+    if (cta == 0 && (raw < 0 || raw > a.max_len)) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+    mine += tiles_of(clamp_len(a, b)) * a.heads;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, m);
+    if (lane >= m) incl += o;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int before = 0, tiles = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    before += w < warp ? s_scan[w] : 0;
+    tiles += s_scan[w];
+  }
+  // no run is empty: with fewer tiles than CTAs the last CTAs have none
+  const int G = max(1, min(static_cast<int>(gridDim.x), tiles));
+  const int r0 = cta < G ? first_tile(cta, tiles, G) : tiles;
+  const int r1 = cta < G ? first_tile(cta + 1, tiles, G) : tiles;
+  {
+    int at = before + incl - mine;  // first tile of this thread's sequences
+    if (r0 < r1 && r0 >= at && r0 < at + mine) {
+      for (int b = b0; b < b1; ++b) {
+        const int len = clamp_len(a, b), nt = tiles_of(len);
+        if (r0 < at + nt * a.heads) {
+          const int in = r0 - at;
+          s_first = Cursor{b, in / nt, in % nt, nt, len};
+          break;
+        }
+        at += nt * a.heads;
+      }
+    }
+  }
+  // Sequences without keys: O = 0, lse = -inf.
+  for (int b = cta; b < a.B; b += gridDim.x) {
+    if (clamp_len(a, b) > 0) continue;
+    for (int x = tid; x < a.H * D / 8; x += kThreads)
+      *reinterpret_cast<uint4*>(a.o + static_cast<long long>(b) * a.H * D + x * 8) =
+          make_uint4(0, 0, 0, 0);
+    for (int h = tid; h < a.H; h += kThreads) a.lse[static_cast<long long>(b) * a.H + h] = -INFINITY;
+    for (int x = tid; x < a.heads; x += kThreads) a.item[static_cast<long long>(b) * a.heads + x] = 0;
+  }
+  __syncthreads();
+  if (r0 >= r1) return;
+
+  const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
+  float* s_sum = reinterpret_cast<float*>(smem + L::kOffSum);
+  uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + L::kOffQ);
+  float2* s_ml = reinterpret_cast<float2*>(smem + L::kOffMl);
+  float* s_qs = reinterpret_cast<float*>(smem + L::kOffQs);
+  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + L::kOffMask) + warp * kStages;
+
+  // ---- loads: this lane looks up key (lane & 15) of the step ----
+  Cursor ld = s_first;
+  int ld_left = r1 - r0;
+  int page = -1, slot = 0;  // of this lane's key at ld
+  auto look_up = [&]() {
+    page = -1;
+    const int key = ld.t * kTileKeys + warp * kStepKeys + (lane & 15);
+    if (ld_left > 0 && key < ld.len) {
+      const int entry = key / a.cache.page_size;
+      slot = key - entry * a.cache.page_size;
+      page = __ldg(a.table + ld.b * a.table_stride + entry);
+      if (page < 0 || page >= a.cache.n_pages) {
+        atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+        page = -1;
+      }
+    }
+  };
+  auto issue = [&](int stage) {
+    constexpr int kLanes = L::kRow / 16;     // of a row
+    constexpr int kRows = 32 / kLanes;       // of an instruction
+    const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+    if (lane == 0) s_mask[stage] = mask;
+    if (mask) {
+      const int g = ld.hh / a.blocks;
+      const long long pg = max(page, 0);
+      const long long ko = pg * a.k_strides[0] + slot * a.k_strides[1] + g * a.k_strides[2];
+      const long long vo = pg * a.v_strides[0] + slot * a.v_strides[1] + g * a.v_strides[2];
+      const uint32_t kt = ring + stage * 2 * L::kTile, vt = kt + L::kTile;
+      const int c = lane % kLanes;
+#pragma unroll
+      for (int i = 0; i < kStepKeys / kRows; ++i) {
+        const int r = i * kRows + lane / kLanes;
+        const bool ok = (mask >> r) & 1;
+        const long long kr = __shfl_sync(0xffffffffu, ko, r);
+        const long long vr = __shfl_sync(0xffffffffu, vo, r);
+        const uint32_t to = tile_offset<L::kRow>(r, c);
+        cp_async16(kt + to, a.k + (ok ? kr + c * 16 : 0), ok);
+        cp_async16(vt + to, a.v + (ok ? vr + c * 16 : 0), ok);
+      }
+    }
+    cp_async_commit();
+    if (--ld_left > 0) advance(ld, a);
+    look_up();
+  };
+  look_up();
+#pragma unroll 1
+  for (int s = 0; s < kStages - 1; ++s) issue(s);
+
+  // ---- the query heads of an item, staged for all warps ----
+  // Row n: query head g G + blk N + n; rotated where asked, rounded to bf16
+  // (the same value the rotation kernel gives); zero behind the group.
+  auto stage_q = [&](const Cursor& c) {
+    constexpr int kPer = kThreads / N;   // threads of a row
+    constexpr int kPairs = D / 2 / kPer; // pairs (x, x + step) of a thread
+    const int n = tid / kPer, i = tid % kPer;
+    const int g = c.hh / a.blocks, blk = c.hh - g * a.blocks;
+    const int hg = blk * N + n;
+    const bool live = hg < a.group;
+    const __nv_bfloat16* q = a.q + c.b * a.q_seq + (static_cast<long long>(g) * a.group + hg) * a.q_head;
+    float x[kPairs], y[kPairs];
+    int ox[kPairs], oy[kPairs];
+    float top = 0.f;
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+      const int pair = i * kPairs + p;
+      const int P = a.rope.n_pairs;
+      if (pair < P) {
+        ox[p] = a.rope.interleaved ? 2 * pair : pair;
+        oy[p] = a.rope.interleaved ? 2 * pair + 1 : pair + P;
+      } else {
+        ox[p] = 2 * pair;
+        oy[p] = 2 * pair + 1;
+      }
+      x[p] = live ? __bfloat162float(q[ox[p]]) : 0.f;
+      y[p] = live ? __bfloat162float(q[oy[p]]) : 0.f;
+      if (pair < P) {
+        const int axis = a.rope.axis[pair];
+        const int pos = a.pos ? __ldg(a.pos + axis * a.pos_axis + c.b) : c.len - 1;
+        float cs, sn;
+        rope_cs(pos, a.rope.turns[pair], 1.f, cs, sn);
+        rope_turn(x[p], y[p], cs, sn);
+        x[p] = __bfloat162float(__float2bfloat16_rn(x[p]));
+        y[p] = __bfloat162float(__float2bfloat16_rn(y[p]));
+      }
+      const float ax = fabsf(x[p]), ay = fabsf(y[p]);
+      top = fmaxf(top, ax < INFINITY ? ax : 0.f);
+      top = fmaxf(top, ay < INFINITY ? ay : 0.f);
+    }
+    if constexpr (F8) {
+#pragma unroll
+      for (int m = kPer / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      // 2^e puts the head's largest element into [2^13, 2^14); e within the
+      // range where 2^e and 2^-e are normal floats
+      const int e = top > 0.f ? min(max(13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -100), 100) : 0;
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      if (i == 0) s_qs[n] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        s_q[n * L::kQRow + ox[p]] = __half_as_ushort(__float2half_rn(x[p] * up));
+        s_q[n * L::kQRow + oy[p]] = __half_as_ushort(__float2half_rn(y[p] * up));
+      }
+    } else {
+      if (i == 0) s_qs[n] = a.scale_log2;
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        s_q[n * L::kQRow + ox[p]] = __bfloat16_as_ushort(__float2bfloat16_rn(x[p]));
+        s_q[n * L::kQRow + oy[p]] = __bfloat16_as_ushort(__float2bfloat16_rn(y[p]));
+      }
+    }
+  };
+
+  uint32_t qf[NB][kKSteps][2];  // the query as the product's column operand
+  float qs[NB][2];              // score factor of this lane's two columns
+  float o[NB][kKSteps][4];
+  float top[NB][2], sum[NB][2];
+  auto begin_item = [&]() {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const uint16_t* row = s_q + (nb * 8 + u8) * L::kQRow;
+#pragma unroll
+      for (int k = 0; k < kKSteps; ++k) {
+        // e4m3: a lane's four consecutive bytes of K serve its two register
+        // halves, so the query's elements are taken in the same order
+        const int e0 = F8 ? k * 16 + 4 * j4 : k * 16 + 2 * j4;
+        const int e1 = F8 ? e0 + 2 : e0 + 8;
+        qf[nb][k][0] = *reinterpret_cast<const uint32_t*>(row + e0);
+        qf[nb][k][1] = *reinterpret_cast<const uint32_t*>(row + e1);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[nb][k][x] = 0.f;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        qs[nb][x] = s_qs[nb * 8 + 2 * j4 + x];
+        top[nb][x] = -INFINITY;
+        sum[nb][x] = 0.f;
+      }
+    }
+  };
+
+  Cursor cur = s_first;
+  int t_begin = cur.t;        // first tile of the item in this run
+  bool first_item = true;
+  stage_q(cur);
+  __syncthreads();
+  begin_item();
+
+  int stage = 0;
+#pragma unroll 1
+  for (int tile = r0; tile < r1; ++tile) {
+    {
+      int into = stage + kStages - 1;
+      if (into >= kStages) into -= kStages;
+      issue(into);
+    }
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const uint32_t mask = s_mask[stage];
+    if (mask) {
+      const uint32_t kt = ring + stage * 2 * L::kTile, vt = kt + L::kTile;
+      // S^T = K Q^T in two chains
+      float s[NB][2][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[nb][0][x] = s[nb][1][x] = 0.f;
+      if constexpr (F8) {
+#pragma unroll
+        for (int k = 0; k < kKSteps; k += 2) {
+          uint32_t r[4];
+          ldmatrix4(r, kt + tile_offset<L::kRow>(lane & 15, k + (lane >> 4)));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t lo = r[2 * x], hi = r[2 * x + 1];
+            const uint32_t f[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(hi), e4m3x2_f16x2(lo >> 16),
+                                   e4m3x2_f16x2(hi >> 16)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma16816<true>(s[nb][x], f, qf[nb][k + x][0], qf[nb][k + x][1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kKSteps; ++k) {
+          uint32_t r[4];
+          ldmatrix4(r, kt + tile_offset<L::kRow>(lane & 15, 2 * k + (lane >> 4)));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            mma16816<false>(s[nb][k & 1], r, qf[nb][k][0], qf[nb][k][1]);
+        }
+      }
+      // online softmax; element x of a lane: key u8 + 8 (x / 2), column 2 j4 + x % 2
+      uint32_t ph[NB][2], pl[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const bool ok = (mask >> (u8 + 8 * (x >> 1))) & 1;
+          v[x] = ok ? (s[nb][0][x] + s[nb][1][x]) * qs[nb][x & 1] : -INFINITY;
+        }
+        float mx[2] = {fmaxf(v[0], v[2]), fmaxf(v[1], v[3])};
+#pragma unroll
+        for (int m = 4; m < 32; m <<= 1) {
+          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], m));
+          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], m));
+        }
+        const bool grew = mx[0] > top[nb][0] || mx[1] > top[nb][1];
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float to = fmaxf(top[nb][x], mx[x]);
+            // -inf to -inf (a column whose scores are all -inf) keeps its zeros
+            const float f = to == top[nb][x] ? 1.f : ex2_approx(top[nb][x] - to);
+            top[nb][x] = to;
+            sum[nb][x] *= f;
+#pragma unroll
+            for (int k = 0; k < kKSteps; ++k) {
+              o[nb][k][x] *= f;
+              o[nb][k][x + 2] *= f;
+            }
+          }
+        }
+        float p[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float ref = top[nb][x & 1] == -INFINITY ? 0.f : top[nb][x & 1];
+          p[x] = ex2_approx(v[x] - (F8 ? ref - kF16Shift : ref));
+          sum[nb][x & 1] += p[x];
+        }
+        if constexpr (F8) {
+          ph[nb][0] = transpose8(pack_f16(p[0], p[1]));
+          ph[nb][1] = transpose8(pack_f16(p[2], p[3]));
+        } else {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t h0 = below(p[2 * x]), h1 = below(p[2 * x + 1]);
+            ph[nb][x] = transpose8(__byte_perm(h0, h1, 0x7632));
+            pl[nb][x] = transpose8(pack_bf16(p[2 * x] - __uint_as_float(h0),
+                                             p[2 * x + 1] - __uint_as_float(h1)));
+          }
+        }
+      }
+      // O^T += V^T P^T
+      if constexpr (F8) {
+        // 16-bit units of V hold two columns of one key: after the transposing
+        // load a register holds columns 2 u8, 2 u8 + 1 of keys 2 j4, 2 j4 + 1,
+        // and rows u8 and u8 + 8 of the product stand for those two columns
+#pragma unroll
+        for (int k = 0; k < kKSteps; k += 2) {
+          uint32_t r[4];
+          ldmatrix4_trans(r, vt + tile_offset<L::kRow>(lane & 15, k + (lane >> 4)));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t w0 = __byte_perm(r[2 * x], 0, 0x3120);
+            const uint32_t w1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
+            const uint32_t f[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1),
+                                   e4m3x2_f16x2(w1 >> 16)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816<true>(o[nb][k + x], f, ph[nb][0], ph[nb][1]);
+          }
+        }
+      } else {
+        const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < kKSteps; ++k) {
+          uint32_t r[4];
+          ldmatrix4_trans(r, vt + tile_offset<L::kRow>(vr, 2 * k + vc));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma16816<false>(o[nb][k], r, ph[nb][0], ph[nb][1]);
+            mma16816<false>(o[nb][k], r, pl[nb][0], pl[nb][1]);
+          }
+        }
+      }
+    }
+    __syncwarp();  // all lanes are done with the stage before it is loaded again
+    if (++stage == kStages) stage = 0;
+
+    const bool item_done = cur.t + 1 == cur.nt;
+    if (item_done || tile + 1 == r1) {
+      // ---- join the four warps ----
+      const bool whole = t_begin == 0 && item_done;
+      const Cursor done = cur;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float l = sum[nb][x];
+#pragma unroll
+          for (int m = 4; m < 32; m <<= 1) l += __shfl_xor_sync(0xffffffffu, l, m);
+          // the reference its weights are relative to; -inf: no weight at all
+          float ref = top[nb][x] == -INFINITY ? 0.f : top[nb][x];
+          if (F8) ref -= kF16Shift;
+          if (top[nb][x] == -INFINITY && l == 0.f) ref = -INFINITY;
+          top[nb][x] = ref;
+          if (u8 == 0) s_ml[warp * N + nb * 8 + 2 * j4 + x] = make_float2(ref, l);
+        }
+      __syncthreads();
+      const bool more = tile + 1 < r1;
+      if (more) {
+        advance(cur, a);
+        stage_q(cur);  // every warp holds the old query in registers
+      }
+      const int g = done.hh / a.blocks, blk = done.hh - g * a.blocks;
+      const long long item = static_cast<long long>(done.b) * a.heads + done.hh;
+      const int part = 2 * cta + (first_item ? 0 : 1);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float f[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float M = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * N + nb * 8 + 2 * j4 + x].x);
+          f[x] = top[nb][x] == -INFINITY ? 0.f : ex2_approx(top[nb][x] - M);
+        }
+        const int row = tid >> 4, c4 = (tid & 15) * 4;  // of the sum below
+        float M = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * N + nb * 8 + row].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 ml = s_ml[w * N + nb * 8 + row];
+          l += ml.x == -INFINITY ? 0.f : ml.y * ex2_approx(ml.x - M);
+        }
+        const int hg = blk * N + nb * 8 + row;
+        const long long head = static_cast<long long>(done.b) * a.H + g * a.group + hg;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += kPassCols) {
+          float* to = s_sum + warp * 8 * kPassRow;
+#pragma unroll
+          for (int k = 0; k < kPassCols / 16; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int col = F8 ? k * 16 + 2 * u8 + (x >> 1) : k * 16 + u8 + 8 * (x >> 1);
+              to[(2 * j4 + (x & 1)) * kPassRow + col] = o[nb][c0 / 16 + k][x] * f[x & 1];
+            }
+          __syncthreads();
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(s_sum + (w * 8 + row) * kPassRow + c4);
+            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+          }
+          if (whole) {
+            if (hg < a.group) {
+              const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+              *reinterpret_cast<uint2*>(a.o + head * D + c0 + c4) =
+                  make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+            }
+          } else {
+            *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(part) * N + nb * 8 + row) * D +
+                                       c0 + c4) = v;
+          }
+          __syncthreads();
+        }
+        if ((tid & 15) == 0) {
+          if (!whole)
+            a.part_ml[static_cast<long long>(part) * N + nb * 8 + row] = make_float2(M, l);
+          else if (hg < a.group)
+            a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+        }
+      }
+      // What the join kernel needs, left by the CTA with the item's first tile:
+      // the item's parts lie in this CTA's slot and the first ones of the next.
+      if (tid == 0 && t_begin == 0) {
+        int parts = 0;
+        if (!item_done) {
+          const int last = tile - done.t + done.nt - 1;  // the item's last tile
+          int c1 = static_cast<int>((static_cast<long long>(last) * G) / tiles);
+          while (first_tile(c1 + 1, tiles, G) <= last) ++c1;
+          parts = c1 - cta + 1;
+        }
+        a.item[item] = parts ? (parts << 16) | part : 0;
+      }
+      first_item = false;
+      t_begin = 0;
+      if (more) begin_item();
+    } else {
+      ++cur.t;
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// Items cut between CTAs: one CTA per (sequence, query head) adds the parts up.
+template <int D, int N>
+__global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kVec = D / 32;  // columns of a lane
+  __shared__ float s_o[kWarps][D];
+  __shared__ float2 s_ml[kWarps];
+  const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
+  const int g = h / a.group, hg = h - g * a.group;
+  const int blk = hg / N, n = hg - blk * N;
+  const int info = __ldg(a.item + static_cast<long long>(b) * a.heads + g * a.blocks + blk);
+  if (info == 0) return;
+  const int parts = info >> 16, at = info & 0xffff;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // part 0 in slot `at`, part p in the first slot of the p-th CTA after it
+  auto slot_of = [&](int p) { return p == 0 ? at : (at / 2 + p) * 2; };
+  float M = -INFINITY, l = 0.f;
+  float o[kVec];
+#pragma unroll
+  for (int x = 0; x < kVec; ++x) o[x] = 0.f;
+  constexpr int kDeep = 4;
+  for (int p0 = warp; p0 < parts; p0 += kWarps * kDeep) {
+    float2 ml[kDeep];
+    float v[kDeep][kVec];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int p = p0 + u * kWarps;
+      const long long row = static_cast<long long>(slot_of(min(p, parts - 1))) * N + n;
+      ml[u] = p < parts ? a.part_ml[row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int x = 0; x < kVec; ++x) v[u][x] = a.part_o[row * D + x * 32 + lane];
+    }
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      if (ml[u].x == -INFINITY) continue;
+      const float to = fmaxf(M, ml[u].x);
+      const float fo = M == -INFINITY ? 0.f : ex2_approx(M - to);
+      const float fn = ex2_approx(ml[u].x - to);
+      l = l * fo + ml[u].y * fn;
+#pragma unroll
+      for (int x = 0; x < kVec; ++x) o[x] = o[x] * fo + v[u][x] * fn;
+      M = to;
+    }
+  }
+  if (lane == 0) s_ml[warp] = make_float2(M, l);
+#pragma unroll
+  for (int x = 0; x < kVec; ++x) s_o[warp][x * 32 + lane] = o[x];
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  M = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w].x);
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float f = s_ml[w].x == -INFINITY ? 0.f : ex2_approx(s_ml[w].x - M);
+    l += s_ml[w].y * f;
+    v += s_o[w][threadIdx.x] * f;
+  }
+  const long long head = static_cast<long long>(b) * a.H + h;
+  const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+  a.o[head * D + threadIdx.x] = __float2bfloat16_rn(v * f);
+  if (threadIdx.x == 0) a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+}
+
+template <int D, int NB, bool F8>
+cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, bool join, cudaStream_t stream) {
+  using L = Layout<D, NB, F8>;
+  static_assert(L::kBytes <= 113 * 1024, "two CTAs share an SM's shared memory");
+  auto kern = decode_kernel<D, NB, F8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(ctas), dim3(kThreads), L::kBytes, stream, a);
+  if (e != cudaSuccess || !join) return e;
+  return launch_pdl(decode_join_kernel<D, L::N>, dim3(static_cast<unsigned>(a.B) * a.H),
+                    dim3(kThreads), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_decode(const DecodeArgs& a, int ctas, bool join, cudaStream_t stream) {
+  const bool f8 = a.cache.type == ATTN_CACHE_E4M3, two = a.rows == 16;
+  if (a.cache.d == 64) {
+    if (f8)
+      return two ? launch_decode_t<64, 2, true>(a, ctas, join, stream)
+                 : launch_decode_t<64, 1, true>(a, ctas, join, stream);
+    return two ? launch_decode_t<64, 2, false>(a, ctas, join, stream)
+               : launch_decode_t<64, 1, false>(a, ctas, join, stream);
+  }
+  if (f8)
+    return two ? launch_decode_t<128, 2, true>(a, ctas, join, stream)
+               : launch_decode_t<128, 1, true>(a, ctas, join, stream);
+  return two ? launch_decode_t<128, 2, false>(a, ctas, join, stream)
+             : launch_decode_t<128, 1, false>(a, ctas, join, stream);
+}
+
+}  // namespace eba

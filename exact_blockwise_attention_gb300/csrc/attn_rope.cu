@@ -1,0 +1,329 @@
+// Rotary positions over several axes (time, height, width of video tokens),
+// and new keys and values written into a paged cache with the keys rotated on
+// the way. The rotation and its angles: rope.cuh.
+//
+// Both kernels are bound by memory: each element is read once and written
+// once, with about 3 flops an element. A thread owns 8 pairs of one token (two
+// 16-byte vectors) and keeps their 8 cosines and sines in registers while it
+// walks several heads, so the trigonometry (about 45 instructions a pair) is
+// paid once per group of heads and not per element.
+#include "rope.cuh"
+
+namespace eba {
+namespace {
+
+constexpr int kRopeThreads = 128;
+constexpr int kUnroll = 4;  // heads whose loads are in flight together
+
+struct Vec16 {  // 16 elements of one head: two 16-byte vectors
+  uint4 a, b;
+};
+
+__device__ __forceinline__ Vec16 load16(const __nv_bfloat16* p, int off_a, int off_b) {
+  Vec16 v;
+  v.a = __ldg(reinterpret_cast<const uint4*>(p + off_a));
+  v.b = __ldg(reinterpret_cast<const uint4*>(p + off_b));
+  return v;
+}
+
+__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
+  x[0] = bf16lo_f32(v.x), x[1] = bf16hi_f32(v.x), x[2] = bf16lo_f32(v.y), x[3] = bf16hi_f32(v.y);
+  x[4] = bf16lo_f32(v.z), x[5] = bf16hi_f32(v.z), x[6] = bf16lo_f32(v.w), x[7] = bf16hi_f32(v.w);
+}
+
+// The cosines and sines of a thread's 8 pairs.
+struct Turn8 {
+  float c[8], s[8];
+};
+
+// 8 pairs: (a[i], b[i]) with halves as pairs, or neighbours (x0 x1) (x2 x3) ...
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn16(float (&a)[8], float (&b)[8], const Turn8& t) {
+  if constexpr (INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      rope_turn(a[2 * i], a[2 * i + 1], t.c[i], t.s[i]);
+      rope_turn(b[2 * i], b[2 * i + 1], t.c[i + 4], t.s[i + 4]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rope_turn(a[i], b[i], t.c[i], t.s[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                    pack_bf16(x[6], x[7]));
+}
+
+// Lane i of a token's D / 16: its two vectors' element offsets. Lanes below
+// n_pairs / 8 hold rotated pairs; the others elements behind the rotated ones.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void lane_offsets(int i, int n_pairs, int& off_a, int& off_b) {
+  if (INTERLEAVED || 8 * i >= n_pairs) {
+    off_a = 16 * i;
+    off_b = 16 * i + 8;
+  } else {
+    off_a = 8 * i;
+    off_b = n_pairs + 8 * i;
+  }
+}
+
+// cos, sin of pairs 8 i .. 8 i + 7 at the positions pos[axis * stride].
+__device__ __forceinline__ void lane_turn(const attn_rope_t& r, int i, const int* pos,
+                                          long long stride, float sign, Turn8& t) {
+  int p[ATTN_MAX_AXES];
+#pragma unroll
+  for (int a = 0; a < ATTN_MAX_AXES; ++a) p[a] = a < r.n_axes ? __ldg(pos + a * stride) : 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int axis = r.axis[8 * i + j];
+    int pj = p[0];
+#pragma unroll
+    for (int a = 1; a < ATTN_MAX_AXES; ++a) pj = axis == a ? p[a] : pj;
+    rope_cs(pj, r.turns[8 * i + j], sign, t.c[j], t.s[j]);
+  }
+}
+
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kLanes = D / 16;
+  const long long id = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
+  const int i = static_cast<int>(id % kLanes);
+  const long long token = id / kLanes;
+  if (token >= a.tokens) return;
+  const long long b = token / a.L;
+  const long long l = token - b * a.L;
+  const int h0 = blockIdx.y * a.heads_per;
+  const int h1 = min(h0 + a.heads_per, a.H[0] + a.H[1]);
+  int off_a, off_b;
+  lane_offsets<INTERLEAVED>(i, a.rope.n_pairs, off_a, off_b);
+  const bool turns = 8 * i < a.rope.n_pairs;
+  const __nv_bfloat16* src[2];
+  __nv_bfloat16* dst[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    src[x] = static_cast<const __nv_bfloat16*>(a.in[x]) + b * a.si[x][0] + l * a.si[x][2];
+    dst[x] = static_cast<__nv_bfloat16*>(a.out[x]) + b * a.so[x][0] + l * a.so[x][2];
+  }
+  auto from = [&](int h) {
+    return h < a.H[0] ? src[0] + h * a.si[0][1] : src[1] + (h - a.H[0]) * a.si[1][1];
+  };
+  auto to = [&](int h) {
+    return h < a.H[0] ? dst[0] + h * a.so[0][1] : dst[1] + (h - a.H[0]) * a.so[1][1];
+  };
+  // the first heads' loads go out before the trigonometry
+  Vec16 v[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u)
+    if (h0 + u < h1) v[u] = load16(from(h0 + u), off_a, off_b);
+  Turn8 t;
+  if (turns) lane_turn(a.rope, i, a.pos + b * a.pos_batch + l, a.pos_axis, a.sign, t);
+  for (int h = h0; h < h1; h += kUnroll) {
+    if (h > h0) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (h + u < h1) v[u] = load16(from(h + u), off_a, off_b);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h + u >= h1) break;
+      __nv_bfloat16* o = to(h + u);
+      if (turns) {
+        float x[8], y[8];
+        widen8(v[u].a, x);
+        widen8(v[u].b, y);
+        turn16<INTERLEAVED>(x, y, t);
+        v[u].a = pack8(x);  // the one rounding, to the output's type
+        v[u].b = pack8(y);
+      }
+      *reinterpret_cast<uint4*>(o + off_a) = v[u].a;
+      *reinterpret_cast<uint4*>(o + off_b) = v[u].b;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// New rows into the pages
+// ---------------------------------------------------------------------------
+
+// The sequence of token t: the s with cu[s] <= t < cu[s + 1], or -1 for a
+// token outside [cu[0], cu[n]).
+__device__ __forceinline__ int find_sequence(const int* cu, int n, long long t) {
+  if (t < __ldg(cu) || t >= __ldg(cu + n)) return -1;
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Where token t goes: its cache position, its page (or -1: it is not written)
+// and its slot. Anything out of range is recorded in the status word.
+__device__ __forceinline__ long long find_page(const AppendArgs& a, long long t, long long& at,
+                                               int& slot) {
+  int s;
+  long long back;  // new tokens of the sequence from this one on
+  if (a.cu_new) {
+    s = find_sequence(a.cu_new, a.n_seqs, t);
+    if (s < 0) return -1;  // behind the last sequence: padding
+    back = __ldg(a.cu_new + s + 1) - t;
+  } else {
+    s = static_cast<int>(t);
+    back = 1;
+  }
+  const int len = __ldg(a.lens + s);
+  if (len == 0) return -1;  // an empty slot of the batch
+  at = len - back;
+  if (at < 0 || at >= static_cast<long long>(a.max_pages) * a.cache.page_size) {
+    atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+    return -1;
+  }
+  const int entry = static_cast<int>(at) / a.cache.page_size;
+  slot = static_cast<int>(at) - entry * a.cache.page_size;
+  const int page = __ldg(a.table + s * a.table_stride + entry);
+  if (page < 0 || page >= a.cache.n_pages) {
+    atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+    return -1;
+  }
+  return page;
+}
+
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv) {
+  return make_uint2(pack_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                    pack_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+}
+
+template <int D, bool INTERLEAVED, bool F8>
+__global__ void __launch_bounds__(kRopeThreads)
+    append_kernel(const __grid_constant__ AppendArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kLanes = D / 16;
+  const long long id = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
+  const int i = static_cast<int>(id % kLanes);
+  const long long token = id / kLanes;
+  if (token >= a.tokens) return;
+  const int h0 = blockIdx.y * a.heads_per;
+  const int h1 = min(h0 + a.heads_per, a.cache.H_kv);
+  int off_a, off_b;
+  lane_offsets<INTERLEAVED>(i, a.rope.n_pairs, off_a, off_b);
+  const bool turns = 8 * i < a.rope.n_pairs;
+  const __nv_bfloat16* ks = static_cast<const __nv_bfloat16*>(a.k) + token * a.k_token;
+  const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(a.v) + token * a.v_token;
+  Vec16 k[kUnroll], v[kUnroll];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h + u < h1) {
+        k[u] = load16(ks + (h + u) * a.k_head, off_a, off_b);
+        v[u] = load16(vs + (h + u) * a.v_head, 16 * i, 16 * i + 8);
+      }
+    }
+  };
+  fetch(h0);
+  long long at = 0;
+  int slot = 0;
+  const long long page = find_page(a, token, at, slot);
+  if (page < 0) return;
+  Turn8 t;
+  if (turns) {
+    if (a.pos) {
+      lane_turn(a.rope, i, a.pos + token, a.pos_axis, 1.f, t);
+    } else {  // one axis: the place in the cache
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        rope_cs(static_cast<int>(at), a.rope.turns[8 * i + j], 1.f, t.c[j], t.s[j]);
+    }
+  }
+  const attn_cache_t& c = a.cache;
+  const long long kd = page * c.k_strides[0] + slot * c.k_strides[1];
+  const long long vd = page * c.v_strides[0] + slot * c.v_strides[1];
+  for (int h = h0; h < h1; h += kUnroll) {
+    if (h > h0) fetch(h);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h + u >= h1) break;
+      const long long ko = kd + (h + u) * c.k_strides[2];
+      const long long vo = vd + (h + u) * c.v_strides[2];
+      float x[8], y[8];
+      if (F8 || turns) {
+        widen8(k[u].a, x);
+        widen8(k[u].b, y);
+        if (turns) turn16<INTERLEAVED>(x, y, t);
+      }
+      if constexpr (F8) {
+        // one rounding: fp32 straight to e4m3 (to nearest, saturating)
+        unsigned char* kp = static_cast<unsigned char*>(c.k) + ko;
+        *reinterpret_cast<uint2*>(kp + off_a) = pack8_e4m3(x, a.k_inv);
+        *reinterpret_cast<uint2*>(kp + off_b) = pack8_e4m3(y, a.k_inv);
+        widen8(v[u].a, x);
+        widen8(v[u].b, y);
+        const uint2 lo = pack8_e4m3(x, a.v_inv), hi = pack8_e4m3(y, a.v_inv);
+        *reinterpret_cast<uint4*>(static_cast<unsigned char*>(c.v) + vo + 16 * i) =
+            make_uint4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        if (turns) {
+          k[u].a = pack8(x);
+          k[u].b = pack8(y);
+        }
+        __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(c.k) + ko;
+        *reinterpret_cast<uint4*>(kp + off_a) = k[u].a;
+        *reinterpret_cast<uint4*>(kp + off_b) = k[u].b;
+        __nv_bfloat16* vp = static_cast<__nv_bfloat16*>(c.v) + vo + 16 * i;
+        *reinterpret_cast<uint4*>(vp) = v[u].a;
+        *reinterpret_cast<uint4*>(vp + 8) = v[u].b;
+      }
+    }
+  }
+}
+
+// Heads a thread walks: 8 where that leaves 512 threads for each SM, fewer for
+// few tokens, where spreading the heads over more threads is what shortens the
+// call.
+int heads_per_thread(long long lanes, int heads) {
+  int per = 8;
+  while (per > 1 && lanes * ((heads + per - 1) / per) < 152ll * 512) per /= 2;
+  return per;
+}
+
+template <typename Args, typename F>
+cudaError_t launch_rows(Args& a, int lanes, int heads, F kern, cudaStream_t stream) {
+  const long long threads = a.tokens * lanes;
+  a.heads_per = heads_per_thread(threads, heads);
+  const dim3 grid(static_cast<unsigned>((threads + kRopeThreads - 1) / kRopeThreads),
+                  static_cast<unsigned>((heads + a.heads_per - 1) / a.heads_per));
+  return launch_pdl(kern, grid, dim3(kRopeThreads), 0, stream, a);
+}
+
+template <int D>
+cudaError_t launch_rope_d(RopeArgs& a, cudaStream_t stream) {
+  const int heads = a.H[0] + a.H[1];
+  return a.rope.interleaved ? launch_rows(a, D / 16, heads, rope_kernel<D, true>, stream)
+                            : launch_rows(a, D / 16, heads, rope_kernel<D, false>, stream);
+}
+
+template <int D, bool F8>
+cudaError_t launch_append_d(AppendArgs& a, cudaStream_t stream) {
+  const int heads = a.cache.H_kv;
+  return a.rope.interleaved ? launch_rows(a, D / 16, heads, append_kernel<D, true, F8>, stream)
+                            : launch_rows(a, D / 16, heads, append_kernel<D, false, F8>, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(RopeArgs& a, int d, cudaStream_t stream) {
+  return d == 64 ? launch_rope_d<64>(a, stream) : launch_rope_d<128>(a, stream);
+}
+
+cudaError_t launch_append(AppendArgs& a, cudaStream_t stream) {
+  const bool f8 = a.cache.type == ATTN_CACHE_E4M3;
+  if (a.cache.d == 64)
+    return f8 ? launch_append_d<64, true>(a, stream) : launch_append_d<64, false>(a, stream);
+  return f8 ? launch_append_d<128, true>(a, stream) : launch_append_d<128, false>(a, stream);
+}
+
+}  // namespace eba

@@ -64,7 +64,8 @@ enum {
   ATTN_ERR_MISALIGNED = 3,  /* a pointer is not 16-byte aligned */
   ATTN_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed */
   ATTN_ERR_TIMEOUT = 5,     /* a bounded in-kernel wait ran out (from attn_poll_device_status) */
-  ATTN_ERR_WORKSPACE = 6    /* workspace missing or smaller than attn_bwd_workspace_size */
+  ATTN_ERR_WORKSPACE = 6,   /* workspace missing or smaller than attn_bwd_workspace_size */
+  ATTN_ERR_PAGE = 7         /* a cached length or page out of range (from attn_poll_device_status) */
 };
 
 /* Maximum number of KV chunks accepted by attn_split_fwd. */
@@ -282,6 +283,133 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
                     const int* cu_seqlens_k, int n_seqs, int H, int d, float scale,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Rotary positions with several axes (time, height and width of video tokens,
+ * or one axis of text positions): pairs of a head's elements are turned by an
+ * angle that grows with the token's position on the pair's axis, so that q . k
+ * depends on position differences alone.
+ *
+ * attn_rope_t describes the rotation; fill it with attn_rope_init and keep it
+ * (host memory, no device state). The first 2 n_pairs elements of each head
+ * are rotated, the others pass unchanged. Pair i is (x_i, x_(i + n_pairs)), or
+ * with `interleaved` (x_2i, x_2i+1). The token at position p of axis axis[i]
+ * turns pair i by p * freq_i radians.
+ */
+#define ATTN_MAX_AXES 4
+#define ATTN_MAX_PAIRS 64
+typedef struct {
+  int n_pairs;      /* a multiple of 8, at most d / 2 */
+  int n_axes;       /* 1 .. ATTN_MAX_AXES */
+  int interleaved;
+  unsigned char axis[ATTN_MAX_PAIRS];
+  unsigned long long turns[ATTN_MAX_PAIRS]; /* freq / (2 pi) mod 1, in units of 2^-64 turns */
+} attn_rope_t;
+
+/*
+ * attn_rope_init - fill *r. axis, freq: HOST arrays of n_pairs (axis[i] in
+ * [0, n_axes); freq[i] finite, radians per position, any sign).
+ */
+int attn_rope_init(attn_rope_t* r, int n_pairs, int n_axes, const int* axis, const double* freq,
+                   int interleaved);
+
+/*
+ * attn_rope - rotate q and k (k may be NULL with H_k = 0).
+ *   q, q_out [B, H_q, L, d], k, k_out [B, H_k, L, d] bf16 with any strides
+ *   (batch, head, token; in elements, multiples of 8, the elements of a head
+ *   contiguous): token-major [T, H, d] tensors are B = 1 with their strides.
+ *   pos: device int32, position of token l of batch b on axis a at
+ *   pos[a * pos_strides[0] + b * pos_strides[1] + l]; pos_strides[1] = 0
+ *   shares the positions among the batch. Any int32 value.
+ *   inverse: rotate by the negative angles. That is the gradient: d(q) =
+ *   inverse rotation of d(q_out).
+ * The angle is exact to 2^-32 turns at every position; the rotation runs in
+ * fp32 and is rounded once. Outputs must not overlap inputs.
+ */
+int attn_rope(const attn_rope_t* r, const void* q, const long long* q_strides, void* q_out,
+              const long long* q_out_strides, const void* k, const long long* k_strides,
+              void* k_out, const long long* k_out_strides, const int* pos,
+              const long long* pos_strides, int B, int H_q, int H_k, int L, int d, int inverse,
+              void* stream);
+
+/*
+ * A paged key-value cache: n_pages pages of page_size tokens of H_kv heads. The
+ * row of a token's head is d contiguous elements of `type`, at page * strides[0]
+ * + slot * strides[1] + head * strides[2] elements; strides and pointers are
+ * multiples of 16 bytes (so [pages, page_size, H_kv, d] and [pages, H_kv,
+ * page_size, d] layouts both serve). An e4m3 element stands for its value times
+ * k_scale (v_scale); bf16 caches have both 1.
+ *
+ * A batch of n_seqs sequences uses it through a page table, device int32
+ * [n_seqs, max_pages] with rows table_stride apart, and seq_lens, device int32
+ * [n_seqs]: token p of sequence b lies in page table[b][p / page_size] at slot
+ * p % page_size. Table entries behind a sequence's last token are not read.
+ * Lengths and tables are read by the GPU, so a captured call follows them.
+ * They cannot be checked before the launch: a length below 0 or above
+ * max_pages * page_size counts as the nearest of the two, the keys of a page
+ * outside [0, n_pages) count as absent (and are not written), nothing out of
+ * range is read or written, and ATTN_ERR_PAGE is recorded in the status word
+ * that attn_poll_device_status reads.
+ */
+enum { ATTN_CACHE_BF16 = 0, ATTN_CACHE_E4M3 = 1 };
+typedef struct {
+  void* k;
+  void* v;
+  long long k_strides[3], v_strides[3];
+  long long n_pages;
+  int page_size, H_kv, d, type;
+  float k_scale, v_scale;
+} attn_cache_t;
+
+/*
+ * attn_cache_append - write new keys and values into the cache, the keys
+ * rotated on the way (rope NULL: as they are).
+ *   k, v [T, H_kv, d] bf16; strides (token, head) in elements, multiples of 8.
+ *   seq_lens are the lengths WITH the new tokens, which are the last ones of
+ *   their sequences. cu_new: device int32 [n_seqs + 1], the new tokens of
+ *   sequence b are rows [cu_new[b], cu_new[b + 1]) of k and v; NULL: one new
+ *   token per sequence (T = n_seqs). Rows outside [cu_new[0], cu_new[n_seqs])
+ *   and rows of a sequence of length 0 (an empty slot of a padded batch) are
+ *   not written. A token whose place would be negative (more new tokens than
+ *   the sequence is long) or behind the table is not written and recorded as
+ *   ATTN_ERR_PAGE.
+ *   pos: device int32 [n_axes, T] with rows pos_stride apart; NULL (n_axes = 1
+ *   only): a token's position is its place in its sequence.
+ * bf16: rounded once. e4m3: value / scale, rounded to nearest once, saturating
+ * at +-448 (NaN stays NaN). The new tokens' pages must not be shared: two
+ * tokens that go to one slot leave a mixture of both there.
+ */
+int attn_cache_append(const attn_cache_t* cache, const void* k, const long long* k_strides,
+                      const void* v, const long long* v_strides, const int* page_table,
+                      long long table_stride, int max_pages, const int* seq_lens, int n_seqs,
+                      const int* cu_new, int T, const attn_rope_t* rope, const int* pos,
+                      long long pos_stride, void* stream);
+
+/* Scratch bytes of attn_decode (0 if an argument is invalid). */
+size_t attn_decode_workspace_size(int B, int H, int H_kv, int d);
+
+/*
+ * attn_decode - attention of one new token per sequence over its cached keys.
+ *   q [B, H, d] bf16, strides (sequence, head) in elements, multiples of 8; H
+ *   a multiple of the cache's H_kv, query head h reads K/V head h / (H / H_kv).
+ *   seq_lens [B]: the keys each sequence attends to, 0 included: O = 0 and
+ *   lse = -inf, as for a sequence whose scores are all -inf.
+ *   rope: q is rotated on the way and rounded to bf16, as attn_rope gives it
+ *   (NULL: q as it is); pos as for attn_cache_append with T = B, NULL: position
+ *   seq_lens[b] - 1.
+ *   o [B, H, d] bf16, lse [B, H] fp32 (contiguous outputs).
+ *   workspace: device scratch of attn_decode_workspace_size(B, H, H_kv, d)
+ *   bytes, 16-byte aligned, contents on entry do not matter; calls that may
+ *   overlap on the GPU need one each.
+ * Deterministic for given lengths, sizes and inputs. Scores, sums and outputs
+ * in fp32; the softmax weights enter the product with V as two bf16 terms
+ * (2^-15), or with an e4m3 cache as fp16 (2^-11).
+ */
+int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_strides,
+                const int* page_table, long long table_stride, int max_pages, const int* seq_lens,
+                int B, int H, float scale, const attn_rope_t* rope, const int* pos,
+                long long pos_stride, void* o, float* lse, void* workspace,
+                size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* attn_status_string(int status);
 
@@ -291,7 +419,8 @@ const char* attn_status_string(int status);
  * library on this device gave up a bounded wait since the last poll,
  * ATTN_ERR_CUDA if the synchronisation itself failed or a backward kernel found
  * its dynamic shared memory not 1024-byte aligned (it then computed nothing;
- * never observed on GB300), else ATTN_OK.
+ * never observed on GB300), ATTN_ERR_PAGE if a paged-cache call met a length or
+ * a page out of range, else ATTN_OK.
  */
 int attn_poll_device_status(void* stream);
 

@@ -18,3 +18,4 @@ from .attention import (  # noqa: F401
     varlen_backward,
     varlen_forward,
 )
+from .cache import decode, gather, rope  # noqa: F401
