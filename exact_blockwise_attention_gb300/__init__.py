@@ -562,54 +562,104 @@ class Rope:
 
 
 def _launch(device, fn, *args):
-    """Call an entry point on the current stream of ``device``."""
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream())
+    """Call an entry point on the current stream of ``device``. (The raw handle:
+    building a Stream object takes longer than the launch.)"""
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream())
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != ATTN_OK:
         raise AttnError(fn.__name__, st)
 
 
-def _rope(q, k, positions, plan, inverse):
+class _Layouts(dict):
+    """What a call's checks made of its tensors' shapes, strides, types and
+    devices, by those alone: calls of the same form skip the checks, which take
+    longer than a small launch. Addresses are checked in every call."""
+
+    def add(self, key, value):
+        if len(self) >= 1024:
+            self.clear()
+        self[key] = value
+        return value
+
+
+def _form(t):
+    """What a tensor's checks depend on (None stays None)."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _off_boundary(name):
+    return ValueError(f"{name}'s rows must start on 16-byte boundaries")
+
+
+_ROPE_LAYOUTS = _Layouts()
+
+
+def _rope_layout(q, k, positions, plan):
+    """Checks a rotation's arguments: sizes, strides (batch, head, token) and the
+    output's strides, as the C ABI takes them."""
     if not isinstance(plan, Rope):
         raise ValueError("plan must be a Rope")
     nd = q.dim() if isinstance(q, torch.Tensor) else 0
     if nd not in (3, 4):
         raise ValueError("q must be a [B, H, L, d] or [T, H, d] tensor")
+    packed = nd == 3
     sq = _rows(q, "q", nd)
     d = q.shape[-1]
     if 2 * plan.n_pairs > d:
         raise ValueError(f"the plan rotates {2 * plan.n_pairs} elements of a head of {d}")
-    packed = nd == 3
     B, H, L = (1, q.shape[1], q.shape[0]) if packed else q.shape[:3]
-    sk, Hk = None, 0
+
+    def order(s):
+        return _Strides3(0, s[1], s[0]) if packed else _Strides3(*s)
+
+    def fresh(heads):
+        return _Strides3(0, d, heads * d) if packed else _Strides3(heads * L * d, L * d, d)
+
+    Hk, sk, sko = 0, None, None
     if k is not None:
-        sk, Hk = _rows(k, "k", nd), k.shape[1]
+        sk = order(_rows(k, "k", nd))
+        Hk = k.shape[1]
         like = (L, Hk, d) if packed else (B, Hk, L, d)
         if tuple(k.shape) != like or k.device != q.device:
             raise ValueError(f"k must be {like} on {q.device}, got {tuple(k.shape)} on {k.device}")
-    dev = q.device
-    if not packed and isinstance(positions, torch.Tensor) and positions.dim() == (
-            3 if plan.n_axes > 1 or positions.dim() == 3 else 2) and positions.shape[-2:] == (B, L):
-        axis, batch = plan._positions(positions, dev, (B, L)), positions.stride(-2)
+        sko = fresh(Hk)
+    per_batch = (not packed and isinstance(positions, torch.Tensor)
+                 and positions.dim() == (2 if plan.n_axes == 1 and positions.dim() < 3 else 3)
+                 and positions.shape[-2] == B)
+    if per_batch:
+        axis, batch = plan._positions(positions, q.device, (B, L)), positions.stride(-2)
     else:
-        axis, batch = plan._positions(positions, dev, (L,)), 0
+        axis, batch = plan._positions(positions, q.device, (L,)), 0
+    return (order(sq), fresh(H), sk, sko, _Strides2(axis, batch), B, H, Hk, L, d)
 
-    def order(s):  # batch, head, token
-        return _Strides3(0, s[1], s[0]) if packed else _Strides3(*s)
 
-    def fresh(t):
-        o = torch.empty(t.shape, device=dev, dtype=torch.bfloat16)
-        return o, order(o.stride()[:-1])
-
-    qo, sqo = fresh(q)
-    ko, sko = (None, None) if k is None else fresh(k)
-    _launch(dev, lib().attn_rope, plan._struct, q.data_ptr(), order(sq), qo.data_ptr(), sqo,
-            None if k is None else k.data_ptr(), None if k is None else order(sk),
-            None if k is None else ko.data_ptr(), sko, positions.data_ptr(),
-            _Strides2(axis, batch), B, H, Hk, L, d, int(inverse))
+def _rope(q, k, positions, plan, inverse):
+    try:
+        key = (_form(q), _form(k), _form(positions), plan.n_axes, plan.n_pairs)
+        lay = _ROPE_LAYOUTS.get(key)
+    except AttributeError:
+        lay = key = None
+    if lay is None:
+        lay = _rope_layout(q, k, positions, plan)
+        _ROPE_LAYOUTS.add(key, lay)
+    sq, sqo, sk, sko, sp, B, H, Hk, L, d = lay
+    qp = q.data_ptr()
+    if qp & 15:
+        raise _off_boundary("q")
+    qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+    ko = kp = kop = None
+    if k is not None:
+        kp = k.data_ptr()
+        if kp & 15:
+            raise _off_boundary("k")
+        ko = torch.empty_like(k, memory_format=torch.contiguous_format)
+        kop = ko.data_ptr()
+    _launch(q.device, lib().attn_rope, plan._struct, qp, sq, qo.data_ptr(), sqo, kp, sk, kop, sko,
+            positions.data_ptr(), sp, B, H, Hk, L, d, inverse)
     return qo, ko
 
 
@@ -629,9 +679,11 @@ def rope_bwd(dq, dk, positions, plan):
 
 def _rotatable(g):
     """A gradient as the kernel reads it: autograd also hands over expanded or transposed ones."""
-    ok = g is None or (g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and
-                       all(s % 8 == 0 for s, n in zip(g.stride()[:-1], g.shape) if n != 1))
-    return g if ok else g.contiguous()
+    if g is None or (g.is_contiguous() and not g.data_ptr() & 15):
+        return g
+    ok = g.stride(-1) == 1 and not g.data_ptr() & 15 and \
+        all(s % 8 == 0 for s, n in zip(g.stride()[:-1], g.shape) if n != 1)
+    return g if ok else g.clone(memory_format=torch.contiguous_format)
 
 
 class _Rotation(torch.autograd.Function):
@@ -646,10 +698,12 @@ class _Rotation(torch.autograd.Function):
     def backward(ctx, dq, dk):
         (positions,) = ctx.saved_tensors
         dq, dk = _rotatable(dq), _rotatable(dk)
+        # (under create_graph the gradient is a rotation with a gradient of its own)
+        turn = _Rotation.apply if torch.is_grad_enabled() else _rope
         if dq is None and dk is not None:
-            dk, dq = _Rotation.apply(dk, None, positions, ctx.plan, not ctx.inverse)
+            dk, dq = turn(dk, None, positions, ctx.plan, not ctx.inverse)
         elif dq is not None:
-            dq, dk = _Rotation.apply(dq, dk, positions, ctx.plan, not ctx.inverse)
+            dq, dk = turn(dq, dk, positions, ctx.plan, not ctx.inverse)
         return dq, dk, None, None, None
 
 
@@ -706,6 +760,7 @@ class PagedCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
         self.n_pages, self.page_size, self.H_kv, self.d = k.shape
         self.device = k.device
+        self._key = (self.H_kv, self.d, self.device)  # what the checks of a call depend on
         self._struct = s
 
     def _at(self):
@@ -753,6 +808,30 @@ def cache_append(cache, k, v, page_table, seq_lens, cu_new=None, rope=None, posi
     [n_axes, T]; without them (one axis) a token's place in its sequence. The
     pages written must not be shared. Lengths and pages out of range write
     nothing and are reported by poll_device_status."""
+    try:
+        key = (_form(k), _form(v), _form(page_table), _form(seq_lens), _form(cu_new), _form(positions),
+               cache._key, None if rope is None else (rope.n_axes, rope.n_pairs))
+        lay = _APPEND_LAYOUTS.get(key)
+    except AttributeError:
+        lay = key = None
+    if lay is None:
+        lay = _append_layout(cache, k, v, page_table, seq_lens, cu_new, rope, positions)
+        _APPEND_LAYOUTS.add(key, lay)
+    sk, sv, row, wide, n, T, stride = lay
+    kp, vp = k.data_ptr(), v.data_ptr()
+    if (kp | vp) & 15:
+        raise _off_boundary("k's or v")
+    _launch(cache.device, lib().attn_cache_append, cache._at(), kp, sk, vp, sv,
+            page_table.data_ptr(), row, wide, seq_lens.data_ptr(), n,
+            None if cu_new is None else cu_new.data_ptr(), T, None if rope is None else rope._struct,
+            None if positions is None else positions.data_ptr(), stride)
+
+
+_APPEND_LAYOUTS = _Layouts()
+
+
+def _append_layout(cache, k, v, page_table, seq_lens, cu_new, rope, positions):
+    """Checks an append's arguments: strides and sizes as the C ABI takes them."""
     if not isinstance(cache, PagedCache):
         raise ValueError("cache must be a PagedCache")
     sk, sv = _rows(k, "k", 3), _rows(v, "v", 3)
@@ -769,11 +848,8 @@ def cache_append(cache, k, v, page_table, seq_lens, cu_new=None, rope=None, posi
             raise ValueError(f"cu_new must have {n + 1} entries, got {cu_new.shape[0]}")
     elif T != n:
         raise ValueError(f"without cu_new there is one new token per sequence: {n}, got {T}")
-    r, pos, stride = cache._turn(rope, positions, T)
-    _launch(cache.device, lib().attn_cache_append, cache._at(), k.data_ptr(), _Strides2(*sk),
-            v.data_ptr(), _Strides2(*sv), page_table.data_ptr(), page_table.stride(0),
-            page_table.shape[1], seq_lens.data_ptr(), n,
-            None if cu_new is None else cu_new.data_ptr(), T, r, pos, stride)
+    stride = cache._turn(rope, positions, T)[2]
+    return (_Strides2(*sk), _Strides2(*sv), page_table.stride(0), page_table.shape[1], n, T, stride)
 
 
 def decode_workspace_size(B, H, H_kv, d) -> int:
@@ -790,29 +866,51 @@ def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None
     positions, int32 [n_axes, B], or, with one axis and none given, by
     seq_lens - 1. page_table and seq_lens as for cache_append; the GPU reads
     them, so a captured call follows their contents."""
+    try:
+        key = (_form(q), _form(page_table), _form(seq_lens), _form(positions), cache._key,
+               None if rope is None else (rope.n_axes, rope.n_pairs))
+        lay = _DECODE_LAYOUTS.get(key)
+    except AttributeError:
+        lay = key = None
+    if lay is None:
+        lay = _decode_layout(cache, q, page_table, seq_lens, rope, positions)
+        _DECODE_LAYOUTS.add(key, lay)
+    sq, row, wide, B, H, d, stride, need = lay
+    dev = cache.device
+    qp = q.data_ptr()
+    if qp & 15:
+        raise _off_boundary("q")
+    if workspace is None:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    elif workspace.numel() * workspace.element_size() < need or workspace.device != dev or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {dev}")
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = torch.empty((B, H), device=dev, dtype=torch.float32)
+    _launch(dev, lib().attn_decode, cache._at(), qp, sq, page_table.data_ptr(), row, wide,
+            seq_lens.data_ptr(), B, H, _scale(scale, d), None if rope is None else rope._struct,
+            None if positions is None else positions.data_ptr(), stride, o.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), need)
+    return o, lse
+
+
+_DECODE_LAYOUTS = _Layouts()
+
+
+def _decode_layout(cache, q, page_table, seq_lens, rope, positions):
+    """Checks a decode's arguments: strides and sizes as the C ABI takes them, and
+    the bytes of workspace."""
     if not isinstance(cache, PagedCache):
         raise ValueError("cache must be a PagedCache")
     sq = _rows(q, "q", 3)
     B, H, d = q.shape
     if d != cache.d or H < 1 or H % cache.H_kv:
         raise ValueError(f"q must be [B, a multiple of {cache.H_kv}, {cache.d}], got {tuple(q.shape)}")
-    dev = cache.device
-    if q.device != dev:
-        raise ValueError(f"q must be on {dev}")
+    if q.device != cache.device:
+        raise ValueError(f"q must be on {cache.device}")
     n = cache._batch(page_table, seq_lens)
     if n != B:
         raise ValueError(f"q holds {B} sequences, seq_lens {n}")
-    r, pos, stride = cache._turn(rope, positions, B)
-    L = lib()
-    need = L.attn_decode_workspace_size(B, H, cache.H_kv, d)
-    if workspace is None:
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    elif workspace.numel() * workspace.element_size() < need or workspace.device != dev or \
-            not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {dev}")
-    o = torch.empty((B, H, d), device=dev, dtype=torch.bfloat16)
-    lse = torch.empty((B, H), device=dev, dtype=torch.float32)
-    _launch(dev, L.attn_decode, cache._at(), q.data_ptr(), _Strides2(*sq), page_table.data_ptr(),
-            page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(), B, H, _scale(scale, d),
-            r, pos, stride, o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), need)
-    return o, lse
+    stride = cache._turn(rope, positions, B)[2]
+    return (_Strides2(*sq), page_table.stride(0), page_table.shape[1], B, H, d, stride,
+            decode_workspace_size(B, H, cache.H_kv, d))

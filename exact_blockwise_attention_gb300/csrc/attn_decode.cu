@@ -29,8 +29,8 @@
 //    that its rounding stays far below that of the bf16 output; e4m3 caches:
 //    K and V widen exactly to fp16, q is scaled per head by a power of two
 //    into fp16's range (exact above 2^-28 of the head's largest element) and P
-//    is held as fp16, 2^15 at the running maximum (2^-12 relative down to
-//    2^-29 of the largest weight).
+//    is held as fp16, 2^7 to 2^15 at the running maximum (2^-11 relative down to
+//    2^-21 of the largest weight, steps of 2^-31 below).
 // Scores, maxima, sums and outputs are fp32 throughout.
 #include <cuda_fp16.h>
 
@@ -47,7 +47,8 @@ constexpr int kRingBytes = 24 * 1024;             // of each warp
 constexpr int kPassCols = 64;                     // columns of O summed over the warps at a time
 constexpr int kPassRow = kPassCols + 4;           // floats; +4: conflict-free column writes
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kF16Shift = 15.f;                 // e4m3 caches: P's largest value is 2^15
+constexpr float kSlack = 8.f;                     // scores may pass the reference by a factor 2^8
+constexpr float kF16Shift = 7.f;                  // e4m3 caches: P's largest value is 2^(8 + 7)
 static_assert(kTileKeys == kDecodeTileKeys, "");
 
 template <int D, int NB, bool F8>
@@ -167,7 +168,9 @@ __device__ __forceinline__ int first_tile(int i, int tiles, int ctas) {
   return static_cast<int>(static_cast<long long>(i) * tiles / ctas);
 }
 
-template <int D, int NB, bool F8>
+// WHOLE: the page size is a multiple of a step's 16 keys, so that a step lies in
+// one page and its rows are one stride apart; otherwise each row is looked up.
+template <int D, int NB, bool F8, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_kernel(const __grid_constant__ DecodeArgs a) {
   using L = Layout<D, NB, F8>;
@@ -244,46 +247,71 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* s_qs = reinterpret_cast<float*>(smem + L::kOffQs);
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + L::kOffMask) + warp * kStages;
 
-  // ---- loads: this lane looks up key (lane & 15) of the step ----
+  // ---- loads: WHOLE: the step's page; else this lane's key (lane & 15) ----
   Cursor ld = s_first;
   int ld_left = r1 - r0;
-  int page = -1, slot = 0;  // of this lane's key at ld
+  int page = -1, slot = 0;
+  bool held = false;  // whether there is such a key; its page is checked when it is used
   auto look_up = [&]() {
-    page = -1;
-    const int key = ld.t * kTileKeys + warp * kStepKeys + (lane & 15);
-    if (ld_left > 0 && key < ld.len) {
+    const int key = ld.t * kTileKeys + warp * kStepKeys + (WHOLE ? 0 : lane & 15);
+    held = ld_left > 0 && key < ld.len;
+    if (held) {
       const int entry = key / a.cache.page_size;
       slot = key - entry * a.cache.page_size;
       page = __ldg(a.table + ld.b * a.table_stride + entry);
-      if (page < 0 || page >= a.cache.n_pages) {
-        atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-        page = -1;
-      }
     }
   };
   auto issue = [&](int stage) {
     constexpr int kLanes = L::kRow / 16;     // of a row
     constexpr int kRows = 32 / kLanes;       // of an instruction
-    const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
-    if (lane == 0) s_mask[stage] = mask;
-    if (mask) {
-      const int g = ld.hh / a.blocks;
-      const long long pg = max(page, 0);
-      const long long ko = pg * a.k_strides[0] + slot * a.k_strides[1] + g * a.k_strides[2];
-      const long long vo = pg * a.v_strides[0] + slot * a.v_strides[1] + g * a.v_strides[2];
-      const uint32_t kt = ring + stage * 2 * L::kTile, vt = kt + L::kTile;
-      const int c = lane % kLanes;
+    if (!held) {
+      page = -1;
+    } else if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.cache.n_pages)) {
+      atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+      page = -1;
+    }
+    const uint32_t kt = ring + stage * 2 * L::kTile, vt = kt + L::kTile;
+    const int c = lane % kLanes, r_lane = lane / kLanes;
+    uint32_t mask;
+    if constexpr (WHOLE) {
+      const int count = page < 0 ? 0 : min(ld.len - ld.t * kTileKeys - warp * kStepKeys, kStepKeys);
+      mask = (1u << count) - 1u;
+      if (count > 0) {
+        const int g = ld.hh / a.blocks;
+        const unsigned char* kp = a.k + (page * a.k_strides[0] + (slot + r_lane) * a.k_strides[1] +
+                                         g * a.k_strides[2] + c * 16);
+        const unsigned char* vp = a.v + (page * a.v_strides[0] + (slot + r_lane) * a.v_strides[1] +
+                                         g * a.v_strides[2] + c * 16);
 #pragma unroll
-      for (int i = 0; i < kStepKeys / kRows; ++i) {
-        const int r = i * kRows + lane / kLanes;
-        const bool ok = (mask >> r) & 1;
-        const long long kr = __shfl_sync(0xffffffffu, ko, r);
-        const long long vr = __shfl_sync(0xffffffffu, vo, r);
-        const uint32_t to = tile_offset<L::kRow>(r, c);
-        cp_async16(kt + to, a.k + (ok ? kr + c * 16 : 0), ok);
-        cp_async16(vt + to, a.v + (ok ? vr + c * 16 : 0), ok);
+        for (int i = 0; i < kStepKeys / kRows; ++i) {
+          const int r = i * kRows + r_lane;  // rows behind the last key read nothing
+          const uint32_t to = tile_offset<L::kRow>(r, c);
+          cp_async16(kt + to, kp, r < count);
+          cp_async16(vt + to, vp, r < count);
+          kp += kRows * a.k_strides[1];
+          vp += kRows * a.v_strides[1];
+        }
+      }
+    } else {
+      mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+      if (mask) {
+        const int g = ld.hh / a.blocks;
+        const long long pg = max(page, 0);
+        const long long ko = pg * a.k_strides[0] + slot * a.k_strides[1] + g * a.k_strides[2];
+        const long long vo = pg * a.v_strides[0] + slot * a.v_strides[1] + g * a.v_strides[2];
+#pragma unroll
+        for (int i = 0; i < kStepKeys / kRows; ++i) {
+          const int r = i * kRows + r_lane;
+          const bool ok = (mask >> r) & 1;
+          const long long kr = __shfl_sync(0xffffffffu, ko, r);
+          const long long vr = __shfl_sync(0xffffffffu, vo, r);
+          const uint32_t to = tile_offset<L::kRow>(r, c);
+          cp_async16(kt + to, a.k + (ok ? kr + c * 16 : 0), ok);
+          cp_async16(vt + to, a.v + (ok ? vr + c * 16 : 0), ok);
+        }
       }
     }
+    if (lane == 0) s_mask[stage] = mask;
     cp_async_commit();
     if (--ld_left > 0) advance(ld, a);
     look_up();
@@ -436,25 +464,33 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // online softmax; element x of a lane: key u8 + 8 (x / 2), column 2 j4 + x % 2
       uint32_t ph[NB][2], pl[NB][2];
+      float v[NB][4];
+      bool grew = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float v[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const bool ok = (mask >> (u8 + 8 * (x >> 1))) & 1;
-          v[x] = ok ? (s[nb][0][x] + s[nb][1][x]) * qs[nb][x & 1] : -INFINITY;
-        }
-        float mx[2] = {fmaxf(v[0], v[2]), fmaxf(v[1], v[3])};
+        for (int x = 0; x < 4; ++x) v[nb][x] = (s[nb][0][x] + s[nb][1][x]) * qs[nb][x & 1];
+        if (mask != 0xffffu) {
 #pragma unroll
-        for (int m = 4; m < 32; m <<= 1) {
-          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], m));
-          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], m));
+          for (int x = 0; x < 4; ++x)
+            if (!((mask >> (u8 + 8 * (x >> 1))) & 1)) v[nb][x] = -INFINITY;
         }
-        const bool grew = mx[0] > top[nb][0] || mx[1] > top[nb][1];
-        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          grew |= fmaxf(v[nb][x], v[nb][x + 2]) > top[nb][x] + kSlack;
+      }
+      // The reference the weights are relative to follows the maximum only when
+      // that has grown by more than kSlack: one vote a step instead of a
+      // maximum over the lanes and a rescaled output.
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float to = fmaxf(top[nb][x], mx[x]);
+            float to = fmaxf(v[nb][x], v[nb][x + 2]);
+#pragma unroll
+            for (int m = 4; m < 32; m <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, m));
+            to = fmaxf(to, top[nb][x]);
             // -inf to -inf (a column whose scores are all -inf) keeps its zeros
             const float f = to == top[nb][x] ? 1.f : ex2_approx(top[nb][x] - to);
             top[nb][x] = to;
@@ -465,12 +501,14 @@ __global__ void __launch_bounds__(kThreads, 2)
               o[nb][k][x + 2] *= f;
             }
           }
-        }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
         float p[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const float ref = top[nb][x & 1] == -INFINITY ? 0.f : top[nb][x & 1];
-          p[x] = ex2_approx(v[x] - (F8 ? ref - kF16Shift : ref));
+          p[x] = ex2_approx(v[nb][x] - (F8 ? ref - kF16Shift : ref));
           sum[nb][x & 1] += p[x];
         }
         if constexpr (F8) {
@@ -700,7 +738,8 @@ template <int D, int NB, bool F8>
 cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, bool join, cudaStream_t stream) {
   using L = Layout<D, NB, F8>;
   static_assert(L::kBytes <= 113 * 1024, "two CTAs share an SM's shared memory");
-  auto kern = decode_kernel<D, NB, F8>;
+  auto kern = a.cache.page_size % kStepKeys == 0 ? decode_kernel<D, NB, F8, true>
+                                                 : decode_kernel<D, NB, F8, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(ctas), dim3(kThreads), L::kBytes, stream, a);

@@ -197,6 +197,8 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv) {
                     pack_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
 
+// blockIdx.z: the keys' or the values' half of the work (a thread that did both
+// would hold twice the registers, and its values would wait for its keys' angles).
 template <int D, bool INTERLEAVED, bool F8>
 __global__ void __launch_bounds__(kRopeThreads)
     append_kernel(const __grid_constant__ AppendArgs a) {
@@ -207,22 +209,21 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int i = static_cast<int>(id % kLanes);
   const long long token = id / kLanes;
   if (token >= a.tokens) return;
+  const bool keys = blockIdx.z == 0;
   const int h0 = blockIdx.y * a.heads_per;
   const int h1 = min(h0 + a.heads_per, a.cache.H_kv);
+  const bool turns = keys && 8 * i < a.rope.n_pairs;
   int off_a, off_b;
-  lane_offsets<INTERLEAVED>(i, a.rope.n_pairs, off_a, off_b);
-  const bool turns = 8 * i < a.rope.n_pairs;
-  const __nv_bfloat16* ks = static_cast<const __nv_bfloat16*>(a.k) + token * a.k_token;
-  const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(a.v) + token * a.v_token;
-  Vec16 k[kUnroll], v[kUnroll];
+  lane_offsets<INTERLEAVED>(i, keys ? a.rope.n_pairs : 0, off_a, off_b);
+  const attn_cache_t& c = a.cache;
+  const long long in_head = keys ? a.k_head : a.v_head;
+  const __nv_bfloat16* in = keys ? static_cast<const __nv_bfloat16*>(a.k) + token * a.k_token
+                                 : static_cast<const __nv_bfloat16*>(a.v) + token * a.v_token;
+  Vec16 v[kUnroll];
   auto fetch = [&](int h) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (h + u < h1) {
-        k[u] = load16(ks + (h + u) * a.k_head, off_a, off_b);
-        v[u] = load16(vs + (h + u) * a.v_head, 16 * i, 16 * i + 8);
-      }
-    }
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + u < h1) v[u] = load16(in + (h + u) * in_head, off_a, off_b);
   };
   fetch(h0);
   long long at = 0;
@@ -239,43 +240,35 @@ __global__ void __launch_bounds__(kRopeThreads)
         rope_cs(static_cast<int>(at), a.rope.turns[8 * i + j], 1.f, t.c[j], t.s[j]);
     }
   }
-  const attn_cache_t& c = a.cache;
-  const long long kd = page * c.k_strides[0] + slot * c.k_strides[1];
-  const long long vd = page * c.v_strides[0] + slot * c.v_strides[1];
+  const long long* st = keys ? c.k_strides : c.v_strides;
+  const long long out_head = st[2];
+  const long long row = page * st[0] + slot * st[1];
   for (int h = h0; h < h1; h += kUnroll) {
     if (h > h0) fetch(h);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (h + u >= h1) break;
-      const long long ko = kd + (h + u) * c.k_strides[2];
-      const long long vo = vd + (h + u) * c.v_strides[2];
+      const long long to = row + (h + u) * out_head;
       float x[8], y[8];
       if (F8 || turns) {
-        widen8(k[u].a, x);
-        widen8(k[u].b, y);
+        widen8(v[u].a, x);
+        widen8(v[u].b, y);
         if (turns) turn16<INTERLEAVED>(x, y, t);
       }
       if constexpr (F8) {
         // one rounding: fp32 straight to e4m3 (to nearest, saturating)
-        unsigned char* kp = static_cast<unsigned char*>(c.k) + ko;
-        *reinterpret_cast<uint2*>(kp + off_a) = pack8_e4m3(x, a.k_inv);
-        *reinterpret_cast<uint2*>(kp + off_b) = pack8_e4m3(y, a.k_inv);
-        widen8(v[u].a, x);
-        widen8(v[u].b, y);
-        const uint2 lo = pack8_e4m3(x, a.v_inv), hi = pack8_e4m3(y, a.v_inv);
-        *reinterpret_cast<uint4*>(static_cast<unsigned char*>(c.v) + vo + 16 * i) =
-            make_uint4(lo.x, lo.y, hi.x, hi.y);
+        unsigned char* p = static_cast<unsigned char*>(keys ? c.k : c.v) + to;
+        const float inv = keys ? a.k_inv : a.v_inv;
+        *reinterpret_cast<uint2*>(p + off_a) = pack8_e4m3(x, inv);
+        *reinterpret_cast<uint2*>(p + off_b) = pack8_e4m3(y, inv);
       } else {
         if (turns) {
-          k[u].a = pack8(x);
-          k[u].b = pack8(y);
+          v[u].a = pack8(x);
+          v[u].b = pack8(y);
         }
-        __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(c.k) + ko;
-        *reinterpret_cast<uint4*>(kp + off_a) = k[u].a;
-        *reinterpret_cast<uint4*>(kp + off_b) = k[u].b;
-        __nv_bfloat16* vp = static_cast<__nv_bfloat16*>(c.v) + vo + 16 * i;
-        *reinterpret_cast<uint4*>(vp) = v[u].a;
-        *reinterpret_cast<uint4*>(vp + 8) = v[u].b;
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(keys ? c.k : c.v) + to;
+        *reinterpret_cast<uint4*>(p + off_a) = v[u].a;
+        *reinterpret_cast<uint4*>(p + off_b) = v[u].b;
       }
     }
   }
@@ -284,33 +277,34 @@ __global__ void __launch_bounds__(kRopeThreads)
 // Heads a thread walks: 8 where that leaves 512 threads for each SM, fewer for
 // few tokens, where spreading the heads over more threads is what shortens the
 // call.
-int heads_per_thread(long long lanes, int heads) {
+int heads_per_thread(long long lanes, int heads) {  // lanes: threads for each head
   int per = 8;
   while (per > 1 && lanes * ((heads + per - 1) / per) < 152ll * 512) per /= 2;
   return per;
 }
 
 template <typename Args, typename F>
-cudaError_t launch_rows(Args& a, int lanes, int heads, F kern, cudaStream_t stream) {
+cudaError_t launch_rows(Args& a, int lanes, int heads, int parts, F kern, cudaStream_t stream) {
   const long long threads = a.tokens * lanes;
-  a.heads_per = heads_per_thread(threads, heads);
+  a.heads_per = heads_per_thread(threads * parts, heads);
   const dim3 grid(static_cast<unsigned>((threads + kRopeThreads - 1) / kRopeThreads),
-                  static_cast<unsigned>((heads + a.heads_per - 1) / a.heads_per));
+                  static_cast<unsigned>((heads + a.heads_per - 1) / a.heads_per),
+                  static_cast<unsigned>(parts));
   return launch_pdl(kern, grid, dim3(kRopeThreads), 0, stream, a);
 }
 
 template <int D>
 cudaError_t launch_rope_d(RopeArgs& a, cudaStream_t stream) {
   const int heads = a.H[0] + a.H[1];
-  return a.rope.interleaved ? launch_rows(a, D / 16, heads, rope_kernel<D, true>, stream)
-                            : launch_rows(a, D / 16, heads, rope_kernel<D, false>, stream);
+  return a.rope.interleaved ? launch_rows(a, D / 16, heads, 1, rope_kernel<D, true>, stream)
+                            : launch_rows(a, D / 16, heads, 1, rope_kernel<D, false>, stream);
 }
 
 template <int D, bool F8>
 cudaError_t launch_append_d(AppendArgs& a, cudaStream_t stream) {
   const int heads = a.cache.H_kv;
-  return a.rope.interleaved ? launch_rows(a, D / 16, heads, append_kernel<D, true, F8>, stream)
-                            : launch_rows(a, D / 16, heads, append_kernel<D, false, F8>, stream);
+  return a.rope.interleaved ? launch_rows(a, D / 16, heads, 2, append_kernel<D, true, F8>, stream)
+                            : launch_rows(a, D / 16, heads, 2, append_kernel<D, false, F8>, stream);
 }
 
 }  // namespace
