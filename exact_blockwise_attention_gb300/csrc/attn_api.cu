@@ -930,14 +930,15 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
   if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
   eba::DecodeArgs a{};
   const long long capacity = static_cast<long long>(max_pages) * cache->page_size;
-  a.max_len = static_cast<int>(std::min(capacity, (1ll << 31) - 1 - eba::kDecodeTileKeys));
+  const int esz = cache->type == ATTN_CACHE_E4M3 ? 1 : 2;
+  const int tile = eba::decode_tile_keys(cache->d * esz);
+  a.max_len = static_cast<int>(std::min(capacity, (1ll << 31) - 1 - tile));
   a.heads = cache->H_kv * p.blocks;
-  const long long item_tiles = (a.max_len + eba::kDecodeTileKeys - 1) / eba::kDecodeTileKeys;
+  const long long item_tiles = (a.max_len + tile - 1) / tile;
   const long long seq_tiles = item_tiles * a.heads;  // < 2^57
   if (seq_tiles >= (1ll << 31) || seq_tiles * B >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
   int* status = status_word_ptr();
   if (!status) return ATTN_ERR_CUDA;
-  const int esz = cache->type == ATTN_CACHE_E4M3 ? 1 : 2;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_seq = q_strides[0];
   a.q_head = q_strides[1];

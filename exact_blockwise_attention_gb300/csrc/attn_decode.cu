@@ -10,12 +10,12 @@
 // Every cached element is read once for its G query heads: 2 G flops per
 // element, far below what the card computes per byte, so the kernel is bound
 // by HBM reads. What it is built around:
-//  - The work is the list of all 64-key tiles of all (sequence, K/V head)
+//  - The work is the list of all 64- or 128-key tiles of all (sequence, K/V head)
 //    items, cut into equal runs, one per CTA (two CTAs per SM): long and short
 //    sequences balance without the host knowing the lengths, and a call can be
 //    captured and replayed with other lengths. An item cut between CTAs leaves
 //    fp32 partials, which the join kernel adds up in the order of the keys.
-//  - A warp owns 16 keys of each tile and walks the CTA's run on its own, with
+//  - A warp owns 16 or 32 keys of each tile and walks the CTA's run on its own, with
 //    its own running maximum and sums: its loads (cp.async, 16 bytes a lane,
 //    rows of whole cache lines) run several tiles ahead, across item borders,
 //    and the four warps meet only at an item's end.
@@ -41,21 +41,27 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStepKeys = 16;                     // keys of a warp's step
-constexpr int kTileKeys = kWarps * kStepKeys;     // 64
+constexpr int kSubKeys = 16;                      // keys of a matrix instruction
 constexpr int kRingBytes = 24 * 1024;             // of each warp
 constexpr int kPassCols = 64;                     // columns of O summed over the warps at a time
 constexpr int kPassRow = kPassCols + 4;           // floats; +4: conflict-free column writes
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 8.f;                     // scores may pass the reference by a factor 2^8
 constexpr float kF16Shift = 7.f;                  // e4m3 caches: P's largest value is 2^(8 + 7)
-static_assert(kTileKeys == kDecodeTileKeys, "");
 
 template <int D, int NB, bool F8>
 struct Layout {
   static constexpr int N = 8 * NB;                    // query heads of a CTA
   static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a cached row
+  // A warp's step: 4 KB each of K and V where two sets of 16 keys do not pass it,
+  // so that what a step costs besides its bytes is paid once for as many bytes
+  // (e4m3, d = 128, 16 heads a group: 131071 keys x 4 heads x 8 at 16 keys a step
+  // 130 us).
+  static constexpr int kSub = kRow == 256 ? 1 : 2;
+  static constexpr int kStepKeys = kSubKeys * kSub;
+  static constexpr int kTileKeys = kWarps * kStepKeys;
   static constexpr int kTile = kStepKeys * kRow;      // of a warp's K (or V) step
+  static_assert(kTileKeys == (kRow == 256 ? 64 : 128), "decode_tile_keys in kernels.h");
   static constexpr int kStages = kRingBytes / (2 * kTile);
   static constexpr int kQRow = D + 8;                 // 16-bit elements of a staged query row
   static constexpr int kRing = kWarps * kRingBytes;
@@ -149,8 +155,12 @@ __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
   const int len = __ldg(a.lens + b);
   return min(max(len, 0), a.max_len);
 }
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
+template <int kTileKeys>
+__device__ __forceinline__ int tiles_of(int len) {
+  return (len + kTileKeys - 1) / kTileKeys;
+}
 
+template <int kTileKeys>
 __device__ __forceinline__ void advance(Cursor& c, const DecodeArgs& a) {
   if (++c.t < c.nt) return;
   c.t = 0;
@@ -159,7 +169,7 @@ __device__ __forceinline__ void advance(Cursor& c, const DecodeArgs& a) {
   c.nt = 0;
   while (c.nt == 0 && ++c.b < a.B) {
     c.len = clamp_len(a, c.b);
-    c.nt = tiles_of(c.len);
+    c.nt = tiles_of<kTileKeys>(c.len);
   }
 }
 
@@ -169,13 +179,15 @@ __device__ __forceinline__ int first_tile(int i, int tiles, int ctas) {
 }
 
 // WHOLE: the page size is a multiple of a step's 16 keys, so that a step lies in
-// one page and its rows are one stride apart; otherwise each row is looked up.
+// one page (two sets of 16, two) and its rows are one stride apart; otherwise each row is looked up.
 template <int D, int NB, bool F8, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_kernel(const __grid_constant__ DecodeArgs a) {
   using L = Layout<D, NB, F8>;
   constexpr int N = L::N;
   constexpr int kStages = L::kStages;
+  constexpr int kSub = L::kSub, kStepKeys = L::kStepKeys, kTileKeys = L::kTileKeys;
+  constexpr uint32_t kAllKeys = kSub == 1 ? 0xffffu : 0xffffffffu;
   constexpr int kKSteps = D / 16;  // 16-element steps of a product over d; 16-row tiles of V^T
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_scan[kWarps];
@@ -194,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int b = b0; b < b1; ++b) {
     const int raw = __ldg(a.lens + b);
     if (cta == 0 && (raw < 0 || raw > a.max_len)) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-    mine += tiles_of(clamp_len(a, b)) * a.heads;
+    mine += tiles_of<kTileKeys>(clamp_len(a, b)) * a.heads;
   }
   int incl = mine;
 #pragma unroll
@@ -218,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int at = before + incl - mine;  // first tile of this thread's sequences
     if (r0 < r1 && r0 >= at && r0 < at + mine) {
       for (int b = b0; b < b1; ++b) {
-        const int len = clamp_len(a, b), nt = tiles_of(len);
+        const int len = clamp_len(a, b), nt = tiles_of<kTileKeys>(len);
         if (r0 < at + nt * a.heads) {
           const int in = r0 - at;
           s_first = Cursor{b, in / nt, in % nt, nt, len};
@@ -247,13 +259,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* s_qs = reinterpret_cast<float*>(smem + L::kOffQs);
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + L::kOffMask) + warp * kStages;
 
-  // ---- loads: WHOLE: the step's page; else this lane's key (lane & 15) ----
+  // ---- loads: the page of each 16 keys (WHOLE; lane % kSub) or of each key ----
   Cursor ld = s_first;
   int ld_left = r1 - r0;
   int page = -1, slot = 0;
   bool held = false;  // whether there is such a key; its page is checked when it is used
   auto look_up = [&]() {
-    const int key = ld.t * kTileKeys + warp * kStepKeys + (WHOLE ? 0 : lane & 15);
+    const int key = ld.t * kTileKeys + warp * kStepKeys + (WHOLE ? lane % kSub * kSubKeys : lane % kStepKeys);
     held = ld_left > 0 && key < ld.len;
     if (held) {
       const int entry = key / a.cache.page_size;
@@ -272,28 +284,41 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     const uint32_t kt = ring + stage * 2 * L::kTile, vt = kt + L::kTile;
     const int c = lane % kLanes, r_lane = lane / kLanes;
-    uint32_t mask;
+    uint32_t mask = 0;
     if constexpr (WHOLE) {
-      const int count = page < 0 ? 0 : min(ld.len - ld.t * kTileKeys - warp * kStepKeys, kStepKeys);
-      mask = (1u << count) - 1u;
-      if (count > 0) {
-        const int g = ld.hh / a.blocks;
-        const unsigned char* kp = a.k + (page * a.k_strides[0] + (slot + r_lane) * a.k_strides[1] +
-                                         g * a.k_strides[2] + c * 16);
-        const unsigned char* vp = a.v + (page * a.v_strides[0] + (slot + r_lane) * a.v_strides[1] +
-                                         g * a.v_strides[2] + c * 16);
+      const int left = ld.len - ld.t * kTileKeys - warp * kStepKeys;
+      const int g = ld.hh / a.blocks;
+      int pg[kSub], sl[kSub], count[kSub];
 #pragma unroll
-        for (int i = 0; i < kStepKeys / kRows; ++i) {
-          const int r = i * kRows + r_lane;  // rows behind the last key read nothing
-          const uint32_t to = tile_offset<L::kRow>(r, c);
-          cp_async16(kt + to, kp, r < count);
-          cp_async16(vt + to, vp, r < count);
-          kp += kRows * a.k_strides[1];
-          vp += kRows * a.v_strides[1];
+      for (int sub = 0; sub < kSub; ++sub) {
+        pg[sub] = kSub == 1 ? page : __shfl_sync(0xffffffffu, page, sub);
+        sl[sub] = kSub == 1 ? slot : __shfl_sync(0xffffffffu, slot, sub);
+        count[sub] = pg[sub] < 0 ? 0 : min(left - sub * kSubKeys, kSubKeys);
+        mask |= ((1u << count[sub]) - 1u) << (sub * kSubKeys);
+      }
+      if (mask) {
+        // keys that do not count are filled with zeros: the weight 0 must not
+        // meet what an earlier step left there
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+          const int pg0 = max(pg[sub], 0), sl0 = count[sub] > 0 ? sl[sub] : 0;
+          const unsigned char* kp = a.k + (pg0 * a.k_strides[0] + (sl0 + r_lane) * a.k_strides[1] +
+                                           g * a.k_strides[2] + c * 16);
+          const unsigned char* vp = a.v + (pg0 * a.v_strides[0] + (sl0 + r_lane) * a.v_strides[1] +
+                                           g * a.v_strides[2] + c * 16);
+#pragma unroll
+          for (int i = 0; i < kSubKeys / kRows; ++i) {
+            const int r = i * kRows + r_lane;  // rows behind the last key read nothing
+            const uint32_t to = tile_offset<L::kRow>(sub * kSubKeys + r, c);
+            cp_async16(kt + to, kp, r < count[sub]);
+            cp_async16(vt + to, vp, r < count[sub]);
+            kp += kRows * a.k_strides[1];
+            vp += kRows * a.v_strides[1];
+          }
         }
       }
     } else {
-      mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+      mask = __ballot_sync(0xffffffffu, page >= 0) & kAllKeys;
       if (mask) {
         const int g = ld.hh / a.blocks;
         const long long pg = max(page, 0);
@@ -313,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (lane == 0) s_mask[stage] = mask;
     cp_async_commit();
-    if (--ld_left > 0) advance(ld, a);
+    if (--ld_left > 0) advance<kTileKeys>(ld, a);
     look_up();
   };
   look_up();
@@ -431,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t mask = s_mask[stage];
     if (mask) {
       const uint32_t kt = ring + stage * 2 * L::kTile, vt = kt + L::kTile;
-      // S^T = K Q^T in two chains
+      // S^T = K Q^T: two chains, of the two halves of d or of two sets of keys
       float s[NB][2][4];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -440,44 +465,53 @@ __global__ void __launch_bounds__(kThreads, 2)
       if constexpr (F8) {
 #pragma unroll
         for (int k = 0; k < kKSteps; k += 2) {
-          uint32_t r[4];
-          ldmatrix4(r, kt + tile_offset<L::kRow>(lane & 15, k + (lane >> 4)));
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t lo = r[2 * x], hi = r[2 * x + 1];
-            const uint32_t f[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(hi), e4m3x2_f16x2(lo >> 16),
-                                   e4m3x2_f16x2(hi >> 16)};
+          for (int sub = 0; sub < kSub; ++sub) {
+            uint32_t r[4];
+            ldmatrix4(r, kt + tile_offset<L::kRow>(sub * kSubKeys + (lane & 15), k + (lane >> 4)));
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma16816<true>(s[nb][x], f, qf[nb][k + x][0], qf[nb][k + x][1]);
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t lo = r[2 * x], hi = r[2 * x + 1];
+              const uint32_t f[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(hi), e4m3x2_f16x2(lo >> 16),
+                                     e4m3x2_f16x2(hi >> 16)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816<true>(s[nb][kSub == 1 ? x : sub], f, qf[nb][k + x][0], qf[nb][k + x][1]);
+            }
           }
         }
       } else {
 #pragma unroll
         for (int k = 0; k < kKSteps; ++k) {
-          uint32_t r[4];
-          ldmatrix4(r, kt + tile_offset<L::kRow>(lane & 15, 2 * k + (lane >> 4)));
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma16816<false>(s[nb][k & 1], r, qf[nb][k][0], qf[nb][k][1]);
+          for (int sub = 0; sub < kSub; ++sub) {
+            uint32_t r[4];
+            ldmatrix4(r, kt + tile_offset<L::kRow>(sub * kSubKeys + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma16816<false>(s[nb][kSub == 1 ? k & 1 : sub], r, qf[nb][k][0], qf[nb][k][1]);
+          }
         }
       }
       // online softmax; element x of a lane: key u8 + 8 (x / 2), column 2 j4 + x % 2
-      uint32_t ph[NB][2], pl[NB][2];
-      float v[NB][4];
+      float v[NB][kSub][4];
       bool grew = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) v[nb][x] = (s[nb][0][x] + s[nb][1][x]) * qs[nb][x & 1];
-        if (mask != 0xffffu) {
+        for (int sub = 0; sub < kSub; ++sub) {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            if (!((mask >> (u8 + 8 * (x >> 1))) & 1)) v[nb][x] = -INFINITY;
-        }
+            v[nb][sub][x] = (kSub == 1 ? s[nb][0][x] + s[nb][1][x] : s[nb][sub][x]) * qs[nb][x & 1];
+          if (mask != kAllKeys) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          grew |= fmaxf(v[nb][x], v[nb][x + 2]) > top[nb][x] + kSlack;
+            for (int x = 0; x < 4; ++x)
+              if (!((mask >> (sub * kSubKeys + u8 + 8 * (x >> 1))) & 1)) v[nb][sub][x] = -INFINITY;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            grew |= fmaxf(v[nb][sub][x], v[nb][sub][x + 2]) > top[nb][x] + kSlack;
+        }
       }
       // The reference the weights are relative to follows the maximum only when
       // that has grown by more than kSlack: one vote a step instead of a
@@ -487,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float to = fmaxf(v[nb][x], v[nb][x + 2]);
+            float to = fmaxf(v[nb][0][x], v[nb][0][x + 2]);
+            if (kSub == 2) to = fmaxf(to, fmaxf(v[nb][kSub - 1][x], v[nb][kSub - 1][x + 2]));
 #pragma unroll
             for (int m = 4; m < 32; m <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, m));
             to = fmaxf(to, top[nb][x]);
@@ -502,57 +537,69 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
       }
+      uint32_t ph[kSub][NB][2], pl[kSub][NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float p[4];
+        float ref[2];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float ref = top[nb][x & 1] == -INFINITY ? 0.f : top[nb][x & 1];
-          p[x] = ex2_approx(v[nb][x] - (F8 ? ref - kF16Shift : ref));
-          sum[nb][x & 1] += p[x];
+        for (int x = 0; x < 2; ++x) {
+          ref[x] = top[nb][x] == -INFINITY ? 0.f : top[nb][x];
+          if (F8) ref[x] -= kF16Shift;
         }
-        if constexpr (F8) {
-          ph[nb][0] = transpose8(pack_f16(p[0], p[1]));
-          ph[nb][1] = transpose8(pack_f16(p[2], p[3]));
-        } else {
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+          float p[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            p[x] = ex2_approx(v[nb][sub][x] - ref[x & 1]);
+            sum[nb][x & 1] += p[x];
+          }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t h0 = below(p[2 * x]), h1 = below(p[2 * x + 1]);
-            ph[nb][x] = transpose8(__byte_perm(h0, h1, 0x7632));
-            pl[nb][x] = transpose8(pack_bf16(p[2 * x] - __uint_as_float(h0),
-                                             p[2 * x + 1] - __uint_as_float(h1)));
+            if constexpr (F8) {
+              ph[sub][nb][x] = transpose8(pack_f16(p[2 * x], p[2 * x + 1]));
+            } else {
+              const uint32_t h0 = below(p[2 * x]), h1 = below(p[2 * x + 1]);
+              ph[sub][nb][x] = transpose8(__byte_perm(h0, h1, 0x7632));
+              pl[sub][nb][x] = transpose8(pack_bf16(p[2 * x] - __uint_as_float(h0),
+                                                    p[2 * x + 1] - __uint_as_float(h1)));
+            }
           }
         }
       }
       // O^T += V^T P^T
-      if constexpr (F8) {
-        // 16-bit units of V hold two columns of one key: after the transposing
-        // load a register holds columns 2 u8, 2 u8 + 1 of keys 2 j4, 2 j4 + 1,
-        // and rows u8 and u8 + 8 of the product stand for those two columns
 #pragma unroll
-        for (int k = 0; k < kKSteps; k += 2) {
-          uint32_t r[4];
-          ldmatrix4_trans(r, vt + tile_offset<L::kRow>(lane & 15, k + (lane >> 4)));
+      for (int sub = 0; sub < kSub; ++sub) {
+        if constexpr (F8) {
+          // 16-bit units of V hold two columns of one key: after the transposing
+          // load a register holds columns 2 u8, 2 u8 + 1 of keys 2 j4, 2 j4 + 1,
+          // and rows u8 and u8 + 8 of the product stand for those two columns
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t w0 = __byte_perm(r[2 * x], 0, 0x3120);
-            const uint32_t w1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
-            const uint32_t f[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1),
-                                   e4m3x2_f16x2(w1 >> 16)};
+          for (int k = 0; k < kKSteps; k += 2) {
+            uint32_t r[4];
+            ldmatrix4_trans(r, vt + tile_offset<L::kRow>(sub * kSubKeys + (lane & 15), k + (lane >> 4)));
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816<true>(o[nb][k + x], f, ph[nb][0], ph[nb][1]);
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t w0 = __byte_perm(r[2 * x], 0, 0x3120);
+              const uint32_t w1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
+              const uint32_t f[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1),
+                                     e4m3x2_f16x2(w1 >> 16)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816<true>(o[nb][k + x], f, ph[sub][nb][0], ph[sub][nb][1]);
+            }
           }
-        }
-      } else {
-        const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+        } else {
+          const int vr = sub * kSubKeys + (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
 #pragma unroll
-        for (int k = 0; k < kKSteps; ++k) {
-          uint32_t r[4];
-          ldmatrix4_trans(r, vt + tile_offset<L::kRow>(vr, 2 * k + vc));
+          for (int k = 0; k < kKSteps; ++k) {
+            uint32_t r[4];
+            ldmatrix4_trans(r, vt + tile_offset<L::kRow>(vr, 2 * k + vc));
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            mma16816<false>(o[nb][k], r, ph[nb][0], ph[nb][1]);
-            mma16816<false>(o[nb][k], r, pl[nb][0], pl[nb][1]);
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816<false>(o[nb][k], r, ph[sub][nb][0], ph[sub][nb][1]);
+              mma16816<false>(o[nb][k], r, pl[sub][nb][0], pl[sub][nb][1]);
+            }
           }
         }
       }
@@ -582,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncthreads();
       const bool more = tile + 1 < r1;
       if (more) {
-        advance(cur, a);
+        advance<kTileKeys>(cur, a);
         stage_q(cur);  // every warp holds the old query in registers
       }
       const int g = done.hh / a.blocks, blk = done.hh - g * a.blocks;
@@ -738,7 +785,7 @@ template <int D, int NB, bool F8>
 cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, bool join, cudaStream_t stream) {
   using L = Layout<D, NB, F8>;
   static_assert(L::kBytes <= 113 * 1024, "two CTAs share an SM's shared memory");
-  auto kern = a.cache.page_size % kStepKeys == 0 ? decode_kernel<D, NB, F8, true>
+  auto kern = a.cache.page_size % kSubKeys == 0 ? decode_kernel<D, NB, F8, true>
                                                  : decode_kernel<D, NB, F8, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;

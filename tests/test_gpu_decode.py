@@ -217,6 +217,27 @@ def test_cache_past_four_gigabytes(eba):
     assert torch.isfinite(o.float()).all()
 
 
+@pytest.mark.parametrize("d,e4m3,page", [(64, False, 16), (128, True, 16), (64, True, 20), (128, False, 32)])
+def test_values_of_one_sequence_never_reach_another(eba, d, e4m3, page):
+    # every other sequence holds NaN values; those between end inside a tile that
+    # the same block loaded NaN into before, or have a page that is none in it
+    lens = [200, 3, 130, 17] * 150
+    g = torch.Generator().manual_seed(21)
+    nan = lambda n: (bf16(g, n, 1, d), torch.full((n, 1, d), math.nan, dtype=torch.bfloat16))
+    p = Paged(lens, page, 1, d, e4m3=e4m3, seed=21,
+              data=[nan(n) if n > 100 else (bf16(g, n, 1, d), bf16(g, n, 1, d)) for n in lens])
+    cache = p.on_gpu(eba)
+    q = bf16(g, len(lens), 2, d).cuda()
+    o, _ = eba.decode(cache, q, p.gtable, p.glens)
+    finite = torch.isfinite(o).all(2).all(1).cpu()
+    assert finite.tolist() == [n < 100 for n in lens]
+    table = p.gtable.clone()
+    table[3::4, 0] = -1  # the first keys of each 17
+    o2, _ = eba.decode(cache, q, table, p.glens)
+    assert eba.poll_device_status() == 7
+    assert torch.isfinite(o2[3::4]).all() and torch.equal(o2[1::4], o[1::4])
+
+
 def test_same_call_same_bits(eba):
     p = Paged([4000, 100, 2500], 16, 2, 64, seed=13)
     cache = p.on_gpu(eba)
