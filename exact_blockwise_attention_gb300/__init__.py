@@ -122,7 +122,7 @@ def _declare(L):
     L.attn_rope_init.argtypes = [rp, i, i, ip, ctypes.POINTER(ctypes.c_double), i]
     L.attn_rope.argtypes = [rp, vp, lp, vp, lp, vp, lp, vp, lp, vp, lp, i, i, i, i, i, i, vp]
     L.attn_cache_append.argtypes = [cp, vp, lp, vp, lp, vp, ll, i, vp, i, vp, i, rp, vp, ll, vp]
-    L.attn_decode_workspace_size.argtypes = [i, i, i, i]
+    L.attn_decode_workspace_size.argtypes = [i, i, i, i, i, ll]
     L.attn_decode_workspace_size.restype = sz
     L.attn_decode.argtypes = [cp, vp, lp, vp, ll, i, vp, i, i, f, rp, vp, ll, vp, vp, vp, sz, vp]
     for name in ("attn_rope_init", "attn_rope", "attn_cache_append", "attn_decode"):
@@ -760,7 +760,8 @@ class PagedCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
         self.n_pages, self.page_size, self.H_kv, self.d = k.shape
         self.device = k.device
-        self._key = (self.H_kv, self.d, self.device)  # what the checks of a call depend on
+        # what the checks of a call depend on
+        self._key = (self.H_kv, self.d, self.page_size, k.dtype, self.device)
         self._struct = s
 
     def _at(self):
@@ -852,8 +853,11 @@ def _append_layout(cache, k, v, page_table, seq_lens, cu_new, rope, positions):
     return (_Strides2(*sk), _Strides2(*sv), page_table.stride(0), page_table.shape[1], n, T, stride)
 
 
-def decode_workspace_size(B, H, H_kv, d) -> int:
-    return int(lib().attn_decode_workspace_size(B, H, H_kv, d))
+def decode_workspace_size(cache, B, H, max_pages) -> int:
+    """Scratch bytes of decode for B sequences of H query heads and a page table of
+    max_pages columns; 0 where none is needed."""
+    return int(lib().attn_decode_workspace_size(B, H, cache.H_kv, cache.d, cache._struct.type,
+                                                max_pages * cache.page_size))
 
 
 def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None, workspace=None):
@@ -880,7 +884,9 @@ def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None
     qp = q.data_ptr()
     if qp & 15:
         raise _off_boundary("q")
-    if workspace is None:
+    if not need:
+        workspace = None
+    elif workspace is None:
         workspace = torch.empty(need, device=dev, dtype=torch.uint8)
     elif workspace.numel() * workspace.element_size() < need or workspace.device != dev or \
             not workspace.is_contiguous():
@@ -890,7 +896,7 @@ def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None
     _launch(dev, lib().attn_decode, cache._at(), qp, sq, page_table.data_ptr(), row, wide,
             seq_lens.data_ptr(), B, H, _scale(scale, d), None if rope is None else rope._struct,
             None if positions is None else positions.data_ptr(), stride, o.data_ptr(),
-            lse.data_ptr(), workspace.data_ptr(), need)
+            lse.data_ptr(), None if workspace is None else workspace.data_ptr(), need)
     return o, lse
 
 
@@ -913,4 +919,4 @@ def _decode_layout(cache, q, page_table, seq_lens, rope, positions):
         raise ValueError(f"q holds {B} sequences, seq_lens {n}")
     stride = cache._turn(rope, positions, B)[2]
     return (_Strides2(*sq), page_table.stride(0), page_table.shape[1], B, H, d, stride,
-            decode_workspace_size(B, H, cache.H_kv, d))
+            decode_workspace_size(cache, B, H, page_table.shape[1]))

@@ -322,15 +322,51 @@ int check_table(const int* table, long long stride, int max_pages, const int* le
   return ATTN_OK;
 }
 
-// Query heads of one K/V head that a decode CTA holds, and blocks of them: the
-// matrix instruction has 8 columns, so groups of up to 8 take one set and
-// larger groups two at a time.
-struct DecodeShape {
-  int rows, blocks;
+// How a decode call is cut up, from what the host knows: the sizes and the keys
+// a table can hold. ok: the sizes are within the limits.
+struct DecodePlan {
+  bool ok;
+  int rows, blocks;      // query heads of a CTA (8 or 16), blocks of them in a group
+  int heads, max_len;    // items of a sequence; keys of a table row
+  int splits, ctas;      // see DecodeArgs; the grid
+  bool join;             // items may be cut between CTAs
+  size_t items, slots;   // of the workspace
+  size_t bytes;
 };
-DecodeShape decode_shape(int group) {
-  const int rows = group <= 8 ? 8 : 16;
-  return {rows, (group + rows - 1) / rows};
+DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int type) {
+  DecodePlan p{};
+  const int group = H / H_kv;
+  // the matrix instruction has 8 columns: groups of up to 8 heads take one set
+  // of them, larger ones two at a time
+  p.rows = group <= 8 ? 8 : 16;
+  p.blocks = (group + p.rows - 1) / p.rows;
+  const int tile = eba::decode_tile_keys(type == ATTN_CACHE_E4M3 ? d : 2 * d);
+  p.max_len = static_cast<int>(std::min(capacity, (1ll << 31) - 1 - tile));
+  p.heads = H_kv * p.blocks;
+  const long long item_tiles = (p.max_len + tile - 1) / tile;
+  const long long items = static_cast<long long>(B) * p.heads;
+  if (items >= (1ll << 31) || item_tiles * p.heads >= (1ll << 31) ||
+      item_tiles * p.heads * B >= (1ll << 31))
+    return p;
+  p.ok = true;
+  // Clusters, where one wave of them leaves each CTA at most 4 tiles: that costs
+  // one launch instead of two and needs no workspace. With more tiles a CTA,
+  // spreading them over all SMs is worth the second launch.
+  int splits = 1;
+  while (splits < 8 && splits < item_tiles && items * splits * 2 <= eba::kDecodeCtas) splits *= 2;
+  if (items * splits <= eba::kDecodeCtas && item_tiles <= 4 * splits) {
+    p.splits = splits;
+    p.ctas = static_cast<int>(items * splits);
+    return p;
+  }
+  // no more CTAs than tiles the tables can hold; a single-tile item is never cut
+  p.ctas = static_cast<int>(std::min<long long>(eba::kDecodeCtas, items * item_tiles));
+  p.join = item_tiles > 1;
+  if (!p.join) return p;
+  p.items = static_cast<size_t>(items);
+  p.slots = 2 * static_cast<size_t>(eba::kDecodeCtas) * p.rows;
+  p.bytes = (p.items * sizeof(int) + 15) / 16 * 16 + p.slots * (d + 2) * sizeof(float);
+  return p;
 }
 
 // Short sequences (at most 64 queries and keys) are packed several to a
@@ -898,12 +934,12 @@ int attn_cache_append(const attn_cache_t* cache, const void* k, const long long*
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
-size_t attn_decode_workspace_size(int B, int H, int H_kv, int d) {
-  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
-  const DecodeShape p = decode_shape(H / H_kv);
-  const size_t items = static_cast<size_t>(B) * H_kv * p.blocks;
-  const size_t slots = 2 * static_cast<size_t>(eba::kDecodeCtas) * p.rows;
-  return (items * sizeof(int) + 15) / 16 * 16 + slots * (d + 2) * sizeof(float);
+size_t attn_decode_workspace_size(int B, int H, int H_kv, int d, int type, long long max_keys) {
+  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128) || max_keys < 1 ||
+      (type != ATTN_CACHE_BF16 && type != ATTN_CACHE_E4M3))
+    return 0;
+  const DecodePlan p = decode_plan(B, H, H_kv, d, max_keys, type);
+  return p.ok ? p.bytes : 0;
 }
 
 int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_strides,
@@ -924,21 +960,17 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
     if ((s = check_rope(*rope, cache->d)) != ATTN_OK) return s;
     if (!pos && rope->n_axes != 1) return ATTN_ERR_INVALID_ARG;
   }
-  const DecodeShape p = decode_shape(H / cache->H_kv);
-  if (!workspace || workspace_bytes < attn_decode_workspace_size(B, H, cache->H_kv, cache->d))
-    return ATTN_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
-  eba::DecodeArgs a{};
-  const long long capacity = static_cast<long long>(max_pages) * cache->page_size;
-  const int esz = cache->type == ATTN_CACHE_E4M3 ? 1 : 2;
-  const int tile = eba::decode_tile_keys(cache->d * esz);
-  a.max_len = static_cast<int>(std::min(capacity, (1ll << 31) - 1 - tile));
-  a.heads = cache->H_kv * p.blocks;
-  const long long item_tiles = (a.max_len + tile - 1) / tile;
-  const long long seq_tiles = item_tiles * a.heads;  // < 2^57
-  if (seq_tiles >= (1ll << 31) || seq_tiles * B >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  const DecodePlan p = decode_plan(B, H, cache->H_kv, cache->d,
+                                   static_cast<long long>(max_pages) * cache->page_size, cache->type);
+  if (!p.ok) return ATTN_ERR_INVALID_ARG;
+  if (p.bytes > 0) {
+    if (!workspace || workspace_bytes < p.bytes) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  }
   int* status = status_word_ptr();
   if (!status) return ATTN_ERR_CUDA;
+  eba::DecodeArgs a{};
+  const int esz = cache->type == ATTN_CACHE_E4M3 ? 1 : 2;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_seq = q_strides[0];
   a.q_head = q_strides[1];
@@ -952,28 +984,29 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
   a.table = page_table;
   a.table_stride = table_stride;
   a.lens = seq_lens;
+  a.max_len = p.max_len;
   a.B = B;
   a.H = H;
   a.group = H / cache->H_kv;
   a.rows = p.rows;
   a.blocks = p.blocks;
+  a.heads = p.heads;
+  a.splits = p.splits;
   a.scale_log2 = scale * kLog2e * cache->k_scale;
   a.o_scale = cache->v_scale;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  const size_t items = static_cast<size_t>(B) * a.heads;
-  const size_t slots = 2 * static_cast<size_t>(eba::kDecodeCtas) * p.rows;
-  a.item = static_cast<int*>(workspace);
-  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                      (items * sizeof(int) + 15) / 16 * 16);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * cache->d);
+  if (p.bytes > 0) {
+    a.item = static_cast<int*>(workspace);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        (p.items * sizeof(int) + 15) / 16 * 16);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + p.slots * cache->d);
+  }
   a.pos = pos;
   a.pos_axis = pos_stride;
   a.status = status;
   if (rope) a.rope = *rope;
-  // no more CTAs than tiles the tables can hold; a single-tile item is never cut
-  const int ctas = static_cast<int>(std::min<long long>(eba::kDecodeCtas, seq_tiles * B));
-  cudaError_t e = eba::launch_decode(a, ctas, item_tiles > 1, static_cast<cudaStream_t>(stream));
+  cudaError_t e = eba::launch_decode(a, p.ctas, p.join, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 

@@ -15,6 +15,9 @@
 //    sequences balance without the host knowing the lengths, and a call can be
 //    captured and replayed with other lengths. An item cut between CTAs leaves
 //    fp32 partials, which the join kernel adds up in the order of the keys.
+//  - Short caches and few heads, where latency is what counts: one cluster of
+//    up to 8 CTAs per item instead, whose parts are joined through the
+//    cluster's shared memory: one launch, no workspace and no list of tiles.
 //  - A warp owns 16 or 32 keys of each tile and walks the CTA's run on its own, with
 //    its own running maximum and sums: its loads (cp.async, 16 bytes a lane,
 //    rows of whole cache lines) run several tiles ahead, across item borders,
@@ -137,6 +140,30 @@ __device__ __forceinline__ uint32_t below(float p) {
   return (max(__float_as_uint(p), 1u) - 1u) & 0xFFFF0000u;
 }
 
+// A cluster's shared memory: the address of `addr` in CTA `rank`, loads from it,
+// and the barrier that orders one CTA's writes before another's reads.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Where 16-byte chunk c of row r lies in a tile of kRow-byte rows, so that the
 // 8 rows of a matrix load fall into 8 different bank groups.
 template <int kRow>
@@ -199,63 +226,82 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int j4 = lane & 3, u8 = lane >> 2;
   const int cta = blockIdx.x;
 
-  // ---- the list of tiles: each thread counts a run of sequences ----
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int raw = __ldg(a.lens + b);
-    if (cta == 0 && (raw < 0 || raw > a.max_len)) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-    mine += tiles_of<kTileKeys>(clamp_len(a, b)) * a.heads;
-  }
-  int incl = mine;
+  int r0, r1;          // this CTA's tiles
+  int G = 1, tiles = 0;  // runs the list of all tiles is cut into, and its length
+  if (a.splits) {
+    // ---- short caches: one cluster of a.splits CTAs per item ----
+    const int it = cta / a.splits, rank = cta - it * a.splits;
+    const int b = it / a.heads, raw = __ldg(a.lens + b);
+    const int len = min(max(raw, 0), a.max_len), nt = tiles_of<kTileKeys>(len);
+    if (tid == 0) {
+      if (raw != len) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+      s_first = Cursor{b, it - b * a.heads, first_tile(rank, nt, a.splits), nt, len};
+    }
+    r0 = first_tile(rank, nt, a.splits);
+    r1 = first_tile(rank + 1, nt, a.splits);
+  } else {
+    // ---- the list of tiles: each thread counts a run of sequences ----
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int raw = __ldg(a.lens + b);
+      if (cta == 0 && (raw < 0 || raw > a.max_len)) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+      mine += tiles_of<kTileKeys>(clamp_len(a, b)) * a.heads;
+    }
+    int incl = mine;
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, m);
-    if (lane >= m) incl += o;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  int before = 0, tiles = 0;
+    for (int m = 1; m < 32; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, m);
+      if (lane >= m) incl += o;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int before = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    before += w < warp ? s_scan[w] : 0;
-    tiles += s_scan[w];
-  }
-  // no run is empty: with fewer tiles than CTAs the last CTAs have none
-  const int G = max(1, min(static_cast<int>(gridDim.x), tiles));
-  const int r0 = cta < G ? first_tile(cta, tiles, G) : tiles;
-  const int r1 = cta < G ? first_tile(cta + 1, tiles, G) : tiles;
-  {
-    int at = before + incl - mine;  // first tile of this thread's sequences
-    if (r0 < r1 && r0 >= at && r0 < at + mine) {
-      for (int b = b0; b < b1; ++b) {
-        const int len = clamp_len(a, b), nt = tiles_of<kTileKeys>(len);
-        if (r0 < at + nt * a.heads) {
-          const int in = r0 - at;
-          s_first = Cursor{b, in / nt, in % nt, nt, len};
-          break;
+    for (int w = 0; w < kWarps; ++w) {
+      before += w < warp ? s_scan[w] : 0;
+      tiles += s_scan[w];
+    }
+    // no run is empty: with fewer tiles than CTAs the last CTAs have none
+    G = max(1, min(static_cast<int>(gridDim.x), tiles));
+    r0 = cta < G ? first_tile(cta, tiles, G) : tiles;
+    r1 = cta < G ? first_tile(cta + 1, tiles, G) : tiles;
+    {
+      int at = before + incl - mine;  // first tile of this thread's sequences
+      if (r0 < r1 && r0 >= at && r0 < at + mine) {
+        for (int b = b0; b < b1; ++b) {
+          const int len = clamp_len(a, b), nt = tiles_of<kTileKeys>(len);
+          if (r0 < at + nt * a.heads) {
+            const int in = r0 - at;
+            s_first = Cursor{b, in / nt, in % nt, nt, len};
+            break;
+          }
+          at += nt * a.heads;
         }
-        at += nt * a.heads;
       }
     }
-  }
-  // Sequences without keys: O = 0, lse = -inf.
-  for (int b = cta; b < a.B; b += gridDim.x) {
-    if (clamp_len(a, b) > 0) continue;
-    for (int x = tid; x < a.H * D / 8; x += kThreads)
-      *reinterpret_cast<uint4*>(a.o + static_cast<long long>(b) * a.H * D + x * 8) =
-          make_uint4(0, 0, 0, 0);
-    for (int h = tid; h < a.H; h += kThreads) a.lse[static_cast<long long>(b) * a.H + h] = -INFINITY;
-    for (int x = tid; x < a.heads; x += kThreads) a.item[static_cast<long long>(b) * a.heads + x] = 0;
+    // Sequences without keys: O = 0, lse = -inf.
+    for (int b = cta; b < a.B; b += gridDim.x) {
+      if (clamp_len(a, b) > 0) continue;
+      for (int x = tid; x < a.H * D / 8; x += kThreads)
+        *reinterpret_cast<uint4*>(a.o + static_cast<long long>(b) * a.H * D + x * 8) =
+            make_uint4(0, 0, 0, 0);
+      for (int h = tid; h < a.H; h += kThreads) a.lse[static_cast<long long>(b) * a.H + h] = -INFINITY;
+      if (a.item)
+        for (int x = tid; x < a.heads; x += kThreads) a.item[static_cast<long long>(b) * a.heads + x] = 0;
+    }
   }
   __syncthreads();
-  if (r0 >= r1) return;
+  if (!a.splits && r0 >= r1) return;
 
   const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
   float* s_sum = reinterpret_cast<float*>(smem + L::kOffSum);
   uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + L::kOffQ);
   float2* s_ml = reinterpret_cast<float2*>(smem + L::kOffMl);
+  // a split item's part, in the ring once all loads are used: [N][D], [N]
+  float* s_part = reinterpret_cast<float*>(smem);
+  float2* s_part_ml = reinterpret_cast<float2*>(smem + N * D * 4);
   float* s_qs = reinterpret_cast<float*>(smem + L::kOffQs);
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + L::kOffMask) + warp * kStages;
 
@@ -439,9 +485,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   Cursor cur = s_first;
   int t_begin = cur.t;        // first tile of the item in this run
   bool first_item = true;
-  stage_q(cur);
-  __syncthreads();
-  begin_item();
+  if (r0 < r1) {
+    stage_q(cur);
+    __syncthreads();
+    begin_item();
+  }
 
   int stage = 0;
 #pragma unroll 1
@@ -673,7 +721,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float4 y = *reinterpret_cast<const float4*>(s_sum + (w * 8 + row) * kPassRow + c4);
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
           }
-          if (whole) {
+          if (a.splits > 1) {
+            *reinterpret_cast<float4*>(s_part + (nb * 8 + row) * D + c0 + c4) = v;
+          } else if (whole) {
             if (hg < a.group) {
               const float f = M == -INFINITY ? 0.f : a.o_scale / l;
               *reinterpret_cast<uint2*>(a.o + head * D + c0 + c4) =
@@ -686,7 +736,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           __syncthreads();
         }
         if ((tid & 15) == 0) {
-          if (!whole)
+          if (a.splits > 1)
+            s_part_ml[nb * 8 + row] = make_float2(M, l);
+          else if (!whole)
             a.part_ml[static_cast<long long>(part) * N + nb * 8 + row] = make_float2(M, l);
           else if (hg < a.group)
             a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
@@ -694,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // What the join kernel needs, left by the CTA with the item's first tile:
       // the item's parts lie in this CTA's slot and the first ones of the next.
-      if (tid == 0 && t_begin == 0) {
+      if (a.item && tid == 0 && t_begin == 0) {
         int parts = 0;
         if (!item_done) {
           const int last = tile - done.t + done.nt - 1;  // the item's last tile
@@ -712,6 +764,37 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   cp_async_wait<0>();
+
+  if (a.splits > 1 || s_first.nt == 0) {
+    // ---- join the cluster's parts, or write an item without keys ----
+    const int g = s_first.hh / a.blocks, blk = s_first.hh - g * a.blocks;
+    const int rank = cta % a.splits;
+    if (r0 >= r1)
+      for (int n = tid; n < N; n += kThreads) s_part_ml[n] = make_float2(-INFINITY, 0.f);
+    cluster_sync();
+    for (int x = rank * kThreads + tid; x < N * D / 4; x += a.splits * kThreads) {
+      const int n = x / (D / 4), hg = blk * N + n;
+      if (hg >= a.group) continue;
+      const uint32_t ml_at = smem_u32(s_part_ml + n), o_at = smem_u32(s_part) + x * 16;
+      float M = -INFINITY, l = 0.f;
+      for (int w = 0; w < a.splits; ++w) M = fmaxf(M, ld_cluster2(map_rank(ml_at, w)).x);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < a.splits; ++w) {
+        const float2 ml = ld_cluster2(map_rank(ml_at, w));
+        if (ml.x == -INFINITY) continue;  // no weight, or no keys and nothing written
+        const float f = ex2_approx(ml.x - M);
+        const float4 y = ld_cluster4(map_rank(o_at, w));
+        l += ml.y * f;
+        v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
+      }
+      const long long head = static_cast<long long>(s_first.b) * a.H + g * a.group + hg;
+      const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+      *reinterpret_cast<uint2*>(a.o + head * D + x % (D / 4) * 4) =
+          make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+      if (x % (D / 4) == 0) a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+    }
+    cluster_sync();  // the parts stay until all have read them
+  }
 }
 
 // Items cut between CTAs: one CTA per (sequence, query head) adds the parts up.
@@ -789,7 +872,19 @@ cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, bool join, cudaStream
                                                  : decode_kernel<D, NB, F8, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3(ctas), dim3(kThreads), L::kBytes, stream, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(a.splits), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess || !join) return e;
   return launch_pdl(decode_join_kernel<D, L::N>, dim3(static_cast<unsigned>(a.B) * a.H),
                     dim3(kThreads), 0, stream, a);

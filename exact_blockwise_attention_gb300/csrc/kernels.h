@@ -282,11 +282,13 @@ struct DecodeArgs {
   int rows;    // query heads a CTA holds: 8 or 16
   int blocks;  // ceil(group / rows)
   int heads;   // H_kv * blocks: items of a sequence
+  int splits;  // > 0: clusters of that many CTAs, one per item; 0: one list of tiles
   float scale_log2;  // scale * log2(e) * the keys' scale
   float o_scale;     // the values' scale
   __nv_bfloat16* o;  // [B, H, d]
   float* lse;        // [B, H]
-  int* item;         // [B, heads]: parts of a cut item << 16 | its first slot; 0: not cut
+  int* item;         // [B, heads]: parts of a cut item << 16 | its first slot; 0: not cut.
+                     // Null where no item can be cut
   float* part_o;     // [2 kDecodeCtas, rows, d]
   float2* part_ml;   // [2 kDecodeCtas, rows]: reference, sum
   const int* pos;

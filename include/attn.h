@@ -384,8 +384,12 @@ int attn_cache_append(const attn_cache_t* cache, const void* k, const long long*
                       const int* cu_new, int T, const attn_rope_t* rope, const int* pos,
                       long long pos_stride, void* stream);
 
-/* Scratch bytes of attn_decode (0 if an argument is invalid). */
-size_t attn_decode_workspace_size(int B, int H, int H_kv, int d);
+/*
+ * Scratch bytes of attn_decode over a cache of this type and a table that holds
+ * max_keys = max_pages * page_size keys a sequence. 0: none is needed (a batch
+ * of short caches), or an argument is invalid.
+ */
+size_t attn_decode_workspace_size(int B, int H, int H_kv, int d, int type, long long max_keys);
 
 /*
  * attn_decode - attention of one new token per sequence over its cached keys.
@@ -397,9 +401,10 @@ size_t attn_decode_workspace_size(int B, int H, int H_kv, int d);
  *   (NULL: q as it is); pos as for attn_cache_append with T = B, NULL: position
  *   seq_lens[b] - 1.
  *   o [B, H, d] bf16, lse [B, H] fp32 (contiguous outputs).
- *   workspace: device scratch of attn_decode_workspace_size(B, H, H_kv, d)
- *   bytes, 16-byte aligned, contents on entry do not matter; calls that may
- *   overlap on the GPU need one each.
+ *   workspace: device scratch of attn_decode_workspace_size(B, H, H_kv, d, type,
+ *   max_pages * page_size) bytes, 16-byte aligned (NULL where that is 0);
+ *   contents on entry do not matter; calls that may overlap on the GPU need one
+ *   each.
  * Deterministic for given lengths, sizes and inputs. Scores, sums and outputs
  * in fp32; the softmax weights enter the product with V as two bf16 terms
  * (2^-15), or with an e4m3 cache as fp16 (2^-11).

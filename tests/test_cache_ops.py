@@ -129,10 +129,11 @@ def test_append_refuses(eba):
 
 def test_decode_refuses(eba):
     L, c = eba.lib(), cache_struct(eba)
-    need = L.attn_decode_workspace_size(3, 6, 2, 64)
+    need = L.attn_decode_workspace_size(3, 6, 2, 64, 0, 2000 * 16)
     assert need > 0
+    assert L.attn_decode_workspace_size(3, 6, 2, 64, 0, 64) == 0  # short: none
 
-    def call(cache=c, q=A16, qs=(384, 64), wide=4, B=3, H=6, scale=0.1, rope=None, pos=None, o=A16,
+    def call(cache=c, q=A16, qs=(384, 64), wide=2000, B=3, H=6, scale=0.1, rope=None, pos=None, o=A16,
              lse=A16, ws=A16, size=need):
         return L.attn_decode(cache, q, ll(*qs), A16, 4, wide, A16, B, H, scale, rope, pos, 0, o, lse, ws,
                              size, None)
@@ -144,7 +145,8 @@ def test_decode_refuses(eba):
         assert call(scale=scale) == 1
     assert call(rope=eba.Rope((8, 12, 12))._struct) == 1
     assert call(ws=None) == 6 and call(size=need - 1) == 6 and call(ws=MIS) == 3
-    for bad in ((0, 6, 2, 64), (3, 0, 2, 64), (3, 6, 0, 64), (3, 6, 4, 64), (3, 6, 2, 96)):
+    for bad in ((0, 6, 2, 64, 0, 32000), (3, 0, 2, 64, 0, 32000), (3, 6, 0, 64, 0, 32000),
+                (3, 6, 4, 64, 0, 32000), (3, 6, 2, 96, 0, 32000), (3, 6, 2, 64, 2, 32000), (3, 6, 2, 64, 0, 0)):
         assert L.attn_decode_workspace_size(*bad) == 0
     # a table of more tiles than can be counted
     assert call(cache=cache_struct(eba, page_size=1 << 30), wide=1 << 30, B=1000, size=1 << 40) == 1

@@ -32,8 +32,8 @@ def status_is_clean(eba):
     assert eba.poll_device_status() == 0
 
 
-def poisoned(eba, B, H, hk, d):
-    n = eba.decode_workspace_size(B, H, hk, d)
+def poisoned(eba, cache, B, H, max_pages):
+    n = eba.decode_workspace_size(cache, B, H, max_pages)
     return torch.full((n,), 255, device="cuda", dtype=torch.uint8)  # NaN as fp32
 
 
@@ -43,7 +43,7 @@ def check(eba, p, q, scale=None, q_gpu=None):
     B, H, d = q.shape
     q_gpu = q.cuda() if q_gpu is None else q_gpu
     o, lse = eba.decode(cache, q_gpu, p.gtable, p.glens, scale,
-                        workspace=poisoned(eba, B, H, cache.H_kv, d))
+                        workspace=poisoned(eba, cache, B, H, p.table.shape[1]))
     scale = 1 / math.sqrt(d) if scale is None else scale
     keys, values = p.contents()
     ro, rl = oracle.decode(q, keys, values, scale)
@@ -244,7 +244,7 @@ def test_same_call_same_bits(eba):
     q = bf16(torch.Generator().manual_seed(8), 3, 8, 64).cuda()
     a = eba.decode(cache, q, p.gtable, p.glens)
     for _ in range(5):
-        b = eba.decode(cache, q, p.gtable, p.glens, workspace=poisoned(eba, 3, 8, 2, 64))
+        b = eba.decode(cache, q, p.gtable, p.glens, workspace=poisoned(eba, cache, 3, 8, p.table.shape[1]))
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
