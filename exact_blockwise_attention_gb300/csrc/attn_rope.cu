@@ -69,25 +69,53 @@ __device__ __forceinline__ void lane_offsets(int i, int n_pairs, int& off_a, int
   }
 }
 
-// cos, sin of pairs 8 i .. 8 i + 7 at the positions pos[axis * stride].
-__device__ __forceinline__ void lane_turn(const attn_rope_t& r, int i, const int* pos,
-                                          long long stride, float sign, Turn8& t) {
-  int p[ATTN_MAX_AXES];
-#pragma unroll
-  for (int a = 0; a < ATTN_MAX_AXES; ++a) p[a] = a < r.n_axes ? __ldg(pos + a * stride) : 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int axis = r.axis[8 * i + j];
-    int pj = p[0];
-#pragma unroll
-    for (int a = 1; a < ATTN_MAX_AXES; ++a) pj = axis == a ? p[a] : pj;
-    rope_cs(pj, r.turns[8 * i + j], sign, t.c[j], t.s[j]);
+// The rotation's table in shared memory. (As a kernel argument it lies in the
+// constant bank, which serves one address at a time: a warp's lanes read 4 or 8
+// different pairs, and 16 such reads a thread took longer than the sines and
+// cosines.)
+struct RopeTable {
+  ulonglong2 turns[ATTN_MAX_PAIRS / 2];
+  uint2 axis[ATTN_MAX_PAIRS / 8];
+};
+
+__device__ __forceinline__ void load_table(RopeTable& t, const attn_rope_t& r) {
+  const int i = threadIdx.x;
+  if (i < ATTN_MAX_PAIRS) {
+    reinterpret_cast<unsigned long long*>(t.turns)[i] = r.turns[i];
+    reinterpret_cast<unsigned char*>(t.axis)[i] = r.axis[i];
   }
+  __syncthreads();
+}
+
+// cos, sin of pairs 8 i .. 8 i + 7 at the positions p of the axes.
+__device__ __forceinline__ void lane_turn(const RopeTable& r, int i, const int (&p)[ATTN_MAX_AXES],
+                                          float sign, Turn8& t) {
+  const uint2 ax = r.axis[i];
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const ulonglong2 turns = r.turns[4 * i + j / 2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int axis = ((j < 4 ? ax.x : ax.y) >> (8 * ((j + u) % 4))) & 0xff;
+      int pj = p[0];
+#pragma unroll
+      for (int a = 1; a < ATTN_MAX_AXES; ++a) pj = axis == a ? p[a] : pj;
+      rope_cs(pj, u ? turns.y : turns.x, sign, t.c[j + u], t.s[j + u]);
+    }
+  }
+}
+
+__device__ __forceinline__ void load_positions(int (&p)[ATTN_MAX_AXES], int n_axes, const int* pos,
+                                               long long stride) {
+#pragma unroll
+  for (int a = 0; a < ATTN_MAX_AXES; ++a) p[a] = a < n_axes ? __ldg(pos + a * stride) : 0;
 }
 
 template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   pdl_launch_dependents();
+  __shared__ RopeTable s_table;
+  load_table(s_table, a.rope);  // kernel arguments alone: before the previous kernel is done
   pdl_wait();
   constexpr int kLanes = D / 16;
   const long long id = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -120,7 +148,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   for (int u = 0; u < kUnroll; ++u)
     if (h0 + u < h1) v[u] = load16(from(h0 + u), off_a, off_b);
   Turn8 t;
-  if (turns) lane_turn(a.rope, i, a.pos + b * a.pos_batch + l, a.pos_axis, a.sign, t);
+  if (turns) {
+    int p[ATTN_MAX_AXES];
+    load_positions(p, a.rope.n_axes, a.pos + b * a.pos_batch + l, a.pos_axis);
+    lane_turn(s_table, i, p, a.sign, t);
+  }
   for (int h = h0; h < h1; h += kUnroll) {
     if (h > h0) {
 #pragma unroll
@@ -161,35 +193,38 @@ __device__ __forceinline__ int find_sequence(const int* cu, int n, long long t) 
   return lo;
 }
 
-// Where token t goes: its cache position, its page (or -1: it is not written)
-// and its slot. Anything out of range is recorded in the status word.
-__device__ __forceinline__ long long find_page(const AppendArgs& a, long long t, long long& at,
-                                               int& slot) {
+// Where token t goes: its place in its sequence, the table entry of its page
+// (null: it is not written) and its slot. A place out of range is recorded in
+// the status word; the entry's page is checked when it is used, so that its load
+// overlaps the trigonometry.
+struct Place {
+  const int* entry;
+  int at, slot;
+};
+__device__ __forceinline__ Place find_place(const AppendArgs& a, long long t) {
+  Place p{nullptr, 0, 0};
   int s;
   long long back;  // new tokens of the sequence from this one on
   if (a.cu_new) {
     s = find_sequence(a.cu_new, a.n_seqs, t);
-    if (s < 0) return -1;  // behind the last sequence: padding
+    if (s < 0) return p;  // behind the last sequence: padding
     back = __ldg(a.cu_new + s + 1) - t;
   } else {
     s = static_cast<int>(t);
     back = 1;
   }
   const int len = __ldg(a.lens + s);
-  if (len == 0) return -1;  // an empty slot of the batch
-  at = len - back;
+  if (len == 0) return p;  // an empty slot of the batch
+  const long long at = len - back;
   if (at < 0 || at >= static_cast<long long>(a.max_pages) * a.cache.page_size) {
     atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-    return -1;
+    return p;
   }
-  const int entry = static_cast<int>(at) / a.cache.page_size;
-  slot = static_cast<int>(at) - entry * a.cache.page_size;
-  const int page = __ldg(a.table + s * a.table_stride + entry);
-  if (page < 0 || page >= a.cache.n_pages) {
-    atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-    return -1;
-  }
-  return page;
+  p.at = static_cast<int>(at);
+  const int entry = p.at / a.cache.page_size;
+  p.slot = p.at - entry * a.cache.page_size;
+  p.entry = a.table + s * a.table_stride + entry;
+  return p;
 }
 
 __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv) {
@@ -200,9 +235,11 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv) {
 // blockIdx.z: the keys' or the values' half of the work (a thread that did both
 // would hold twice the registers, and its values would wait for its keys' angles).
 template <int D, bool INTERLEAVED, bool F8>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 6)
     append_kernel(const __grid_constant__ AppendArgs a) {
   pdl_launch_dependents();
+  __shared__ RopeTable s_table;
+  load_table(s_table, a.rope);  // kernel arguments alone: before the previous kernel is done
   pdl_wait();
   constexpr int kLanes = D / 16;
   const long long id = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -226,23 +263,23 @@ __global__ void __launch_bounds__(kRopeThreads)
       if (h + u < h1) v[u] = load16(in + (h + u) * in_head, off_a, off_b);
   };
   fetch(h0);
-  long long at = 0;
-  int slot = 0;
-  const long long page = find_page(a, token, at, slot);
-  if (page < 0) return;
+  int pos[ATTN_MAX_AXES] = {};
+  if (turns && a.pos) load_positions(pos, a.rope.n_axes, a.pos + token, a.pos_axis);
+  const Place place = find_place(a, token);
+  if (!place.entry) return;
+  const int page = __ldg(place.entry);
   Turn8 t;
   if (turns) {
-    if (a.pos) {
-      lane_turn(a.rope, i, a.pos + token, a.pos_axis, 1.f, t);
-    } else {  // one axis: the place in the cache
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        rope_cs(static_cast<int>(at), a.rope.turns[8 * i + j], 1.f, t.c[j], t.s[j]);
-    }
+    if (!a.pos) pos[0] = place.at;  // one axis: the place in the sequence
+    lane_turn(s_table, i, pos, 1.f, t);
+  }
+  if (page < 0 || page >= c.n_pages) {
+    atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+    return;
   }
   const long long* st = keys ? c.k_strides : c.v_strides;
   const long long out_head = st[2];
-  const long long row = page * st[0] + slot * st[1];
+  const long long row = page * st[0] + place.slot * st[1];
   for (int h = h0; h < h1; h += kUnroll) {
     if (h > h0) fetch(h);
 #pragma unroll
