@@ -314,6 +314,10 @@ int check_cache(const attn_cache_t* c) {
   const int multiple = c->type == ATTN_CACHE_E4M3 ? 16 : 8;
   if (s == ATTN_OK) s = check_strides(c->k_strides, 3, multiple);
   if (s == ATTN_OK) s = check_strides(c->v_strides, 3, multiple);
+  const long long sizes[3] = {c->n_pages, c->page_size, c->H_kv};
+  for (int i = 0; i < 3 && s == ATTN_OK; ++i)
+    for (long long st : {c->k_strides[i], c->v_strides[i]})
+      if (sizes[i] > 1 && st < c->d) s = ATTN_ERR_INVALID_ARG;  // rows apart
   return s;
 }
 
@@ -352,19 +356,20 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
   // Clusters, where one wave of them leaves each CTA at most 4 tiles: that costs
   // one launch instead of two and needs no workspace. With more tiles a CTA,
   // spreading them over all SMs is worth the second launch.
+  constexpr int wave = eba::kDecodeCtas;
   int splits = 1;
-  while (splits < 8 && splits < item_tiles && items * splits * 2 <= eba::kDecodeCtas) splits *= 2;
-  if (items * splits <= eba::kDecodeCtas && item_tiles <= 4 * splits) {
+  while (splits < 8 && splits < item_tiles && items * splits * 2 <= wave) splits *= 2;
+  if (items * splits <= wave && item_tiles <= 4 * splits) {
     p.splits = splits;
     p.ctas = static_cast<int>(items * splits);
     return p;
   }
   // no more CTAs than tiles the tables can hold; a single-tile item is never cut
-  p.ctas = static_cast<int>(std::min<long long>(eba::kDecodeCtas, items * item_tiles));
+  p.ctas = static_cast<int>(std::min<long long>(wave, items * item_tiles));
   p.join = item_tiles > 1;
   if (!p.join) return p;
   p.items = static_cast<size_t>(items);
-  p.slots = 2 * static_cast<size_t>(eba::kDecodeCtas) * p.rows;
+  p.slots = 2 * static_cast<size_t>(wave) * p.rows;
   p.bytes = (p.items * sizeof(int) + 15) / 16 * 16 + p.slots * (d + 2) * sizeof(float);
   return p;
 }
@@ -1006,6 +1011,7 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
   a.pos_axis = pos_stride;
   a.status = status;
   if (rope) a.rope = *rope;
+  a.limit_ns = g_wait_limit_ns.load();
   cudaError_t e = eba::launch_decode(a, p.ctas, p.join, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }

@@ -43,11 +43,10 @@ namespace eba {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kThreads = 32 * kWarps;             // that compute
+constexpr int kBlock = kThreads + 64;             // and the two warps that load
+constexpr int kAhead = 2;                         // tiles a page number is fetched ahead of its load
 constexpr int kSubKeys = 16;                      // keys of a matrix instruction
-constexpr int kRingBytes = 24 * 1024;             // of each warp
-constexpr int kPassCols = 64;                     // columns of O summed over the warps at a time
-constexpr int kPassRow = kPassCols + 4;           // floats; +4: conflict-free column writes
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 8.f;                     // scores may pass the reference by a factor 2^8
 constexpr float kF16Shift = 7.f;                  // e4m3 caches: P's largest value is 2^(8 + 7)
@@ -57,25 +56,28 @@ struct Layout {
   static constexpr int N = 8 * NB;                    // query heads of a CTA
   static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a cached row
   // A warp's step: 4 KB each of K and V where two sets of 16 keys do not pass it,
-  // so that what a step costs besides its bytes is paid once for as many bytes
-  // (e4m3, d = 128, 16 heads a group: 131071 keys x 4 heads x 8 at 16 keys a step
-  // 130 us).
+  // so that what a step costs besides its bytes is paid once for as many bytes.
   static constexpr int kSub = kRow == 256 ? 1 : 2;
   static constexpr int kStepKeys = kSubKeys * kSub;
   static constexpr int kTileKeys = kWarps * kStepKeys;
-  static constexpr int kTile = kStepKeys * kRow;      // of a warp's K (or V) step
-  static_assert(kTileKeys == (kRow == 256 ? 64 : 128), "decode_tile_keys in kernels.h");
-  static constexpr int kStages = kRingBytes / (2 * kTile);
+  static constexpr int kBoxes = kTileKeys / kSubKeys; // sets of 16 keys
+  static constexpr int kStep = kStepKeys * kRow;      // bytes of a warp's K (or V) step
+  static constexpr int kTile = kWarps * kStep;
+  static constexpr int kStages = 96 * 1024 / (2 * kTile);  // K and V slots of the ring
   static constexpr int kQRow = D + 8;                 // 16-bit elements of a staged query row
-  static constexpr int kRing = kWarps * kRingBytes;
-  static constexpr int kSum = kWarps * 8 * kPassRow * 4;
-  static constexpr int kQ = N * kQRow * 2;
-  static constexpr int kOffSum = kRing;
-  static constexpr int kOffQ = kOffSum + kSum;
-  static constexpr int kOffMl = kOffQ + kQ;           // per warp and row: reference, sum
+  static constexpr int kPassCols = 64;                // of O, summed over the warps at a time
+  static constexpr int kPassRow = kPassCols + 4;      // floats; +4: conflict-free column writes
+  static constexpr int kOffSum = 2 * kStages * kTile;
+  static constexpr int kOffQ = kOffSum + kWarps * 8 * kPassRow * 4;
+  static constexpr int kOffMl = kOffQ + N * kQRow * 2;    // per warp and row: reference, sum
   static constexpr int kOffQs = kOffMl + kWarps * N * 8;  // per row: score factor
-  static constexpr int kOffMask = kOffQs + N * 4;     // per warp and stage: keys that count
-  static constexpr int kBytes = kOffMask + kWarps * kStages * 4;
+  static constexpr int kOffKeys = kOffQs + N * 4;         // per stage and 16 keys: those that count
+  static constexpr int kOffBar = kOffKeys + kStages * kBoxes * 2;  // filled K, V, emptied K, V
+  static constexpr int kOffScan = kOffBar + kStages * 32;
+  static constexpr int kOffFirst = kOffScan + kWarps * 4;
+  static constexpr int kOffAbort = kOffFirst + 20;
+  static constexpr int kBytes = kOffAbort + 4;
+  static_assert(kTileKeys == decode_tile_keys(kRow) && kOffBar % 8 == 0, "");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -83,13 +85,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
                "r"(valid ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
+// Arrive on `bar` once this lane's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -164,13 +164,16 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Where 16-byte chunk c of row r lies in a tile of kRow-byte rows, so that the
-// 8 rows of a matrix load fall into 8 different bank groups.
+// Where 16-byte chunk c of row r lies in a tile of kRow-byte rows: permuted so that
+// the 8 rows of a matrix load fall into 8 different bank groups.
 template <int kRow>
 __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
   if constexpr (kRow >= 128) return static_cast<uint32_t>(r * kRow + ((c ^ (r & 7)) << 4));
   return static_cast<uint32_t>(r * kRow + ((c ^ ((r >> 1) & 3)) << 4));
 }
+
+// The barrier of the computing warps.
+__device__ __forceinline__ void sync_compute() { named_bar_sync(1, kThreads); }
 
 // A place in the list of tiles: tile t of nt of sequence b (len keys), head hh
 // (K/V head and block of query heads).
@@ -205,21 +208,135 @@ __device__ __forceinline__ int first_tile(int i, int tiles, int ctas) {
   return static_cast<int>(static_cast<long long>(i) * tiles / ctas);
 }
 
-// WHOLE: the page size is a multiple of a step's 16 keys, so that a step lies in
-// one page (two sets of 16, two) and its rows are one stride apart; otherwise each row is looked up.
+// A loading warp (one for K, one for V): runs through the CTA's tiles ahead of the
+// computing warps and fills the ring's slots as these empty them. Page numbers wait
+// in line behind the card's streaming reads, so they are fetched kAhead tiles early.
+// The copies are cp.async, 16 bytes a lane: a key that does not count reads nothing
+// and leaves zeros, so that its weight 0 gives 0. (Tiled loads of 16 rows by TMA
+// took 5 to 15 % longer here: pages of 16 keys make them small, and one thread
+// issues each.)
+// WHOLE: the page size is a multiple of 16 keys, so that each 16 lie in one page and
+// are looked up once; else each key is looked up by itself.
+template <typename L, bool WHOLE>
+__device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned char* from,
+                                           const long long (&strides)[3], int half,
+                                           unsigned char* smem, Cursor ld, int tiles,
+                                           volatile int* s_abort) {
+  constexpr int kStages = L::kStages, kTileKeys = L::kTileKeys, kBoxes = L::kBoxes;
+  constexpr int kPer = WHOLE ? 1 : kTileKeys / 32;  // look-ups of a lane and tile
+  constexpr int kLanes = L::kRow / 16;              // of a row: 16 bytes each
+  constexpr int kRows = 32 / kLanes;                // of an instruction
+  const int lane = threadIdx.x & 31;
+  const int c = lane % kLanes, r_lane = lane / kLanes;
+  const uint32_t ring = smem_u32(smem) + half * L::kTile;
+  const uint32_t bars = smem_u32(smem + L::kOffBar) + half * 8;
+  uint16_t* s_keys = reinterpret_cast<uint16_t*>(smem + L::kOffKeys);
+  const DeviceStatus st{a.status, a.limit_ns};
+  const unsigned char* at = from + c * 16 + (WHOLE ? r_lane * strides[1] : 0);
+  Cursor look = ld;
+  int look_left = tiles;
+  int page_of[kAhead][kPer], slot_of[kAhead][kPer];  // slot -1: no such key
+  auto look_up = [&]() {
+#pragma unroll
+    for (int i = 0; i + 1 < kAhead; ++i)
+#pragma unroll
+      for (int x = 0; x < kPer; ++x)
+        page_of[i][x] = page_of[i + 1][x], slot_of[i][x] = slot_of[i + 1][x];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int in = WHOLE ? lane * kSubKeys : lane + 32 * x;
+      const int key = look.t * kTileKeys + in;
+      page_of[kAhead - 1][x] = 0;
+      slot_of[kAhead - 1][x] = -1;
+      if (look_left > 0 && in < kTileKeys && key < look.len) {
+        const int entry = key / a.cache.page_size;
+        slot_of[kAhead - 1][x] = key - entry * a.cache.page_size;
+        page_of[kAhead - 1][x] = __ldg(a.table + look.b * a.table_stride + entry);
+      }
+    }
+    if (--look_left > 0) advance<kTileKeys>(look, a);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) look_up();
+
+  int stage = 0, lap = 0;
+#pragma unroll 1
+  for (int i = 0; i < tiles; ++i) {
+    const long long head = (ld.hh / a.blocks) * strides[2];
+    uint32_t keys[kPer];   // that count: WHOLE of this lane's 16, else of 32
+    long long off[kPer];   // of the looked-up rows
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int page = page_of[0][x], slot = slot_of[0][x];
+      const bool held = slot >= 0;
+      const bool ok = held && static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages);
+      if (held && !ok) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+      off[x] = ok ? page * strides[0] + slot * strides[1] + head : 0;
+      keys[x] = WHOLE ? (ok ? (1u << min(ld.len - ld.t * kTileKeys - lane * kSubKeys, kSubKeys)) - 1u : 0u)
+                      : __ballot_sync(0xffffffffu, ok);
+    }
+    look_up();
+    const uint32_t full = bars + stage * 16, empty = full + kStages * 16;
+    const uint32_t to = ring + stage * 2 * L::kTile;
+    if (lap > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (lap - 1) & 1, s_abort, st))) break;
+    if (half == 0) {
+      if (WHOLE) {
+        if (lane < kBoxes) s_keys[stage * kBoxes + lane] = static_cast<uint16_t>(keys[0]);
+      } else if (lane < 2) {
+#pragma unroll
+        for (int x = 0; x < kPer; ++x)
+          s_keys[stage * kBoxes + 2 * x + lane] = static_cast<uint16_t>(keys[x] >> (16 * lane));
+      }
+    }
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int bx = 0; bx < kBoxes; ++bx) {
+        const uint32_t mask = __shfl_sync(0xffffffffu, keys[0], bx);
+        const unsigned char* p = at + __shfl_sync(0xffffffffu, off[0], bx);
+#pragma unroll
+        for (int i = 0; i < kSubKeys / kRows; ++i) {
+          const int r = i * kRows + r_lane;
+          cp_async16(to + tile_offset<L::kRow>(bx * kSubKeys + r, c), p, (mask >> r) & 1);
+          p += kRows * strides[1];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < kPer; ++x)
+#pragma unroll
+        for (int i = 0; i < 32 / kRows; ++i) {
+          const int r = i * kRows + r_lane;
+          cp_async16(to + tile_offset<L::kRow>(32 * x + r, c), at + __shfl_sync(0xffffffffu, off[x], r),
+                     (keys[x] >> r) & 1);
+        }
+    }
+    cp_async_arrive(full);
+    if (i + 1 < tiles) advance<kTileKeys>(ld, a);
+    if (++stage == kStages) stage = 0, ++lap;
+  }
+  cp_async_wait_all();  // also after a wait that gave up
+}
+
 template <int D, int NB, bool F8, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kBlock, 2)
     decode_kernel(const __grid_constant__ DecodeArgs a) {
   using L = Layout<D, NB, F8>;
   constexpr int N = L::N;
   constexpr int kStages = L::kStages;
-  constexpr int kSub = L::kSub, kStepKeys = L::kStepKeys, kTileKeys = L::kTileKeys;
+  constexpr int kPassCols = L::kPassCols, kPassRow = L::kPassRow;
+  constexpr int kSub = L::kSub, kTileKeys = L::kTileKeys;
   constexpr uint32_t kAllKeys = kSub == 1 ? 0xffffu : 0xffffffffu;
   constexpr int kKSteps = D / 16;  // 16-element steps of a product over d; 16-row tiles of V^T
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int s_scan[kWarps];
-  __shared__ Cursor s_first;
+  int* s_scan = reinterpret_cast<int*>(smem + L::kOffScan);
+  Cursor& s_first = *reinterpret_cast<Cursor*>(smem + L::kOffFirst);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
   pdl_launch_dependents();
+  const uint32_t bars = smem_u32(smem + L::kOffBar);
+  if (threadIdx.x < 4 * kStages)  // filled by 32 lanes, emptied by 4 warps
+    mbar_init(bars + threadIdx.x * 8, threadIdx.x < 2 * kStages ? 32 : kWarps);
+  if (threadIdx.x == 0) *s_abort = 0;
+  fence_mbar_init();
   pdl_wait();
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -242,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else {
     // ---- the list of tiles: each thread counts a run of sequences ----
     const int per = (a.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    const int b0 = min(tid * per, a.B), b1 = tid < kThreads ? min(b0 + per, a.B) : b0;
     int mine = 0;
     for (int b = b0; b < b1; ++b) {
       const int raw = __ldg(a.lens + b);
@@ -255,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int o = __shfl_up_sync(0xffffffffu, incl, m);
       if (lane >= m) incl += o;
     }
-    if (lane == 31) s_scan[warp] = incl;
+    if (lane == 31 && warp < kWarps) s_scan[warp] = incl;
     __syncthreads();
     int before = 0;
 #pragma unroll
@@ -284,18 +401,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     // Sequences without keys: O = 0, lse = -inf.
     for (int b = cta; b < a.B; b += gridDim.x) {
       if (clamp_len(a, b) > 0) continue;
-      for (int x = tid; x < a.H * D / 8; x += kThreads)
+      for (int x = tid; x < a.H * D / 8; x += kBlock)
         *reinterpret_cast<uint4*>(a.o + static_cast<long long>(b) * a.H * D + x * 8) =
             make_uint4(0, 0, 0, 0);
-      for (int h = tid; h < a.H; h += kThreads) a.lse[static_cast<long long>(b) * a.H + h] = -INFINITY;
+      for (int h = tid; h < a.H; h += kBlock) a.lse[static_cast<long long>(b) * a.H + h] = -INFINITY;
       if (a.item)
-        for (int x = tid; x < a.heads; x += kThreads) a.item[static_cast<long long>(b) * a.heads + x] = 0;
+        for (int x = tid; x < a.heads; x += kBlock) a.item[static_cast<long long>(b) * a.heads + x] = 0;
     }
   }
   __syncthreads();
   if (!a.splits && r0 >= r1) return;
 
-  const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
   float* s_sum = reinterpret_cast<float*>(smem + L::kOffSum);
   uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + L::kOffQ);
   float2* s_ml = reinterpret_cast<float2*>(smem + L::kOffMl);
@@ -303,93 +419,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* s_part = reinterpret_cast<float*>(smem);
   float2* s_part_ml = reinterpret_cast<float2*>(smem + N * D * 4);
   float* s_qs = reinterpret_cast<float*>(smem + L::kOffQs);
-  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + L::kOffMask) + warp * kStages;
 
-  // ---- loads: the page of each 16 keys (WHOLE; lane % kSub) or of each key ----
-  Cursor ld = s_first;
-  int ld_left = r1 - r0;
-  int page = -1, slot = 0;
-  bool held = false;  // whether there is such a key; its page is checked when it is used
-  auto look_up = [&]() {
-    const int key = ld.t * kTileKeys + warp * kStepKeys + (WHOLE ? lane % kSub * kSubKeys : lane % kStepKeys);
-    held = ld_left > 0 && key < ld.len;
-    if (held) {
-      const int entry = key / a.cache.page_size;
-      slot = key - entry * a.cache.page_size;
-      page = __ldg(a.table + ld.b * a.table_stride + entry);
+  if (warp >= kWarps) {
+    const bool keys = warp == kWarps;
+    if (r0 < r1)
+      load_tiles<L, WHOLE>(a, keys ? a.k : a.v, keys ? a.k_strides : a.v_strides, keys ? 0 : 1, smem,
+                           s_first, r1 - r0, s_abort);
+    if (a.splits > 1 || s_first.nt == 0) {  // the cluster's barriers below
+      cluster_sync();
+      cluster_sync();
     }
-  };
-  auto issue = [&](int stage) {
-    constexpr int kLanes = L::kRow / 16;     // of a row
-    constexpr int kRows = 32 / kLanes;       // of an instruction
-    if (!held) {
-      page = -1;
-    } else if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.cache.n_pages)) {
-      atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-      page = -1;
-    }
-    const uint32_t kt = ring + stage * 2 * L::kTile, vt = kt + L::kTile;
-    const int c = lane % kLanes, r_lane = lane / kLanes;
-    uint32_t mask = 0;
-    if constexpr (WHOLE) {
-      const int left = ld.len - ld.t * kTileKeys - warp * kStepKeys;
-      const int g = ld.hh / a.blocks;
-      int pg[kSub], sl[kSub], count[kSub];
-#pragma unroll
-      for (int sub = 0; sub < kSub; ++sub) {
-        pg[sub] = kSub == 1 ? page : __shfl_sync(0xffffffffu, page, sub);
-        sl[sub] = kSub == 1 ? slot : __shfl_sync(0xffffffffu, slot, sub);
-        count[sub] = pg[sub] < 0 ? 0 : min(left - sub * kSubKeys, kSubKeys);
-        mask |= ((1u << count[sub]) - 1u) << (sub * kSubKeys);
-      }
-      if (mask) {
-        // keys that do not count are filled with zeros: the weight 0 must not
-        // meet what an earlier step left there
-#pragma unroll
-        for (int sub = 0; sub < kSub; ++sub) {
-          const int pg0 = max(pg[sub], 0), sl0 = count[sub] > 0 ? sl[sub] : 0;
-          const unsigned char* kp = a.k + (pg0 * a.k_strides[0] + (sl0 + r_lane) * a.k_strides[1] +
-                                           g * a.k_strides[2] + c * 16);
-          const unsigned char* vp = a.v + (pg0 * a.v_strides[0] + (sl0 + r_lane) * a.v_strides[1] +
-                                           g * a.v_strides[2] + c * 16);
-#pragma unroll
-          for (int i = 0; i < kSubKeys / kRows; ++i) {
-            const int r = i * kRows + r_lane;  // rows behind the last key read nothing
-            const uint32_t to = tile_offset<L::kRow>(sub * kSubKeys + r, c);
-            cp_async16(kt + to, kp, r < count[sub]);
-            cp_async16(vt + to, vp, r < count[sub]);
-            kp += kRows * a.k_strides[1];
-            vp += kRows * a.v_strides[1];
-          }
-        }
-      }
-    } else {
-      mask = __ballot_sync(0xffffffffu, page >= 0) & kAllKeys;
-      if (mask) {
-        const int g = ld.hh / a.blocks;
-        const long long pg = max(page, 0);
-        const long long ko = pg * a.k_strides[0] + slot * a.k_strides[1] + g * a.k_strides[2];
-        const long long vo = pg * a.v_strides[0] + slot * a.v_strides[1] + g * a.v_strides[2];
-#pragma unroll
-        for (int i = 0; i < kStepKeys / kRows; ++i) {
-          const int r = i * kRows + r_lane;
-          const bool ok = (mask >> r) & 1;
-          const long long kr = __shfl_sync(0xffffffffu, ko, r);
-          const long long vr = __shfl_sync(0xffffffffu, vo, r);
-          const uint32_t to = tile_offset<L::kRow>(r, c);
-          cp_async16(kt + to, a.k + (ok ? kr + c * 16 : 0), ok);
-          cp_async16(vt + to, a.v + (ok ? vr + c * 16 : 0), ok);
-        }
-      }
-    }
-    if (lane == 0) s_mask[stage] = mask;
-    cp_async_commit();
-    if (--ld_left > 0) advance<kTileKeys>(ld, a);
-    look_up();
-  };
-  look_up();
-#pragma unroll 1
-  for (int s = 0; s < kStages - 1; ++s) issue(s);
+    return;
+  }
 
   // ---- the query heads of an item, staged for all warps ----
   // Row n: query head g G + blk N + n; rotated where asked, rounded to bf16
@@ -487,25 +528,32 @@ __global__ void __launch_bounds__(kThreads, 2)
   bool first_item = true;
   if (r0 < r1) {
     stage_q(cur);
-    __syncthreads();
+    sync_compute();
     begin_item();
   }
 
+  // A wait that gives up is recorded and ends all waits of the CTA; its warps still
+  // meet at every barrier, and what they write is undefined.
+  const DeviceStatus st{a.status, a.limit_ns};
+  bool live = true;
+  auto wait_filled = [&](uint32_t bar, uint32_t parity) {
+    if (live) live = __all_sync(0xffffffffu, mbar_wait(bar, parity, s_abort, st));
+  };
   int stage = 0;
+  uint32_t parity = 0;
 #pragma unroll 1
   for (int tile = r0; tile < r1; ++tile) {
+    const uint32_t kt = smem_u32(smem) + stage * 2 * L::kTile + warp * L::kStep, vt = kt + L::kTile;
+    const uint32_t full = bars + stage * 16, empty = full + kStages * 16;  // K's; V's 8 behind
+    wait_filled(full, parity);
+    uint32_t mask;  // the step's keys that count
     {
-      int into = stage + kStages - 1;
-      if (into >= kStages) into -= kStages;
-      issue(into);
+      const unsigned char* at = smem + L::kOffKeys + (stage * L::kBoxes + warp * kSub) * 2;
+      mask = kSub == 1 ? *reinterpret_cast<const uint16_t*>(at) : *reinterpret_cast<const uint32_t*>(at);
     }
-    cp_async_wait<kStages - 1>();
-    __syncwarp();
-    const uint32_t mask = s_mask[stage];
+    // S^T = K Q^T: two chains, of the two halves of d or of two sets of keys
+    float s[NB][2][4];
     if (mask) {
-      const uint32_t kt = ring + stage * 2 * L::kTile, vt = kt + L::kTile;
-      // S^T = K Q^T: two chains, of the two halves of d or of two sets of keys
-      float s[NB][2][4];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -541,6 +589,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
+    }
+    __syncwarp();  // all lanes have read the mask and are done with K
+    if (lane == 0) mbar_arrive(empty);
+    uint32_t ph[kSub][NB][2], pl[kSub][NB][2];
+    if (mask) {
       // online softmax; element x of a lane: key u8 + 8 (x / 2), column 2 j4 + x % 2
       float v[NB][kSub][4];
       bool grew = false;
@@ -585,7 +638,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
       }
-      uint32_t ph[kSub][NB][2], pl[kSub][NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float ref[2];
@@ -615,6 +667,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
+    }
+    wait_filled(full + 8, parity);
+    if (mask) {
       // O^T += V^T P^T
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
@@ -652,8 +707,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
-    __syncwarp();  // all lanes are done with the stage before it is loaded again
-    if (++stage == kStages) stage = 0;
+    __syncwarp();  // all lanes are done with V
+    if (lane == 0) mbar_arrive(empty + 8);
+    if (++stage == kStages) stage = 0, parity ^= 1;
 
     const bool item_done = cur.t + 1 == cur.nt;
     if (item_done || tile + 1 == r1) {
@@ -674,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           top[nb][x] = ref;
           if (u8 == 0) s_ml[warp * N + nb * 8 + 2 * j4 + x] = make_float2(ref, l);
         }
-      __syncthreads();
+      sync_compute();
       const bool more = tile + 1 < r1;
       if (more) {
         advance<kTileKeys>(cur, a);
@@ -693,7 +749,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * N + nb * 8 + 2 * j4 + x].x);
           f[x] = top[nb][x] == -INFINITY ? 0.f : ex2_approx(top[nb][x] - M);
         }
-        const int row = tid >> 4, c4 = (tid & 15) * 4;  // of the sum below
+        constexpr int kCols = kPassCols / 16;  // of a thread in the sum below
+        const int row = tid >> 4, c4 = (tid & 15) * kCols;
         float M = -INFINITY, l = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * N + nb * 8 + row].x);
@@ -714,26 +771,32 @@ __global__ void __launch_bounds__(kThreads, 2)
               const int col = F8 ? k * 16 + 2 * u8 + (x >> 1) : k * 16 + u8 + 8 * (x >> 1);
               to[(2 * j4 + (x & 1)) * kPassRow + col] = o[nb][c0 / 16 + k][x] * f[x & 1];
             }
-          __syncthreads();
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          sync_compute();
+          float v[kCols] = {};
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float4 y = *reinterpret_cast<const float4*>(s_sum + (w * 8 + row) * kPassRow + c4);
-            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+            const float* y = s_sum + (w * 8 + row) * kPassRow + c4;
+#pragma unroll
+            for (int x = 0; x < kCols; x += 2) {
+              const float2 two = *reinterpret_cast<const float2*>(y + x);
+              v[x] += two.x, v[x + 1] += two.y;
+            }
           }
-          if (a.splits > 1) {
-            *reinterpret_cast<float4*>(s_part + (nb * 8 + row) * D + c0 + c4) = v;
-          } else if (whole) {
+          if (whole && a.splits <= 1) {
             if (hg < a.group) {
               const float f = M == -INFINITY ? 0.f : a.o_scale / l;
-              *reinterpret_cast<uint2*>(a.o + head * D + c0 + c4) =
-                  make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+#pragma unroll
+              for (int x = 0; x < kCols; x += 2)
+                *reinterpret_cast<uint32_t*>(a.o + head * D + c0 + c4 + x) = pack_bf16(v[x] * f, v[x + 1] * f);
             }
           } else {
-            *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(part) * N + nb * 8 + row) * D +
-                                       c0 + c4) = v;
+            float* to = a.splits > 1 ? s_part + (nb * 8 + row) * D
+                                     : a.part_o + (static_cast<long long>(part) * N + nb * 8 + row) * D;
+#pragma unroll
+            for (int x = 0; x < kCols; x += 2)
+              *reinterpret_cast<float2*>(to + c0 + c4 + x) = make_float2(v[x], v[x + 1]);
           }
-          __syncthreads();
+          sync_compute();
         }
         if ((tid & 15) == 0) {
           if (a.splits > 1)
@@ -763,8 +826,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++cur.t;
     }
   }
-  cp_async_wait<0>();
-
   if (a.splits > 1 || s_first.nt == 0) {
     // ---- join the cluster's parts, or write an item without keys ----
     const int g = s_first.hh / a.blocks, blk = s_first.hh - g * a.blocks;
@@ -874,7 +935,7 @@ cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, bool join, cudaStream
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kBlock);
   cfg.dynamicSmemBytes = L::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

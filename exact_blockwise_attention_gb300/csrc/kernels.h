@@ -294,6 +294,7 @@ struct DecodeArgs {
   const int* pos;
   long long pos_axis;
   int* status;
+  unsigned long long limit_ns;
   attn_rope_t rope;
 };
 cudaError_t launch_decode(const DecodeArgs& a, int ctas, bool join, cudaStream_t stream);
