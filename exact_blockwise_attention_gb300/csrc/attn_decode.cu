@@ -175,6 +175,13 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
 // The barrier of the computing warps.
 __device__ __forceinline__ void sync_compute() { named_bar_sync(1, kThreads); }
 
+// e4m3: a lane's four consecutive bytes of K serve the two halves of its register
+// operand (elements 0, 1 and 8, 9 of the product's order), so the query's elements
+// are staged in that order.
+__device__ __forceinline__ int q_place(int e) {
+  return (e & ~15) + ((e >> 2) & 3) * 2 + (e & 1) + ((e & 2) ? 8 : 0);
+}
+
 // A place in the list of tiles: tile t of nt of sequence b (len keys), head hh
 // (K/V head and block of query heads).
 struct Cursor {
@@ -482,8 +489,8 @@ __global__ void __launch_bounds__(kBlock, 2)
       if (i == 0) s_qs[n] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
-        s_q[n * L::kQRow + ox[p]] = __half_as_ushort(__float2half_rn(x[p] * up));
-        s_q[n * L::kQRow + oy[p]] = __half_as_ushort(__float2half_rn(y[p] * up));
+        s_q[n * L::kQRow + q_place(ox[p])] = __half_as_ushort(__float2half_rn(x[p] * up));
+        s_q[n * L::kQRow + q_place(oy[p])] = __half_as_ushort(__float2half_rn(y[p] * up));
       }
     } else {
       if (i == 0) s_qs[n] = a.scale_log2;
@@ -495,22 +502,22 @@ __global__ void __launch_bounds__(kBlock, 2)
     }
   };
 
-  uint32_t qf[NB][kKSteps][2];  // the query as the product's column operand
+  // The query as the product's column operand: registers for one set of columns;
+  // two sets would not fit the 168 registers that 12 warps leave each, and are
+  // read in every step.
+  uint32_t qf[NB == 1 ? kKSteps / 2 : 1][4];
+  auto load_q = [&](uint32_t (&f)[4], int nb, int k) {  // of steps k and k + 1
+    ldmatrix4(f, smem_u32(s_q + (nb * 8 + (lane & 7)) * L::kQRow + (2 * k + (lane >> 3)) * 8));
+  };
   float qs[NB][2];              // score factor of this lane's two columns
   float o[NB][kKSteps][4];
   float top[NB][2], sum[NB][2];
   auto begin_item = [&]() {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const uint16_t* row = s_q + (nb * 8 + u8) * L::kQRow;
 #pragma unroll
       for (int k = 0; k < kKSteps; ++k) {
-        // e4m3: a lane's four consecutive bytes of K serve its two register
-        // halves, so the query's elements are taken in the same order
-        const int e0 = F8 ? k * 16 + 4 * j4 : k * 16 + 2 * j4;
-        const int e1 = F8 ? e0 + 2 : e0 + 8;
-        qf[nb][k][0] = *reinterpret_cast<const uint32_t*>(row + e0);
-        qf[nb][k][1] = *reinterpret_cast<const uint32_t*>(row + e1);
+        if (NB == 1 && k % 2 == 0) load_q(qf[k / 2], 0, k);
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[nb][k][x] = 0.f;
       }
@@ -558,13 +565,24 @@ __global__ void __launch_bounds__(kBlock, 2)
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[nb][0][x] = s[nb][1][x] = 0.f;
-      if constexpr (F8) {
 #pragma unroll
-        for (int k = 0; k < kKSteps; k += 2) {
+      for (int k = 0; k < kKSteps; k += 2) {
+        uint32_t q[NB][4];
 #pragma unroll
-          for (int sub = 0; sub < kSub; ++sub) {
+        for (int nb = 0; nb < NB; ++nb) {
+          if constexpr (NB == 1) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) q[nb][x] = qf[k / 2][x];
+          } else {
+            load_q(q[nb], nb, k);
+          }
+        }
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+          const int row = sub * kSubKeys + (lane & 15);
+          if constexpr (F8) {
             uint32_t r[4];
-            ldmatrix4(r, kt + tile_offset<L::kRow>(sub * kSubKeys + (lane & 15), k + (lane >> 4)));
+            ldmatrix4(r, kt + tile_offset<L::kRow>(row, k + (lane >> 4)));
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const uint32_t lo = r[2 * x], hi = r[2 * x + 1];
@@ -572,20 +590,17 @@ __global__ void __launch_bounds__(kBlock, 2)
                                      e4m3x2_f16x2(hi >> 16)};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
-                mma16816<true>(s[nb][kSub == 1 ? x : sub], f, qf[nb][k + x][0], qf[nb][k + x][1]);
+                mma16816<true>(s[nb][kSub == 1 ? x : sub], f, q[nb][2 * x], q[nb][2 * x + 1]);
             }
-          }
-        }
-      } else {
+          } else {
 #pragma unroll
-        for (int k = 0; k < kKSteps; ++k) {
+            for (int x = 0; x < 2; ++x) {
+              uint32_t r[4];
+              ldmatrix4(r, kt + tile_offset<L::kRow>(row, 2 * (k + x) + (lane >> 4)));
 #pragma unroll
-          for (int sub = 0; sub < kSub; ++sub) {
-            uint32_t r[4];
-            ldmatrix4(r, kt + tile_offset<L::kRow>(sub * kSubKeys + (lane & 15), 2 * k + (lane >> 4)));
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma16816<false>(s[nb][kSub == 1 ? k & 1 : sub], r, qf[nb][k][0], qf[nb][k][1]);
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816<false>(s[nb][kSub == 1 ? x : sub], r, q[nb][2 * x], q[nb][2 * x + 1]);
+            }
           }
         }
       }
