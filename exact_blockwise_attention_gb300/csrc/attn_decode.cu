@@ -55,10 +55,11 @@ template <int D, int NB, bool F8>
 struct Layout {
   static constexpr int N = 8 * NB;                    // query heads of a CTA
   static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a cached row
-  // A warp's step: 4 KB each of K and V where two sets of 16 keys do not pass it,
-  // so that what a step costs besides its bytes is paid once for as many bytes.
+  // A warp's step: 4 KB each of K and V, so that what a step costs besides its
+  // bytes is paid once for as many bytes.
   static constexpr int kSub = kRow == 256 ? 1 : 2;
-  static constexpr int kStepKeys = kSubKeys * kSub;
+  static constexpr int kRounds = kRow == 64 ? 2 : 1;  // of kSub sets of keys in a step
+  static constexpr int kStepKeys = kSubKeys * kSub * kRounds;
   static constexpr int kTileKeys = kWarps * kStepKeys;
   static constexpr int kBoxes = kTileKeys / kSubKeys; // sets of 16 keys
   static constexpr int kStep = kStepKeys * kRow;      // bytes of a warp's K (or V) step
@@ -80,10 +81,18 @@ struct Layout {
   static_assert(kTileKeys == decode_tile_keys(kRow) && kOffBar % 8 == 0, "");
 };
 
+// 16 bytes; the hint keeps L2 from fetching more than a row (64-byte rows of
+// several heads lie side by side, and the others are read by other CTAs).
+template <int kRow>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
+  if constexpr (kRow == 64)
+    asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
 }
 // Arrive on `bar` once this lane's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -303,7 +312,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned c
 #pragma unroll
         for (int i = 0; i < kSubKeys / kRows; ++i) {
           const int r = i * kRows + r_lane;
-          cp_async16(to + tile_offset<L::kRow>(bx * kSubKeys + r, c), p, (mask >> r) & 1);
+          cp_async16<L::kRow>(to + tile_offset<L::kRow>(bx * kSubKeys + r, c), p, (mask >> r) & 1);
           p += kRows * strides[1];
         }
       }
@@ -313,7 +322,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned c
 #pragma unroll
         for (int i = 0; i < 32 / kRows; ++i) {
           const int r = i * kRows + r_lane;
-          cp_async16(to + tile_offset<L::kRow>(32 * x + r, c), at + __shfl_sync(0xffffffffu, off[x], r),
+          cp_async16<L::kRow>(to + tile_offset<L::kRow>(32 * x + r, c), at + __shfl_sync(0xffffffffu, off[x], r),
                      (keys[x] >> r) & 1);
         }
     }
@@ -553,9 +562,12 @@ __global__ void __launch_bounds__(kBlock, 2)
     const uint32_t kt = smem_u32(smem) + stage * 2 * L::kTile + warp * L::kStep, vt = kt + L::kTile;
     const uint32_t full = bars + stage * 16, empty = full + kStages * 16;  // K's; V's 8 behind
     wait_filled(full, parity);
-    uint32_t mask;  // the step's keys that count
+#pragma unroll 1
+    for (int round = 0; round < L::kRounds; ++round) {
+    uint32_t mask;  // the keys that count
     {
-      const unsigned char* at = smem + L::kOffKeys + (stage * L::kBoxes + warp * kSub) * 2;
+      const unsigned char* at =
+          smem + L::kOffKeys + (stage * L::kBoxes + (warp * L::kRounds + round) * kSub) * 2;
       mask = kSub == 1 ? *reinterpret_cast<const uint16_t*>(at) : *reinterpret_cast<const uint32_t*>(at);
     }
     // S^T = K Q^T: two chains, of the two halves of d or of two sets of keys
@@ -579,7 +591,7 @@ __global__ void __launch_bounds__(kBlock, 2)
         }
 #pragma unroll
         for (int sub = 0; sub < kSub; ++sub) {
-          const int row = sub * kSubKeys + (lane & 15);
+          const int row = (round * kSub + sub) * kSubKeys + (lane & 15);
           if constexpr (F8) {
             uint32_t r[4];
             ldmatrix4(r, kt + tile_offset<L::kRow>(row, k + (lane >> 4)));
@@ -605,8 +617,10 @@ __global__ void __launch_bounds__(kBlock, 2)
         }
       }
     }
-    __syncwarp();  // all lanes have read the mask and are done with K
-    if (lane == 0) mbar_arrive(empty);
+    if (round + 1 == L::kRounds) {
+      __syncwarp();  // all lanes have read the masks and are done with K
+      if (lane == 0) mbar_arrive(empty);
+    }
     uint32_t ph[kSub][NB][2], pl[kSub][NB][2];
     if (mask) {
       // online softmax; element x of a lane: key u8 + 8 (x / 2), column 2 j4 + x % 2
@@ -683,7 +697,7 @@ __global__ void __launch_bounds__(kBlock, 2)
         }
       }
     }
-    wait_filled(full + 8, parity);
+    if (round == 0) wait_filled(full + 8, parity);
     if (mask) {
       // O^T += V^T P^T
 #pragma unroll
@@ -695,7 +709,7 @@ __global__ void __launch_bounds__(kBlock, 2)
 #pragma unroll
           for (int k = 0; k < kKSteps; k += 2) {
             uint32_t r[4];
-            ldmatrix4_trans(r, vt + tile_offset<L::kRow>(sub * kSubKeys + (lane & 15), k + (lane >> 4)));
+            ldmatrix4_trans(r, vt + tile_offset<L::kRow>((round * kSub + sub) * kSubKeys + (lane & 15), k + (lane >> 4)));
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const uint32_t w0 = __byte_perm(r[2 * x], 0, 0x3120);
@@ -708,7 +722,7 @@ __global__ void __launch_bounds__(kBlock, 2)
             }
           }
         } else {
-          const int vr = sub * kSubKeys + (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+          const int vr = (round * kSub + sub) * kSubKeys + (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
 #pragma unroll
           for (int k = 0; k < kKSteps; ++k) {
             uint32_t r[4];
@@ -721,6 +735,7 @@ __global__ void __launch_bounds__(kBlock, 2)
           }
         }
       }
+    }
     }
     __syncwarp();  // all lanes are done with V
     if (lane == 0) mbar_arrive(empty + 8);

@@ -264,8 +264,8 @@ cudaError_t launch_append(AppendArgs& a, cudaStream_t stream);
 // One new token per sequence over the paged cache. The grid is fixed (two CTAs
 // on each of 152 SMs); any number of SMs gives the same results.
 constexpr int kDecodeCtas = 304;
-// Keys of a work item's tile: 32 KB of keys and values where 128 keys do not pass it.
-constexpr int decode_tile_keys(int row_bytes) { return row_bytes == 256 ? 64 : 128; }
+// Keys of a work item's tile: 32 KB of keys and values.
+constexpr int decode_tile_keys(int row_bytes) { return 16384 / row_bytes; }
 struct DecodeArgs {
   const __nv_bfloat16* q;  // [B, H, d], strides below
   long long q_seq, q_head;
