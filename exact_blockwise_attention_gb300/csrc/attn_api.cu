@@ -331,6 +331,7 @@ int check_table(const int* table, long long stride, int max_pages, const int* le
 struct DecodePlan {
   bool ok;
   int rows, blocks;      // query heads of a CTA (8 or 16), blocks of them in a group
+  int per_item;          // K/V heads of an item
   int heads, max_len;    // items of a sequence; keys of a table row
   int splits, ctas;      // see DecodeArgs; the grid
   bool join;             // items may be cut between CTAs
@@ -344,11 +345,13 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
   // of them, larger ones two at a time
   p.rows = group <= 8 ? 8 : 16;
   p.blocks = (group + p.rows - 1) / p.rows;
-  const int tile = eba::decode_tile_keys(type == ATTN_CACHE_E4M3 ? d : 2 * d);
+  const int row = type == ATTN_CACHE_E4M3 ? d : 2 * d;
+  int tile = eba::decode_tile_keys(row);
+  p.per_item = 1;
   p.max_len = static_cast<int>(std::min(capacity, (1ll << 31) - 1 - tile));
   p.heads = H_kv * p.blocks;
-  const long long item_tiles = (p.max_len + tile - 1) / tile;
-  const long long items = static_cast<long long>(B) * p.heads;
+  long long item_tiles = (p.max_len + tile - 1) / tile;
+  long long items = static_cast<long long>(B) * p.heads;
   if (items >= (1ll << 31) || item_tiles * p.heads >= (1ll << 31) ||
       item_tiles * p.heads * B >= (1ll << 31))
     return p;
@@ -364,12 +367,21 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
     p.ctas = static_cast<int>(items * splits);
     return p;
   }
+  // Rows of at most 128 bytes: four neighbouring heads to an item, so that a CTA
+  // reads their rows of a token together.
+  if (row <= 128 && H_kv % 4 == 0 && group <= 8) {
+    p.per_item = 4;
+    p.heads /= 4;
+    items /= 4;
+    tile /= 4;
+    item_tiles = (p.max_len + tile - 1) / tile;
+  }
   // no more CTAs than tiles the tables can hold; a single-tile item is never cut
   p.ctas = static_cast<int>(std::min<long long>(wave, items * item_tiles));
   p.join = item_tiles > 1;
   if (!p.join) return p;
   p.items = static_cast<size_t>(items);
-  p.slots = 2 * static_cast<size_t>(wave) * p.rows;
+  p.slots = 2 * static_cast<size_t>(wave) * p.rows * p.per_item;
   p.bytes = (p.items * sizeof(int) + 15) / 16 * 16 + p.slots * (d + 2) * sizeof(float);
   return p;
 }
@@ -995,6 +1007,7 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
   a.group = H / cache->H_kv;
   a.rows = p.rows;
   a.blocks = p.blocks;
+  a.per_item = p.per_item;
   a.heads = p.heads;
   a.splits = p.splits;
   a.scale_log2 = scale * kLog2e * cache->k_scale;

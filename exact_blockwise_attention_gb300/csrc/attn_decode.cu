@@ -10,7 +10,7 @@
 // Every cached element is read once for its G query heads: 2 G flops per
 // element, far below what the card computes per byte, so the kernel is bound
 // by HBM reads. What it is built around:
-//  - The work is the list of all 64- or 128-key tiles of all (sequence, K/V head)
+//  - The work is the list of all 32 KB tiles of all (sequence, K/V head)
 //    items, cut into equal runs, one per CTA (two CTAs per SM): long and short
 //    sequences balance without the host knowing the lengths, and a call can be
 //    captured and replayed with other lengths. An item cut between CTAs leaves
@@ -51,34 +51,38 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 8.f;                     // scores may pass the reference by a factor 2^8
 constexpr float kF16Shift = 7.f;                  // e4m3 caches: P's largest value is 2^(8 + 7)
 
-template <int D, int NB, bool F8>
+// QUAD: an item is four neighbouring K/V heads, one for each computing warp; else it
+// is one head, and the warps share its keys.
+template <int D, int NB, bool F8, bool QUAD>
 struct Layout {
-  static constexpr int N = 8 * NB;                    // query heads of a CTA
+  static constexpr bool kQuad = QUAD;
+  static constexpr int kHeads = QUAD ? kWarps : 1;    // K/V heads of an item
+  static constexpr int N = 8 * NB;                    // query heads of a K/V head
   static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a cached row
   // A warp's step: 4 KB each of K and V, so that what a step costs besides its
   // bytes is paid once for as many bytes.
   static constexpr int kSub = kRow == 256 ? 1 : 2;
   static constexpr int kRounds = kRow == 64 ? 2 : 1;  // of kSub sets of keys in a step
   static constexpr int kStepKeys = kSubKeys * kSub * kRounds;
-  static constexpr int kTileKeys = kWarps * kStepKeys;
+  static constexpr int kTileKeys = kWarps / kHeads * kStepKeys;
   static constexpr int kBoxes = kTileKeys / kSubKeys; // sets of 16 keys
   static constexpr int kStep = kStepKeys * kRow;      // bytes of a warp's K (or V) step
-  static constexpr int kTile = kWarps * kStep;
+  static constexpr int kTile = kWarps * kStep;        // of a tile
   static constexpr int kStages = 96 * 1024 / (2 * kTile);  // K and V slots of the ring
   static constexpr int kQRow = D + 8;                 // 16-bit elements of a staged query row
-  static constexpr int kPassCols = 64;                // of O, summed over the warps at a time
+  static constexpr int kPassCols = QUAD && D == 128 ? 32 : 64;  // of O, written out at a time
   static constexpr int kPassRow = kPassCols + 4;      // floats; +4: conflict-free column writes
   static constexpr int kOffSum = 2 * kStages * kTile;
   static constexpr int kOffQ = kOffSum + kWarps * 8 * kPassRow * 4;
-  static constexpr int kOffMl = kOffQ + N * kQRow * 2;    // per warp and row: reference, sum
+  static constexpr int kOffMl = kOffQ + kHeads * N * kQRow * 2;    // per warp and row: reference, sum
   static constexpr int kOffQs = kOffMl + kWarps * N * 8;  // per row: score factor
-  static constexpr int kOffKeys = kOffQs + N * 4;         // per stage and 16 keys: those that count
-  static constexpr int kOffBar = kOffKeys + kStages * kBoxes * 2;  // filled K, V, emptied K, V
+  static constexpr int kOffKeys = kOffQs + kHeads * N * 4;  // per stage and 16 keys: those that count
+  static constexpr int kOffBar = (kOffKeys + kStages * kBoxes * 2 + 7) / 8 * 8;  // filled K, V, emptied
   static constexpr int kOffScan = kOffBar + kStages * 32;
   static constexpr int kOffFirst = kOffScan + kWarps * 4;
   static constexpr int kOffAbort = kOffFirst + 20;
   static constexpr int kBytes = kOffAbort + 4;
-  static_assert(kTileKeys == decode_tile_keys(kRow) && kOffBar % 8 == 0, "");
+  static_assert(kTileKeys * kHeads == decode_tile_keys(kRow), "");
 };
 
 // 16 bytes; the hint keeps L2 from fetching more than a row (64-byte rows of
@@ -241,14 +245,16 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned c
   constexpr int kStages = L::kStages, kTileKeys = L::kTileKeys, kBoxes = L::kBoxes;
   constexpr int kPer = WHOLE ? 1 : kTileKeys / 32;  // look-ups of a lane and tile
   constexpr int kLanes = L::kRow / 16;              // of a row: 16 bytes each
-  constexpr int kRows = 32 / kLanes;                // of an instruction
+  constexpr int kRows = 32 / (kLanes * L::kHeads);  // keys of an instruction, for each head
+  static_assert(kRows >= 1, "");
   const int lane = threadIdx.x & 31;
-  const int c = lane % kLanes, r_lane = lane / kLanes;
-  const uint32_t ring = smem_u32(smem) + half * L::kTile;
+  const int c = lane % kLanes, r_lane = lane / (kLanes * L::kHeads);
+  const int head_lane = lane / kLanes % L::kHeads;
+  const uint32_t ring = smem_u32(smem) + half * L::kTile + head_lane * L::kStep;
   const uint32_t bars = smem_u32(smem + L::kOffBar) + half * 8;
   uint16_t* s_keys = reinterpret_cast<uint16_t*>(smem + L::kOffKeys);
   const DeviceStatus st{a.status, a.limit_ns};
-  const unsigned char* at = from + c * 16 + (WHOLE ? r_lane * strides[1] : 0);
+  const unsigned char* at = from + c * 16 + head_lane * strides[2] + (WHOLE ? r_lane * strides[1] : 0);
   Cursor look = ld;
   int look_left = tiles;
   int page_of[kAhead][kPer], slot_of[kAhead][kPer];  // slot -1: no such key
@@ -278,7 +284,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned c
   int stage = 0, lap = 0;
 #pragma unroll 1
   for (int i = 0; i < tiles; ++i) {
-    const long long head = (ld.hh / a.blocks) * strides[2];
+    const long long head = (L::kQuad ? ld.hh * L::kHeads : ld.hh / a.blocks) * strides[2];
     uint32_t keys[kPer];   // that count: WHOLE of this lane's 16, else of 32
     long long off[kPer];   // of the looked-up rows
 #pragma unroll
@@ -333,10 +339,10 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned c
   cp_async_wait_all();  // also after a wait that gave up
 }
 
-template <int D, int NB, bool F8, bool WHOLE>
+template <int D, int NB, bool F8, bool WHOLE, bool QUAD>
 __global__ void __launch_bounds__(kBlock, 2)
     decode_kernel(const __grid_constant__ DecodeArgs a) {
-  using L = Layout<D, NB, F8>;
+  using L = Layout<D, NB, F8, QUAD>;
   constexpr int N = L::N;
   constexpr int kStages = L::kStages;
   constexpr int kPassCols = L::kPassCols, kPassRow = L::kPassRow;
@@ -441,73 +447,75 @@ __global__ void __launch_bounds__(kBlock, 2)
     if (r0 < r1)
       load_tiles<L, WHOLE>(a, keys ? a.k : a.v, keys ? a.k_strides : a.v_strides, keys ? 0 : 1, smem,
                            s_first, r1 - r0, s_abort);
-    if (a.splits > 1 || s_first.nt == 0) {  // the cluster's barriers below
+    if (!QUAD && (a.splits > 1 || s_first.nt == 0)) {  // the cluster's barriers below
       cluster_sync();
       cluster_sync();
     }
     return;
   }
 
-  // ---- the query heads of an item, staged for all warps ----
+  // ---- the query heads of an item: staged for all warps, QUAD: each its own ----
   // Row n: query head g G + blk N + n; rotated where asked, rounded to bf16
   // (the same value the rotation kernel gives); zero behind the group.
+  if (QUAD) {
+    s_q += warp * N * L::kQRow;
+    s_qs += warp * N;
+  }
+  auto sync_staged = [&]() {
+    if (QUAD) __syncwarp(); else sync_compute();
+  };
   auto stage_q = [&](const Cursor& c) {
-    constexpr int kPer = kThreads / N;   // threads of a row
-    constexpr int kPairs = D / 2 / kPer; // pairs (x, x + step) of a thread
-    const int n = tid / kPer, i = tid % kPer;
-    const int g = c.hh / a.blocks, blk = c.hh - g * a.blocks;
-    const int hg = blk * N + n;
-    const bool live = hg < a.group;
+    constexpr int kPer = (QUAD ? 32 : kThreads) / N;  // threads of a row
+    constexpr int kPairs = D / 2 / kPer;              // pairs of elements of a thread
+    const int n = (QUAD ? lane : tid) / kPer, i = (QUAD ? lane : tid) % kPer;
+    const int g = QUAD ? c.hh * L::kHeads + warp : c.hh / a.blocks;
+    const int hg = (QUAD ? 0 : c.hh - g * a.blocks) * N + n;
     const __nv_bfloat16* q = a.q + c.b * a.q_seq + (static_cast<long long>(g) * a.group + hg) * a.q_head;
-    float x[kPairs], y[kPairs];
-    int ox[kPairs], oy[kPairs];
+    const int P = a.rope.n_pairs;
+    auto places = [&](int pair, int& x, int& y) {
+      const bool half = pair < P && !a.rope.interleaved;
+      x = half ? pair : 2 * pair;
+      y = half ? pair + P : 2 * pair + 1;
+    };
+    uint32_t both[kPairs];
     float top = 0.f;
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
       const int pair = i * kPairs + p;
-      const int P = a.rope.n_pairs;
+      int ox, oy;
+      places(pair, ox, oy);
+      float x = hg < a.group ? __bfloat162float(q[ox]) : 0.f;
+      float y = hg < a.group ? __bfloat162float(q[oy]) : 0.f;
       if (pair < P) {
-        ox[p] = a.rope.interleaved ? 2 * pair : pair;
-        oy[p] = a.rope.interleaved ? 2 * pair + 1 : pair + P;
-      } else {
-        ox[p] = 2 * pair;
-        oy[p] = 2 * pair + 1;
-      }
-      x[p] = live ? __bfloat162float(q[ox[p]]) : 0.f;
-      y[p] = live ? __bfloat162float(q[oy[p]]) : 0.f;
-      if (pair < P) {
-        const int axis = a.rope.axis[pair];
-        const int pos = a.pos ? __ldg(a.pos + axis * a.pos_axis + c.b) : c.len - 1;
+        const int pos = a.pos ? __ldg(a.pos + a.rope.axis[pair] * a.pos_axis + c.b) : c.len - 1;
         float cs, sn;
         rope_cs(pos, a.rope.turns[pair], 1.f, cs, sn);
-        rope_turn(x[p], y[p], cs, sn);
-        x[p] = __bfloat162float(__float2bfloat16_rn(x[p]));
-        y[p] = __bfloat162float(__float2bfloat16_rn(y[p]));
+        rope_turn(x, y, cs, sn);
       }
-      const float ax = fabsf(x[p]), ay = fabsf(y[p]);
-      top = fmaxf(top, ax < INFINITY ? ax : 0.f);
-      top = fmaxf(top, ay < INFINITY ? ay : 0.f);
+      both[p] = pack_bf16(x, y);
+      x = fabsf(bf16lo_f32(both[p])), y = fabsf(bf16hi_f32(both[p]));
+      top = fmaxf(top, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
     }
+    float up = 1.f, down = 1.f;
     if constexpr (F8) {
 #pragma unroll
       for (int m = kPer / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      // 2^e puts the head's largest element into [2^13, 2^14); e within the
+      // up = 2^e puts the head's largest element into [2^13, 2^14); e within the
       // range where 2^e and 2^-e are normal floats
       const int e = top > 0.f ? min(max(13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -100), 100) : 0;
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      if (i == 0) s_qs[n] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
+    if (i == 0) s_qs[n] = a.scale_log2 * down;
 #pragma unroll
-      for (int p = 0; p < kPairs; ++p) {
-        s_q[n * L::kQRow + q_place(ox[p])] = __half_as_ushort(__float2half_rn(x[p] * up));
-        s_q[n * L::kQRow + q_place(oy[p])] = __half_as_ushort(__float2half_rn(y[p] * up));
-      }
-    } else {
-      if (i == 0) s_qs[n] = a.scale_log2;
-#pragma unroll
-      for (int p = 0; p < kPairs; ++p) {
-        s_q[n * L::kQRow + ox[p]] = __bfloat16_as_ushort(__float2bfloat16_rn(x[p]));
-        s_q[n * L::kQRow + oy[p]] = __bfloat16_as_ushort(__float2bfloat16_rn(y[p]));
-      }
+    for (int p = 0; p < kPairs; ++p) {
+      int ox, oy;
+      places(i * kPairs + p, ox, oy);
+      const float x = bf16lo_f32(both[p]) * up, y = bf16hi_f32(both[p]) * up;
+      s_q[n * L::kQRow + (F8 ? q_place(ox) : ox)] =
+          F8 ? __half_as_ushort(__float2half_rn(x)) : static_cast<uint16_t>(both[p]);
+      s_q[n * L::kQRow + (F8 ? q_place(oy) : oy)] =
+          F8 ? __half_as_ushort(__float2half_rn(y)) : static_cast<uint16_t>(both[p] >> 16);
     }
   };
 
@@ -544,7 +552,7 @@ __global__ void __launch_bounds__(kBlock, 2)
   bool first_item = true;
   if (r0 < r1) {
     stage_q(cur);
-    sync_compute();
+    sync_staged();
     begin_item();
   }
 
@@ -567,7 +575,8 @@ __global__ void __launch_bounds__(kBlock, 2)
     uint32_t mask;  // the keys that count
     {
       const unsigned char* at =
-          smem + L::kOffKeys + (stage * L::kBoxes + (warp * L::kRounds + round) * kSub) * 2;
+          smem + L::kOffKeys +
+          (stage * L::kBoxes + ((QUAD ? 0 : warp * L::kRounds) + round) * kSub) * 2;
       mask = kSub == 1 ? *reinterpret_cast<const uint16_t*>(at) : *reinterpret_cast<const uint32_t*>(at);
     }
     // S^T = K Q^T: two chains, of the two halves of d or of two sets of keys
@@ -743,7 +752,7 @@ __global__ void __launch_bounds__(kBlock, 2)
 
     const bool item_done = cur.t + 1 == cur.nt;
     if (item_done || tile + 1 == r1) {
-      // ---- join the four warps ----
+      // ---- the item's end, or the run's: join the four warps, or write each's head ----
       const bool whole = t_begin == 0 && item_done;
       const Cursor done = cur;
 #pragma unroll
@@ -758,17 +767,62 @@ __global__ void __launch_bounds__(kBlock, 2)
           if (F8) ref -= kF16Shift;
           if (top[nb][x] == -INFINITY && l == 0.f) ref = -INFINITY;
           top[nb][x] = ref;
-          if (u8 == 0) s_ml[warp * N + nb * 8 + 2 * j4 + x] = make_float2(ref, l);
+          sum[nb][x] = l;
+          if (!QUAD && u8 == 0) s_ml[warp * N + nb * 8 + 2 * j4 + x] = make_float2(ref, l);
         }
-      sync_compute();
+      if (!QUAD) sync_compute();
       const bool more = tile + 1 < r1;
       if (more) {
         advance<kTileKeys>(cur, a);
         stage_q(cur);  // every warp holds the old query in registers
       }
-      const int g = done.hh / a.blocks, blk = done.hh - g * a.blocks;
       const long long item = static_cast<long long>(done.b) * a.heads + done.hh;
       const int part = 2 * cta + (first_item ? 0 : 1);
+      // O's columns [c0, c0 + kPassCols) of the warp's rows into its own part of s_sum
+      auto put = [&](int nb, int c0, const float (&f)[2]) {
+        float* to = s_sum + warp * 8 * kPassRow;
+#pragma unroll
+        for (int k = 0; k < kPassCols / 16; ++k)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int col = F8 ? k * 16 + 2 * u8 + (x >> 1) : k * 16 + u8 + 8 * (x >> 1);
+            to[(2 * j4 + (x & 1)) * kPassRow + col] = o[nb][c0 / 16 + k][x] * f[x & 1];
+          }
+      };
+      if constexpr (QUAD) {
+        const int g = done.hh * L::kHeads + warp;
+        const long long head0 = static_cast<long long>(done.b) * a.H + g * a.group;
+        const long long part0 = (static_cast<long long>(part) * L::kHeads + warp) * N;
+        float f[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int row = 2 * j4 + x;
+          const float M = top[0][x], l = sum[0][x];
+          f[x] = !whole ? 1.f : M == -INFINITY ? 0.f : a.o_scale / l;
+          if (u8 == 0 && !whole) a.part_ml[part0 + row] = make_float2(M, l);
+          if (u8 == 0 && whole && row < a.group)
+            a.lse[head0 + row] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+        }
+        constexpr int kCols = kPassCols / 4;  // of a lane
+        const int row = lane >> 2, c4 = (lane & 3) * kCols;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += kPassCols) {
+          put(0, c0, f);
+          __syncwarp();
+          const float* y = s_sum + (warp * 8 + row) * kPassRow + c4;
+#pragma unroll
+          for (int x = 0; x < kCols; x += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(y + x);
+            if (!whole)
+              *reinterpret_cast<float4*>(a.part_o + (part0 + row) * D + c0 + c4 + x) = v;
+            else if (row < a.group)
+              *reinterpret_cast<uint2*>(a.o + (head0 + row) * D + c0 + c4 + x) =
+                  make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+          }
+          __syncwarp();
+        }
+      } else {
+      const int g = done.hh / a.blocks, blk = done.hh - g * a.blocks;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float f[2];
@@ -793,14 +847,7 @@ __global__ void __launch_bounds__(kBlock, 2)
         const long long head = static_cast<long long>(done.b) * a.H + g * a.group + hg;
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += kPassCols) {
-          float* to = s_sum + warp * 8 * kPassRow;
-#pragma unroll
-          for (int k = 0; k < kPassCols / 16; ++k)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int col = F8 ? k * 16 + 2 * u8 + (x >> 1) : k * 16 + u8 + 8 * (x >> 1);
-              to[(2 * j4 + (x & 1)) * kPassRow + col] = o[nb][c0 / 16 + k][x] * f[x & 1];
-            }
+          put(nb, c0, f);
           sync_compute();
           float v[kCols] = {};
 #pragma unroll
@@ -837,6 +884,7 @@ __global__ void __launch_bounds__(kBlock, 2)
             a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
         }
       }
+      }
       // What the join kernel needs, left by the CTA with the item's first tile:
       // the item's parts lie in this CTA's slot and the first ones of the next.
       if (a.item && tid == 0 && t_begin == 0) {
@@ -851,12 +899,15 @@ __global__ void __launch_bounds__(kBlock, 2)
       }
       first_item = false;
       t_begin = 0;
-      if (more) begin_item();
+      if (more) {
+        if (QUAD) __syncwarp();  // (else the sums' barriers lie between)
+        begin_item();
+      }
     } else {
       ++cur.t;
     }
   }
-  if (a.splits > 1 || s_first.nt == 0) {
+  if (!QUAD && (a.splits > 1 || s_first.nt == 0)) {
     // ---- join the cluster's parts, or write an item without keys ----
     const int g = s_first.hh / a.blocks, blk = s_first.hh - g * a.blocks;
     const int rank = cta % a.splits;
@@ -889,7 +940,7 @@ __global__ void __launch_bounds__(kBlock, 2)
 }
 
 // Items cut between CTAs: one CTA per (sequence, query head) adds the parts up.
-template <int D, int N>
+template <int D>
 __global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
   pdl_launch_dependents();
   pdl_wait();
@@ -898,8 +949,12 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_cons
   __shared__ float2 s_ml[kWarps];
   const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
   const int g = h / a.group, hg = h - g * a.group;
-  const int blk = hg / N, n = hg - blk * N;
-  const int info = __ldg(a.item + static_cast<long long>(b) * a.heads + g * a.blocks + blk);
+  // its item, and its row of the item's N
+  const int N = a.rows * a.per_item;
+  const int blk = hg / a.rows;  // 0 where an item holds several heads
+  const int hh = a.per_item > 1 ? g / a.per_item : g * a.blocks + blk;
+  const int n = g % a.per_item * a.rows + hg - blk * a.rows;
+  const int info = __ldg(a.item + static_cast<long long>(b) * a.heads + hh);
   if (info == 0) return;
   const int parts = info >> 16, at = info & 0xffff;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -955,12 +1010,12 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_cons
   if (threadIdx.x == 0) a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
 }
 
-template <int D, int NB, bool F8>
+template <int D, int NB, bool F8, bool QUAD>
 cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, bool join, cudaStream_t stream) {
-  using L = Layout<D, NB, F8>;
+  using L = Layout<D, NB, F8, QUAD>;
   static_assert(L::kBytes <= 113 * 1024, "two CTAs share an SM's shared memory");
-  auto kern = a.cache.page_size % kSubKeys == 0 ? decode_kernel<D, NB, F8, true>
-                                                 : decode_kernel<D, NB, F8, false>;
+  auto kern = a.cache.page_size % kSubKeys == 0 ? decode_kernel<D, NB, F8, true, QUAD>
+                                                : decode_kernel<D, NB, F8, false, QUAD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -977,26 +1032,29 @@ cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, bool join, cudaStream
   cfg.numAttrs = a.splits > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess || !join) return e;
-  return launch_pdl(decode_join_kernel<D, L::N>, dim3(static_cast<unsigned>(a.B) * a.H),
+  return launch_pdl(decode_join_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.H),
                     dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_decode(const DecodeArgs& a, int ctas, bool join, cudaStream_t stream) {
-  const bool f8 = a.cache.type == ATTN_CACHE_E4M3, two = a.rows == 16;
+  const bool f8 = a.cache.type == ATTN_CACHE_E4M3, two = a.rows == 16, quad = a.per_item > 1;
   if (a.cache.d == 64) {
     if (f8)
-      return two ? launch_decode_t<64, 2, true>(a, ctas, join, stream)
-                 : launch_decode_t<64, 1, true>(a, ctas, join, stream);
-    return two ? launch_decode_t<64, 2, false>(a, ctas, join, stream)
-               : launch_decode_t<64, 1, false>(a, ctas, join, stream);
+      return quad  ? launch_decode_t<64, 1, true, true>(a, ctas, join, stream)
+             : two ? launch_decode_t<64, 2, true, false>(a, ctas, join, stream)
+                   : launch_decode_t<64, 1, true, false>(a, ctas, join, stream);
+    return quad  ? launch_decode_t<64, 1, false, true>(a, ctas, join, stream)
+           : two ? launch_decode_t<64, 2, false, false>(a, ctas, join, stream)
+                 : launch_decode_t<64, 1, false, false>(a, ctas, join, stream);
   }
   if (f8)
-    return two ? launch_decode_t<128, 2, true>(a, ctas, join, stream)
-               : launch_decode_t<128, 1, true>(a, ctas, join, stream);
-  return two ? launch_decode_t<128, 2, false>(a, ctas, join, stream)
-             : launch_decode_t<128, 1, false>(a, ctas, join, stream);
+    return quad  ? launch_decode_t<128, 1, true, true>(a, ctas, join, stream)
+           : two ? launch_decode_t<128, 2, true, false>(a, ctas, join, stream)
+                 : launch_decode_t<128, 1, true, false>(a, ctas, join, stream);
+  return two ? launch_decode_t<128, 2, false, false>(a, ctas, join, stream)
+             : launch_decode_t<128, 1, false, false>(a, ctas, join, stream);
 }
 
 }  // namespace eba

@@ -264,7 +264,7 @@ cudaError_t launch_append(AppendArgs& a, cudaStream_t stream);
 // One new token per sequence over the paged cache. The grid is fixed (two CTAs
 // on each of 152 SMs); any number of SMs gives the same results.
 constexpr int kDecodeCtas = 304;
-// Keys of a work item's tile: 32 KB of keys and values.
+// Keys of a tile, 32 KB of keys and values (of each head, a quarter with four).
 constexpr int decode_tile_keys(int row_bytes) { return 16384 / row_bytes; }
 struct DecodeArgs {
   const __nv_bfloat16* q;  // [B, H, d], strides below
@@ -281,7 +281,8 @@ struct DecodeArgs {
   int group;   // query heads per K/V head
   int rows;    // query heads a CTA holds: 8 or 16
   int blocks;  // ceil(group / rows)
-  int heads;   // H_kv * blocks: items of a sequence
+  int per_item;  // K/V heads of an item: 1, or 4 neighbouring ones
+  int heads;   // H_kv * blocks / per_item: items of a sequence
   int splits;  // > 0: clusters of that many CTAs, one per item; 0: one list of tiles
   float scale_log2;  // scale * log2(e) * the keys' scale
   float o_scale;     // the values' scale
@@ -289,8 +290,8 @@ struct DecodeArgs {
   float* lse;        // [B, H]
   int* item;         // [B, heads]: parts of a cut item << 16 | its first slot; 0: not cut.
                      // Null where no item can be cut
-  float* part_o;     // [2 kDecodeCtas, rows, d]
-  float2* part_ml;   // [2 kDecodeCtas, rows]: reference, sum
+  float* part_o;     // [2 kDecodeCtas, per_item rows, d]
+  float2* part_ml;   // [2 kDecodeCtas, per_item rows]: reference, sum
   const int* pos;
   long long pos_axis;
   int* status;

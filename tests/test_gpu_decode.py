@@ -76,6 +76,13 @@ CASES = [
     ([5000, 4999, 12], 2, 1, 64, 33, False, False),
     ([20000], 2, 2, 128, 128, False, False),               # one sequence over all CTAs
     ([30001], 8, 1, 64, 64, True, False),
+    # short rows, heads in fours
+    ([5000, 4999, 0, 12], 4, 4, 64, 48, False, False),
+    ([9000, 3], 32, 4, 64, 33, True, True),
+    ([7000, 1, 65], 24, 8, 128, 16, True, False),
+    ([6000, 0, 100, 1], 40, 8, 64, 16, True, False),
+    ([4100, 31], 32, 16, 64, 20, False, True),
+    ([3000, 2999], 64, 8, 128, 40, True, True),
 ]
 
 
@@ -86,12 +93,13 @@ def test_decode_matches_oracle(eba, lens, H, hk, d, page, e4m3, heads_first):
     check(eba, p, bf16(torch.Generator().manual_seed(1), len(lens), H, d))
 
 
-@pytest.mark.parametrize("d,e4m3", [(64, False), (128, True)])
-def test_many_sequences_of_mixed_lengths(eba, d, e4m3):
+@pytest.mark.parametrize("H,hk,d,e4m3,page", [(6, 2, 64, False, 16), (6, 2, 128, True, 16), (4, 4, 64, True, 16),
+                                              (8, 4, 128, True, 24), (12, 4, 64, False, 32), (3, 1, 128, False, 5)])
+def test_many_sequences_of_mixed_lengths(eba, H, hk, d, e4m3, page):
     r = np.random.default_rng(d)
     lens = [int(x) for x in r.integers(0, 200, size=333)]
-    p = Paged(lens, 16, 2, d, e4m3=e4m3, seed=3)
-    check(eba, p, bf16(torch.Generator().manual_seed(2), len(lens), 6, d))
+    p = Paged(lens, page, hk, d, e4m3=e4m3, seed=3)
+    check(eba, p, bf16(torch.Generator().manual_seed(2), len(lens), H, d))
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
@@ -217,17 +225,19 @@ def test_cache_past_four_gigabytes(eba):
     assert torch.isfinite(o.float()).all()
 
 
-@pytest.mark.parametrize("d,e4m3,page", [(64, False, 16), (128, True, 16), (64, True, 20), (128, False, 32)])
-def test_values_of_one_sequence_never_reach_another(eba, d, e4m3, page):
+@pytest.mark.parametrize("hk", [1, 4])
+@pytest.mark.parametrize("d,e4m3,page", [(64, False, 16), (128, True, 16), (64, True, 20), (128, False, 32),
+                                         (64, True, 16)])
+def test_values_of_one_sequence_never_reach_another(eba, d, e4m3, page, hk):
     # every other sequence holds NaN values; those between end inside a tile that
     # the same block loaded NaN into before, or have a page that is none in it
     lens = [200, 3, 130, 17] * 150
     g = torch.Generator().manual_seed(21)
-    nan = lambda n: (bf16(g, n, 1, d), torch.full((n, 1, d), math.nan, dtype=torch.bfloat16))
-    p = Paged(lens, page, 1, d, e4m3=e4m3, seed=21,
-              data=[nan(n) if n > 100 else (bf16(g, n, 1, d), bf16(g, n, 1, d)) for n in lens])
+    nan = lambda n: (bf16(g, n, hk, d), torch.full((n, hk, d), math.nan, dtype=torch.bfloat16))
+    p = Paged(lens, page, hk, d, e4m3=e4m3, seed=21,
+              data=[nan(n) if n > 100 else (bf16(g, n, hk, d), bf16(g, n, hk, d)) for n in lens])
     cache = p.on_gpu(eba)
-    q = bf16(g, len(lens), 2, d).cuda()
+    q = bf16(g, len(lens), 2 * hk, d).cuda()
     o, _ = eba.decode(cache, q, p.gtable, p.glens)
     finite = torch.isfinite(o).all(2).all(1).cpu()
     assert finite.tolist() == [n < 100 for n in lens]
@@ -288,11 +298,12 @@ def test_two_streams_at_once(eba):
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("axes,pairing,d", [((64,), "half", 128), ((10, 11, 11), "interleaved", 64),
                                             ((8, 16), "half", 128)])
-def test_query_rotated_on_the_way(eba, axes, pairing, d, e4m3):
+@pytest.mark.parametrize("H,hk,longest", [(18, 2, 300), (8, 4, 3000)])
+def test_query_rotated_on_the_way(eba, H, hk, longest, axes, pairing, d, e4m3):
     # bit for bit the rotation kernel's query
-    p = Paged([300, 0, 45], 16, 2, d, e4m3=e4m3, seed=19)
+    p = Paged([longest, 0, 45], 16, hk, d, e4m3=e4m3, seed=19)
     cache = p.on_gpu(eba)
-    q = bf16(torch.Generator().manual_seed(10), 3, 18, d).cuda()
+    q = bf16(torch.Generator().manual_seed(10), 3, H, d).cuda()
     plan = eba.Rope(axes, pairing=pairing)
     pos = torch.randint(-1000, 10 ** 6, (len(axes), 3), device="cuda", dtype=torch.int32)
     turned, _ = eba.rope_fwd(q, None, pos, plan)
