@@ -216,7 +216,8 @@ __device__ __forceinline__ Place find_place(const AppendArgs& a, long long t) {
   const int len = __ldg(a.lens + s);
   if (len == 0) return p;  // an empty slot of the batch
   const long long at = len - back;
-  if (at < 0 || at >= static_cast<long long>(a.max_pages) * a.cache.page_size) {
+  // (at >= len: offsets that decrease)
+  if (at < 0 || at >= len || at >= static_cast<long long>(a.max_pages) * a.cache.page_size) {
     atomicCAS(a.status, 0, ATTN_ERR_PAGE);
     return p;
   }

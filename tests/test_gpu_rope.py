@@ -312,6 +312,20 @@ def test_append_reports_bad_places(eba):
     assert torch.equal(after, before)
 
 
+def test_append_with_offsets_that_decrease_writes_in_no_other_place(eba):
+    p = Paged([20, 20, 20], 16, 1, 64)
+    cache = p.on_gpu(eba)
+    held = torch.zeros((p.n_pages, 16), dtype=torch.bool)
+    for r in p.rows:  # the places of tokens
+        held[r[0]], held[r[1], :4] = True, True
+    before = p.gk.view(torch.uint8).clone()
+    k = bf16(torch.Generator().manual_seed(1), 6, 1, 64).cuda()
+    for cu in ([0, 5, 1, 6], [0, 2, -3, 6], [3, 0, 0, 6], [0, 2 ** 31 - 1, -2 ** 31, 6]):
+        eba.cache_append(cache, k, k, p.gtable, p.glens, torch.tensor(cu, device="cuda", dtype=torch.int32))
+    eba.poll_device_status()
+    assert torch.equal(p.gk.view(torch.uint8).cpu()[~held], before.cpu()[~held])
+
+
 def test_append_from_one_projection_and_captured(eba):
     p = Paged([64, 70], 16, 2, 64, seed=4)
     q = Paged([64, 70], 16, 2, 64, seed=4)
