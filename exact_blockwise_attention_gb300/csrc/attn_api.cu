@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "attn.h"
+#include "cache_kernels.h"
 #include "kernels.h"
 
 namespace {

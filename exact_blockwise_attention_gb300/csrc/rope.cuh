@@ -14,6 +14,7 @@
 // multiply-adds it takes.
 #pragma once
 
+#include "cache_kernels.h"
 #include "common.cuh"
 #include "kernels.h"
 
