@@ -336,8 +336,7 @@ struct DecodePlan {
   int heads, max_len;    // items of a sequence; keys of a table row
   int splits, ctas;      // see DecodeArgs; the grid
   bool join;             // items may be cut between CTAs
-  size_t items, slots;   // of the workspace
-  size_t bytes;
+  size_t slots, bytes;   // of the workspace: parts, all
 };
 DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int type) {
   DecodePlan p{};
@@ -357,20 +356,28 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
       item_tiles * p.heads * B >= (1ll << 31))
     return p;
   p.ok = true;
-  // Clusters, where one wave of them leaves each CTA at most 4 tiles: that costs
-  // one launch instead of two and needs no workspace. With more tiles a CTA,
-  // spreading them over all SMs is worth the second launch.
+  // Clusters, where one wave of them leaves each CTA few tiles: one launch instead of
+  // two and no workspace, but only as even as the lengths, and with less than a full
+  // wave not all SMs. Measured, cluster against list (us; longest sequence, others
+  // random down to an eighth): 64 CTAs at 2 tiles each 6.8 / 7.0, at 4 8.2 / 7.9
+  // (1 x 8 heads of 128, bf16); 256 CTAs at 8 tiles 12.8 / 14.1 (16 x 8 heads) and
+  // 15.9 / 16.4 (e4m3), at 16 20.1 / 20.2 and 23.5 / 20.4.
   constexpr int wave = eba::kDecodeCtas;
   int splits = 1;
   while (splits < 8 && splits < item_tiles && items * splits * 2 <= wave) splits *= 2;
-  if (items * splits <= wave && item_tiles <= 4 * splits) {
+  const int most = items * splits >= wave * 3 / 4 ? 8 : 2;  // tiles of a CTA
+  if (items * splits <= wave && item_tiles <= most * splits) {
     p.splits = splits;
     p.ctas = static_cast<int>(items * splits);
     return p;
   }
-  // Rows of at most 128 bytes: four neighbouring heads to an item, so that a CTA
-  // reads their rows of a token together.
-  if (row <= 128 && H_kv % 4 == 0 && group <= 8) {
+  // Rows of at most 128 bytes, and at least 8 of them side by side: four neighbouring
+  // heads to an item, so that a CTA reads their rows of a token together; unless that
+  // leaves so few items that each is cut into many parts. Measured, fours against
+  // single heads (us): 16 sequences x 16 heads of 64, bf16, up to 32000 keys 225 /
+  // 255; 32 x 8 heads of 64, e4m3, 16000 keys 57 / 60; 1 x 16 heads of 64 29 / 27;
+  // 4 heads of 128, e4m3, 55 / 52.
+  if (row <= 128 && H_kv % 4 == 0 && H_kv >= 8 && group <= 8 && items / 4 >= 16) {
     p.per_item = 4;
     p.heads /= 4;
     items /= 4;
@@ -381,9 +388,8 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
   p.ctas = static_cast<int>(std::min<long long>(wave, items * item_tiles));
   p.join = item_tiles > 1;
   if (!p.join) return p;
-  p.items = static_cast<size_t>(items);
   p.slots = 2 * static_cast<size_t>(wave) * p.rows * p.per_item;
-  p.bytes = (p.items * sizeof(int) + 15) / 16 * 16 + p.slots * (d + 2) * sizeof(float);
+  p.bytes = wave * sizeof(int2) + p.slots * (d + 2) * sizeof(float);
   return p;
 }
 
@@ -1016,9 +1022,8 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   if (p.bytes > 0) {
-    a.item = static_cast<int*>(workspace);
-    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        (p.items * sizeof(int) + 15) / 16 * 16);
+    a.cut = static_cast<int2*>(workspace);
+    a.part_o = reinterpret_cast<float*>(a.cut + eba::kDecodeCtas);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + p.slots * cache->d);
   }
   a.pos = pos;

@@ -339,6 +339,13 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned c
   cp_async_wait_all();  // also after a wait that gave up
 }
 
+// The run that tile t is in: the last one that does not begin behind it.
+__device__ __forceinline__ int run_of(int t, int tiles, int ctas) {
+  int i = static_cast<int>(static_cast<long long>(t) * ctas / tiles);
+  while (i + 1 < ctas && first_tile(i + 1, tiles, ctas) <= t) ++i;
+  return i;
+}
+
 template <int D, int NB, bool F8, bool WHOLE, bool QUAD>
 __global__ void __launch_bounds__(kBlock, 2)
     decode_kernel(const __grid_constant__ DecodeArgs a) {
@@ -427,12 +434,13 @@ __global__ void __launch_bounds__(kBlock, 2)
         *reinterpret_cast<uint4*>(a.o + static_cast<long long>(b) * a.H * D + x * 8) =
             make_uint4(0, 0, 0, 0);
       for (int h = tid; h < a.H; h += kBlock) a.lse[static_cast<long long>(b) * a.H + h] = -INFINITY;
-      if (a.item)
-        for (int x = tid; x < a.heads; x += kBlock) a.item[static_cast<long long>(b) * a.heads + x] = 0;
     }
   }
   __syncthreads();
-  if (!a.splits && r0 >= r1) return;
+  if (!a.splits && r0 >= r1) {
+    if (a.cut && tid == 0) a.cut[cta] = make_int2(0, 0);
+    return;
+  }
 
   float* s_sum = reinterpret_cast<float*>(smem + L::kOffSum);
   uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + L::kOffQ);
@@ -776,7 +784,6 @@ __global__ void __launch_bounds__(kBlock, 2)
         advance<kTileKeys>(cur, a);
         stage_q(cur);  // every warp holds the old query in registers
       }
-      const long long item = static_cast<long long>(done.b) * a.heads + done.hh;
       const int part = 2 * cta + (first_item ? 0 : 1);
       // O's columns [c0, c0 + kPassCols) of the warp's rows into its own part of s_sum
       auto put = [&](int nb, int c0, const float (&f)[2]) {
@@ -885,17 +892,17 @@ __global__ void __launch_bounds__(kBlock, 2)
         }
       }
       }
-      // What the join kernel needs, left by the CTA with the item's first tile:
-      // the item's parts lie in this CTA's slot and the first ones of the next.
-      if (a.item && tid == 0 && t_begin == 0) {
-        int parts = 0;
-        if (!item_done) {
-          const int last = tile - done.t + done.nt - 1;  // the item's last tile
-          int c1 = static_cast<int>((static_cast<long long>(last) * G) / tiles);
-          while (first_tile(c1 + 1, tiles, G) <= last) ++c1;
-          parts = c1 - cta + 1;
+      // What the join kernel needs: the item that this CTA's run ends in the middle of,
+      // if the item has its first tile here or covers the whole run.
+      if (a.cut && tid == 0 && tile + 1 == r1) {
+        int2 cut = make_int2(0, 0);
+        if (!item_done && (t_begin == 0 || first_item)) {
+          const int t0 = tile - done.t, t1 = t0 + done.nt;  // the item's tiles
+          const int c0 = run_of(t0, tiles, G), parts = run_of(t1 - 1, tiles, G) - c0 + 1;
+          const int slot = first_tile(c0, tiles, G) == t0 ? 0 : 1;  // of its first part in c0
+          cut = make_int2(done.b * a.heads + done.hh, (parts << 16) | ((cta - c0) << 1) | slot);
         }
-        a.item[item] = parts ? (parts << 16) | part : 0;
+        a.cut[cta] = cut;
       }
       first_item = false;
       t_begin = 0;
@@ -939,72 +946,102 @@ __global__ void __launch_bounds__(kBlock, 2)
   }
 }
 
-// Items cut between CTAs: one CTA per (sequence, query head) adds the parts up.
+// Items cut between CTAs: their parts are added up in the order of the keys. What
+// that costs is the latency of three loads in a row (the cut, the parts, the output)
+// and the CTAs that find nothing to do, so there is one CTA for each run (and 8 rows
+// of an item): few parts, and the one whose run the item begins in takes a row a
+// warp; many, and the first 8 whose runs the item covers take a row each, with all
+// their warps. A warp has the loads of 8 parts under way.
+constexpr int kJoinWarps = 8, kDeep = 8, kFewParts = 16;
 template <int D>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    decode_join_kernel(const __grid_constant__ DecodeArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kVec = D / 32;  // columns of a lane
-  __shared__ float s_o[kWarps][D];
-  __shared__ float2 s_ml[kWarps];
-  const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
-  const int g = h / a.group, hg = h - g * a.group;
-  // its item, and its row of the item's N
-  const int N = a.rows * a.per_item;
-  const int blk = hg / a.rows;  // 0 where an item holds several heads
-  const int hh = a.per_item > 1 ? g / a.per_item : g * a.blocks + blk;
-  const int n = g % a.per_item * a.rows + hg - blk * a.rows;
-  const int info = __ldg(a.item + static_cast<long long>(b) * a.heads + hh);
-  if (info == 0) return;
-  const int parts = info >> 16, at = info & 0xffff;
+  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps];
+  const int2 cut = a.cut[blockIdx.x];
+  const int parts = cut.y >> 16, rank = (cut.y >> 1) & 0x7fff;
+  const bool few = parts <= kFewParts;
+  if (parts == 0 || rank >= (few ? 1 : kJoinWarps)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // part 0 in slot `at`, part p in the first slot of the p-th CTA after it
-  auto slot_of = [&](int p) { return p == 0 ? at : (at / 2 + p) * 2; };
+  const int n = blockIdx.y * kJoinWarps + (few ? warp : rank);  // row of the item
+  const int b = cut.x / a.heads, hh = cut.x - b * a.heads;
+  // its query head: of one of the item's K/V heads, or of a block of one head's group
+  const int g = a.per_item > 1 ? hh * a.per_item + n / a.rows : hh / a.blocks;
+  const int hg = a.per_item > 1 ? n % a.rows : hh % a.blocks * a.rows + n;
+  if (hg >= a.group) return;  // (few: a warp of its own; else all warps alike)
+  const int c0 = blockIdx.x - rank, N = a.rows * a.per_item;
   float M = -INFINITY, l = 0.f;
-  float o[kVec];
-#pragma unroll
-  for (int x = 0; x < kVec; ++x) o[x] = 0.f;
-  constexpr int kDeep = 4;
-  for (int p0 = warp; p0 < parts; p0 += kWarps * kDeep) {
+  float o[kVec] = {};
+  const int step = few ? 1 : kJoinWarps;
+  for (int p0 = few ? 0 : warp; p0 < parts; p0 += step * kDeep) {
     float2 ml[kDeep];
     float v[kDeep][kVec];
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
-      const int p = p0 + u * kWarps;
-      const long long row = static_cast<long long>(slot_of(min(p, parts - 1))) * N + n;
-      ml[u] = p < parts ? a.part_ml[row] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int x = 0; x < kVec; ++x) v[u][x] = a.part_o[row * D + x * 32 + lane];
+      const int p = p0 + u * step;
+      if (p >= parts) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+        continue;
+      }
+      // part p in the first slot of the p-th CTA after c0, part 0 as recorded
+      const long long row = static_cast<long long>(2 * (c0 + p) + (p == 0 ? cut.y & 1 : 0)) * N + n;
+      ml[u] = a.part_ml[row];
+      const float* from = a.part_o + row * D + lane * kVec;
+      if constexpr (kVec == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(from);
+        v[u][0] = y.x, v[u][1] = y.y, v[u][2] = y.z, v[u][3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(from);
+        v[u][0] = y.x, v[u][1] = y.y;
+      }
     }
+    float to = M;
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) to = fmaxf(to, ml[u].x);
+    if (to == -INFINITY) continue;  // no weight so far
+    const float f = M == -INFINITY ? 0.f : ex2_approx(M - to);
+    M = to;
+    l *= f;
+#pragma unroll
+    for (int x = 0; x < kVec; ++x) o[x] *= f;
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
       if (ml[u].x == -INFINITY) continue;
-      const float to = fmaxf(M, ml[u].x);
-      const float fo = M == -INFINITY ? 0.f : ex2_approx(M - to);
-      const float fn = ex2_approx(ml[u].x - to);
-      l = l * fo + ml[u].y * fn;
+      const float w = ex2_approx(ml[u].x - to);
+      l += ml[u].y * w;
 #pragma unroll
-      for (int x = 0; x < kVec; ++x) o[x] = o[x] * fo + v[u][x] * fn;
-      M = to;
+      for (int x = 0; x < kVec; ++x) o[x] += v[u][x] * w;
     }
+  }
+  const long long head = static_cast<long long>(b) * a.H + static_cast<long long>(g) * a.group + hg;
+  if (few) {
+    const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+#pragma unroll
+    for (int x = 0; x < kVec; x += 2)
+      *reinterpret_cast<uint32_t*>(a.o + head * D + lane * kVec + x) = pack_bf16(o[x] * f, o[x + 1] * f);
+    if (lane == 0) a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+    return;
   }
   if (lane == 0) s_ml[warp] = make_float2(M, l);
 #pragma unroll
-  for (int x = 0; x < kVec; ++x) s_o[warp][x * 32 + lane] = o[x];
+  for (int x = 0; x < kVec; ++x) s_o[warp][lane * kVec + x] = o[x];
   __syncthreads();
   if (threadIdx.x >= D) return;
   M = -INFINITY;
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w].x);
+  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_ml[w].x);
   float v = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = s_ml[w].x == -INFINITY ? 0.f : ex2_approx(s_ml[w].x - M);
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (s_ml[w].x == -INFINITY) continue;
+    const float f = ex2_approx(s_ml[w].x - M);
     l += s_ml[w].y * f;
     v += s_o[w][threadIdx.x] * f;
   }
-  const long long head = static_cast<long long>(b) * a.H + h;
   const float f = M == -INFINITY ? 0.f : a.o_scale / l;
   a.o[head * D + threadIdx.x] = __float2bfloat16_rn(v * f);
   if (threadIdx.x == 0) a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
@@ -1032,8 +1069,8 @@ cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, bool join, cudaStream
   cfg.numAttrs = a.splits > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess || !join) return e;
-  return launch_pdl(decode_join_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.H),
-                    dim3(kThreads), 0, stream, a);
+  return launch_pdl(decode_join_kernel<D>, dim3(ctas, a.rows * a.per_item / kJoinWarps),
+                    dim3(32 * kJoinWarps), 0, stream, a);
 }
 
 }  // namespace

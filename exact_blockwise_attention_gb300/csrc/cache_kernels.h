@@ -76,8 +76,11 @@ struct DecodeArgs {
   float o_scale;     // the values' scale
   __nv_bfloat16* o;  // [B, H, d]
   float* lse;        // [B, H]
-  int* item;         // [B, heads]: parts of a cut item << 16 | its first slot; 0: not cut.
-                     // Null where no item can be cut
+  // Null where no item can be cut between CTAs. Else [kDecodeCtas]: the item that the
+  // CTA's run ends in the middle of, and its parts << 16 | runs since its first one << 1
+  // | the slot of its first part in that run; parts 0: none that begins in or covers the
+  // run.
+  int2* cut;
   float* part_o;     // [2 kDecodeCtas, per_item rows, d]
   float2* part_ml;   // [2 kDecodeCtas, per_item rows]: reference, sum
   const int* pos;

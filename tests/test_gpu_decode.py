@@ -77,12 +77,15 @@ CASES = [
     ([20000], 2, 2, 128, 128, False, False),               # one sequence over all CTAs
     ([30001], 8, 1, 64, 64, True, False),
     # short rows, heads in fours
-    ([5000, 4999, 0, 12], 4, 4, 64, 48, False, False),
+    ([5000, 4999, 0, 12], 16, 16, 64, 48, False, False),
+    ([3000, 3, 0, 0, 64, 65, 31, 32], 64, 8, 64, 33, True, True),
+    ([2500, 1, 65, 0, 100, 700, 32, 33], 24, 8, 128, 16, True, False),
+    ([2000, 0, 100, 1], 80, 16, 64, 16, True, False),
+    ([4100, 31] + [5] * 6, 16, 8, 64, 20, False, True),
+    ([3000, 2999, 1, 2], 32, 16, 128, 40, True, True),
+    # the same few items as single heads, cut into many parts
     ([9000, 3], 32, 4, 64, 33, True, True),
-    ([7000, 1, 65], 24, 8, 128, 16, True, False),
-    ([6000, 0, 100, 1], 40, 8, 64, 16, True, False),
-    ([4100, 31], 32, 16, 64, 20, False, True),
-    ([3000, 2999], 64, 8, 128, 40, True, True),
+    ([7000], 24, 8, 128, 16, True, False),
 ]
 
 
@@ -93,8 +96,8 @@ def test_decode_matches_oracle(eba, lens, H, hk, d, page, e4m3, heads_first):
     check(eba, p, bf16(torch.Generator().manual_seed(1), len(lens), H, d))
 
 
-@pytest.mark.parametrize("H,hk,d,e4m3,page", [(6, 2, 64, False, 16), (6, 2, 128, True, 16), (4, 4, 64, True, 16),
-                                              (8, 4, 128, True, 24), (12, 4, 64, False, 32), (3, 1, 128, False, 5)])
+@pytest.mark.parametrize("H,hk,d,e4m3,page", [(6, 2, 64, False, 16), (6, 2, 128, True, 16), (8, 8, 64, True, 16),
+                                              (16, 8, 128, True, 24), (24, 8, 64, False, 32), (3, 1, 128, False, 5)])
 def test_many_sequences_of_mixed_lengths(eba, H, hk, d, e4m3, page):
     r = np.random.default_rng(d)
     lens = [int(x) for x in r.integers(0, 200, size=333)]
@@ -225,13 +228,13 @@ def test_cache_past_four_gigabytes(eba):
     assert torch.isfinite(o.float()).all()
 
 
-@pytest.mark.parametrize("hk", [1, 4])
+@pytest.mark.parametrize("hk", [1, 8])
 @pytest.mark.parametrize("d,e4m3,page", [(64, False, 16), (128, True, 16), (64, True, 20), (128, False, 32),
                                          (64, True, 16)])
 def test_values_of_one_sequence_never_reach_another(eba, d, e4m3, page, hk):
     # every other sequence holds NaN values; those between end inside a tile that
     # the same block loaded NaN into before, or have a page that is none in it
-    lens = [200, 3, 130, 17] * 150
+    lens = [200, 3, 130, 17] * (150 if hk == 1 else 40)
     g = torch.Generator().manual_seed(21)
     nan = lambda n: (bf16(g, n, hk, d), torch.full((n, hk, d), math.nan, dtype=torch.bfloat16))
     p = Paged(lens, page, hk, d, e4m3=e4m3, seed=21,
@@ -248,13 +251,16 @@ def test_values_of_one_sequence_never_reach_another(eba, d, e4m3, page, hk):
     assert torch.isfinite(o2[3::4]).all() and torch.equal(o2[1::4], o[1::4])
 
 
-def test_same_call_same_bits(eba):
-    p = Paged([4000, 100, 2500], 16, 2, 64, seed=13)
+@pytest.mark.parametrize("lens,hk", [([4000, 100, 2500], 2), ([4000, 100] * 2, 16), ([500, 100], 8)],
+                         ids=["list", "four_heads", "cluster"])
+def test_same_call_same_bits(eba, lens, hk):
+    p = Paged(lens, 16, hk, 64, seed=13)
     cache = p.on_gpu(eba)
-    q = bf16(torch.Generator().manual_seed(8), 3, 8, 64).cuda()
+    B, H = len(lens), 2 * hk
+    q = bf16(torch.Generator().manual_seed(8), B, H, 64).cuda()
     a = eba.decode(cache, q, p.gtable, p.glens)
     for _ in range(5):
-        b = eba.decode(cache, q, p.gtable, p.glens, workspace=poisoned(eba, cache, 3, 8, p.table.shape[1]))
+        b = eba.decode(cache, q, p.gtable, p.glens, workspace=poisoned(eba, cache, B, H, p.table.shape[1]))
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
@@ -298,14 +304,14 @@ def test_two_streams_at_once(eba):
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("axes,pairing,d", [((64,), "half", 128), ((10, 11, 11), "interleaved", 64),
                                             ((8, 16), "half", 128)])
-@pytest.mark.parametrize("H,hk,longest", [(18, 2, 300), (8, 4, 3000)])
+@pytest.mark.parametrize("H,hk,longest", [(18, 2, 300), (32, 16, 3000)])
 def test_query_rotated_on_the_way(eba, H, hk, longest, axes, pairing, d, e4m3):
     # bit for bit the rotation kernel's query
-    p = Paged([longest, 0, 45], 16, hk, d, e4m3=e4m3, seed=19)
+    p = Paged([longest, 0, 45, 1], 16, hk, d, e4m3=e4m3, seed=19)
     cache = p.on_gpu(eba)
-    q = bf16(torch.Generator().manual_seed(10), 3, H, d).cuda()
+    q = bf16(torch.Generator().manual_seed(10), 4, H, d).cuda()
     plan = eba.Rope(axes, pairing=pairing)
-    pos = torch.randint(-1000, 10 ** 6, (len(axes), 3), device="cuda", dtype=torch.int32)
+    pos = torch.randint(-1000, 10 ** 6, (len(axes), 4), device="cuda", dtype=torch.int32)
     turned, _ = eba.rope_fwd(q, None, pos, plan)
     ref = eba.decode(cache, turned, p.gtable, p.glens)
     got = eba.decode(cache, q, p.gtable, p.glens, rope=plan, positions=pos)
