@@ -9,7 +9,16 @@
 //
 // Every cached element is read once for its G query heads: 2 G flops per
 // element, far below what the card computes per byte, so the kernel is bound
-// by HBM reads. What it is built around:
+// by HBM reads. Measured on GB300, of the rate of a plain copy (6.79 TB/s):
+// 64 ragged sequences of up to 8191 keys, 8 heads of 128 for 32, bf16, 1.1 GB
+// 176 us, 94 %; 2 x 36864 keys of 32 heads of 128, 1.2 GB 184 us, 95 %; 8 x up
+// to 131071 keys, 4 heads of 128 for 64, e4m3, 0.6 GB 105 us, 86 %; 16 x up to
+// 12544 keys of 16 heads of 64, bf16, 0.4 GB 71 us, 86 %. What is left is about
+// 4 us until the first keys arrive, 3 us of the join, and that the SMs are not
+// equally fast: on equal shares the first CTA is done after 137 us, the median
+// after 155 and the last after 169. (Handing out the end of each share to who is
+// done first cost more in changes of place than it gained.) What it is built
+// around:
 //  - The work is the list of all 32 KB tiles of all (sequence, K/V head)
 //    items, cut into equal runs, one per CTA (two CTAs per SM): long and short
 //    sequences balance without the host knowing the lengths, and a call can be
@@ -17,23 +26,31 @@
 //    fp32 partials, which the join kernel adds up in the order of the keys.
 //  - Short caches and few heads, where latency is what counts: one cluster of
 //    up to 8 CTAs per item instead, whose parts are joined through the
-//    cluster's shared memory: one launch, no workspace and no list of tiles.
-//  - A warp owns 16 or 32 keys of each tile and walks the CTA's run on its own, with
-//    its own running maximum and sums: its loads (cp.async, 16 bytes a lane,
-//    rows of whole cache lines) run several tiles ahead, across item borders,
-//    and the four warps meet only at an item's end.
+//    cluster's shared memory: one launch, no workspace and no list of tiles
+//    (333 keys of 8 heads of 128 for 32: 6.2 us, and 5 us less on the host).
+//  - Two warps of a CTA load and four compute. The loads (cp.async, 16 bytes a
+//    lane) fill a ring of three K and three V slots, across item borders; 96 KB
+//    of a CTA's 112 are on their way most of the time. Loads by the computing
+//    warps themselves left these waiting for addresses (1.1 GB case 181 us,
+//    rows of 128 bytes 85 us), TMA tiles of 16 rows arrived later.
+//  - A computing warp owns 4 KB of K and of V of each tile, with its own running
+//    maximum and sums; the four warps meet only at an item's end.
+//  - Four neighbouring K/V heads are one item where rows are short and there are
+//    enough of them: their rows of a token are read together (16 heads of 64,
+//    e4m3: 57 -> 44 us).
 //  - The products use the 16x8x16 warp matrix instruction with the keys as its
 //    16 rows and the G query heads as its 8 columns: S^T = K Q^T, then
 //    O^T += V^T P^T, with K and V read from shared memory as they lie there
 //    (V transposed by ldmatrix) and P^T made from S^T by an 8x8 register
 //    transpose. A 128-row tensor-core tile would be almost empty at these
-//    heights, and the matrix pipe is not what bounds the kernel.
+//    heights, and the matrix pipe is 13 % busy (33 % with e4m3 and 16 heads).
 //  - bf16 caches: P is split into two bf16 terms (P = hi + lo to 2^-15), so
 //    that its rounding stays far below that of the bf16 output; e4m3 caches:
 //    K and V widen exactly to fp16, q is scaled per head by a power of two
 //    into fp16's range (exact above 2^-28 of the head's largest element) and P
 //    is held as fp16, 2^7 to 2^15 at the running maximum (2^-11 relative down to
-//    2^-21 of the largest weight, steps of 2^-31 below).
+//    2^-21 of the largest weight, steps of 2^-31 below). (The e4m3 warp
+//    instruction takes K as it is, but is slower: 129 instead of 105 us.)
 // Scores, maxima, sums and outputs are fp32 throughout.
 #include <cuda_fp16.h>
 
@@ -60,7 +77,8 @@ struct Layout {
   static constexpr int N = 8 * NB;                    // query heads of a K/V head
   static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a cached row
   // A warp's step: 4 KB each of K and V, so that what a step costs besides its
-  // bytes is paid once for as many bytes.
+  // bytes is paid once for as many bytes (16 keys a step whatever their size:
+  // e4m3, 16 heads, 130 instead of 105 us).
   static constexpr int kSub = kRow == 256 ? 1 : 2;
   static constexpr int kRounds = kRow == 64 ? 2 : 1;  // of kSub sets of keys in a step
   static constexpr int kStepKeys = kSubKeys * kSub * kRounds;
@@ -328,8 +346,8 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned c
 #pragma unroll
         for (int i = 0; i < 32 / kRows; ++i) {
           const int r = i * kRows + r_lane;
-          cp_async16<L::kRow>(to + tile_offset<L::kRow>(32 * x + r, c), at + __shfl_sync(0xffffffffu, off[x], r),
-                     (keys[x] >> r) & 1);
+          const unsigned char* p = at + __shfl_sync(0xffffffffu, off[x], r);
+          cp_async16<L::kRow>(to + tile_offset<L::kRow>(32 * x + r, c), p, (keys[x] >> r) & 1);
         }
     }
     cp_async_arrive(full);
@@ -510,7 +528,8 @@ __global__ void __launch_bounds__(kBlock, 2)
       for (int m = kPer / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
       // up = 2^e puts the head's largest element into [2^13, 2^14); e within the
       // range where 2^e and 2^-e are normal floats
-      const int e = top > 0.f ? min(max(13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -100), 100) : 0;
+      const int floor_log2 = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+      const int e = top > 0.f ? min(max(13 - floor_log2, -100), 100) : 0;
       up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
@@ -580,179 +599,180 @@ __global__ void __launch_bounds__(kBlock, 2)
     wait_filled(full, parity);
 #pragma unroll 1
     for (int round = 0; round < L::kRounds; ++round) {
-    uint32_t mask;  // the keys that count
-    {
-      const unsigned char* at =
-          smem + L::kOffKeys +
-          (stage * L::kBoxes + ((QUAD ? 0 : warp * L::kRounds) + round) * kSub) * 2;
-      mask = kSub == 1 ? *reinterpret_cast<const uint16_t*>(at) : *reinterpret_cast<const uint32_t*>(at);
-    }
-    // S^T = K Q^T: two chains, of the two halves of d or of two sets of keys
-    float s[NB][2][4];
-    if (mask) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[nb][0][x] = s[nb][1][x] = 0.f;
-#pragma unroll
-      for (int k = 0; k < kKSteps; k += 2) {
-        uint32_t q[NB][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          if constexpr (NB == 1) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) q[nb][x] = qf[k / 2][x];
-          } else {
-            load_q(q[nb], nb, k);
-          }
-        }
-#pragma unroll
-        for (int sub = 0; sub < kSub; ++sub) {
-          const int row = (round * kSub + sub) * kSubKeys + (lane & 15);
-          if constexpr (F8) {
-            uint32_t r[4];
-            ldmatrix4(r, kt + tile_offset<L::kRow>(row, k + (lane >> 4)));
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t lo = r[2 * x], hi = r[2 * x + 1];
-              const uint32_t f[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(hi), e4m3x2_f16x2(lo >> 16),
-                                     e4m3x2_f16x2(hi >> 16)};
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma16816<true>(s[nb][kSub == 1 ? x : sub], f, q[nb][2 * x], q[nb][2 * x + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t r[4];
-              ldmatrix4(r, kt + tile_offset<L::kRow>(row, 2 * (k + x) + (lane >> 4)));
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma16816<false>(s[nb][kSub == 1 ? x : sub], r, q[nb][2 * x], q[nb][2 * x + 1]);
-            }
-          }
-        }
+      uint32_t mask;  // the keys that count
+      {
+        const unsigned char* at =
+            smem + L::kOffKeys +
+            (stage * L::kBoxes + ((QUAD ? 0 : warp * L::kRounds) + round) * kSub) * 2;
+        mask = kSub == 1 ? *reinterpret_cast<const uint16_t*>(at) : *reinterpret_cast<const uint32_t*>(at);
       }
-    }
-    if (round + 1 == L::kRounds) {
-      __syncwarp();  // all lanes have read the masks and are done with K
-      if (lane == 0) mbar_arrive(empty);
-    }
-    uint32_t ph[kSub][NB][2], pl[kSub][NB][2];
-    if (mask) {
-      // online softmax; element x of a lane: key u8 + 8 (x / 2), column 2 j4 + x % 2
-      float v[NB][kSub][4];
-      bool grew = false;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-        for (int sub = 0; sub < kSub; ++sub) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            v[nb][sub][x] = (kSub == 1 ? s[nb][0][x] + s[nb][1][x] : s[nb][sub][x]) * qs[nb][x & 1];
-          if (mask != kAllKeys) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (!((mask >> (sub * kSubKeys + u8 + 8 * (x >> 1))) & 1)) v[nb][sub][x] = -INFINITY;
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            grew |= fmaxf(v[nb][sub][x], v[nb][sub][x + 2]) > top[nb][x] + kSlack;
-        }
-      }
-      // The reference the weights are relative to follows the maximum only when
-      // that has grown by more than kSlack: one vote a step instead of a
-      // maximum over the lanes and a rescaled output.
-      if (__any_sync(0xffffffffu, grew)) {
+      // S^T = K Q^T: two chains, of the two halves of d or of two sets of keys
+      float s[NB][2][4];
+      if (mask) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float to = fmaxf(v[nb][0][x], v[nb][0][x + 2]);
-            if (kSub == 2) to = fmaxf(to, fmaxf(v[nb][kSub - 1][x], v[nb][kSub - 1][x + 2]));
+          for (int x = 0; x < 4; ++x) s[nb][0][x] = s[nb][1][x] = 0.f;
 #pragma unroll
-            for (int m = 4; m < 32; m <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, m));
-            to = fmaxf(to, top[nb][x]);
-            // -inf to -inf (a column whose scores are all -inf) keeps its zeros
-            const float f = to == top[nb][x] ? 1.f : ex2_approx(top[nb][x] - to);
-            top[nb][x] = to;
-            sum[nb][x] *= f;
+        for (int k = 0; k < kKSteps; k += 2) {
+          uint32_t q[NB][4];
 #pragma unroll
-            for (int k = 0; k < kKSteps; ++k) {
-              o[nb][k][x] *= f;
-              o[nb][k][x + 2] *= f;
-            }
-          }
-      }
+          for (int nb = 0; nb < NB; ++nb) {
+            if constexpr (NB == 1) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float ref[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          ref[x] = top[nb][x] == -INFINITY ? 0.f : top[nb][x];
-          if (F8) ref[x] -= kF16Shift;
-        }
-#pragma unroll
-        for (int sub = 0; sub < kSub; ++sub) {
-          float p[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            p[x] = ex2_approx(v[nb][sub][x] - ref[x & 1]);
-            sum[nb][x & 1] += p[x];
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if constexpr (F8) {
-              ph[sub][nb][x] = transpose8(pack_f16(p[2 * x], p[2 * x + 1]));
+              for (int x = 0; x < 4; ++x) q[nb][x] = qf[k / 2][x];
             } else {
-              const uint32_t h0 = below(p[2 * x]), h1 = below(p[2 * x + 1]);
-              ph[sub][nb][x] = transpose8(__byte_perm(h0, h1, 0x7632));
-              pl[sub][nb][x] = transpose8(pack_bf16(p[2 * x] - __uint_as_float(h0),
-                                                    p[2 * x + 1] - __uint_as_float(h1)));
+              load_q(q[nb], nb, k);
+            }
+          }
+#pragma unroll
+          for (int sub = 0; sub < kSub; ++sub) {
+            const int row = (round * kSub + sub) * kSubKeys + (lane & 15);
+            if constexpr (F8) {
+              uint32_t r[4];
+              ldmatrix4(r, kt + tile_offset<L::kRow>(row, k + (lane >> 4)));
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t lo = r[2 * x], hi = r[2 * x + 1];
+                const uint32_t f[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(hi), e4m3x2_f16x2(lo >> 16),
+                                       e4m3x2_f16x2(hi >> 16)};
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  mma16816<true>(s[nb][kSub == 1 ? x : sub], f, q[nb][2 * x], q[nb][2 * x + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                uint32_t r[4];
+                ldmatrix4(r, kt + tile_offset<L::kRow>(row, 2 * (k + x) + (lane >> 4)));
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  mma16816<false>(s[nb][kSub == 1 ? x : sub], r, q[nb][2 * x], q[nb][2 * x + 1]);
+              }
             }
           }
         }
       }
-    }
-    if (round == 0) wait_filled(full + 8, parity);
-    if (mask) {
-      // O^T += V^T P^T
+      if (round + 1 == L::kRounds) {
+        __syncwarp();  // all lanes have read the masks and are done with K
+        if (lane == 0) mbar_arrive(empty);
+      }
+      uint32_t ph[kSub][NB][2], pl[kSub][NB][2];
+      if (mask) {
+        // online softmax; element x of a lane: key u8 + 8 (x / 2), column 2 j4 + x % 2
+        float v[NB][kSub][4];
+        bool grew = false;
 #pragma unroll
-      for (int sub = 0; sub < kSub; ++sub) {
-        if constexpr (F8) {
-          // 16-bit units of V hold two columns of one key: after the transposing
-          // load a register holds columns 2 u8, 2 u8 + 1 of keys 2 j4, 2 j4 + 1,
-          // and rows u8 and u8 + 8 of the product stand for those two columns
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int k = 0; k < kKSteps; k += 2) {
-            uint32_t r[4];
-            ldmatrix4_trans(r, vt + tile_offset<L::kRow>((round * kSub + sub) * kSubKeys + (lane & 15), k + (lane >> 4)));
+          for (int sub = 0; sub < kSub; ++sub) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              v[nb][sub][x] = (kSub == 1 ? s[nb][0][x] + s[nb][1][x] : s[nb][sub][x]) * qs[nb][x & 1];
+            if (mask != kAllKeys) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (!((mask >> (sub * kSubKeys + u8 + 8 * (x >> 1))) & 1)) v[nb][sub][x] = -INFINITY;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              grew |= fmaxf(v[nb][sub][x], v[nb][sub][x + 2]) > top[nb][x] + kSlack;
+          }
+        }
+        // The reference the weights are relative to follows the maximum only when
+        // that has grown by more than kSlack: one vote a step instead of a
+        // maximum over the lanes and a rescaled output.
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint32_t w0 = __byte_perm(r[2 * x], 0, 0x3120);
-              const uint32_t w1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
-              const uint32_t f[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1),
-                                     e4m3x2_f16x2(w1 >> 16)};
+              float to = fmaxf(v[nb][0][x], v[nb][0][x + 2]);
+              if (kSub == 2) to = fmaxf(to, fmaxf(v[nb][kSub - 1][x], v[nb][kSub - 1][x + 2]));
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma16816<true>(o[nb][k + x], f, ph[sub][nb][0], ph[sub][nb][1]);
+              for (int m = 4; m < 32; m <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, m));
+              to = fmaxf(to, top[nb][x]);
+              // -inf to -inf (a column whose scores are all -inf) keeps its zeros
+              const float f = to == top[nb][x] ? 1.f : ex2_approx(top[nb][x] - to);
+              top[nb][x] = to;
+              sum[nb][x] *= f;
+#pragma unroll
+              for (int k = 0; k < kKSteps; ++k) {
+                o[nb][k][x] *= f;
+                o[nb][k][x + 2] *= f;
+              }
             }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float ref[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            ref[x] = top[nb][x] == -INFINITY ? 0.f : top[nb][x];
+            if (F8) ref[x] -= kF16Shift;
           }
-        } else {
-          const int vr = (round * kSub + sub) * kSubKeys + (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
 #pragma unroll
-          for (int k = 0; k < kKSteps; ++k) {
-            uint32_t r[4];
-            ldmatrix4_trans(r, vt + tile_offset<L::kRow>(vr, 2 * k + vc));
+          for (int sub = 0; sub < kSub; ++sub) {
+            float p[4];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma16816<false>(o[nb][k], r, ph[sub][nb][0], ph[sub][nb][1]);
-              mma16816<false>(o[nb][k], r, pl[sub][nb][0], pl[sub][nb][1]);
+            for (int x = 0; x < 4; ++x) {
+              p[x] = ex2_approx(v[nb][sub][x] - ref[x & 1]);
+              sum[nb][x & 1] += p[x];
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if constexpr (F8) {
+                ph[sub][nb][x] = transpose8(pack_f16(p[2 * x], p[2 * x + 1]));
+              } else {
+                const uint32_t h0 = below(p[2 * x]), h1 = below(p[2 * x + 1]);
+                ph[sub][nb][x] = transpose8(__byte_perm(h0, h1, 0x7632));
+                pl[sub][nb][x] = transpose8(pack_bf16(p[2 * x] - __uint_as_float(h0),
+                                                      p[2 * x + 1] - __uint_as_float(h1)));
+              }
             }
           }
         }
       }
-    }
+      if (round == 0) wait_filled(full + 8, parity);
+      if (mask) {
+        // O^T += V^T P^T
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+          const int set = (round * kSub + sub) * kSubKeys;  // its first row
+          if constexpr (F8) {
+            // 16-bit units of V hold two columns of one key: after the transposing
+            // load a register holds columns 2 u8, 2 u8 + 1 of keys 2 j4, 2 j4 + 1,
+            // and rows u8 and u8 + 8 of the product stand for those two columns
+#pragma unroll
+            for (int k = 0; k < kKSteps; k += 2) {
+              uint32_t r[4];
+              ldmatrix4_trans(r, vt + tile_offset<L::kRow>(set + (lane & 15), k + (lane >> 4)));
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t w0 = __byte_perm(r[2 * x], 0, 0x3120);
+                const uint32_t w1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
+                const uint32_t f[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1),
+                                       e4m3x2_f16x2(w1 >> 16)};
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  mma16816<true>(o[nb][k + x], f, ph[sub][nb][0], ph[sub][nb][1]);
+              }
+            }
+          } else {
+            const int vr = set + (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+#pragma unroll
+            for (int k = 0; k < kKSteps; ++k) {
+              uint32_t r[4];
+              ldmatrix4_trans(r, vt + tile_offset<L::kRow>(vr, 2 * k + vc));
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                mma16816<false>(o[nb][k], r, ph[sub][nb][0], ph[sub][nb][1]);
+                mma16816<false>(o[nb][k], r, pl[sub][nb][0], pl[sub][nb][1]);
+              }
+            }
+          }
+        }
+      }
     }
     __syncwarp();  // all lanes are done with V
     if (lane == 0) mbar_arrive(empty + 8);
@@ -829,68 +849,69 @@ __global__ void __launch_bounds__(kBlock, 2)
           __syncwarp();
         }
       } else {
-      const int g = done.hh / a.blocks, blk = done.hh - g * a.blocks;
+        const int g = done.hh / a.blocks, blk = done.hh - g * a.blocks;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float f[2];
+        for (int nb = 0; nb < NB; ++nb) {
+          float f[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float M = -INFINITY;
+          for (int x = 0; x < 2; ++x) {
+            float M = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * N + nb * 8 + 2 * j4 + x].x);
-          f[x] = top[nb][x] == -INFINITY ? 0.f : ex2_approx(top[nb][x] - M);
-        }
-        constexpr int kCols = kPassCols / 16;  // of a thread in the sum below
-        const int row = tid >> 4, c4 = (tid & 15) * kCols;
-        float M = -INFINITY, l = 0.f;
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * N + nb * 8 + 2 * j4 + x].x);
+            f[x] = top[nb][x] == -INFINITY ? 0.f : ex2_approx(top[nb][x] - M);
+          }
+          constexpr int kCols = kPassCols / 16;  // of a thread in the sum below
+          const int row = tid >> 4, c4 = (tid & 15) * kCols;
+          float M = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * N + nb * 8 + row].x);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 ml = s_ml[w * N + nb * 8 + row];
-          l += ml.x == -INFINITY ? 0.f : ml.y * ex2_approx(ml.x - M);
-        }
-        const int hg = blk * N + nb * 8 + row;
-        const long long head = static_cast<long long>(done.b) * a.H + g * a.group + hg;
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += kPassCols) {
-          put(nb, c0, f);
-          sync_compute();
-          float v[kCols] = {};
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * N + nb * 8 + row].x);
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float* y = s_sum + (w * 8 + row) * kPassRow + c4;
-#pragma unroll
-            for (int x = 0; x < kCols; x += 2) {
-              const float2 two = *reinterpret_cast<const float2*>(y + x);
-              v[x] += two.x, v[x + 1] += two.y;
-            }
+            const float2 ml = s_ml[w * N + nb * 8 + row];
+            l += ml.x == -INFINITY ? 0.f : ml.y * ex2_approx(ml.x - M);
           }
-          if (whole && a.splits <= 1) {
-            if (hg < a.group) {
-              const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+          const int hg = blk * N + nb * 8 + row;
+          const long long head = static_cast<long long>(done.b) * a.H + g * a.group + hg;
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += kPassCols) {
+            put(nb, c0, f);
+            sync_compute();
+            float v[kCols] = {};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              const float* y = s_sum + (w * 8 + row) * kPassRow + c4;
+#pragma unroll
+              for (int x = 0; x < kCols; x += 2) {
+                const float2 two = *reinterpret_cast<const float2*>(y + x);
+                v[x] += two.x, v[x + 1] += two.y;
+              }
+            }
+            if (whole && a.splits <= 1) {
+              if (hg < a.group) {
+                const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+#pragma unroll
+                for (int x = 0; x < kCols; x += 2)
+                  *reinterpret_cast<uint32_t*>(a.o + head * D + c0 + c4 + x) =
+                      pack_bf16(v[x] * f, v[x + 1] * f);
+              }
+            } else {
+              float* to = a.splits > 1 ? s_part + (nb * 8 + row) * D
+                                       : a.part_o + (static_cast<long long>(part) * N + nb * 8 + row) * D;
 #pragma unroll
               for (int x = 0; x < kCols; x += 2)
-                *reinterpret_cast<uint32_t*>(a.o + head * D + c0 + c4 + x) = pack_bf16(v[x] * f, v[x + 1] * f);
+                *reinterpret_cast<float2*>(to + c0 + c4 + x) = make_float2(v[x], v[x + 1]);
             }
-          } else {
-            float* to = a.splits > 1 ? s_part + (nb * 8 + row) * D
-                                     : a.part_o + (static_cast<long long>(part) * N + nb * 8 + row) * D;
-#pragma unroll
-            for (int x = 0; x < kCols; x += 2)
-              *reinterpret_cast<float2*>(to + c0 + c4 + x) = make_float2(v[x], v[x + 1]);
+            sync_compute();
           }
-          sync_compute();
+          if ((tid & 15) == 0) {
+            if (a.splits > 1)
+              s_part_ml[nb * 8 + row] = make_float2(M, l);
+            else if (!whole)
+              a.part_ml[static_cast<long long>(part) * N + nb * 8 + row] = make_float2(M, l);
+            else if (hg < a.group)
+              a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+          }
         }
-        if ((tid & 15) == 0) {
-          if (a.splits > 1)
-            s_part_ml[nb * 8 + row] = make_float2(M, l);
-          else if (!whole)
-            a.part_ml[static_cast<long long>(part) * N + nb * 8 + row] = make_float2(M, l);
-          else if (hg < a.group)
-            a.lse[head] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
-        }
-      }
       }
       // What the join kernel needs: the item that this CTA's run ends in the middle of,
       // if the item has its first tile here or covers the whole run.
