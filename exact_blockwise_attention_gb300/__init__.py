@@ -677,15 +677,6 @@ def rope_bwd(dq, dk, positions, plan):
     return _rope(dq, dk, positions, plan, True)
 
 
-def _rotatable(g):
-    """A gradient as the kernel reads it: autograd also hands over expanded or transposed ones."""
-    if g is None or (g.is_contiguous() and not g.data_ptr() & 15):
-        return g
-    ok = g.stride(-1) == 1 and not g.data_ptr() & 15 and \
-        all(s % 8 == 0 for s, n in zip(g.stride()[:-1], g.shape) if n != 1)
-    return g if ok else g.clone(memory_format=torch.contiguous_format)
-
-
 class _Rotation(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, positions, plan, inverse):
@@ -697,13 +688,21 @@ class _Rotation(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dq, dk):
         (positions,) = ctx.saved_tensors
-        dq, dk = _rotatable(dq), _rotatable(dk)
         # (under create_graph the gradient is a rotation with a gradient of its own)
         turn = _Rotation.apply if torch.is_grad_enabled() else _rope
-        if dq is None and dk is not None:
-            dk, dq = turn(dk, None, positions, ctx.plan, not ctx.inverse)
-        elif dq is not None:
-            dq, dk = turn(dq, dk, positions, ctx.plan, not ctx.inverse)
+        plan, back = ctx.plan, not ctx.inverse
+        try:
+            if dq is not None:
+                dq, dk = turn(dq, dk, positions, plan, back)
+            elif dk is not None:
+                dk, dq = turn(dk, None, positions, plan, back)
+        except ValueError:  # autograd also hands over expanded and transposed gradients
+            dq, dk = (g if g is None else g.clone(memory_format=torch.contiguous_format)
+                      for g in (dq, dk))
+            if dq is not None:
+                dq, dk = turn(dq, dk, positions, plan, back)
+            else:
+                dk, dq = turn(dk, None, positions, plan, back)
         return dq, dk, None, None, None
 
 

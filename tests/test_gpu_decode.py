@@ -76,6 +76,8 @@ CASES = [
     ([5000, 4999, 12], 2, 1, 64, 33, False, False),
     ([20000], 2, 2, 128, 128, False, False),               # one sequence over all CTAs
     ([30001], 8, 1, 64, 64, True, False),
+    ([9000, 50], 40, 2, 128, 16, False, False),            # a group in two blocks, over all CTAs
+    ([6000, 700], 80, 4, 64, 24, True, False),
     # short rows, heads in fours
     ([5000, 4999, 0, 12], 16, 16, 64, 48, False, False),
     ([3000, 3, 0, 0, 64, 65, 31, 32], 64, 8, 64, 33, True, True),
@@ -264,17 +266,19 @@ def test_same_call_same_bits(eba, lens, hk):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_captured_call_follows_lengths_and_tables(eba):
-    p = Paged([500, 1200, 64], 16, 2, 128, seed=17)
+@pytest.mark.parametrize("longest,H,hk,d", [(2500, 8, 2, 128), (300, 8, 2, 128), (2500, 32, 32, 64)],
+                         ids=["list", "cluster", "four_heads"])
+def test_captured_call_follows_lengths_and_tables(eba, longest, H, hk, d):
+    p = Paged([longest - 70, longest, 64], 16, hk, d, seed=17)
     cache = p.on_gpu(eba)
-    q = bf16(torch.Generator().manual_seed(9), 3, 8, 128).cuda()
+    q = bf16(torch.Generator().manual_seed(9), 3, H, d).cuda()
     lens, table = p.glens.clone(), p.gtable.clone()
     eba.decode(cache, q, table, lens)  # loads the kernels before the capture
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         o, lse = eba.decode(cache, q, table, lens)
         o2, lse2 = eba.decode(cache, q, table, lens)  # two calls in one graph
-    for new in ([500, 1200, 64], [1, 0, 63], [0, 0, 0], [499, 700, 2]):
+    for new in ([longest - 70, longest, 64], [1, 0, 63], [0, 0, 0], [longest - 71, longest // 2, 2]):
         lens.copy_(torch.tensor(new, dtype=torch.int32))
         q.copy_(q.roll(1, 1))
         graph.replay()
@@ -321,3 +325,48 @@ def test_query_rotated_on_the_way(eba, H, hk, longest, axes, pairing, d, e4m3):
         ref = eba.decode(cache, turned, p.gtable, p.glens)
         got = eba.decode(cache, q, p.gtable, p.glens, rope=plan)
         assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+
+
+def test_two_captured_calls_share_a_workspace(eba):
+    # one workspace for all layers: what a call leaves there does not matter to the
+    # next, in whatever order the graphs are replayed
+    ps = [Paged([3000, 17, 900], 16, 2, 64, seed=s) for s in (31, 32)]
+    caches = [p.on_gpu(eba) for p in ps]
+    qs = [bf16(torch.Generator().manual_seed(s), 3, 8, 64).cuda() for s in (5, 6)]
+    refs = [eba.decode(c, q, p.gtable, p.glens) for c, q, p in zip(caches, qs, ps)]
+    ws = poisoned(eba, caches[0], 3, 8, ps[0].table.shape[1])
+    graphs, outs = [], []
+    for c, q, p in zip(caches, qs, ps):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(eba.decode(c, q, p.gtable, p.glens, workspace=ws))
+    for i in (0, 1, 1, 0, 0, 1):
+        graphs[i].replay()
+        assert torch.equal(outs[i][0], refs[i][0]) and torch.equal(outs[i][1], refs[i][1])
+
+
+def test_keys_and_values_side_by_side_and_shared_pages(eba):
+    # one tensor [pages, 2, slots, heads, d]; two sequences that begin with the same pages
+    g = torch.Generator().manual_seed(33)
+    both = bf16(g, 40, 2, 16, 2, 128).cuda()
+    k, v = both[:, 0], both[:, 1]
+    table = torch.randperm(40, generator=g)[:36].view(2, 18).to(torch.int32)
+    table[1, :10] = table[0, :10]
+    lens = torch.tensor([280, 170], dtype=torch.int32)
+    q = bf16(g, 2, 4, 128)
+    o, lse = eba.decode(eba.PagedCache(k, v), q.cuda(), table.cuda(), lens.cuda())
+    keys = [oracle.gather(np64(k), r, n) for r, n in zip(table.tolist(), lens.tolist())]
+    values = [oracle.gather(np64(v), r, n) for r, n in zip(table.tolist(), lens.tolist())]
+    ro, rl = oracle.decode(q, keys, values, 1 / math.sqrt(128))
+    to, tl = decode_tolerances(q, keys, values, 1 / math.sqrt(128), ro, rl, False)
+    assert (np.abs(np64(o) - ro) <= to).all() and (np.abs(np64(lse) - rl) <= tl).all()
+
+
+@pytest.mark.parametrize("hk,d", [(1, 128), (8, 64)])
+def test_thousands_of_sequences(eba, hk, d):
+    # many more sequences than counting threads and CTAs, most of them empty or short
+    r = np.random.default_rng(3)
+    lens = np.where(r.random(3001) < 0.5, 0, r.integers(1, 40, size=3001))
+    lens[[0, 1500, 3000]] = 0, 2000, 33
+    p = Paged([int(x) for x in lens], 16, hk, d, seed=35)
+    check(eba, p, bf16(torch.Generator().manual_seed(36), 3001, hk, d))

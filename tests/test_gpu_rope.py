@@ -276,6 +276,27 @@ def test_append_matches_oracle(eba, lens, new, H, d, page, kw):
     append_case(eba, lens, new, H, d, page, seed=sum(lens), **kw)
 
 
+def test_append_offsets_that_begin_behind_the_first_rows(eba):
+    p = Paged([20, 9], 8, 2, 64, seed=41)
+    cache = p.on_gpu(eba)
+    k = bf16(torch.Generator().manual_seed(1), 10, 2, 64).cuda()
+    before = p.gk.clone()
+    eba.cache_append(cache, k, k, p.gtable, p.glens, torch.tensor([3, 5, 6], device="cuda", dtype=torch.int32))
+    rows = {(p.rows[0][2], 2): 3, (p.rows[0][2], 3): 4, (p.rows[1][1], 0): 5}
+    for (page, slot), t in rows.items():
+        assert torch.equal(p.gk[page, slot], k[t]) and torch.equal(p.gv[page, slot], k[t])
+        before[page, slot] = k[t]
+    assert torch.equal(p.gk.view(torch.uint8), before.view(torch.uint8))
+
+
+def test_positions_shared_by_the_axes(eba):
+    plan = eba.Rope((16, 16))
+    x = bf16(torch.Generator().manual_seed(2), 30, 3, 64).cuda()
+    pos = torch.arange(30, device="cuda", dtype=torch.int32)
+    both = pos.expand(2, 30)  # a stride of 0
+    assert torch.equal(eba.rope_fwd(x, None, both, plan)[0], eba.rope_fwd(x, None, both.contiguous(), plan)[0])
+
+
 def test_append_to_hundreds_of_sequences(eba):
     r = np.random.default_rng(1)
     new = [int(x) for x in r.integers(0, 6, size=300)]
