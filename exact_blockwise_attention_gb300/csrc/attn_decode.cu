@@ -653,6 +653,7 @@ __global__ void __launch_bounds__(kBlock, 2)
           }
         }
       }
+      if (round == 0) wait_filled(full + 8, parity);  // V's reads overlap the softmax
       if (round + 1 == L::kRounds) {
         __syncwarp();  // all lanes have read the masks and are done with K
         if (lane == 0) mbar_arrive(empty);
@@ -732,9 +733,6 @@ __global__ void __launch_bounds__(kBlock, 2)
             }
           }
         }
-      }
-      if (round == 0) wait_filled(full + 8, parity);
-      if (mask) {
         // O^T += V^T P^T
 #pragma unroll
         for (int sub = 0; sub < kSub; ++sub) {
