@@ -220,7 +220,7 @@ struct Cursor {
 };
 
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
-  const int len = __ldg(a.lens + b);
+  const int len = a.lens[b];
   return min(max(len, 0), a.max_len);
 }
 template <int kTileKeys>
@@ -291,7 +291,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned c
       if (look_left > 0 && in < kTileKeys && key < look.len) {
         const int entry = key / a.cache.page_size;
         slot_of[kAhead - 1][x] = key - entry * a.cache.page_size;
-        page_of[kAhead - 1][x] = __ldg(a.table + look.b * a.table_stride + entry);
+        page_of[kAhead - 1][x] = a.table[look.b * a.table_stride + entry];
       }
     }
     if (--look_left > 0) advance<kTileKeys>(look, a);
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kBlock, 2)
   if (a.splits) {
     // ---- short caches: one cluster of a.splits CTAs per item ----
     const int it = cta / a.splits, rank = cta - it * a.splits;
-    const int b = it / a.heads, raw = __ldg(a.lens + b);
+    const int b = it / a.heads, raw = a.lens[b];
     const int len = min(max(raw, 0), a.max_len), nt = tiles_of<kTileKeys>(len);
     if (tid == 0) {
       if (raw != len) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kBlock, 2)
     const int b0 = min(tid * per, a.B), b1 = tid < kThreads ? min(b0 + per, a.B) : b0;
     int mine = 0;
     for (int b = b0; b < b1; ++b) {
-      const int raw = __ldg(a.lens + b);
+      const int raw = a.lens[b];
       if (cta == 0 && (raw < 0 || raw > a.max_len)) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
       mine += tiles_of<kTileKeys>(clamp_len(a, b)) * a.heads;
     }
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kBlock, 2)
       float x = hg < a.group ? __bfloat162float(q[ox]) : 0.f;
       float y = hg < a.group ? __bfloat162float(q[oy]) : 0.f;
       if (pair < P) {
-        const int pos = a.pos ? __ldg(a.pos + a.rope.axis[pair] * a.pos_axis + c.b) : c.len - 1;
+        const int pos = a.pos ? a.pos[a.rope.axis[pair] * a.pos_axis + c.b] : c.len - 1;
         float cs, sn;
         rope_cs(pos, a.rope.turns[pair], 1.f, cs, sn);
         rope_turn(x, y, cs, sn);

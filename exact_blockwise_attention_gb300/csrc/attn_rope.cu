@@ -15,14 +15,17 @@ namespace {
 constexpr int kRopeThreads = 128;
 constexpr int kUnroll = 4;  // heads whose loads are in flight together
 
+// Inputs are read by ordinary loads, not through the read-only path: a kernel that
+// begins before the one in front of it is done (pdl_wait) sees them change in its
+// lifetime.
 struct Vec16 {  // 16 elements of one head: two 16-byte vectors
   uint4 a, b;
 };
 
 __device__ __forceinline__ Vec16 load16(const __nv_bfloat16* p, int off_a, int off_b) {
   Vec16 v;
-  v.a = __ldg(reinterpret_cast<const uint4*>(p + off_a));
-  v.b = __ldg(reinterpret_cast<const uint4*>(p + off_b));
+  v.a = *reinterpret_cast<const uint4*>(p + off_a);
+  v.b = *reinterpret_cast<const uint4*>(p + off_b);
   return v;
 }
 
@@ -108,7 +111,7 @@ __device__ __forceinline__ void lane_turn(const RopeTable& r, int i, const int (
 __device__ __forceinline__ void load_positions(int (&p)[ATTN_MAX_AXES], int n_axes, const int* pos,
                                                long long stride) {
 #pragma unroll
-  for (int a = 0; a < ATTN_MAX_AXES; ++a) p[a] = a < n_axes ? __ldg(pos + a * stride) : 0;
+  for (int a = 0; a < ATTN_MAX_AXES; ++a) p[a] = a < n_axes ? pos[a * stride] : 0;
 }
 
 template <int D, bool INTERLEAVED>
@@ -184,11 +187,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 // The sequence of token t: the s with cu[s] <= t < cu[s + 1], or -1 for a
 // token outside [cu[0], cu[n]).
 __device__ __forceinline__ int find_sequence(const int* cu, int n, long long t) {
-  if (t < __ldg(cu) || t >= __ldg(cu + n)) return -1;
+  if (t < cu[0] || t >= cu[n]) return -1;
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
+    if (cu[mid] <= t) lo = mid; else hi = mid;
   }
   return lo;
 }
@@ -208,12 +211,12 @@ __device__ __forceinline__ Place find_place(const AppendArgs& a, long long t) {
   if (a.cu_new) {
     s = find_sequence(a.cu_new, a.n_seqs, t);
     if (s < 0) return p;  // behind the last sequence: padding
-    back = __ldg(a.cu_new + s + 1) - t;
+    back = a.cu_new[s + 1] - t;
   } else {
     s = static_cast<int>(t);
     back = 1;
   }
-  const int len = __ldg(a.lens + s);
+  const int len = a.lens[s];
   if (len == 0) return p;  // an empty slot of the batch
   const long long at = len - back;
   // (at >= len: offsets that decrease)
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
   if (turns && a.pos) load_positions(pos, a.rope.n_axes, a.pos + token, a.pos_axis);
   const Place place = find_place(a, token);
   if (!place.entry) return;
-  const int page = __ldg(place.entry);
+  const int page = *place.entry;
   Turn8 t;
   if (turns) {
     if (!a.pos) pos[0] = place.at;  // one axis: the place in the sequence

@@ -420,3 +420,33 @@ def test_prompt_then_tokens_through_the_cache(eba, H, Hk, d, axes):
         ro, rl = oracle.varlen_forward(qr, kr, va, list(range(B + 1)), cu_k, 1 / math.sqrt(d))
         assert np.abs(np64(o) - ro).max() <= 2.0 ** -8 * np.abs(ro).max() + 1e-3
         assert np.abs(np64(lse) - rl.T).max() <= 1e-4
+
+
+@pytest.mark.parametrize("longest", [100, 3000])
+def test_calls_right_behind_each_other_see_what_was_written(eba, longest):
+    """Rotate, append what was rotated, decode with it: 40 times over the same few
+    addresses, with a pause after every call, without, and in a graph."""
+    plan, pos = eba.Rope((64,)), torch.tensor([1, 77], device="cuda", dtype=torch.int32)
+    start = bf16(torch.Generator().manual_seed(3), 2, 4, 128).cuda()
+    p = Paged([longest, 64], 16, 2, 128, seed=9)
+    cache = p.on_gpu(eba)
+
+    def run(pause=lambda: None):
+        x, outs = start, []
+        for _ in range(40):
+            x, _ = eba.rope_fwd(x, None, pos, plan)
+            pause()
+            eba.cache_append(cache, x[:, :2], x[:, 2:], p.gtable, p.glens)
+            pause()
+            outs.append(eba.decode(cache, x, p.gtable, p.glens)[0])
+            pause()
+        return torch.stack(outs)
+
+    ref = run(torch.cuda.synchronize)
+    assert torch.equal(run(), ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for _ in range(3):
+        graph.replay()
+        assert torch.equal(out, ref)
