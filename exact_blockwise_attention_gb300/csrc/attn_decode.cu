@@ -327,6 +327,10 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const unsigned c
         for (int x = 0; x < kPer; ++x)
           s_keys[stage * kBoxes + 2 * x + lane] = static_cast<uint16_t>(keys[x] >> (16 * lane));
       }
+      // The copies' arrives below order the copies alone; the masks are ordinary stores
+      // and are released by an ordinary arrive.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
     }
     if constexpr (WHOLE) {
 #pragma unroll
@@ -380,8 +384,10 @@ __global__ void __launch_bounds__(kBlock, 2)
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
   pdl_launch_dependents();
   const uint32_t bars = smem_u32(smem + L::kOffBar);
-  if (threadIdx.x < 4 * kStages)  // filled by 32 lanes, emptied by 4 warps
-    mbar_init(bars + threadIdx.x * 8, threadIdx.x < 2 * kStages ? 32 : kWarps);
+  // filled: by the copies of 32 lanes, K's also by the masks' arrive; emptied: by 4 warps
+  if (threadIdx.x < 4 * kStages)
+    mbar_init(bars + threadIdx.x * 8,
+              threadIdx.x >= 2 * kStages ? kWarps : threadIdx.x % 2 == 0 ? 33 : 32);
   if (threadIdx.x == 0) *s_abort = 0;
   fence_mbar_init();
   pdl_wait();

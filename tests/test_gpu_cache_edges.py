@@ -1,0 +1,88 @@
+"""The rotation, the paged cache and the decode where they are most easily wrong:
+absent pages, special values and far-out sizes on every path of the decode, exact
+roundings of an e4m3 cache, and several threads at once."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from cache_util import Paged, bf16, decode_tolerances, np64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def eba():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from exact_blockwise_attention_gb300 import _build
+
+    _build.build()
+    import exact_blockwise_attention_gb300 as m
+
+    return m
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean(eba):
+    eba.poll_device_status()
+    yield
+    assert eba.poll_device_status() == 0
+
+
+def compare(o, lse, q, keys, values, scale, e4m3):
+    """o, lse against the oracle over the given keys and values, element by element."""
+    ro, rl = oracle.decode(q, keys, values, scale)
+    to, tl = decode_tolerances(q, keys, values, scale, ro, rl, e4m3)
+    o, lse = np64(o), np64(lse)
+    empty = np.isneginf(rl)
+    assert (np.isneginf(lse) == empty).all() and (o[empty] == 0).all()
+    assert (np.abs(o - ro) <= to).all(), np.max(np.abs(o - ro) - to)
+    assert (np.abs(lse[~empty] - rl[~empty]) <= tl[~empty]).all()
+
+
+# sequences, keys, H, H_kv, d, page, e4m3: what the calls are cut into
+PATHS = {
+    "cluster": (1, 700, 16, 4, 128, 16, False),
+    "many_parts": (3, 20000, 4, 2, 128, 16, False),
+    "few_parts": (5, 4000, 16, 8, 128, 32, False),
+    "few_parts_odd_pages": (5, 4000, 16, 8, 128, 20, False),
+    "two_column_sets_e4m3": (3, 20000, 32, 2, 128, 64, True),
+    "two_blocks": (3, 6000, 40, 2, 64, 16, False),
+    "four_heads": (5, 3000, 16, 16, 64, 48, False),
+    "four_heads_odd_pages_e4m3": (5, 3000, 32, 16, 64, 40, True),
+}
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_tiles_without_a_key(eba, path):
+    # whole tiles whose pages are none, between tiles that hold keys: their masks are
+    # empty, and their zeros and the keys around them must not count or be lost. In the
+    # first sequence the tiles of 128 keys take turns at random, the second holds none
+    # at all, the third begins with a long run of none (parts without weight), the others
+    # are whole.
+    B, n, H, hk, d, page, e4m3 = PATHS[path]
+    scales = dict(k_scale=0.03, v_scale=0.5) if e4m3 else {}
+    p = Paged([n] * min(B, 3) + [n - 77] * (B - 3), page, hk, d, e4m3=e4m3, seed=n + H, **scales)
+    cache = p.on_gpu(eba)
+    q = bf16(torch.Generator().manual_seed(n), B, H, d)
+    r = np.random.default_rng(n)
+    first = np.arange(len(p.rows[0])) * page // 128  # of each page: its tile of 128 keys
+    absent = [r.random(first.max() + 1)[first] < 0.5]
+    if B > 1:
+        absent += [np.ones(len(first), bool), np.arange(len(first)) < 0.7 * len(first)]
+    table = p.table.clone()
+    keys, values = p.contents()
+    for b, gone in enumerate(absent):
+        table[b, :len(gone)][torch.tensor(gone)] = torch.tensor([p.n_pages, -1])[b % 2].int()
+        held = ~gone[np.arange(n) // page]
+        keys[b], values[b] = keys[b][held], values[b][held]
+    o, lse = eba.decode(cache, q.cuda(), table.cuda(), p.glens)
+    assert eba.poll_device_status() == 7
+    for _ in range(3):
+        o2, lse2 = eba.decode(cache, q.cuda(), table.cuda(), p.glens)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert eba.poll_device_status() == 7
+    compare(o, lse, q, keys, values, 1 / math.sqrt(d), e4m3)
