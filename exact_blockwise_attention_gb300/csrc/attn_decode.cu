@@ -532,10 +532,12 @@ __global__ void __launch_bounds__(kBlock, 2)
     if constexpr (F8) {
 #pragma unroll
       for (int m = kPer / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      // up = 2^e puts the head's largest element into [2^13, 2^14); e within the
-      // range where 2^e and 2^-e are normal floats
+      // up = 2^e puts the head's largest element into [2^13, 2^14). e is at least
+      // 13 - 127, and at most 126, so that 2^-e is a normal float too: that leaves
+      // smaller heads below 2^13, where fp16 still holds all bits that bf16 has there
+      // (its smallest number, 2^-133, becomes 2^-7).
       const int floor_log2 = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-      const int e = top > 0.f ? min(max(13 - floor_log2, -100), 100) : 0;
+      const int e = top > 0.f ? min(13 - floor_log2, 126) : 0;
       up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }

@@ -86,3 +86,30 @@ def test_tiles_without_a_key(eba, path):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
     assert eba.poll_device_status() == 7
     compare(o, lse, q, keys, values, 1 / math.sqrt(d), e4m3)
+
+
+E4M3_PATHS = {
+    "cluster": (1, 700, 16, 4, 128, 16),
+    "two_column_sets": (2, 6000, 32, 2, 64, 64),
+    "few_parts": (5, 4000, 16, 8, 128, 20),
+    "four_heads": (5, 3000, 32, 16, 64, 40),
+}
+
+
+@pytest.mark.parametrize("power", [-130, -100, -50, 0, 99, 116, 127])
+@pytest.mark.parametrize("path", E4M3_PATHS)
+def test_queries_of_any_size_on_an_e4m3_cache(eba, path, power):
+    # from bf16's smallest to its largest numbers, with keys so scaled that the scores
+    # are ordinary numbers; the odd heads are 2^10 smaller than the even ones
+    B, n, H, hk, d, page = E4M3_PATHS[path]
+    p = Paged([n] * B, page, hk, d, e4m3=True, seed=n)
+    p.k_scale = 2.0 ** min(max(-power, -126), 126)
+    g = torch.Generator().manual_seed(power + 200)
+    q = (torch.rand(B, H, d, generator=g) * 1.5 + 0.49) * torch.randn(B, H, d, generator=g).sign()
+    q = (q.double() * 2.0 ** power).float()
+    if power > -100:
+        q[:, 1::2] *= 2.0 ** -10
+    q = q.to(torch.bfloat16)
+    assert torch.isfinite(q).all() and (q != 0).all()
+    o, lse = eba.decode(p.on_gpu(eba), q.cuda(), p.gtable, p.glens)
+    compare(o, lse, q, *p.contents(), 1 / math.sqrt(d), True)
