@@ -978,7 +978,7 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
   if ((s = check_table(page_table, table_stride, max_pages, seq_lens, B)) != ATTN_OK) return s;
   if (H < 1 || H % cache->H_kv != 0) return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * H >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * kLog2e) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
   if ((s = check_ptrs({q, o, lse})) != ATTN_OK) return s;
   if ((s = check_strides(q_strides, 2, 8)) != ATTN_OK) return s;
   if (rope) {
@@ -1018,7 +1018,7 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
   a.per_item = p.per_item;
   a.heads = p.heads;
   a.splits = p.splits;
-  a.scale_log2 = scale * kLog2e * cache->k_scale;
+  a.scale_log2 = scale * kLog2e;
   a.o_scale = cache->v_scale;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;

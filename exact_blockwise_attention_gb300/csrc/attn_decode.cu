@@ -54,6 +54,8 @@
 // Scores, maxima, sums and outputs are fp32 throughout.
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "rope.cuh"
 
 namespace eba {
@@ -541,7 +543,9 @@ __global__ void __launch_bounds__(kBlock, 2)
       up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
-    if (i == 0) s_qs[n] = a.scale_log2 * down;
+    // The keys' scale times a power of two is exact. A factor beyond fp32's largest number
+    // stays finite, so that scores of 0 are 0.
+    if (i == 0) s_qs[n] = fminf(a.scale_log2 * (a.cache.k_scale * down), FLT_MAX);
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
       int ox, oy;

@@ -72,7 +72,7 @@ struct DecodeArgs {
   int per_item;  // K/V heads of an item: 1, or 4 neighbouring ones
   int heads;   // H_kv * blocks / per_item: items of a sequence
   int splits;  // > 0: clusters of that many CTAs, one per item; 0: one list of tiles
-  float scale_log2;  // scale * log2(e) * the keys' scale
+  float scale_log2;  // scale * log2(e)
   float o_scale;     // the values' scale
   __nv_bfloat16* o;  // [B, H, d]
   float* lse;        // [B, H]

@@ -395,6 +395,7 @@ size_t attn_decode_workspace_size(int B, int H, int H_kv, int d, int type, long 
  * attn_decode - attention of one new token per sequence over its cached keys.
  *   q [B, H, d] bf16, strides (sequence, head) in elements, multiples of 8; H
  *   a multiple of the cache's H_kv, query head h reads K/V head h / (H / H_kv).
+ *   scale: positive, scale * log2(e) finite in fp32.
  *   seq_lens [B]: the keys each sequence attends to, 0 included: O = 0 and
  *   lse = -inf, as for a sequence whose scores are all -inf.
  *   rope: q is rotated on the way and rounded to bf16, as attn_rope gives it

@@ -113,3 +113,15 @@ def test_queries_of_any_size_on_an_e4m3_cache(eba, path, power):
     assert torch.isfinite(q).all() and (q != 0).all()
     o, lse = eba.decode(p.on_gpu(eba), q.cuda(), p.gtable, p.glens)
     compare(o, lse, q, *p.contents(), 1 / math.sqrt(d), True)
+
+
+@pytest.mark.parametrize("e4m3,k_scale,scale,size", [
+    (True, 1.0, 2.0 ** 40, 2.0 ** 126), (True, 2.0 ** 100, 2.0 ** 100, 1.0), (False, 1.0, 2.0 ** 127, 0.0)], ids=str)
+def test_scores_of_zero_are_zero_at_any_scale(eba, e4m3, k_scale, scale, size):
+    # the factors of the scores, together or the scale alone, are beyond fp32's largest number
+    d, n = 64, 100
+    zero, v = torch.zeros(n, 1, d, dtype=torch.bfloat16), bf16(torch.Generator().manual_seed(1), n, 1, d)
+    p = Paged([n], 16, 1, d, e4m3=e4m3, k_scale=k_scale, data=[(zero, v)])
+    q = torch.full((1, 2, d), size, dtype=torch.bfloat16)
+    o, lse = eba.decode(p.on_gpu(eba), q.cuda(), p.gtable, p.glens, scale)
+    compare(o, lse, q, *p.contents(), scale, e4m3)
