@@ -231,6 +231,12 @@ __device__ __forceinline__ Place find_place(const AppendArgs& a, long long t) {
   return p;
 }
 
+// x times the rounded reciprocal of the scale, and e4m3 to nearest: the product is within
+// 2^-23 of the quotient, so next to a tie of two e4m3 numbers it may take the other one
+// (of the 65280 finite bf16 numbers, 30 at scale 0.03, none at 0.0125). The quotient costs
+// more than that is worth: 5 x 4999 tokens of 8 heads of 128 take 43 us by division, 33
+// by the product corrected with its remainder and 30 with the reciprocal as two floats,
+// instead of 27.6.
 __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv) {
   return make_uint2(pack_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
                     pack_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
         if (turns) turn16<INTERLEAVED>(x, y, t);
       }
       if constexpr (F8) {
-        // one rounding: fp32 straight to e4m3 (to nearest, saturating)
+        // no bf16 in between: fp32 straight to e4m3 (to nearest, saturating)
         unsigned char* p = static_cast<unsigned char*>(keys ? c.k : c.v) + to;
         const float inv = keys ? a.k_inv : a.v_inv;
         *reinterpret_cast<uint2*>(p + off_a) = pack8_e4m3(x, inv);

@@ -374,8 +374,9 @@ typedef struct {
  *   ATTN_ERR_PAGE.
  *   pos: device int32 [n_axes, T] with rows pos_stride apart; NULL (n_axes = 1
  *   only): a token's position is its place in its sequence.
- * bf16: rounded once. e4m3: value / scale, rounded to nearest once, saturating
- * at +-448 (NaN stays NaN). The new tokens' pages must not be shared: two
+ * bf16: rounded once. e4m3: the value (a rotated key in fp32) times the fp32
+ * reciprocal of the scale, an fp32 product, rounded to nearest, saturating at
+ * +-448 (NaN stays NaN). The new tokens' pages must not be shared: two
  * tokens that go to one slot leave a mixture of both there.
  */
 int attn_cache_append(const attn_cache_t* cache, const void* k, const long long* k_strides,

@@ -125,3 +125,21 @@ def test_scores_of_zero_are_zero_at_any_scale(eba, e4m3, k_scale, scale, size):
     q = torch.full((1, 2, d), size, dtype=torch.bfloat16)
     o, lse = eba.decode(p.on_gpu(eba), q.cuda(), p.gtable, p.glens, scale)
     compare(o, lse, q, *p.contents(), scale, e4m3)
+
+
+@pytest.mark.parametrize("scale", [0.03, 7.0, 0.3, 0.02, 1.0, 1.9999999, 3e-10, 2.0 ** -120, 2.0 ** 127])
+def test_append_to_e4m3_multiplies_by_the_reciprocal(eba, scale):
+    # every bf16 number that is one, bit for bit: times the fp32 reciprocal of the scale, rounded to e4m3
+    x = torch.arange(2 ** 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = torch.where(torch.isnan(x), torch.zeros_like(x), x).view(-1, 1, 64)
+    T = x.shape[0]
+    p = Paged([T], 32, 1, 64, e4m3=True, k_scale=scale, v_scale=scale)
+    cache = p.on_gpu(eba)
+    cu = torch.tensor([0, T], device="cuda", dtype=torch.int32)
+    eba.cache_append(cache, x.cuda(), x.flip(0).cuda(), p.gtable, p.glens, cu)
+    with np.errstate(over="ignore"):
+        exact = x.float().numpy() * (np.float32(1) / np.float32(scale))
+    want = torch.tensor(np.clip(exact, -448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    for pages, w in ((p.gk, want), (p.gv, want.flip(0))):
+        got = pages.cpu().view(torch.uint8)[torch.tensor(p.rows[0])].view(-1, 1, 64)[:T]
+        assert torch.equal(got, w), int((got != w).sum())
