@@ -295,6 +295,14 @@ int check_rope(const attn_rope_t& r, int d) {
   return ATTN_OK;
 }
 
+// x mod 1 in units of 2^-64, to nearest.
+unsigned long long fraction64(double x) {
+  x = std::ldexp(x - std::trunc(x), 32);  // exact, as is each step but the last
+  const double whole = std::trunc(x);
+  return (static_cast<unsigned long long>(static_cast<long long>(whole)) << 32) +
+         static_cast<unsigned long long>(std::llrint(std::ldexp(x - whole, 32)));
+}
+
 // Grid limits of the per-row kernels (a thread per 16 elements, heads in y).
 bool rows_fit(long long tokens, int d, long long heads) {
   return tokens * (d / 16) < (1ll << 37) && heads <= 65535;
@@ -859,11 +867,13 @@ int attn_rope_init(attn_rope_t* r, int n_pairs, int n_axes, const int* axis, con
   r->n_axes = n_axes;
   r->interleaved = interleaved != 0;
   for (int i = 0; i < n_pairs; ++i) {
-    constexpr double kTwoPi = 6.283185307179586476925;
-    double x = freq[i] / kTwoPi;
-    x -= std::floor(x);  // [0, 1], 1 by rounding of a tiny negative number
+    // The product with 1 / (2 pi) in two doubles, off by |freq| 2^-107: in one alone the
+    // table would hold 55 bits, which positions near 2^31 bring up to 2^-24 turns.
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+    const double x = freq[i] * kHi;
+    const double rest = std::fma(freq[i], kHi, -x) + freq[i] * kLo;
     r->axis[i] = static_cast<unsigned char>(axis[i]);
-    r->turns[i] = x < 1.0 ? static_cast<unsigned long long>(std::ldexp(x, 64)) : 0ull;
+    r->turns[i] = fraction64(x) + fraction64(rest);
   }
   return ATTN_OK;
 }

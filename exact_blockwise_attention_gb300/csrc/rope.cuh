@@ -5,10 +5,12 @@
 // position on the pair's axis and f the pair's frequency:
 //   (x, y) -> (x cos a - y sin a, x sin a + y cos a),
 // and its gradient by -a. Angles are kept as fixed point fractions of a turn:
-// f / (2 pi) mod 1 is held as a 64-bit integer (attn_rope_t.turns), the product
-// with the integer position wraps modulo a whole turn by itself, and its top 32
-// bits, read as a signed number, are the angle in [-1/2, 1/2) turns with an
-// error of 2^-32 turns. A float product would be off by p f 2^-24 radians
+// f / (2 pi) mod 1 is held as a 64-bit integer (attn_rope_t.turns, off by one unit
+// at most), the product with the integer position wraps modulo a whole turn by
+// itself, and its top 32 bits, read as a signed number, are the angle in
+// [-1/2, 1/2) turns, off by 2^31 units of 2^-64 and the bits cut off: less than
+// 2^-31 turns, whatever the position. What the sine and cosine take is that rounded
+// to fp32, 2^-26 turns. A float product would be off by p f 2^-24 radians
 // (6e-2 at position 10^6), and the double product that avoids this costs far
 // more here (FP64 runs at about 1/60 of the FP32 rate) than the three integer
 // multiply-adds it takes.

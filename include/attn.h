@@ -302,7 +302,7 @@ typedef struct {
   int n_axes;       /* 1 .. ATTN_MAX_AXES */
   int interleaved;
   unsigned char axis[ATTN_MAX_PAIRS];
-  unsigned long long turns[ATTN_MAX_PAIRS]; /* freq / (2 pi) mod 1, in units of 2^-64 turns */
+  unsigned long long turns[ATTN_MAX_PAIRS]; /* freq / (2 pi) mod 1, in units of 2^-64 turns, to 1 */
 } attn_rope_t;
 
 /*
@@ -322,8 +322,9 @@ int attn_rope_init(attn_rope_t* r, int n_pairs, int n_axes, const int* axis, con
  *   shares the positions among the batch. Any int32 value.
  *   inverse: rotate by the negative angles. That is the gradient: d(q) =
  *   inverse rotation of d(q_out).
- * The angle is exact to 2^-32 turns at every position; the rotation runs in
- * fp32 and is rounded once. Outputs must not overlap inputs.
+ * The angle is formed to 2^-31 turns at every position (for |freq| up to 2^40)
+ * and rounded to fp32 (2^-26 turns) for its sine and cosine; the rotation runs
+ * in fp32 and is rounded once. Outputs must not overlap inputs.
  */
 int attn_rope(const attn_rope_t* r, const void* q, const long long* q_strides, void* q_out,
               const long long* q_out_strides, const void* k, const long long* k_strides,

@@ -2,6 +2,8 @@
 exact bits of a rotation's table, arguments of another type, gradients that are not
 asked for."""
 import ctypes
+import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -15,6 +17,48 @@ def eba():
     import exact_blockwise_attention_gb300 as m
 
     return m
+
+
+def two_pi():
+    """2 pi to 1300 bits: 8 (4 atan(1/5) - atan(1/239)), the arctangents' series in integers."""
+    one = 1 << 1330
+
+    def atan_inverse(n):
+        term, total, k = one // n, 0, 0
+        while term:
+            total += (-1) ** k * (term // (2 * k + 1))
+            term //= n * n
+            k += 1
+        return total
+
+    return Fraction(8 * (4 * atan_inverse(5) - atan_inverse(239)), one)
+
+
+@pytest.mark.parametrize("freq", [
+    [1.0, 0.5, -1.0, 0.0, 2 * math.pi, 100.0, 1e-12, -1e-30],
+    [10000.0 ** (-i / 64) for i in range(64)], [500000.0 ** (-i / 22) for i in range(24)],
+    [-3.7, 12345.678, -1e6, 1e9, -1e15, 1e22, 5e-324, -5e-324]], ids=["mixed", "text", "axis", "far"])
+def test_rope_table_holds_all_its_bits(eba, freq):
+    # a step is 2^-64 turns; the two-part 1 / (2 pi) adds |f| 2^-107 turns
+    table = eba.Rope((len(freq),), frequencies=freq)._struct.turns
+    turn = two_pi()
+    for f, t in zip(freq, table):
+        exact = Fraction(f) / turn * 2 ** 64
+        off = (t - exact) % 2 ** 64
+        off = min(off, 2 ** 64 - off)
+        assert off <= 1 + Fraction(abs(f)) / 2 ** 43, (f, float(off))
+
+
+def test_far_positions_are_as_exact_as_near_ones(eba):
+    # the fixed-point angle, as the kernels form it, within 2^-31 turns at every position
+    freq = [10000.0 ** (-i / 64) for i in range(64)]
+    table = eba.Rope((64,), frequencies=freq)._struct.turns
+    turn = two_pi()
+    for p in (1, 12345, 2 ** 31 - 1, -2 ** 31):
+        for f, t in zip(freq, table):
+            angle = (p * t) % 2 ** 64 >> 32
+            off = (angle - Fraction(f) * p / turn * 2 ** 32) % 2 ** 32
+            assert min(off, 2 ** 32 - off) <= 2, (p, f)
 
 
 def test_scales_that_no_factor_holds_are_refused(eba):
