@@ -793,7 +793,8 @@ class PagedCache:
             if rope.n_axes != 1:
                 raise ValueError("positions are needed for a rope with several axes")
             return rope._struct, None, 0
-        return rope._struct, positions.data_ptr(), rope._positions(positions, self.device, (tokens,))
+        stride = rope._positions(positions, self.device, (tokens,))
+        return rope._struct, positions.data_ptr(), stride
 
 
 def cache_append(cache, k, v, page_table, seq_lens, cu_new=None, rope=None, positions=None):

@@ -61,6 +61,14 @@ def test_far_positions_are_as_exact_as_near_ones(eba):
             assert min(off, 2 ** 32 - off) <= 2, (p, f)
 
 
+def test_positions_that_are_no_tensor_are_refused(eba):
+    pages = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    cache, plan = eba.PagedCache(pages, pages.clone()), eba.Rope((32,))
+    for positions in ([1, 2, 3], 7, "123"):
+        with pytest.raises(ValueError):
+            cache._turn(plan, positions, 3)
+
+
 def test_scales_that_no_factor_holds_are_refused(eba):
     c, L, at = eba._CacheStruct(), eba.lib(), 1 << 20  # an address that is never used
     c.k = c.v = at
