@@ -691,6 +691,9 @@ class _Rotation(torch.autograd.Function):
         # (under create_graph the gradient is a rotation with a gradient of its own)
         turn = _Rotation.apply if torch.is_grad_enabled() else _rope
         plan, back = ctx.plan, not ctx.inverse
+        # (an output's gradient comes also where its input wants none)
+        need_q, need_k = ctx.needs_input_grad[:2]
+        dq, dk = dq if need_q else None, dk if need_k else None
         try:
             if dq is not None:
                 dq, dk = turn(dq, dk, positions, plan, back)

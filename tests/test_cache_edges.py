@@ -77,3 +77,23 @@ def test_scales_that_no_factor_holds_are_refused(eba):
     strides = (ctypes.c_longlong * 2)(128, 64)
     for c.type in (0, 1):
         assert L.attn_decode(c, at, strides, at, 4, 4, at, 3, 2, 3e38, None, None, 0, at, at, at, 1 << 30, None) == 1
+
+
+@pytest.mark.parametrize("again", [False, True], ids=["once", "create_graph"])
+@pytest.mark.parametrize("trained", ["q", "k", "qk"])
+def test_gradients_nobody_asks_for_are_not_computed(eba, monkeypatch, trained, again):
+    calls = []
+
+    def turn(q, k, positions, plan, inverse):
+        calls.append((inverse, q, k))
+        return q * 1.0, None if k is None else k * 1.0
+
+    monkeypatch.setattr(eba, "_rope", turn)
+    q, k = torch.ones(3, 2, 4, requires_grad="q" in trained), torch.ones(3, 1, 4, requires_grad="k" in trained)
+    qo, ko = eba.rope(q, k, torch.arange(3), None)
+    inputs = [x for x in (q, k) if x.requires_grad]
+    grads = torch.autograd.grad((qo * ko).sum(), inputs, create_graph=again)
+    assert [g.shape for g in grads] == [x.shape for x in inputs]
+    inverse, dq, dk = calls[1]
+    assert inverse and len(calls) == 2
+    assert dq.shape == inputs[0].shape and (dk is None) == (trained != "qk")
