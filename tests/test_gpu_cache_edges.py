@@ -1,6 +1,7 @@
 """The rotation, the paged cache and the decode where they are most easily wrong:
 absent pages, special values and far-out sizes on every path of the decode, exact
 roundings of an e4m3 cache, and several threads at once."""
+import concurrent.futures
 import math
 
 import numpy as np
@@ -143,3 +144,163 @@ def test_append_to_e4m3_multiplies_by_the_reciprocal(eba, scale):
     for pages, w in ((p.gk, want), (p.gv, want.flip(0))):
         got = pages.cpu().view(torch.uint8)[torch.tensor(p.rows[0])].view(-1, 1, 64)[:T]
         assert torch.equal(got, w), int((got != w).sum())
+
+
+SPECIAL_PATHS = {
+    "cluster": (1, 300, 8, 64, 16),
+    "few_parts": (4, 3000, 8, 128, 16),
+    "many_parts": (1, 9000, 8, 128, 20),
+    "four_heads": (8, 2000, 16, 64, 16),
+    "four_heads_many_parts": (4, 9000, 16, 64, 48),
+}
+
+
+@pytest.mark.parametrize("group", [2, 9])
+@pytest.mark.parametrize("path", SPECIAL_PATHS)
+def test_special_values_on_every_path(eba, path, group):
+    # per K/V head: 0 all scores -inf (no weight at all: O = 0), 1 one NaN key, 2 one
+    # +inf score, 3 keys of score -inf among others, 4 an infinite value, 5 -inf scores
+    # for the first two thirds (parts without weight), 6 one NaN value; the others plain
+    B, n, hk, d, page = SPECIAL_PATHS[path]
+    H, at = group * hk, n // 2
+    g = torch.Generator().manual_seed(n + group)
+    data = []
+    for _ in range(B):
+        k, v = bf16(g, n, hk, d), bf16(g, n, hk, d)
+        k[:, 0] = -math.inf
+        k[at, 1] = math.nan
+        k[at + 1, 2] = math.inf
+        k[at + 2::7, 3] = -math.inf
+        v[at + 3, 4] = math.inf
+        k[:2 * n // 3, 5] = -math.inf
+        v[at + 4, 6, 3] = math.nan
+        data.append((k, v))
+    q = torch.rand(B, H, d, generator=g).add(0.5).to(torch.bfloat16)  # positive
+    p = Paged([n] * B, page, hk, d, data=data)
+    o, lse = eba.decode(p.on_gpu(eba), q.cuda(), p.gtable, p.glens)
+    o4, l4 = np64(o).reshape(B, hk, group, d), np64(lse).reshape(B, hk, group)
+    assert (o4[:, 0] == 0).all() and np.isneginf(l4[:, 0]).all()
+    assert np.isnan(o4[:, 1:3]).all() and np.isnan(l4[:, 1:3]).all()
+    assert np.isposinf(o4[:, 4]).all() and np.isfinite(l4[:, 4]).all()
+    assert np.isnan(o4[:, 6, :, 3]).all() and np.isfinite(l4[:, 6]).all()
+    keys, values = p.contents()
+    dropped = np.arange(n) >= at + 2
+    dropped &= (np.arange(n) - at - 2) % 7 == 0
+    for head, keep in ((3, ~dropped), (5, np.arange(n) >= 2 * n // 3), (7, np.ones(n, bool)), (4, None), (6, None)):
+        mine = slice(head * group, (head + 1) * group)
+        ks, vs = ([x[:, head:head + 1] if keep is None else x[keep][:, head:head + 1] for x in y]
+                  for y in (keys, values))
+        if keep is None:  # the scores do not know of the value; the other columns neither
+            vs = [np.where(np.isfinite(x), x, 0) for x in vs]
+            good = np.isfinite(o4[0, head, 0])
+            ro, rl = oracle.decode(np64(q)[:, mine], ks, vs, 1 / math.sqrt(d))
+            to, tl = decode_tolerances(np64(q)[:, mine], ks, vs, 1 / math.sqrt(d), ro, rl, False)
+            assert (np.abs(l4[:, head] - rl) <= tl).all()
+            assert (np.abs(o4[:, head] - ro) <= to)[..., good].all()
+        else:
+            compare(o[:, mine], lse[:, mine], q[:, mine], ks, vs, 1 / math.sqrt(d), False)
+
+
+@pytest.mark.parametrize("path", E4M3_PATHS)
+def test_special_values_on_an_e4m3_cache(eba, path):
+    # e4m3 has NaN and no infinities: infinite scores come from the query. Keys' first
+    # elements are positive. K/V head 0: plain; 1: one NaN key; 2 (where there are so
+    # many): one NaN value. Query heads of each: 0 an element of -inf (all scores -inf:
+    # O = 0), 1 one of +inf (NaN), 2 (where there is one) plain.
+    B, n, H, hk, d, page = E4M3_PATHS[path]
+    group, at = H // hk, n // 2
+    g = torch.Generator().manual_seed(n)
+    data = []
+    for _ in range(B):
+        k, v = bf16(g, n, hk, d), bf16(g, n, hk, d)
+        k[..., 0] = k[..., 0].abs() + 0.5
+        k[at, 1, 5] = math.nan
+        if hk > 2:
+            v[at, 2, 7] = math.nan
+        data.append((k, v))
+    p = Paged([n] * B, page, hk, d, e4m3=True, data=data)
+    q = bf16(g, B, hk, group, d)
+    q[:, :, 0, 0], q[:, :, 1, 0] = -math.inf, math.inf
+    q = q.view(B, H, d)
+    o, lse = eba.decode(p.on_gpu(eba), q.cuda(), p.gtable, p.glens)
+    o4, l4 = np64(o).reshape(B, hk, group, d), np64(lse).reshape(B, hk, group)
+    plain = [h for h in range(hk) if h not in (1, 2)]
+    assert (o4[:, plain, 0] == 0).all() and np.isneginf(l4[:, plain, 0]).all()
+    assert np.isnan(o4[:, plain, 1]).all() and np.isnan(l4[:, plain, 1]).all()
+    assert np.isnan(o4[:, 1]).all() and np.isnan(l4[:, 1]).all()
+    keys, values = p.contents()
+    if hk > 2 and group > 2:
+        assert np.isnan(o4[:, 2, 2:, 7]).all() and np.isfinite(l4[:, 2, 2:]).all()
+    for head in plain[:2]:
+        if group > 2:
+            mine = slice(head * group + 2, (head + 1) * group)
+            one = slice(head, head + 1)
+            compare(o[:, mine], lse[:, mine], q[:, mine], [x[:, one] for x in keys], [x[:, one] for x in values],
+                    1 / math.sqrt(d), True)
+
+
+@pytest.mark.parametrize("lens,H,hk,e4m3", [([333], 32, 8, False), ([40, 0, 700, 5] * 16, 8, 2, False),
+                                            ([900, 3], 32, 2, True)], ids=["one", "many", "e4m3"])
+def test_a_table_far_wider_than_the_lengths(eba, lens, H, hk, e4m3):
+    # as a captured call holds it for the longest sequence it may ever see: another way of
+    # cutting up the work, the same attention
+    p = Paged(lens, 16, hk, 128, e4m3=e4m3, seed=7, k_scale=0.03 if e4m3 else 1.0)
+    cache = p.on_gpu(eba)
+    q = bf16(torch.Generator().manual_seed(12), len(lens), H, 128)
+    wide = torch.full((len(lens), 8192), -1, dtype=torch.int32)
+    wide[:, :p.table.shape[1]] = p.table
+    for table in (p.gtable, wide.cuda()):
+        o, lse = eba.decode(cache, q.cuda(), table, p.glens)
+        compare(o, lse, q, *p.contents(), 1 / math.sqrt(128), e4m3)
+
+
+def test_threads_at_once(eba):
+    # each with a stream of its own, one plan and one read-only cache for all of them
+    plan, n = eba.Rope((64,)), 4
+    shared = Paged([2500, 100], 16, 2, 128, seed=50)
+    common = shared.on_gpu(eba)
+    own = [Paged([900 + 50 * i, 64], 16, 2, 128, seed=51 + i) for i in range(n)]
+    caches = [p.on_gpu(eba) for p in own]
+    pos = torch.tensor([5, 6], device="cuda", dtype=torch.int32)
+    start = [bf16(torch.Generator().manual_seed(60 + i), 2, 4, 128).cuda() for i in range(n)]
+    torch.cuda.synchronize()
+
+    def run(i):
+        outs, x = [], start[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(25):
+                x, _ = eba.rope_fwd(x, None, pos, plan)
+                eba.cache_append(caches[i], x[:, :2], x[:, 2:], own[i].gtable, own[i].glens, rope=plan)
+                outs.append(eba.decode(caches[i], x, own[i].gtable, own[i].glens, rope=plan)[0])
+                outs.append(eba.decode(common, x, shared.gtable, shared.glens)[0])
+            torch.cuda.current_stream().synchronize()
+        return torch.stack(outs)
+
+    alone = [run(i) for i in range(n)]
+    with concurrent.futures.ThreadPoolExecutor(n) as pool:
+        for a, b in zip(alone, pool.map(run, range(n))):
+            assert torch.equal(a, b)
+
+
+def test_rotation_refuses_forward_mode_and_vmap(eba):
+    plan, pos = eba.Rope((32,)), torch.arange(6, device="cuda", dtype=torch.int32)
+    x = bf16(torch.Generator().manual_seed(1), 3, 6, 2, 64).cuda()
+    with pytest.raises(RuntimeError):
+        torch.func.vmap(lambda y: eba.rope(y, None, pos, plan)[0])(x)
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda y: eba.rope(y, None, pos, plan)[0], (x[0],), (x[1],))
+
+
+def test_one_of_two_inputs_trained(eba):
+    # the other's gradient is not asked for: the trained one's is as with both
+    g = torch.Generator().manual_seed(14)
+    plan, pos = eba.Rope((8, 12, 12)), torch.randint(0, 99, (3, 20), generator=g).to(torch.int32).cuda()
+    q, k = bf16(g, 20, 4, 64).cuda(), bf16(g, 20, 2, 64).cuda()
+    gq, gk = bf16(g, 20, 4, 64).cuda(), bf16(g, 20, 2, 64).cuda()
+    want = eba.rope_bwd(gq, gk, pos, plan)
+    for i, trained in enumerate((q, k)):
+        trained.requires_grad_()
+        outs = eba.rope(q, k, pos, plan)
+        got, = torch.autograd.grad(outs, trained, (gq, gk))
+        trained.requires_grad_(False)
+        assert torch.equal(got, want[i])
