@@ -368,9 +368,13 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
   // two and no workspace, but only as even as the lengths, and with less than a full
   // wave not all SMs. Measured, cluster against list (us; longest sequence, others
   // random down to an eighth): 64 CTAs at 2 tiles each 6.8 / 7.0, at 4 8.2 / 7.9
-  // (1 x 8 heads of 128, bf16; the host needs 16 / 19 for a call), at 8 11.2 / 8.7;
+  // (1 x 8 heads of 128, bf16; the 0.3 us are lost in a replayed graph, but the host
+  // needs 18 / 24 for a call), at 8 11.2 / 8.7;
   // 256 CTAs at 8 tiles 12.8 / 14.1 (16 x 8 heads) and
-  // 15.9 / 16.4 (e4m3), at 16 20.1 / 20.2 and 23.5 / 20.4.
+  // 15.9 / 16.4 (e4m3), at 16 20.1 / 20.2 and 23.5 / 20.4. The table decides, not the
+  // lengths, which the host does not know: with a table of 131072 keys instead of a tight
+  // one (list against cluster) 1 x 333 keys take 7.6 / 6.1, 16 x up to 500 11.3 / 8.7,
+  // 4 x up to 2000 of 2 heads 8.3 / 7.9.
   constexpr int wave = eba::kDecodeCtas;
   int splits = 1;
   while (splits < 8 && splits < item_tiles && items * splits * 2 <= wave) splits *= 2;

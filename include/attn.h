@@ -396,7 +396,8 @@ size_t attn_decode_workspace_size(int B, int H, int H_kv, int d, int type, long 
 /*
  * attn_decode - attention of one new token per sequence over its cached keys.
  *   q [B, H, d] bf16, strides (sequence, head) in elements, multiples of 8; H
- *   a multiple of the cache's H_kv, query head h reads K/V head h / (H / H_kv).
+ *   a multiple of the cache's H_kv, query head h reads K/V head h / (H / H_kv);
+ *   more than 16 heads on one are worked through 16 at a time.
  *   scale: positive, scale * log2(e) finite in fp32.
  *   seq_lens [B]: the keys each sequence attends to, 0 included: O = 0 and
  *   lse = -inf, as for a sequence whose scores are all -inf.
