@@ -872,7 +872,7 @@ int attn_rope_init(attn_rope_t* r, int n_pairs, int n_axes, const int* axis, con
   r->interleaved = interleaved != 0;
   for (int i = 0; i < n_pairs; ++i) {
     // The product with 1 / (2 pi) in two doubles, off by |freq| 2^-107: in one alone the
-    // table would hold 55 bits, which positions near 2^31 bring up to 2^-24 turns.
+    // table would hold 55 bits, which positions near 2^31 bring up to 2^-25 turns.
     constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
     const double x = freq[i] * kHi;
     const double rest = std::fma(freq[i], kHi, -x) + freq[i] * kLo;
