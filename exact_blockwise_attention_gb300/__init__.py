@@ -22,7 +22,12 @@ Entry points (same names as the C ABI):
   rope(q, k, positions, plan)                   -> (q, k)   (autograd-aware)
   cache_append(cache, k, v, page_table, seq_lens, cu_new=None, rope=None, positions=None)
   decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None) -> (o, lse)
-with the handles Rope (a rotation: axes, frequencies, pairs) and PagedCache (key and value pages).
+  pages_release(pool, page_table, first, last), pages_reserve(pool, page_table, seq_lens, new_lens),
+  pages_fork(pool, page_table, seq_lens, src, dst) -> (from_pages, to_pages)   page tables kept on the GPU
+  cache_copy(cache, from_pages, to_pages)       whole pages within a cache
+  cache_gather(cache, page_table, places, cu, to_table=None, to_start=None)   chosen tokens together
+with the handles Rope (a rotation: axes, frequencies, pairs), PagedCache (key and value pages) and
+PagePool (which pages are free).
 Tensors are CUDA, contiguous, [B, H, L, d] with d in {64, 128}; q, k, v, o,
 do are bfloat16, lse and partials float32. The default scale is 1/sqrt(d).
 fwd, bwd and attention also take k, v with fewer heads H_kv dividing H
@@ -48,7 +53,8 @@ __all__ = [
     "bwd_workspace_size", "poll_device_status", "set_wait_limit_ns", "status_string",
     "MAX_CHUNKS", "MAX_SEQS", "fwd_varlen", "bwd_varlen", "bwd_varlen_workspace_size", "fwd_fp8",
     "attention_varlen", "Rope", "rope_fwd", "rope_bwd", "rope", "PagedCache", "cache_append",
-    "decode", "decode_workspace_size",
+    "decode", "decode_workspace_size", "PagePool", "pages_release", "pages_fork", "pages_reserve",
+    "cache_copy", "cache_gather",
 ]
 
 ATTN_OK = 0
@@ -72,6 +78,12 @@ class _CacheStruct(ctypes.Structure):
                 ("n_pages", ctypes.c_longlong), ("page_size", ctypes.c_int),
                 ("H_kv", ctypes.c_int), ("d", ctypes.c_int), ("type", ctypes.c_int),
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class _PoolStruct(ctypes.Structure):
+    """attn_pool_t"""
+    _fields_ = [("refs", ctypes.c_void_p), ("scratch", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int)]
 
 
 class AttnError(RuntimeError):
@@ -125,7 +137,15 @@ def _declare(L):
     L.attn_decode_workspace_size.argtypes = [i, i, i, i, i, ll]
     L.attn_decode_workspace_size.restype = sz
     L.attn_decode.argtypes = [cp, vp, lp, vp, ll, i, vp, i, i, f, rp, vp, ll, vp, vp, vp, sz, vp]
-    for name in ("attn_rope_init", "attn_rope", "attn_cache_append", "attn_decode"):
+    pp = ctypes.POINTER(_PoolStruct)
+    L.attn_pages_release.argtypes = [pp, vp, ll, i, vp, vp, i, vp]
+    L.attn_pages_fork.argtypes = [pp, vp, ll, i, vp, i, vp, vp, i, vp, vp, vp]
+    L.attn_pages_reserve.argtypes = [pp, vp, ll, i, vp, vp, i, vp]
+    L.attn_cache_copy.argtypes = [cp, vp, vp, i, vp]
+    L.attn_cache_gather.argtypes = [cp, vp, ll, i, i, vp, vp, i, vp, ll, i, vp, vp]
+    for name in ("attn_rope_init", "attn_rope", "attn_cache_append", "attn_decode",
+                 "attn_pages_release", "attn_pages_fork", "attn_pages_reserve", "attn_cache_copy",
+                 "attn_cache_gather"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("attn_fwd", "attn_bwd", "attn_partial_fwd", "attn_split_fwd", "attn_merge",
                  "attn_poll_device_status", "attn_fwd_varlen", "attn_bwd_varlen", "attn_fwd_gqa",
@@ -923,3 +943,179 @@ def _decode_layout(cache, q, page_table, seq_lens, rope, positions):
     stride = cache._turn(rope, positions, B)[2]
     return (_Strides2(*sq), page_table.stride(0), page_table.shape[1], B, H, d, stride,
             decode_workspace_size(cache, B, H, page_table.shape[1]))
+
+
+# ---------------------------------------------------------------------------
+# The cache's pages
+# ---------------------------------------------------------------------------
+
+class PagePool:
+    """The pages of a cache (or of several that go by one page table, as a model's
+    layers do) and how many table entries name each: refs, int32 [n_pages] on the
+    device, 0 for a free page. A fresh pool's are all 0; the tensor stays the
+    caller's, and pages_release, pages_fork and pages_reserve keep it. They take the
+    lowest free pages, in order of the sequences, so what they give depends on the
+    counts and tables alone. Calls on one pool run one after the other."""
+
+    def __init__(self, refs, page_size):
+        if not isinstance(refs, torch.Tensor) or refs.dtype != torch.int32 or refs.dim() != 1:
+            raise ValueError("refs must be an int32 [n_pages] tensor")
+        if refs.numel() < 1 or refs.numel() > 1 << 30 or not refs.is_contiguous():
+            raise ValueError("refs must be contiguous, for 1 to 2^30 pages")
+        page_size = int(page_size)
+        if not 1 <= page_size < 1 << 31:
+            raise ValueError("page_size must be positive")
+        self.refs, self.page_size, self.n_pages, self.device = refs, page_size, refs.numel(), refs.device
+        self._scratch = torch.empty_like(refs)
+        self._struct = _PoolStruct(0, self._scratch.data_ptr(), self.n_pages, page_size)
+
+    def _at(self):
+        if self.device.type != "cuda":
+            raise ValueError("the pool must be on a CUDA device")
+        self._struct.refs = self.refs.data_ptr()
+        return self._struct
+
+
+_POOL_LAYOUTS = _Layouts()
+
+
+def _pool_layout(pool, page_table, lengths, pairs):
+    """Checks a pool call's arguments: the table's row stride and columns, the
+    sequences, the pairs."""
+    if not isinstance(pool, PagePool):
+        raise ValueError("pool must be a PagePool")
+    _int32(page_table, "page_table", pool.device, 2)
+    n, wide = page_table.shape
+    if n < 1 or wide < 1 or n * wide >= 1 << 31:
+        raise ValueError(f"page_table must be [n_seqs, max_pages], got {tuple(page_table.shape)}")
+    if n > 1 and page_table.stride(0) < wide:
+        raise ValueError("page_table's rows must not overlap")
+    for name, t in lengths:
+        _int32(t, name, pool.device, 1)
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must hold {n} sequences, got {t.shape[0]}")
+    for name, t in pairs:
+        _int32(t, name, pool.device, 1)
+        if t.shape != pairs[0][1].shape:
+            raise ValueError("src and dst must have the same length")
+    return page_table.stride(0), wide, n
+
+
+def _pool_call(pool, page_table, lengths, pairs=()):
+    try:
+        key = (pool.device, _form(page_table), *((name, _form(t)) for name, t in (*lengths, *pairs)))
+        lay = _POOL_LAYOUTS.get(key)
+    except AttributeError:
+        lay = key = None
+    if lay is None:
+        lay = _pool_layout(pool, page_table, lengths, pairs)
+        _POOL_LAYOUTS.add(key, lay)
+    return lay
+
+
+def pages_release(pool, page_table, first, last):
+    """Give back the pages that lie wholly within the keys first[b] .. last[b] - 1 of
+    each sequence (int32 [n_seqs] on the device): their entries become -1. A page is
+    free once no entry names it."""
+    row, wide, n = _pool_call(pool, page_table, (("first", first), ("last", last)))
+    _launch(pool.device, lib().attn_pages_release, pool._at(), page_table.data_ptr(), row, wide,
+            first.data_ptr(), last.data_ptr(), n)
+
+
+def pages_fork(pool, page_table, seq_lens, src, dst):
+    """Sequence dst[i] becomes a copy of sequence src[i] (int32 [n] on the device), its
+    length too: they share the pages that src fills, and the last one, where it is
+    not full, dst has of its own. Returns the pages to copy for that, (from_pages,
+    to_pages), for cache_copy of each cache that goes by this table; -1 where there
+    is nothing to copy. dst's former pages are not given back here. Pairs out of
+    range, or whose dst is used twice or forked from, are left out and reported by
+    poll_device_status, as is a pool without a free page."""
+    row, wide, n = _pool_call(pool, page_table, (("seq_lens", seq_lens),), (("src", src), ("dst", dst)))
+    old, new = torch.empty_like(src), torch.empty_like(src)
+    if src.shape[0]:
+        _launch(pool.device, lib().attn_pages_fork, pool._at(), page_table.data_ptr(), row, wide,
+                seq_lens.data_ptr(), n, src.data_ptr(), dst.data_ptr(), src.shape[0], old.data_ptr(),
+                new.data_ptr())
+    return old, new
+
+
+def pages_reserve(pool, page_table, seq_lens, new_lens):
+    """Room for each sequence to grow from seq_lens[b] to new_lens[b] keys (int32
+    [n_seqs] on the device): the entries for them that hold no page get a free one.
+    An entry for which none is left stays -1, and poll_device_status reports it."""
+    row, wide, n = _pool_call(pool, page_table, (("seq_lens", seq_lens), ("new_lens", new_lens)))
+    _launch(pool.device, lib().attn_pages_reserve, pool._at(), page_table.data_ptr(), row, wide,
+            seq_lens.data_ptr(), new_lens.data_ptr(), n)
+
+
+def cache_copy(cache, from_pages, to_pages):
+    """Copy the cache's pages from_pages[i] to pages to_pages[i], keys and values
+    (int32 [n] on the device; a pair with an index below 0 is skipped). No page may be
+    written twice, or both written and read."""
+    if not isinstance(cache, PagedCache):
+        raise ValueError("cache must be a PagedCache")
+    _int32(from_pages, "from_pages", cache.device, 1)
+    _int32(to_pages, "to_pages", cache.device, 1)
+    n = from_pages.shape[0]
+    if to_pages.shape[0] != n:
+        raise ValueError("from_pages and to_pages must have the same length")
+    if n:
+        _launch(cache.device, lib().attn_cache_copy, cache._at(), from_pages.data_ptr(),
+                to_pages.data_ptr(), n)
+
+
+_GATHER_LAYOUTS = _Layouts()
+
+
+def cache_gather(cache, page_table, places, cu, to_table=None, to_start=None):
+    """Move chosen tokens' keys and values together: sequence b's tokens at places[cu[b]]
+    .. places[cu[b + 1] - 1] go to its places to_start[b], to_start[b] + 1, .. (without
+    to_start 0, 1, ..). places int32 [T], cu int32 [n_seqs + 1] and to_start int32
+    [n_seqs] on the device.
+
+    Without to_table within the sequence's own pages, as the accepted tokens of a
+    draft move up behind their context: no token may move to a later place. With
+    to_table, int32 [n_seqs, to_max_pages], into the pages of that table, none of
+    which this call reads. What is out of range or order is left out and reported by
+    poll_device_status. The pages written must not be shared."""
+    try:
+        key = (cache._key, _form(page_table), _form(places), _form(cu), _form(to_table), _form(to_start))
+        lay = _GATHER_LAYOUTS.get(key)
+    except AttributeError:
+        lay = key = None
+    if lay is None:
+        lay = _gather_layout(cache, page_table, places, cu, to_table, to_start)
+        _GATHER_LAYOUTS.add(key, lay)
+    row, wide, n, T, to_row, to_wide = lay
+    if T:
+        _launch(cache.device, lib().attn_cache_gather, cache._at(), page_table.data_ptr(), row, wide, n,
+                places.data_ptr(), cu.data_ptr(), T, None if to_table is None else to_table.data_ptr(),
+                to_row, to_wide, None if to_start is None else to_start.data_ptr())
+
+
+def _gather_layout(cache, page_table, places, cu, to_table, to_start):
+    """Checks a gather's arguments: the tables' row strides and columns, the sequences
+    and the tokens."""
+    if not isinstance(cache, PagedCache):
+        raise ValueError("cache must be a PagedCache")
+    _int32(page_table, "page_table", cache.device, 2)
+    n, wide = page_table.shape
+    if n < 1 or wide < 1:
+        raise ValueError(f"page_table must be [n_seqs, max_pages], got {tuple(page_table.shape)}")
+    _int32(places, "places", cache.device, 1)
+    if places.shape[0] > 1 << 30:
+        raise ValueError("places must hold at most 2^30 tokens")
+    _int32(cu, "cu", cache.device, 1)
+    if cu.shape[0] != n + 1:
+        raise ValueError(f"cu must have {n + 1} entries, got {cu.shape[0]}")
+    to_row = to_wide = 0
+    if to_table is not None:
+        _int32(to_table, "to_table", cache.device, 2)
+        if to_table.shape[0] != n or to_table.shape[1] < 1:
+            raise ValueError(f"to_table must be [{n}, to_max_pages], got {tuple(to_table.shape)}")
+        to_row, to_wide = to_table.stride(0), to_table.shape[1]
+    if to_start is not None:
+        _int32(to_start, "to_start", cache.device, 1)
+        if to_start.shape[0] != n:
+            raise ValueError(f"to_start must hold {n} sequences, got {to_start.shape[0]}")
+    return page_table.stride(0), wide, n, places.shape[0], to_row, to_wide

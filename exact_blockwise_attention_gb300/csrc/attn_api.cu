@@ -14,6 +14,7 @@
 #include "attn.h"
 #include "cache_kernels.h"
 #include "kernels.h"
+#include "pages_kernels.h"
 
 namespace {
 
@@ -333,6 +334,31 @@ int check_cache(const attn_cache_t* c) {
 int check_table(const int* table, long long stride, int max_pages, const int* lens, int n_seqs) {
   if (!table || !lens || max_pages < 1 || n_seqs < 1 || stride < 0) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
+}
+
+int check_pool(const attn_pool_t* p, const int* table, long long stride, int max_pages, int n_seqs) {
+  if (!p || !p->refs || !p->scratch || p->n_pages < 1 || p->n_pages > (1 << 30) || p->page_size < 1)
+    return ATTN_ERR_INVALID_ARG;
+  if (!table || max_pages < 1 || n_seqs < 1 || stride < 0) return ATTN_ERR_INVALID_ARG;
+  if (n_seqs > 1 && stride < max_pages) return ATTN_ERR_INVALID_ARG;  // the rows are written
+  if (static_cast<long long>(n_seqs) * max_pages >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+// A cache's rows as bytes, for the copies.
+template <typename Args>
+void cache_bytes(Args& a, const attn_cache_t& c) {
+  const int esz = c.type == ATTN_CACHE_E4M3 ? 1 : 2;
+  a.k = static_cast<unsigned char*>(c.k);
+  a.v = static_cast<unsigned char*>(c.v);
+  for (int i = 0; i < 3; ++i) {
+    a.k_strides[i] = c.k_strides[i] * esz;
+    a.v_strides[i] = c.v_strides[i] * esz;
+  }
+  a.n_pages = static_cast<int>(c.n_pages);
+  a.page_size = c.page_size;
+  a.H_kv = c.H_kv;
+  a.row = c.d * esz;
 }
 
 // How a decode call is cut up, from what the host knows: the sizes and the keys
@@ -1047,6 +1073,111 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
   if (rope) a.rope = *rope;
   a.limit_ns = g_wait_limit_ns.load();
   cudaError_t e = eba::launch_decode(a, p.ctas, p.join, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+int attn_pages_release(const attn_pool_t* pool, int* page_table, long long table_stride,
+                       int max_pages, const int* first, const int* last, int n_seqs, void* stream) {
+  int s = check_pool(pool, page_table, table_stride, max_pages, n_seqs);
+  if (s != ATTN_OK) return s;
+  if (!first || !last) return ATTN_ERR_INVALID_ARG;
+  int* status = status_word_ptr();
+  if (!status) return ATTN_ERR_CUDA;
+  const eba::ReleaseArgs a{*pool, page_table, table_stride, max_pages, n_seqs, first, last, status};
+  cudaError_t e = eba::launch_release(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+int attn_pages_fork(const attn_pool_t* pool, int* page_table, long long table_stride, int max_pages,
+                    int* seq_lens, int n_seqs, const int* src, const int* dst, int n, int* from,
+                    int* to, void* stream) {
+  int s = check_pool(pool, page_table, table_stride, max_pages, n_seqs);
+  if (s != ATTN_OK) return s;
+  if (!seq_lens || !src || !dst || !from || !to || n < 1) return ATTN_ERR_INVALID_ARG;
+  int* status = status_word_ptr();
+  if (!status) return ATTN_ERR_CUDA;
+  eba::PoolArgs a{};
+  a.pool = *pool;
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.n_seqs = n_seqs;
+  a.n = n;
+  a.lens = seq_lens;
+  a.src = src;
+  a.dst = dst;
+  a.from = from;
+  a.to = to;
+  a.status = status;
+  cudaError_t e = eba::launch_fork(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+int attn_pages_reserve(const attn_pool_t* pool, int* page_table, long long table_stride,
+                       int max_pages, const int* seq_lens, const int* new_lens, int n_seqs,
+                       void* stream) {
+  int s = check_pool(pool, page_table, table_stride, max_pages, n_seqs);
+  if (s != ATTN_OK) return s;
+  if (!seq_lens || !new_lens) return ATTN_ERR_INVALID_ARG;
+  int* status = status_word_ptr();
+  if (!status) return ATTN_ERR_CUDA;
+  eba::PoolArgs a{};
+  a.pool = *pool;
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.n_seqs = a.n = n_seqs;
+  a.lens = const_cast<int*>(seq_lens);
+  a.new_lens = new_lens;
+  a.status = status;
+  cudaError_t e = eba::launch_reserve(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+int attn_cache_copy(const attn_cache_t* cache, const int* from, const int* to, int n, void* stream) {
+  int s = check_cache(cache);
+  if (s != ATTN_OK) return s;
+  if (!from || !to || n < 1) return ATTN_ERR_INVALID_ARG;
+  int* status = status_word_ptr();
+  if (!status) return ATTN_ERR_CUDA;
+  eba::CopyArgs a{};
+  cache_bytes(a, *cache);
+  a.from = from;
+  a.to = to;
+  a.n = n;
+  a.status = status;
+  cudaError_t e = eba::launch_copy(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+int attn_cache_gather(const attn_cache_t* cache, const int* page_table, long long table_stride,
+                      int max_pages, int n_seqs, const int* places, const int* cu, int T,
+                      const int* to_table, long long to_stride, int to_max_pages,
+                      const int* to_start, void* stream) {
+  int s = check_cache(cache);
+  if (s != ATTN_OK) return s;
+  if (!page_table || max_pages < 1 || n_seqs < 1 || table_stride < 0) return ATTN_ERR_INVALID_ARG;
+  if (!places || !cu || T < 1 || T > (1 << 30)) return ATTN_ERR_INVALID_ARG;
+  if (to_table && (to_max_pages < 1 || to_stride < 0)) return ATTN_ERR_INVALID_ARG;
+  if (cache->H_kv > 16384) return ATTN_ERR_UNSUPPORTED;  // the grid's second dimension
+  int* status = status_word_ptr();
+  if (!status) return ATTN_ERR_CUDA;
+  eba::GatherArgs a{};
+  cache_bytes(a, *cache);
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.n_seqs = n_seqs;
+  a.places = places;
+  a.cu = cu;
+  a.T = T;
+  a.in_place = !to_table;
+  a.to_table = to_table ? to_table : page_table;
+  a.to_stride = to_table ? to_stride : table_stride;
+  a.to_max_pages = to_table ? to_max_pages : max_pages;
+  a.to_start = to_start;
+  a.status = status;
+  cudaError_t e = eba::launch_gather(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 

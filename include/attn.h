@@ -419,6 +419,88 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
                 long long pos_stride, void* o, float* lse, void* workspace,
                 size_t workspace_bytes, void* stream);
 
+/*
+ * The pages of a cache whose page tables the GPU keeps: sequences share pages, take
+ * free ones and give them back without the host knowing which.
+ *
+ * refs: device int32 [n_pages], how many table entries name each page; 0: it is
+ * free. scratch: device int32 [n_pages], contents do not matter; calls on one pool
+ * that may overlap on the GPU are an error, as they change its counts. 1 <= n_pages
+ * <= 2^30. A table entry below 0 (-1) holds no page; one of n_pages or more counts
+ * as none where it is met and is recorded as ATTN_ERR_PAGE. Calls with n_seqs *
+ * max_pages of 2^31 or more are refused. Pages are handed out lowest number first,
+ * in the order of the sequences (pairs) and of their entries, so that results
+ * depend on the counts and tables alone. Several caches (a model's layers) may go
+ * by one pool and table.
+ */
+typedef struct {
+  int* refs;
+  int* scratch;
+  int n_pages, page_size;
+} attn_pool_t;
+
+/*
+ * attn_pages_release - give back the pages that lie wholly within the keys
+ * [first[b], last[b]) of each sequence: the entries become -1, the pages' counts
+ * one less. (A sequence that ends: 0 and max_pages * page_size; rejected drafts:
+ * the length to keep and the same; what a window has left behind: the sinks and
+ * the window's first key.) Bounds outside the table count as its ends. A page
+ * whose count is 0 already stays at 0 and is recorded as ATTN_ERR_PAGE.
+ */
+int attn_pages_release(const attn_pool_t* pool, int* page_table, long long table_stride,
+                       int max_pages, const int* first, const int* last, int n_seqs, void* stream);
+
+/*
+ * attn_pages_fork - n pairs: sequence dst[i] becomes a copy of sequence src[i], its
+ * length too. The pages that src fills are shared (their counts one more). The last
+ * one, if it is not full, is not: dst gets a free page in its place, and from[i],
+ * to[i] name the two for attn_cache_copy; -1, -1 where there is nothing to copy
+ * (also where no page is free: dst's entry is then -1 and ATTN_ERR_PAGE recorded).
+ * What dst's row held before is not given back. A pair whose index, or whose
+ * source's length, is out of range, whose dst is another pair's src, its own or an
+ * earlier pair's dst, is left out and recorded as ATTN_ERR_PAGE.
+ */
+int attn_pages_fork(const attn_pool_t* pool, int* page_table, long long table_stride, int max_pages,
+                    int* seq_lens, int n_seqs, const int* src, const int* dst, int n, int* from,
+                    int* to, void* stream);
+
+/*
+ * attn_pages_reserve - room for each sequence to grow from seq_lens[b] to
+ * new_lens[b] keys: those of its entries behind its last key's that hold no page
+ * get a free one. Where none is left the entry stays -1 and ATTN_ERR_PAGE is
+ * recorded. A sequence whose lengths are out of range gets none and is recorded.
+ */
+int attn_pages_reserve(const attn_pool_t* pool, int* page_table, long long table_stride,
+                       int max_pages, const int* seq_lens, const int* new_lens, int n_seqs,
+                       void* stream);
+
+/*
+ * attn_cache_copy - n pages of the cache copied, keys and values, page from[i] to
+ * page to[i] (device int32 [n]). A pair with an index below 0 is skipped, one with
+ * an index of n_pages or more too and recorded as ATTN_ERR_PAGE. No page may be
+ * written twice, or written and read.
+ */
+int attn_cache_copy(const attn_cache_t* cache, const int* from, const int* to, int n, void* stream);
+
+/*
+ * attn_cache_gather - move chosen tokens' keys and values together: sequence b's
+ * tokens at places[cu[b]], ..., places[cu[b + 1] - 1] go to its places to_start[b],
+ * to_start[b] + 1, ... (NULL: 0, 1, ...).
+ *   places: device int32 [T]; cu: device int32 [n_seqs + 1]. Entries of places outside
+ *   [cu[0], cu[n_seqs]) are not used.
+ *   to_table NULL: within the sequence's own pages (the accepted tokens of a draft
+ *   moved up behind its context). No token may move to a later place; a place may
+ *   be moved several times. The pages must not be shared.
+ *   to_table [n_seqs, to_max_pages]: into the pages of another table, none of which
+ *   is read in this call (long caches thinned out to the keys that count).
+ * Rows are copied as they are. A place, a page or a later place that is out of
+ * range or order is left out and recorded as ATTN_ERR_PAGE.
+ */
+int attn_cache_gather(const attn_cache_t* cache, const int* page_table, long long table_stride,
+                      int max_pages, int n_seqs, const int* places, const int* cu, int T,
+                      const int* to_table, long long to_stride, int to_max_pages,
+                      const int* to_start, void* stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* attn_status_string(int status);
 
