@@ -21,7 +21,8 @@ Entry points (same names as the C ABI):
   rope_fwd(q, k, positions, plan), rope_bwd(dq, dk, positions, plan) -> (q, k)   rotary positions
   rope(q, k, positions, plan)                   -> (q, k)   (autograd-aware)
   cache_append(cache, k, v, page_table, seq_lens, cu_new=None, rope=None, positions=None)
-  decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None) -> (o, lse)
+  decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None, window=None, sinks=0)
+      -> (o, lse)
   pages_release(pool, page_table, first, last), pages_reserve(pool, page_table, seq_lens, new_lens),
   pages_fork(pool, page_table, seq_lens, src, dst) -> (from_pages, to_pages)   page tables kept on the GPU
   cache_copy(cache, from_pages, to_pages)       whole pages within a cache
@@ -137,13 +138,17 @@ def _declare(L):
     L.attn_decode_workspace_size.argtypes = [i, i, i, i, i, ll]
     L.attn_decode_workspace_size.restype = sz
     L.attn_decode.argtypes = [cp, vp, lp, vp, ll, i, vp, i, i, f, rp, vp, ll, vp, vp, vp, sz, vp]
+    L.attn_decode_window_workspace_size.argtypes = [i, i, i, i, i, ll, i, i]
+    L.attn_decode_window_workspace_size.restype = sz
+    L.attn_decode_window.argtypes = [cp, vp, lp, vp, ll, i, vp, i, i, i, i, f, rp, vp, ll, vp, vp, vp,
+                                     sz, vp]
     pp = ctypes.POINTER(_PoolStruct)
     L.attn_pages_release.argtypes = [pp, vp, ll, i, vp, vp, i, vp]
     L.attn_pages_fork.argtypes = [pp, vp, ll, i, vp, i, vp, vp, i, vp, vp, vp]
     L.attn_pages_reserve.argtypes = [pp, vp, ll, i, vp, vp, i, vp]
     L.attn_cache_copy.argtypes = [cp, vp, vp, i, vp]
     L.attn_cache_gather.argtypes = [cp, vp, ll, i, i, vp, vp, i, vp, ll, i, vp, vp]
-    for name in ("attn_rope_init", "attn_rope", "attn_cache_append", "attn_decode",
+    for name in ("attn_rope_init", "attn_rope", "attn_cache_append", "attn_decode", "attn_decode_window",
                  "attn_pages_release", "attn_pages_fork", "attn_pages_reserve", "attn_cache_copy",
                  "attn_cache_gather"):
         getattr(L, name).restype = ctypes.c_int
@@ -876,14 +881,30 @@ def _append_layout(cache, k, v, page_table, seq_lens, cu_new, rope, positions):
     return (_Strides2(*sk), _Strides2(*sv), page_table.stride(0), page_table.shape[1], n, T, stride)
 
 
-def decode_workspace_size(cache, B, H, max_pages) -> int:
+def decode_workspace_size(cache, B, H, max_pages, window=None, sinks=0) -> int:
     """Scratch bytes of decode for B sequences of H query heads and a page table of
     max_pages columns; 0 where none is needed."""
+    if window is not None:
+        return int(lib().attn_decode_window_workspace_size(
+            B, H, cache.H_kv, cache.d, cache._struct.type, max_pages * cache.page_size, window, sinks))
     return int(lib().attn_decode_workspace_size(B, H, cache.H_kv, cache.d, cache._struct.type,
                                                 max_pages * cache.page_size))
 
 
-def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None, workspace=None):
+def _window(window, sinks):
+    """Checks the window and sinks of a cache call: ints, (None, 0) for no window."""
+    if window is None:
+        if sinks:
+            raise ValueError("sinks are used with a window only")
+        return None, 0
+    for name, x, least in (("window", window, 1), ("sinks", sinks, 0)):
+        if not isinstance(x, int) or not least <= x < 1 << 31:
+            raise ValueError(f"{name} must be an int of at least {least}, got {x!r}")
+    return window, sinks
+
+
+def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None, workspace=None,
+           window=None, sinks=0):
     """Attention of one new token per sequence, q [B, H, d] bf16, over the
     seq_lens[b] keys and values its sequence has in the cache: (o bf16 [B, H, d],
     lse fp32 [B, H]); a sequence of length 0 gives o = 0 and lse = -inf.
@@ -892,15 +913,18 @@ def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None
     q is rotated on the way (and rounded to bf16, as rope_fwd gives it) by
     positions, int32 [n_axes, B], or, with one axis and none given, by
     seq_lens - 1. page_table and seq_lens as for cache_append; the GPU reads
-    them, so a captured call follows their contents."""
+    them, so a captured call follows their contents.
+
+    With a ``window`` the token sees the last that many of its sequence's keys and
+    the first ``sinks``; pages that hold none of these need not be there."""
     try:
-        key = (_form(q), _form(page_table), _form(seq_lens), _form(positions), cache._key,
+        key = (_form(q), _form(page_table), _form(seq_lens), _form(positions), cache._key, window, sinks,
                None if rope is None else (rope.n_axes, rope.n_pairs))
         lay = _DECODE_LAYOUTS.get(key)
     except AttributeError:
         lay = key = None
     if lay is None:
-        lay = _decode_layout(cache, q, page_table, seq_lens, rope, positions)
+        lay = _decode_layout(cache, q, page_table, seq_lens, rope, positions, window, sinks)
         _DECODE_LAYOUTS.add(key, lay)
     sq, row, wide, B, H, d, stride, need = lay
     dev = cache.device
@@ -916,17 +940,22 @@ def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None
         raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {dev}")
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
     lse = torch.empty((B, H), device=dev, dtype=torch.float32)
-    _launch(dev, lib().attn_decode, cache._at(), qp, sq, page_table.data_ptr(), row, wide,
-            seq_lens.data_ptr(), B, H, _scale(scale, d), None if rope is None else rope._struct,
+    args = (_scale(scale, d), None if rope is None else rope._struct,
             None if positions is None else positions.data_ptr(), stride, o.data_ptr(),
             lse.data_ptr(), None if workspace is None else workspace.data_ptr(), need)
+    if window is None:
+        _launch(dev, lib().attn_decode, cache._at(), qp, sq, page_table.data_ptr(), row, wide,
+                seq_lens.data_ptr(), B, H, *args)
+    else:
+        _launch(dev, lib().attn_decode_window, cache._at(), qp, sq, page_table.data_ptr(), row, wide,
+                seq_lens.data_ptr(), B, H, window, sinks, *args)
     return o, lse
 
 
 _DECODE_LAYOUTS = _Layouts()
 
 
-def _decode_layout(cache, q, page_table, seq_lens, rope, positions):
+def _decode_layout(cache, q, page_table, seq_lens, rope, positions, window, sinks):
     """Checks a decode's arguments: strides and sizes as the C ABI takes them, and
     the bytes of workspace."""
     if not isinstance(cache, PagedCache):
@@ -941,8 +970,9 @@ def _decode_layout(cache, q, page_table, seq_lens, rope, positions):
     if n != B:
         raise ValueError(f"q holds {B} sequences, seq_lens {n}")
     stride = cache._turn(rope, positions, B)[2]
+    window, sinks = _window(window, sinks)
     return (_Strides2(*sq), page_table.stride(0), page_table.shape[1], B, H, d, stride,
-            decode_workspace_size(cache, B, H, page_table.shape[1]))
+            decode_workspace_size(cache, B, H, page_table.shape[1], window, sinks))
 
 
 # ---------------------------------------------------------------------------

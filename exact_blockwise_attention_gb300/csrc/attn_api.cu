@@ -372,7 +372,9 @@ struct DecodePlan {
   bool join;             // items may be cut between CTAs
   size_t slots, bytes;   // of the workspace: parts, all
 };
-DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int type) {
+// window > 0: a token sees that many last keys, and the `sinks` first ones.
+DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int type, int window = 0,
+                       int sinks = 0) {
   DecodePlan p{};
   const int group = H / H_kv;
   // the matrix instruction has 8 columns: groups of up to 8 heads take one set
@@ -384,7 +386,16 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
   p.per_item = 1;
   p.max_len = static_cast<int>(std::min(capacity, (1ll << 31) - 1 - tile));
   p.heads = H_kv * p.blocks;
-  long long item_tiles = (p.max_len + tile - 1) / tile;
+  auto tiles_of = [&](int tile_keys) {
+    const long long all = (p.max_len + tile_keys - 1) / tile_keys;
+    if (window == 0) return all;
+    // the window's first 16 keys may hold 15 before it; no more tiles than the table
+    // holds, but for the sinks' last tile and the window's shift against the tiles
+    const long long most = (std::min(sinks, p.max_len) + tile_keys - 1) / tile_keys +
+                           (static_cast<long long>(window) + 15 + tile_keys - 1) / tile_keys;
+    return std::min(all + 2, most);
+  };
+  long long item_tiles = tiles_of(tile);
   long long items = static_cast<long long>(B) * p.heads;
   if (items >= (1ll << 31) || item_tiles * p.heads >= (1ll << 31) ||
       item_tiles * p.heads * B >= (1ll << 31))
@@ -421,7 +432,7 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
     p.heads /= 4;
     items /= 4;
     tile /= 4;
-    item_tiles = (p.max_len + tile - 1) / tile;
+    item_tiles = tiles_of(tile);
   }
   // no more CTAs than tiles the tables can hold; a single-tile item is never cut
   p.ctas = static_cast<int>(std::min<long long>(wave, items * item_tiles));
@@ -430,6 +441,80 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
   p.slots = 2 * static_cast<size_t>(wave) * p.rows * p.per_item;
   p.bytes = wave * sizeof(int2) + p.slots * (d + 2) * sizeof(float);
   return p;
+}
+
+// Both decodes; window 0: all of a sequence's keys.
+int decode(const attn_cache_t* cache, const void* q, const long long* q_strides,
+           const int* page_table, long long table_stride, int max_pages, const int* seq_lens, int B,
+           int H, int window, int sinks, float scale, const attn_rope_t* rope, const int* pos,
+           long long pos_stride, void* o, float* lse, void* workspace, size_t workspace_bytes,
+           void* stream) {
+  int s = check_cache(cache);
+  if (s != ATTN_OK) return s;
+  if (!q_strides) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_table(page_table, table_stride, max_pages, seq_lens, B)) != ATTN_OK) return s;
+  if (H < 1 || H % cache->H_kv != 0) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * H >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * kLog2e) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_ptrs({q, o, lse})) != ATTN_OK) return s;
+  if ((s = check_strides(q_strides, 2, 8)) != ATTN_OK) return s;
+  if (rope) {
+    if ((s = check_rope(*rope, cache->d)) != ATTN_OK) return s;
+    if (!pos && rope->n_axes != 1) return ATTN_ERR_INVALID_ARG;
+  }
+  const DecodePlan p = decode_plan(B, H, cache->H_kv, cache->d,
+                                   static_cast<long long>(max_pages) * cache->page_size, cache->type,
+                                   window, sinks);
+  if (!p.ok) return ATTN_ERR_INVALID_ARG;
+  if (p.bytes > 0) {
+    if (!workspace || workspace_bytes < p.bytes) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  }
+  int* status = status_word_ptr();
+  if (!status) return ATTN_ERR_CUDA;
+  eba::DecodeArgs a{};
+  const int esz = cache->type == ATTN_CACHE_E4M3 ? 1 : 2;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_seq = q_strides[0];
+  a.q_head = q_strides[1];
+  a.k = static_cast<const unsigned char*>(cache->k);
+  a.v = static_cast<const unsigned char*>(cache->v);
+  for (int i = 0; i < 3; ++i) {
+    a.k_strides[i] = cache->k_strides[i] * esz;
+    a.v_strides[i] = cache->v_strides[i] * esz;
+  }
+  a.cache = *cache;
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.lens = seq_lens;
+  a.max_len = p.max_len;
+  a.window = window;
+  a.sinks = sinks;
+  a.B = B;
+  a.H = H;
+  a.group = H / cache->H_kv;
+  a.rows = p.rows;
+  a.blocks = p.blocks;
+  a.per_item = p.per_item;
+  a.heads = p.heads;
+  a.splits = p.splits;
+  a.scale_log2 = scale * kLog2e;
+  a.o_scale = cache->v_scale;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  if (p.bytes > 0) {
+    a.cut = static_cast<int2*>(workspace);
+    a.part_o = reinterpret_cast<float*>(a.cut + eba::kDecodeCtas);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + p.slots * cache->d);
+  }
+  a.pos = pos;
+  a.pos_axis = pos_stride;
+  a.status = status;
+  if (rope) a.rope = *rope;
+  a.limit_ns = g_wait_limit_ns.load();
+  const auto launch = window > 0 ? eba::launch_decode_window : eba::launch_decode;
+  cudaError_t e = launch(a, p.ctas, p.join, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
 // Short sequences (at most 64 queries and keys) are packed several to a
@@ -1012,68 +1097,27 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
                 int B, int H, float scale, const attn_rope_t* rope, const int* pos,
                 long long pos_stride, void* o, float* lse, void* workspace,
                 size_t workspace_bytes, void* stream) {
-  int s = check_cache(cache);
-  if (s != ATTN_OK) return s;
-  if (!q_strides) return ATTN_ERR_INVALID_ARG;
-  if ((s = check_table(page_table, table_stride, max_pages, seq_lens, B)) != ATTN_OK) return s;
-  if (H < 1 || H % cache->H_kv != 0) return ATTN_ERR_INVALID_ARG;
-  if (static_cast<long long>(B) * H >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale * kLog2e) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
-  if ((s = check_ptrs({q, o, lse})) != ATTN_OK) return s;
-  if ((s = check_strides(q_strides, 2, 8)) != ATTN_OK) return s;
-  if (rope) {
-    if ((s = check_rope(*rope, cache->d)) != ATTN_OK) return s;
-    if (!pos && rope->n_axes != 1) return ATTN_ERR_INVALID_ARG;
-  }
-  const DecodePlan p = decode_plan(B, H, cache->H_kv, cache->d,
-                                   static_cast<long long>(max_pages) * cache->page_size, cache->type);
-  if (!p.ok) return ATTN_ERR_INVALID_ARG;
-  if (p.bytes > 0) {
-    if (!workspace || workspace_bytes < p.bytes) return ATTN_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
-  }
-  int* status = status_word_ptr();
-  if (!status) return ATTN_ERR_CUDA;
-  eba::DecodeArgs a{};
-  const int esz = cache->type == ATTN_CACHE_E4M3 ? 1 : 2;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.q_seq = q_strides[0];
-  a.q_head = q_strides[1];
-  a.k = static_cast<const unsigned char*>(cache->k);
-  a.v = static_cast<const unsigned char*>(cache->v);
-  for (int i = 0; i < 3; ++i) {
-    a.k_strides[i] = cache->k_strides[i] * esz;
-    a.v_strides[i] = cache->v_strides[i] * esz;
-  }
-  a.cache = *cache;
-  a.table = page_table;
-  a.table_stride = table_stride;
-  a.lens = seq_lens;
-  a.max_len = p.max_len;
-  a.B = B;
-  a.H = H;
-  a.group = H / cache->H_kv;
-  a.rows = p.rows;
-  a.blocks = p.blocks;
-  a.per_item = p.per_item;
-  a.heads = p.heads;
-  a.splits = p.splits;
-  a.scale_log2 = scale * kLog2e;
-  a.o_scale = cache->v_scale;
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.lse = lse;
-  if (p.bytes > 0) {
-    a.cut = static_cast<int2*>(workspace);
-    a.part_o = reinterpret_cast<float*>(a.cut + eba::kDecodeCtas);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + p.slots * cache->d);
-  }
-  a.pos = pos;
-  a.pos_axis = pos_stride;
-  a.status = status;
-  if (rope) a.rope = *rope;
-  a.limit_ns = g_wait_limit_ns.load();
-  cudaError_t e = eba::launch_decode(a, p.ctas, p.join, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+  return decode(cache, q, q_strides, page_table, table_stride, max_pages, seq_lens, B, H, 0, 0, scale,
+                rope, pos, pos_stride, o, lse, workspace, workspace_bytes, stream);
+}
+
+size_t attn_decode_window_workspace_size(int B, int H, int H_kv, int d, int type,
+                                         long long max_keys, int window, int sinks) {
+  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128) || max_keys < 1 ||
+      (type != ATTN_CACHE_BF16 && type != ATTN_CACHE_E4M3) || window < 1 || sinks < 0)
+    return 0;
+  const DecodePlan p = decode_plan(B, H, H_kv, d, max_keys, type, window, sinks);
+  return p.ok ? p.bytes : 0;
+}
+
+int attn_decode_window(const attn_cache_t* cache, const void* q, const long long* q_strides,
+                       const int* page_table, long long table_stride, int max_pages,
+                       const int* seq_lens, int B, int H, int window, int sinks, float scale,
+                       const attn_rope_t* rope, const int* pos, long long pos_stride, void* o,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return decode(cache, q, q_strides, page_table, table_stride, max_pages, seq_lens, B, H, window,
+                sinks, scale, rope, pos, pos_stride, o, lse, workspace, workspace_bytes, stream);
 }
 
 int attn_pages_release(const attn_pool_t* pool, int* page_table, long long table_stride,

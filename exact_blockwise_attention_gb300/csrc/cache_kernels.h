@@ -65,6 +65,7 @@ struct DecodeArgs {
   long long table_stride;
   const int* lens;
   int max_len;  // keys a table row can hold
+  int window, sinks;  // windowed: the last and the first keys that a token sees
   int B, H;
   int group;   // query heads per K/V head
   int rows;    // query heads a CTA holds: 8 or 16
@@ -90,5 +91,6 @@ struct DecodeArgs {
   attn_rope_t rope;
 };
 cudaError_t launch_decode(const DecodeArgs& a, int ctas, bool join, cudaStream_t stream);
+cudaError_t launch_decode_window(const DecodeArgs& a, int ctas, bool join, cudaStream_t stream);
 
 }  // namespace eba

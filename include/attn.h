@@ -420,6 +420,21 @@ int attn_decode(const attn_cache_t* cache, const void* q, const long long* q_str
                 size_t workspace_bytes, void* stream);
 
 /*
+ * attn_decode_window - attn_decode within a sliding window: the token of a sequence
+ * of n keys sees the last `window` of them, [n - window, n), and the first `sinks`
+ * (a key that is both counts once). window >= 1, sinks >= 0. Pages without a visible
+ * key are not looked up: their table entries may hold anything. Everything else as
+ * attn_decode; workspace of attn_decode_window_workspace_size(...) bytes.
+ */
+size_t attn_decode_window_workspace_size(int B, int H, int H_kv, int d, int type,
+                                         long long max_keys, int window, int sinks);
+int attn_decode_window(const attn_cache_t* cache, const void* q, const long long* q_strides,
+                       const int* page_table, long long table_stride, int max_pages,
+                       const int* seq_lens, int B, int H, int window, int sinks, float scale,
+                       const attn_rope_t* rope, const int* pos, long long pos_stride, void* o,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The pages of a cache whose page tables the GPU keeps: sequences share pages, take
  * free ones and give them back without the host knowing which.
  *
