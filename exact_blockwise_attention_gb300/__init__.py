@@ -18,6 +18,9 @@ Entry points (same names as the C ABI):
   fwd_varlen(q, k, v, cu_q, cu_k, scale=None)   -> (o, lse)      packed sequences
   fwd_fp8(q8, k8, vt8, q_scale, k_scale, v_scale, scale=None) -> (o, lse)   e4m3, d = 128
   bwd_varlen(q, k, v, o, do, lse, cu_q, cu_k, scale=None) -> (dq, dk, dv)
+  fwd_window(q, k, v, left, right=0, sinks=0, scale=None) -> (o, lse)   a sliding window and first tokens
+  bwd_window(q, k, v, o, do, lse, left, right=0, sinks=0, scale=None) -> (dq, dk, dv)
+  attention_window(q, k, v, left, right=0, sinks=0, scale=None) -> o   (autograd-aware)
   rope_fwd(q, k, positions, plan), rope_bwd(dq, dk, positions, plan) -> (q, k)   rotary positions
   rope(q, k, positions, plan)                   -> (q, k)   (autograd-aware)
   cache_append(cache, k, v, page_table, seq_lens, cu_new=None, rope=None, positions=None)
@@ -55,7 +58,8 @@ __all__ = [
     "MAX_CHUNKS", "MAX_SEQS", "fwd_varlen", "bwd_varlen", "bwd_varlen_workspace_size", "fwd_fp8",
     "attention_varlen", "Rope", "rope_fwd", "rope_bwd", "rope", "PagedCache", "cache_append",
     "decode", "decode_workspace_size", "PagePool", "pages_release", "pages_fork", "pages_reserve",
-    "cache_copy", "cache_gather",
+    "cache_copy", "cache_gather", "fwd_window", "bwd_window", "bwd_window_workspace_size",
+    "attention_window",
 ]
 
 ATTN_OK = 0
@@ -121,6 +125,13 @@ def _declare(L):
     L.attn_fwd_fp8.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, f, f, f, vp]
     L.attn_bwd_gqa.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, vp, sz,
                                vp]
+    L.attn_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f, vp]
+    L.attn_fwd_window.restype = ctypes.c_int
+    L.attn_bwd_window_workspace_size.argtypes = [i, i, i, i, i, i, i, i, i]
+    L.attn_bwd_window_workspace_size.restype = sz
+    L.attn_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f, vp,
+                                  sz, vp]
+    L.attn_bwd_window.restype = ctypes.c_int
     ip = ctypes.POINTER(i)
     L.attn_fwd_varlen.argtypes = [vp, vp, vp, vp, vp, ip, ip, i, i, i, f, vp]
     L.attn_bwd_varlen_workspace_size.argtypes = [i, i, i, i]
@@ -469,6 +480,82 @@ class _Attention(torch.autograd.Function):
 def attention(q, k, v, scale=None):
     """Autograd-aware exact attention; only o and lse are saved for backward."""
     return _Attention.apply(q, k, v, scale)
+
+
+def _sides(left, right, sinks):
+    """left, right and sinks as the C ABI takes them (None: no end to that side)."""
+    out = []
+    for name, x in (("left", left), ("right", right), ("sinks", sinks)):
+        if x is None and name != "sinks":
+            x = -1
+        elif not isinstance(x, int) or not 0 <= x < 1 << 31:
+            raise ValueError(f"{name} must be an int of at least 0, got {x!r}")
+        out.append(x)
+    return out
+
+
+def fwd_window(q, k, v, left, right=0, sinks=0, scale=None):
+    """Attention within a sliding window and to the first tokens: (o bf16 [B,H,Lq,d],
+    lse fp32 [B,H,Lq]).
+
+    Query i stands at the place p = i + Lk - Lq, the last query at the last key, and
+    sees the keys p - left to p + right and, up to p + right, the first ``sinks``. left
+    or right None: no end to that side (left=None is plain causal attention). A query
+    that sees no key gives o = 0 and lse = -inf. k, v may have H_kv < H heads."""
+    B, H, Hkv, Lq, Lk, d = _qkv(q, k, v, gqa=True)
+    left, right, sinks = _sides(left, right, sinks)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, Lq), device=q.device, dtype=torch.float32)
+    _launch(q.device, lib().attn_fwd_window, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv,
+            Lq, Lk, d, left, right, sinks, _scale(scale, d))
+    return o, lse
+
+
+def bwd_window_workspace_size(B, H, H_kv, Lq, Lk, d, left, right=0, sinks=0) -> int:
+    return int(lib().attn_bwd_window_workspace_size(B, H, H_kv, Lq, Lk, d, *_sides(left, right, sinks)))
+
+
+def bwd_window(q, k, v, o, do, lse, left, right=0, sinks=0, scale=None, workspace=None):
+    """Gradients (dq, dk, dv) of sum(o * do) for fwd_window; P is recomputed from lse.
+    Keys that no query sees, and queries that see no key, have zero gradients."""
+    B, H, Hkv, Lq, Lk, d = _bwd_inputs(q, k, v, o, do, lse, gqa=True)
+    left, right, sinks = _sides(left, right, sinks)
+    need = int(lib().attn_bwd_window_workspace_size(B, H, Hkv, Lq, Lk, d, left, right, sinks))
+    if workspace is None:
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+    elif workspace.numel() * workspace.element_size() < need or workspace.device != q.device or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {q.device}")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    _launch(q.device, lib().attn_bwd_window, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse),
+            _ptr(dq), _ptr(dk), _ptr(dv), B, H, Hkv, Lq, Lk, d, left, right, sinks, _scale(scale, d),
+            _ptr(workspace), need)
+    return dq, dk, dv
+
+
+class _AttentionWindow(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, left, right, sinks, scale):
+        o, lse = fwd_window(q, k, v, left, right, sinks, scale)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.window = (left, right, sinks, scale)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse = ctx.saved_tensors
+        do = do.contiguous()
+        if do.data_ptr() & 15:  # autograd also hands over views
+            do = do.clone()
+        grads = bwd_window(q, k, v, o, do, lse, *ctx.window)
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None,
+                None)
+
+
+def attention_window(q, k, v, left, right=0, sinks=0, scale=None):
+    """Autograd-aware fwd_window; only o and lse are saved for backward."""
+    return _AttentionWindow.apply(q, k, v, left, right, sinks, scale)
 
 
 class _AttentionVarlen(torch.autograd.Function):

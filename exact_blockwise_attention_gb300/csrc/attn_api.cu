@@ -608,6 +608,42 @@ int fwd_common(const void* q, const void* k, const void* v, void* o, float* lse,
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
+// The window of a call: what its sizes make of left, right (-1: no end) and sinks.
+// False: out of range.
+bool window_tiles(int Lq, int Lk, int left, int right, int sinks, long long heads,
+                  eba::WindowTiles* w) {
+  constexpr int kMost = 1 << 29;  // places and their sums stay within an int
+  if (Lq > kMost || Lk > kMost || left < -1 || right < -1 || sinks < 0) return false;
+  const int all = Lq + Lk;  // beyond every distance
+  *w = eba::WindowTiles{};
+  w->left = left < 0 ? all : std::min(left, all);
+  w->right = right < 0 ? all : std::min(right, all);
+  w->sinks = std::min(sinks, Lk);
+  w->off = Lk - Lq;
+  const bool left_end = w->left < all, right_end = w->right < all;
+  w->by_cost = left_end == right_end ? 0 : right_end ? 1 : -1;
+  constexpr int R = eba::kTileRows;
+  const int n_qtiles = (Lq + R - 1) / R;
+  w->run_tiles = left_end && right_end ? std::min(n_qtiles, (w->left + w->right + R - 1) / R + 2) : n_qtiles;
+  if (!left_end || w->sinks == 0) return true;
+  // Pieces as long as an ordinary item, at least 8 query tiles (each leaves 2 x 128 x d
+  // floats). Many sinks' key tiles keep all SMs busy by themselves and stay whole.
+  const int sink_tiles = (w->sinks + R - 1) / R;
+  const int piece = std::max(w->run_tiles, 8);
+  if (sink_tiles * heads > 4 * 152) {
+    w->by_cost = 1;
+    return true;
+  }
+  w->piece = piece;
+  w->pieces = (n_qtiles + piece - 1) / piece;
+  if (w->pieces > 1) w->cut_tiles = sink_tiles; else w->pieces = w->piece = 0;
+  return true;
+}
+
+size_t window_part_bytes(const eba::WindowTiles& w, long long heads, int d) {
+  return static_cast<size_t>(heads) * w.cut_tiles * w.pieces * 2 * eba::kTileRows * d * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -827,6 +863,101 @@ int attn_bwd_gqa(const void* q, const void* k, const void* v, const void* o, con
   a.limit_ns = g_wait_limit_ns.load();
   if (static_cast<long long>(a.n_ktiles) * BHkv >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
   cudaError_t e = eba::launch_bwd(tq, tk, tv, tdo, tdqa, a, d, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
+                    int H_kv, int Lq, int Lk, int d, int left, int right, int sinks, float scale,
+                    void* stream) {
+  int s = check_sizes(B, H, Lq, Lk, d, scale);
+  if (s != ATTN_OK) return s;
+  if (H_kv < 1 || H % H_kv != 0) return ATTN_ERR_INVALID_ARG;
+  const long long BH = static_cast<long long>(B) * H, BHkv = static_cast<long long>(B) * H_kv;
+  eba::WindowTiles w;
+  if (!window_tiles(Lq, Lk, left, right, sinks, BHkv, &w)) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_ptrs({q, k, v, o, lse})) != ATTN_OK) return s;
+  eba::FwdArgs a{};
+  a.B = B;
+  a.H = H;
+  a.group = H / H_kv;
+  a.Lq = Lq;
+  a.Lk = Lk;
+  a.n_qtiles = (Lq + eba::kTileRows - 1) / eba::kTileRows;
+  a.n_pairs = (a.n_qtiles + 1) / 2;
+  a.n_chunks = 1;
+  a.scale_log2 = scale * kLog2e;
+  a.bounds[1] = Lk;
+  a.o = o;
+  a.lse = lse;
+  if (static_cast<long long>(a.n_pairs) * BH >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  a.status = status_word_ptr();
+  if (!a.status) return ATTN_ERR_CUDA;
+  a.limit_ns = g_wait_limit_ns.load();
+  CUtensorMap tq, tk, tv;
+  if (!make_map(&tq, q, BH, Lq, d) || !make_map(&tk, k, BHkv, Lk, d) || !make_map(&tv, v, BHkv, Lk, d))
+    return ATTN_ERR_CUDA;
+  cudaError_t e = eba::launch_fwd_window(tq, tk, tv, a, w, d, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+size_t attn_bwd_window_workspace_size(int B, int H, int H_kv, int Lq, int Lk, int d, int left,
+                                      int right, int sinks) {
+  if (check_sizes(B, H, Lq, Lk, d, 1.0f) != ATTN_OK || H_kv < 1 || H % H_kv != 0) return 0;
+  const long long heads = static_cast<long long>(B) * H_kv;
+  eba::WindowTiles w;
+  if (!window_tiles(Lq, Lk, left, right, sinks, heads, &w)) return 0;
+  return attn_bwd_workspace_size(B, H, Lq, Lk, d) + window_part_bytes(w, heads, d);
+}
+
+int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                    const float* lse, void* dq, void* dk, void* dv, int B, int H, int H_kv, int Lq,
+                    int Lk, int d, int left, int right, int sinks, float scale, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int s = check_sizes(B, H, Lq, Lk, d, scale);
+  if (s != ATTN_OK) return s;
+  if (H_kv < 1 || H % H_kv != 0) return ATTN_ERR_INVALID_ARG;
+  const long long BH = static_cast<long long>(B) * H, BHkv = static_cast<long long>(B) * H_kv;
+  eba::WindowTiles w;
+  if (!window_tiles(Lq, Lk, left, right, sinks, BHkv, &w)) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_ptrs({q, k, v, o, dO, lse, dq, dk, dv})) != ATTN_OK) return s;
+  const size_t plain = attn_bwd_workspace_size(B, H, Lq, Lk, d);
+  if (!workspace || workspace_bytes < plain + window_part_bytes(w, BHkv, d)) return ATTN_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  float* ws = static_cast<float*>(workspace);
+  eba::BwdArgs a{};
+  a.B = B;
+  a.H = H;
+  a.group = H / H_kv;
+  a.H_kv = H_kv;
+  a.Lq = Lq;
+  a.Lk = Lk;
+  a.n_qtiles = (Lq + eba::kTileRows - 1) / eba::kTileRows;
+  a.n_ktiles = (Lk + eba::kTileRows - 1) / eba::kTileRows;
+  a.Lq_pad = a.n_qtiles * eba::kTileRows;
+  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
+  a.o = o;
+  a.dO = dO;
+  a.lse = lse;
+  a.dq_acc = ws;
+  a.nlse2 = ws + BH * Lq * d;
+  a.delta = a.nlse2 + BH * a.Lq_pad;
+  a.part = ws + plain / sizeof(float);
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  const long long items = (a.n_ktiles + static_cast<long long>(w.cut_tiles) * (w.pieces - 1)) * BHkv;
+  if (items >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  a.status = status_word_ptr();
+  if (!a.status) return ATTN_ERR_CUDA;
+  a.limit_ns = g_wait_limit_ns.load();
+  CUtensorMap tq, tk, tv, tdo, tdqa;
+  if (!make_map(&tq, q, BH, Lq, d) || !make_map(&tk, k, BHkv, Lk, d) ||
+      !make_map(&tv, v, BHkv, Lk, d) || !make_map(&tdo, dO, BH, Lq, d) ||
+      !make_map_f32(&tdqa, ws, BH, Lq, d))
+    return ATTN_ERR_CUDA;
+  cudaError_t e =
+      eba::launch_bwd_window(tq, tk, tv, tdo, tdqa, a, w, d, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 

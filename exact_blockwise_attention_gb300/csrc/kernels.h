@@ -79,6 +79,7 @@ struct BwdArgs {
   void* dq;         // bf16 [B,H,Lq,d]
   void* dk;         // bf16 [B,H/group,Lk,d]
   void* dv;         // bf16 [B,H/group,Lk,d]
+  float* part;      // windowed: fp32 dV, dK of the cut key tiles' pieces, [part, 2, 128, d]
   int* status;
   unsigned long long limit_ns;
 };
@@ -157,6 +158,22 @@ struct PackedTiles {
   int Lq, Lk;  // per sequence
 };
 
+// A sliding window and first tokens ("sinks"): query i stands at place p = i + off and
+// sees the keys p - left to p + right and, up to p + right, the first `sinks`.
+//
+// by_cost: one side has no end, so items differ: 1 (no left end, the last queries see
+// and the first keys are seen most), -1 (no right end: the other way round), 0 (equal).
+// Items then run through the heads, the largest first.
+// Backward: the first cut_tiles key tiles hold sinks, which all later queries see. Each
+// is cut in `pieces` of `piece` query tiles, which leave fp32 parts that a last kernel
+// adds up: else one such item is as long as the whole sequence and the others wait.
+struct WindowTiles {
+  int left, right, sinks, off;
+  int by_cost;
+  int cut_tiles, pieces, piece;
+  int run_tiles;  // query tiles of an ordinary backward item
+};
+
 struct MergeArgs {
   const float* o_parts;
   const float* lse_parts;
@@ -174,6 +191,11 @@ cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
                        const CUtensorMap& tdo, const CUtensorMap& tdqa, const BwdArgs& a, int d,
                        cudaStream_t stream);
 cudaError_t launch_merge(const MergeArgs& a, int d, cudaStream_t stream);
+cudaError_t launch_fwd_window(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const FwdArgs& a, const WindowTiles& wt, int d, cudaStream_t stream);
+cudaError_t launch_bwd_window(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tdo, const CUtensorMap& tdqa, const BwdArgs& a,
+                              const WindowTiles& wt, int d, cudaStream_t stream);
 
 // Forward over sequences of at most kShortMax queries and keys (CUDA cores).
 constexpr int kShortMax = 8;

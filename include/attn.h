@@ -228,6 +228,31 @@ int attn_merge(const float* o_parts, const float* lse_parts, int n_chunks, void*
                int B, int H, int Lq, int d, void* stream);
 
 /*
+ * attn_fwd_window / attn_bwd_window - attention within a sliding window and to the
+ * first tokens ("sinks"), grouped-query heads as for attn_fwd_gqa. Query i stands at
+ * the place p = i + Lk - Lq (the last query at the last key) and sees key j if
+ *   j <= p + right  and  (j >= p - left  or  j < sinks).
+ * left, right >= 0, or -1: no end to that side (right = 0: causal; left = -1, right = 0:
+ * plain causal attention); sinks >= 0. Lq, Lk <= 2^29. A query that sees no key (its
+ * place lies before the first one) gives O = 0, lse = -inf and zero gradients; a key
+ * that no query sees gets zero dK, dV. Tiles of 128 x 128 pairs without a visible one
+ * are neither read nor computed; within the others a masked weight is exactly 0, which
+ * keeps out every finite value (a NaN or infinite element of q, k, v or dO may reach
+ * the rows of the tiles that it is in).
+ *   workspace: attn_bwd_window_workspace_size(...) bytes. dQ is accumulated with atomic
+ *   adds as in attn_bwd (its low bits may vary from run to run; dK, dV do not).
+ */
+int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
+                    int H_kv, int Lq, int Lk, int d, int left, int right, int sinks, float scale,
+                    void* stream);
+size_t attn_bwd_window_workspace_size(int B, int H, int H_kv, int Lq, int Lk, int d, int left,
+                                      int right, int sinks);
+int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                    const float* lse, void* dq, void* dk, void* dv, int B, int H, int H_kv, int Lq,
+                    int Lk, int d, int left, int right, int sinks, float scale, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
  * Packed variable-length sequences ("sequence packing" of the NeMo video
  * foundation-model page: many sequences of different lengths, e.g. image and
  * video token sequences, laid back to back with no padding).
