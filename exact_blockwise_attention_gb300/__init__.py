@@ -26,6 +26,7 @@ Entry points (same names as the C ABI):
   cache_append(cache, k, v, page_table, seq_lens, cu_new=None, rope=None, positions=None)
   decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None, window=None, sinks=0)
       -> (o, lse)
+  decode_tree(cache, q, page_table, seq_lens, cu_q=None, mask=None, window=None, sinks=0) -> (o, lse)
   pages_release(pool, page_table, first, last), pages_reserve(pool, page_table, seq_lens, new_lens),
   pages_fork(pool, page_table, seq_lens, src, dst) -> (from_pages, to_pages)   page tables kept on the GPU
   cache_copy(cache, from_pages, to_pages)       whole pages within a cache
@@ -59,7 +60,7 @@ __all__ = [
     "attention_varlen", "Rope", "rope_fwd", "rope_bwd", "rope", "PagedCache", "cache_append",
     "decode", "decode_workspace_size", "PagePool", "pages_release", "pages_fork", "pages_reserve",
     "cache_copy", "cache_gather", "fwd_window", "bwd_window", "bwd_window_workspace_size",
-    "attention_window",
+    "attention_window", "decode_tree", "decode_tree_workspace_size",
 ]
 
 ATTN_OK = 0
@@ -67,6 +68,7 @@ MAX_CHUNKS = 64
 MAX_SEQS = 1024
 MAX_AXES = 4
 MAX_PAIRS = 64
+MAX_MASK_WORDS = 16
 _LIB = None
 
 
@@ -159,7 +161,12 @@ def _declare(L):
     L.attn_pages_reserve.argtypes = [pp, vp, ll, i, vp, vp, i, vp]
     L.attn_cache_copy.argtypes = [cp, vp, vp, i, vp]
     L.attn_cache_gather.argtypes = [cp, vp, ll, i, i, vp, vp, i, vp, ll, i, vp, vp]
+    L.attn_decode_tree_workspace_size.argtypes = [i, i, i, i, i]
+    L.attn_decode_tree_workspace_size.restype = sz
+    L.attn_decode_tree.argtypes = [cp, vp, lp, vp, ll, i, vp, i, vp, i, i, vp, ll, i, i, i, f, vp, vp,
+                                   vp, sz, vp]
     for name in ("attn_rope_init", "attn_rope", "attn_cache_append", "attn_decode", "attn_decode_window",
+                 "attn_decode_tree",
                  "attn_pages_release", "attn_pages_fork", "attn_pages_reserve", "attn_cache_copy",
                  "attn_cache_gather"):
         getattr(L, name).restype = ctypes.c_int
@@ -1060,6 +1067,106 @@ def _decode_layout(cache, q, page_table, seq_lens, rope, positions, window, sink
     window, sinks = _window(window, sinks)
     return (_Strides2(*sq), page_table.stride(0), page_table.shape[1], B, H, d, stride,
             decode_workspace_size(cache, B, H, page_table.shape[1], window, sinks))
+
+
+# ---------------------------------------------------------------------------
+# Several drafted tokens per sequence
+# ---------------------------------------------------------------------------
+
+def decode_tree_workspace_size(cache, T, B, H) -> int:
+    """Scratch bytes of decode_tree for T tokens of B sequences with H query heads."""
+    return int(lib().attn_decode_tree_workspace_size(T, B, H, cache.H_kv, cache.d))
+
+
+def decode_tree(cache, q, page_table, seq_lens, cu_q=None, mask=None, window=None, sinks=0, scale=None,
+                workspace=None):
+    """Attention of several drafted tokens per sequence, q [T, H, d] bf16, over the
+    cached keys and values of its sequence, the drafted ones among them: (o bf16
+    [T, H, d], lse fp32 [T, H]).
+
+    cu_q int32 [B + 1] on the device: sequence b's tokens are rows cu_q[b] ..
+    cu_q[b + 1], and the last ones of its seq_lens[b] keys; without it each sequence
+    has one. A token sees the keys before its sequence's drafted ones and, of these,
+    those that its mask names, int64 [T] or [T, words] on the device: bit x % 64 of
+    word x // 64 for the sequence's x-th drafted token, its own bit among them;
+    without a mask those up to itself (a chain of drafts, or the next tokens of a
+    prompt).
+
+    With a ``window`` a token at place p sees of the keys before the drafts (without a
+    mask: of all) those after p - window and the first ``sinks``; its place is that
+    of the drafts' first key plus its place in the chain, or plus the number of its
+    mask's bits less one. Pages between the sinks and the window of a token at the
+    drafts' first key need not be there. q is taken as it is: rotate it with rope_fwd, the new keys
+    in cache_append.
+
+    A token that sees nothing, or whose sequence has length 0, gives o = 0 and
+    lse = -inf; rows of no sequence are not written. The GPU reads lengths, offsets,
+    masks and tables, so a captured call follows their contents."""
+    try:
+        key = (_form(q), _form(page_table), _form(seq_lens), _form(cu_q), _form(mask), cache._key, window,
+               sinks)
+        lay = _TREE_LAYOUTS.get(key)
+    except AttributeError:
+        lay = key = None
+    if lay is None:
+        lay = _tree_layout(cache, q, page_table, seq_lens, cu_q, mask, window, sinks)
+        _TREE_LAYOUTS.add(key, lay)
+    sq, row, wide, B, T, H, d, mask_row, words, need = lay
+    dev = cache.device
+    qp = q.data_ptr()
+    if qp & 15:
+        raise _off_boundary("q")
+    if workspace is None:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    elif workspace.numel() * workspace.element_size() < need or workspace.device != dev or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {dev}")
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = torch.empty((T, H), device=dev, dtype=torch.float32)
+    _launch(dev, lib().attn_decode_tree, cache._at(), qp, sq, page_table.data_ptr(), row, wide,
+            seq_lens.data_ptr(), B, None if cu_q is None else cu_q.data_ptr(), T, H,
+            None if mask is None else mask.data_ptr(), mask_row, words, window or 0, sinks,
+            _scale(scale, d), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), need)
+    return o, lse
+
+
+_TREE_LAYOUTS = _Layouts()
+
+
+def _tree_layout(cache, q, page_table, seq_lens, cu_q, mask, window, sinks):
+    """Checks a tree decode's arguments: strides and sizes as the C ABI takes them, and
+    the bytes of workspace."""
+    if not isinstance(cache, PagedCache):
+        raise ValueError("cache must be a PagedCache")
+    sq = _rows(q, "q", 3)
+    T, H, d = q.shape
+    if T < 1 or d != cache.d or H < 1 or H % cache.H_kv:
+        raise ValueError(f"q must be [T, a multiple of {cache.H_kv}, {cache.d}], got {tuple(q.shape)}")
+    if q.device != cache.device:
+        raise ValueError(f"q must be on {cache.device}")
+    B = cache._batch(page_table, seq_lens)
+    if cu_q is not None:
+        _int32(cu_q, "cu_q", cache.device, 1)
+        if cu_q.shape[0] != B + 1:
+            raise ValueError(f"cu_q must have {B + 1} entries, got {cu_q.shape[0]}")
+    elif T != B:
+        raise ValueError(f"without cu_q there is one token per sequence: {B}, got {T}")
+    mask_row = words = 0
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dtype != torch.int64 or mask.dim() not in (1, 2):
+            raise ValueError("mask must be an int64 [T] or [T, words] tensor")
+        words = mask.shape[1] if mask.dim() == 2 else 1
+        if mask.device != cache.device or mask.shape[0] != T or not 1 <= words <= MAX_MASK_WORDS:
+            raise ValueError(f"mask must be [{T}] or [{T}, 1 to {MAX_MASK_WORDS}] on {cache.device}, "
+                             f"got {tuple(mask.shape)} on {mask.device}")
+        if words > 1 and mask.stride(1) != 1:
+            raise ValueError("mask must be contiguous in its last dimension")
+        mask_row = mask.stride(0)
+        if mask_row < 0:
+            raise ValueError("mask's rows must not run backwards")
+    window, sinks = _window(window, sinks)
+    return (_Strides2(*sq), page_table.stride(0), page_table.shape[1], B, T, H, d, mask_row, words,
+            decode_tree_workspace_size(cache, T, B, H))
 
 
 # ---------------------------------------------------------------------------

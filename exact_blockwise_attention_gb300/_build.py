@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libattn.so")
 
 SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_merge.cu", "attn_short.cu",
            "attn_noalloc.cu", "attn_rope.cu", "attn_decode.cu",
-           "attn_decode_window.cu", "attn_pages.cu", "attn_window_fwd.cu", "attn_window_bwd.cu"]
+           "attn_decode_window.cu", "attn_pages.cu", "attn_window_fwd.cu", "attn_window_bwd.cu",
+           "attn_tree.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

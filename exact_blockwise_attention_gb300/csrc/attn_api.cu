@@ -15,6 +15,7 @@
 #include "cache_kernels.h"
 #include "kernels.h"
 #include "pages_kernels.h"
+#include "tree_kernels.h"
 
 namespace {
 
@@ -441,6 +442,12 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
   p.slots = 2 * static_cast<size_t>(wave) * p.rows * p.per_item;
   p.bytes = wave * sizeof(int2) + p.slots * (d + 2) * sizeof(float);
   return p;
+}
+
+// The workspace of a tree decode: see TreeArgs.
+size_t tree_bytes(int d) {
+  constexpr size_t kParts = 2 * eba::kTreeCtas * static_cast<size_t>(eba::kTreeRows);
+  return eba::kTreeCtas * (sizeof(int4) + sizeof(int2)) + kParts * (d + 2) * sizeof(float);
 }
 
 // Both decodes; window 0: all of a sequence's keys.
@@ -1249,6 +1256,82 @@ int attn_decode_window(const attn_cache_t* cache, const void* q, const long long
   if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
   return decode(cache, q, q_strides, page_table, table_stride, max_pages, seq_lens, B, H, window,
                 sinks, scale, rope, pos, pos_stride, o, lse, workspace, workspace_bytes, stream);
+}
+
+size_t attn_decode_tree_workspace_size(int T, int B, int H, int H_kv, int d) {
+  if (T < 1 || B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
+  return tree_bytes(d);
+}
+
+int attn_decode_tree(const attn_cache_t* cache, const void* q, const long long* q_strides,
+                     const int* page_table, long long table_stride, int max_pages,
+                     const int* seq_lens, int B, const int* cu_q, int T, int H,
+                     const long long* mask, long long mask_stride, int mask_words, int window,
+                     int sinks, float scale, void* o, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  int s = check_cache(cache);
+  if (s != ATTN_OK) return s;
+  if (!q_strides) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_table(page_table, table_stride, max_pages, seq_lens, B)) != ATTN_OK) return s;
+  if (T < 1 || (!cu_q && T != B) || H < 1 || H % cache->H_kv != 0) return ATTN_ERR_INVALID_ARG;
+  if (mask && (mask_words < 1 || mask_stride < 0)) return ATTN_ERR_INVALID_ARG;
+  if (mask && mask_words > ATTN_MAX_MASK_WORDS) return ATTN_ERR_UNSUPPORTED;
+  if (window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * kLog2e) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  if ((s = check_ptrs({q, o, lse})) != ATTN_OK) return s;
+  if ((s = check_strides(q_strides, 2, 8)) != ATTN_OK) return s;
+  const int group = H / cache->H_kv;
+  const long long max_len = std::min(static_cast<long long>(max_pages) * cache->page_size,
+                                     (1ll << 31) - 1 - 4 * eba::kTreeKeys);
+  // items of 128 rows, tiles of 128 keys (the sinks' and the window's may each be partly filled)
+  const long long rows = static_cast<long long>(T) * group;
+  const double items = (static_cast<double>(rows) / eba::kTreeRows + std::min(T, B)) * cache->H_kv;
+  const double item_tiles = static_cast<double>(max_len) / eba::kTreeKeys + 2;
+  if (static_cast<long long>(T) * H >= (1ll << 31) - eba::kTreeRows || items * item_tiles >= 2147483647.0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < tree_bytes(cache->d)) return ATTN_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  eba::TreeArgs a{};
+  const int esz = cache->type == ATTN_CACHE_E4M3 ? 1 : 2;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_token = q_strides[0];
+  a.q_head = q_strides[1];
+  a.k = static_cast<const unsigned char*>(cache->k);
+  a.v = static_cast<const unsigned char*>(cache->v);
+  for (int i = 0; i < 3; ++i) {
+    a.k_strides[i] = cache->k_strides[i] * esz;
+    a.v_strides[i] = cache->v_strides[i] * esz;
+  }
+  a.cache = *cache;
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.lens = seq_lens;
+  a.cu = cu_q;
+  a.mask = mask;
+  a.mask_stride = mask_stride;
+  a.words = mask_words;
+  a.max_len = static_cast<int>(max_len);
+  a.T = T;
+  a.B = B;
+  a.H = H;
+  a.group = group;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale_log2 = scale * kLog2e;
+  a.o_scale = cache->v_scale;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.item = static_cast<int4*>(workspace);
+  a.cut = reinterpret_cast<int2*>(a.item + eba::kTreeCtas);
+  a.part_o = reinterpret_cast<float*>(a.cut + eba::kTreeCtas);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + 2 * eba::kTreeCtas * static_cast<size_t>(eba::kTreeRows) * cache->d);
+  a.status = status_word_ptr();
+  if (!a.status) return ATTN_ERR_CUDA;
+  a.limit_ns = g_wait_limit_ns.load();
+  const int ctas = static_cast<int>(std::min<double>(eba::kTreeCtas, std::ceil(items * item_tiles)));
+  cudaError_t e = eba::launch_tree(a, ctas, max_len > eba::kTreeKeys || (window > 0 && sinks > 0),
+                                   static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
 int attn_pages_release(const attn_pool_t* pool, int* page_table, long long table_stride,

@@ -1,0 +1,953 @@
+// Attention of several drafted tokens per sequence over a paged key-value cache.
+//
+// The rows of a K/V head are the sequence's n tokens times the G query heads that read
+// it, n G rows in items of 128. Row r (token i) sees context key j < c within its window
+// and those drafted keys c + x whose bit x its mask has:
+//   s_j = scale q . k_j,  M = max s_j,  O = sum e^(s_j - M) v_j / L,  L = sum e^(s_j - M),
+//   lse = M + ln L,
+// and parts of the keys join exactly as in the single-token decode (decode.cuh).
+//
+// Each cached element is read once for up to 128 rows: up to 256 flops a byte (bf16),
+// which the warp matrix instruction of the single-token kernel cannot keep up with and
+// tcgen05 can: of a tile of 128 keys of 128 elements, 64 KB and 1.4 us of an SM's share
+// of the HBM rate, the products take 0.75 us. So the kernel is built to keep loads on
+// their way:
+//  - The list of all 128-key tiles of all (sequence, K/V head, 128 rows) items is cut
+//    into equal runs, one per CTA, as in decode.cuh: lengths need not be known to the
+//    host. Items cut between CTAs leave fp32 parts that the join kernel adds up in order.
+//  - Four warps load. bf16: cp.async, 16 bytes a lane, straight into the swizzled tiles,
+//    three K and three V tiles, four halves ahead. e4m3: into 16 KB stages, each lane's
+//    own, from which it widens its bytes to fp16 (exact) into two K and two V tiles.
+//    A lane looks its row's page up two tiles ahead. Keys that no row of the item sees
+//    are not read: their rows are zeros.
+//  - Two softmax warpgroups take the tiles in turn, each with its own maximum, sums and
+//    accumulator in tensor memory; a thread owns a row. At an item's end each thread
+//    joins one half of a row's columns of both. S_t and P_t share 128 columns:
+//    P is two bf16 terms (P = hi + lo to 2^-15, as in decode.cuh), or with an e4m3
+//    cache fp16 (2^-12, and q scaled per row by a power of two into fp16's range).
+//  - The QK and the two PV products are issued by threads of three warps (see fwd.cuh
+//    for why one is not enough).
+// Tensor memory: S_0 [0,128) S_1 [128,256) O_0 [256,256+d) O_1 [256+d,256+2d); P_t at S_t.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cfloat>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tree_kernels.h"
+
+namespace eba {
+namespace {
+
+constexpr int kSoftmax = 256;  // threads: two warpgroups
+constexpr int kWarpLoad = 8, kWarpIssue = 12;  // first warps of the loaders and the issuers
+constexpr int kBlock = 512;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kRegsSoftmax = 184, kRegsLoad = 88, kRegsIssue = 56;
+constexpr int kRegsAtLaunch = (256 * kRegsSoftmax + 128 * kRegsLoad + 128 * kRegsIssue) / kBlock;
+static_assert(kRegsAtLaunch == 128, "register split must add up to the launch allocation");
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kSlack = 8.f;     // scores may pass the reference by a factor 2^8
+constexpr float kF16Shift = 7.f;  // e4m3 caches: P's largest value is 2^(8 + 7)
+
+template <int D, bool F8>
+struct Layout {
+  static constexpr int kRow = D * (F8 ? 1 : 2);        // bytes of a cached row
+  static constexpr int kTile = kTreeKeys * D * 2;      // of 16-bit elements, for the products
+  static constexpr int kAtom = kTreeKeys * 128;        // 64 elements wide
+  static constexpr int kSlots = F8 ? 2 : 3;            // of K, and of V
+  static constexpr int kAhead = 4;                     // halves (K or V tiles) on their way
+  static constexpr int kRaw = F8 ? kTreeKeys * kRow : 0;  // a stage of stored bytes
+  static constexpr int kMasks = 8;                     // tiles whose key masks are kept
+  static constexpr int offQ = 0;
+  static constexpr int offK = offQ + kTreeRows * D * 2;
+  static constexpr int offV = offK + kSlots * kTile;
+  static constexpr int offRaw = offV + kSlots * kTile;
+  static constexpr int offMl = offRaw + kAhead * kRaw;     // [2][128] a warpgroup's reference and sum
+  static constexpr int offQs = offMl + 2 * kTreeRows * 8;  // [128] score factors (e4m3)
+  static constexpr int offKeys = offQs + (F8 ? kTreeRows * 4 : 0);  // [kMasks][4]: keys that are there
+  static constexpr int nBar = 4 * kSlots + 2 + 6 + 1 + 3;
+  static constexpr int offBar = offKeys + kMasks * 16;
+  static constexpr int offMisc = offBar + nBar * 8;          // tensor memory's address, abort flag
+  static constexpr int offScan = offMisc + 8;                // [16]
+  static constexpr int offFirst = offScan + 64;
+  static constexpr int kBytes = offFirst + 64;
+  // d = 128 fills shared memory to within a few hundred bytes of the limit, leaving no room
+  // to realign the base: the kernel checks instead that it lies on a 1024-byte boundary.
+  static constexpr bool kAlignSlack = D == 64;
+  static constexpr int kAlloc = kBytes + (kAlignSlack ? 1024 : 0);
+  static_assert(kAlloc <= 232448, "shared memory over the limit");
+  static constexpr uint32_t cS = 0, cO = 256;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Two e4m3 bytes -> two fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+// The largest bf16 strictly below p > 0 (0 for 0), as fp32 bits (see decode.cuh).
+__device__ __forceinline__ uint32_t below(float p) {
+  return (max(__float_as_uint(p), 1u) - 1u) & 0xFFFF0000u;
+}
+// Instruction descriptor of fp16 operands: idesc_bf16 without the type bits.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn, bool f16) {
+  return idesc_bf16(M, N, false, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// ---- the list of tiles -----------------------------------------------------------------
+
+// A sequence: its first row of q, tokens, cached keys (the tokens are the last ones).
+// Without its tokens in the cache (an empty slot of a padded batch) it has no items.
+struct Seq {
+  int c0, n, len, items;
+};
+__device__ __forceinline__ Seq sequence(const TreeArgs& a, int b) {
+  Seq s;
+  const int c0 = a.cu ? a.cu[b] : b, c1 = a.cu ? a.cu[b + 1] : b + 1;
+  s.c0 = min(max(c0, 0), a.T);
+  s.n = min(max(c1, s.c0), a.T) - s.c0;
+  s.len = min(max(a.lens[b], 0), a.max_len);
+  s.items = s.len >= s.n ? (s.n * a.group + kTreeRows - 1) / kTreeRows : 0;
+  return s;
+}
+// What is wrong with a sequence's numbers.
+__device__ __forceinline__ bool faulty(const TreeArgs& a, int b) {
+  const int raw = a.lens[b], c0 = a.cu ? a.cu[b] : b, c1 = a.cu ? a.cu[b + 1] : b + 1;
+  return raw < 0 || raw > a.max_len || c0 < 0 || c1 < c0 || c1 > a.T || (raw > 0 && raw < c1 - c0);
+}
+
+// Keys that any row of an item sees: the sinks [0, sunk), then [low, high).
+struct Keys {
+  int sunk, low, high;
+  __device__ __forceinline__ int sink_tiles() const { return (sunk + kTreeKeys - 1) / kTreeKeys; }
+  __device__ __forceinline__ int tiles() const {
+    return sink_tiles() + (high - low + kTreeKeys - 1) / kTreeKeys;
+  }
+  // first key of tile t, and the end of those that count
+  __device__ __forceinline__ int from(int t) const {
+    return t < sink_tiles() ? t * kTreeKeys : low + (t - sink_tiles()) * kTreeKeys;
+  }
+  __device__ __forceinline__ int end(int t) const { return t < sink_tiles() ? sunk : high; }
+};
+__device__ __forceinline__ Keys item_keys(const TreeArgs& a, const Seq& s, int qt) {
+  const int ctx = s.len - s.n;
+  const int i0 = qt * kTreeRows / a.group, i1 = min((qt * kTreeRows + kTreeRows - 1) / a.group, s.n - 1);
+  Keys k;
+  // a row's place is ctx + i, or, of a tree, at least ctx
+  k.low = a.window == 0 ? 0 : max(0, ctx + (a.mask ? 0 : i0) + 1 - a.window);
+  k.high = a.mask ? s.len : ctx + i1 + 1;
+  k.sunk = min(a.sinks, k.low);
+  return k;
+}
+
+// A place in the list: tile t of nt of an item.
+struct Cursor {
+  int b, hh, qt, t, nt;
+  Seq s;
+  Keys k;
+};
+__device__ __forceinline__ void set_item(Cursor& c, const TreeArgs& a) {
+  c.k = item_keys(a, c.s, c.qt);
+  c.nt = c.k.tiles();
+  c.t = 0;
+}
+__device__ __forceinline__ void next_item(Cursor& c, const TreeArgs& a) {
+  if (++c.qt == c.s.items) {
+    c.qt = 0;
+    if (++c.hh == a.cache.H_kv) {
+      c.hh = 0;
+      do {
+        if (++c.b == a.B) return;  // behind the list: not used
+        c.s = sequence(a, c.b);
+      } while (c.s.items == 0);
+    }
+  }
+  set_item(c, a);
+}
+__device__ __forceinline__ void advance(Cursor& c, const TreeArgs& a) {
+  if (++c.t == c.nt) next_item(c, a);
+}
+// Tiles of one of a sequence's heads.
+__device__ __forceinline__ int head_tiles(const TreeArgs& a, const Seq& s) {
+  int n = 0;
+  for (int qt = 0; qt < s.items; ++qt) n += item_keys(a, s, qt).tiles();
+  return n;
+}
+
+__device__ __forceinline__ int first_tile(int i, int tiles, int ctas) {
+  return static_cast<int>(static_cast<long long>(i) * tiles / ctas);
+}
+// The run that tile t is in.
+__device__ __forceinline__ int run_of(int t, int tiles, int ctas) {
+  int i = static_cast<int>(static_cast<long long>(t) * ctas / tiles);
+  while (i + 1 < ctas && first_tile(i + 1, tiles, ctas) <= t) ++i;
+  return i;
+}
+
+// ---- masks -------------------------------------------------------------------------------
+
+// Bits [lo, hi) of a 32-bit word.
+__device__ __forceinline__ uint32_t bits(int lo, int hi) {
+  lo = min(max(lo, 0), 32);
+  hi = min(max(hi, 0), 32);
+  const uint32_t below_hi = hi == 32 ? ~0u : (1u << hi) - 1u, below_lo = lo == 32 ? ~0u : (1u << lo) - 1u;
+  return below_hi & ~below_lo;
+}
+// Bits x .. x + 31 of a mask of `words` 64-bit words (0 outside).
+__device__ __forceinline__ uint32_t mask_bits(const long long* m, int words, int x) {
+  if (x <= -32 || x >= 64 * words) return 0u;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(m);
+  const int at = x >> 5, sh = x & 31;  // (x may be negative: at = -1)
+  const uint32_t lo = at >= 0 ? w[at] : 0u, hi = at + 1 < 2 * words ? w[at + 1] : 0u;
+  return __funnelshift_r(lo, hi, sh);
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
+  using L = Layout<D, F8>;
+  constexpr int kSlots = L::kSlots, kAhead = L::kAhead;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  if (!L::kAlignSlack && (raw_base & 1023u) != 0) {
+    pdl_wait();
+    if (threadIdx.x == 0) atomicExch(a.status, DEV_SMEM_ALIGN);
+    return;
+  }
+  const uint32_t sbase = (raw_base + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw_base);
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const uint32_t bar0 = sbase + L::offBar;
+  auto k_full = [&](int s) { return bar0 + 8u * s; };
+  auto k_empty = [&](int s) { return bar0 + 8u * (kSlots + s); };
+  auto v_full = [&](int s) { return bar0 + 8u * (2 * kSlots + s); };
+  auto v_empty = [&](int s) { return bar0 + 8u * (3 * kSlots + s); };
+  const uint32_t b1 = bar0 + 8u * (4 * kSlots);
+  const uint32_t q_full = b1, q_empty = b1 + 8;
+  auto s_full = [&](int t) { return b1 + 16 + 8u * t; };
+  auto p_full = [&](int t) { return b1 + 32 + 8u * t; };
+  auto o_done = [&](int t) { return b1 + 48 + 8u * t; };
+  const uint32_t o_free = b1 + 64;  // the item's end has read both accumulators
+  auto mma_done = [&](int i) { return b1 + 72 + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
+  int* s_scan = reinterpret_cast<int*>(smem + L::offScan);
+  Cursor& s_first = *reinterpret_cast<Cursor*>(smem + L::offFirst);
+  static_assert(sizeof(Cursor) <= 64, "");
+  const DeviceStatus st{a.status, a.limit_ns};
+
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(k_full(s), 128);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 128);
+      mbar_init(v_empty(s), 1);
+    }
+    mbar_init(q_full, 128);
+    mbar_init(q_empty, F8 ? 1 + kSoftmax : 1);  // the item's last product; its factors are read
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full(t), 2);  // the product's commit, and the issuing thread
+      mbar_init(p_full(t), 128);
+      mbar_init(o_done(t), 1);
+    }
+    mbar_init(o_free, kSoftmax);
+    for (int i = 0; i < 3; ++i) mbar_init(mma_done(i), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpIssue) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+
+  // ---- this CTA's run: each thread counts a run of sequences ----
+  const int cta = blockIdx.x;
+  const int per = (a.B + kBlock - 1) / kBlock;
+  const int b0 = min(tid * per, a.B), b_end = min(b0 + per, a.B);
+  int mine = 0;
+  for (int b = b0; b < b_end; ++b) {
+    if (cta == 0 && faulty(a, b)) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+    mine += head_tiles(a, sequence(a, b)) * a.cache.H_kv;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, m);
+    if (lane >= m) incl += o;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int before = 0, tiles = 0;
+#pragma unroll
+  for (int w = 0; w < kBlock / 32; ++w) {
+    before += w < warp ? s_scan[w] : 0;
+    tiles += s_scan[w];
+  }
+  const int G = max(1, min(static_cast<int>(gridDim.x), tiles));  // no run is empty
+  const int r0 = cta < G ? first_tile(cta, tiles, G) : tiles;
+  const int r1 = cta < G ? first_tile(cta + 1, tiles, G) : tiles;
+  {
+    int at = before + incl - mine;
+    if (r0 < r1 && r0 >= at && r0 < at + mine) {
+      for (int b = b0; b < b_end; ++b) {
+        Cursor c;
+        c.s = sequence(a, b);
+        const int ht = head_tiles(a, c.s);
+        if (r0 < at + ht * a.cache.H_kv) {
+          int in = r0 - at;
+          c.b = b;
+          c.hh = in / ht;
+          in -= c.hh * ht;
+          for (c.qt = 0;; ++c.qt) {
+            set_item(c, a);
+            if (in < c.nt) break;
+            in -= c.nt;
+          }
+          c.t = in;
+          s_first = c;
+          break;
+        }
+        at += ht * a.cache.H_kv;
+      }
+    }
+  }
+  // Sequences without keys: O = 0, lse = -inf.
+  for (int b = cta; b < a.B; b += gridDim.x) {
+    const Seq s = sequence(a, b);
+    if (s.items > 0) continue;
+    const long long row0 = static_cast<long long>(s.c0) * a.H, rows = static_cast<long long>(s.n) * a.H;
+    for (long long x = tid; x < rows * (D / 8); x += kBlock)
+      *reinterpret_cast<uint4*>(a.o + row0 * D + x * 8) = make_uint4(0, 0, 0, 0);
+    for (long long x = tid; x < rows; x += kBlock) a.lse[row0 + x] = -INFINITY;
+  }
+  __syncthreads();
+  const int n_tiles = r1 - r0;
+
+  if (warp >= kWarpIssue) {
+    regs_decrease<kRegsIssue>();
+    const int role = warp - kWarpIssue;  // 0: QK, 1 / 2: PV of the even / odd tiles
+    if (role < 3 && lane == 0) {
+      constexpr uint32_t hi = sdesc_hi(1024);
+      constexpr uint32_t id_qk = idesc(kTreeRows, kTreeKeys, false, F8);
+      constexpr uint32_t id_pv = idesc(kTreeRows, D, true, F8);
+      const uint32_t q_lo = sdesc_lo(sbase + L::offQ, 16), k_lo = sdesc_lo(sbase + L::offK, 16);
+      const uint32_t v_lo = sdesc_lo(sbase + L::offV, L::kAtom);
+      bool ok = true;
+      Cursor c = s_first;
+      int item = 0;   // running index in this CTA
+      int own = -1;   // PV: the item of this thread's last tile
+      for (int n = 0; n < n_tiles && ok; ++n) {
+        const int slot = n % kSlots, t = n & 1;
+        const uint32_t sp = (n / kSlots) & 1;
+        const bool last = c.t + 1 == c.nt;
+        if (role == 0) {
+          if (c.t == 0 || n == 0) {
+            if (!(ok = mbar_wait(q_full, item & 1, abort_flag, st))) break;
+          }
+          if (!(ok = mbar_wait(k_full(slot), sp, abort_flag, st))) break;
+          // P_t of this accumulator's previous tile has been used
+          if (n > 1 && !(ok = mbar_wait(o_done(t), ((n >> 1) - 1) & 1, abort_flag, st))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * L::kAtom + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + L::cS + t * kTreeKeys, sdesc_join(q_lo + off, hi),
+                   sdesc_join(k_lo + slot * (L::kTile >> 4) + off, hi), id_qk, kk > 0);
+          }
+          mma_commit(k_empty(slot));
+          if (last) mma_commit(q_empty);
+          mma_commit(s_full(t));
+          mbar_arrive(s_full(t));  // what the loaders wrote for the softmax is visible behind this
+        } else if (t == role - 1) {
+          const bool first = own != item;  // this accumulator's first tile of the item
+          if (!(ok = mbar_wait(p_full(t), (n >> 1) & 1, abort_flag, st))) break;
+          if (!(ok = mbar_wait(v_full(slot), sp, abort_flag, st))) break;
+          if (first && item > 0 && !(ok = mbar_wait(o_free, (item - 1) & 1, abort_flag, st))) break;
+          own = item;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kTreeKeys / 16; ++kk) {
+            const uint64_t b = sdesc_join(v_lo + slot * (L::kTile >> 4) + kk * (2048 >> 4), hi);
+            const uint32_t p = tmem + L::cS + t * kTreeKeys + kk * (F8 ? 8 : 16), o = tmem + L::cO + t * D;
+            mma_ts(o, p, b, id_pv, !first || kk > 0);
+            if constexpr (!F8) mma_ts(o, p + 8, b, id_pv, 1u);
+          }
+          mma_commit(v_empty(slot));
+          mma_commit(o_done(t));
+        }
+        if (last) ++item;
+        if (n + 1 < n_tiles) advance(c, a);
+      }
+      // Every MMA this thread issued must be finished before tensor memory is released.
+      mma_commit(mma_done(role));
+      mbar_wait_drain(mma_done(role), 0, st);
+    }
+  } else if (warp >= kWarpLoad) {
+    regs_decrease<kRegsLoad>();
+    const int w = warp - kWarpLoad;           // rows 32 w .. 32 w + 31 of each tile
+    constexpr int kLanes = L::kRow / 16;      // of a row: 16 bytes each
+    constexpr int kRows = 32 / kLanes;        // of an instruction
+    const int c16 = lane % kLanes, r_lane = lane / kLanes;
+    uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + L::offKeys);
+    // look-ups, two tiles ahead of the loads
+    Cursor look = s_first;
+    int look_left = n_tiles;
+    int page_of[2] = {}, slot_of[2] = {-1, -1};  // slot -1: no such key
+    long long head_of[2] = {};                   // K/V head
+    auto look_up = [&]() {
+      page_of[0] = page_of[1], slot_of[0] = slot_of[1], head_of[0] = head_of[1];
+      page_of[1] = 0, slot_of[1] = -1;
+      if (look_left <= 0) return;
+      const int key = look.k.from(look.t) + 32 * w + lane;
+      head_of[1] = look.hh;
+      if (key < look.k.end(look.t)) {
+        const int entry = key / a.cache.page_size;
+        slot_of[1] = key - entry * a.cache.page_size;
+        page_of[1] = a.table[look.b * a.table_stride + entry];
+      }
+      if (--look_left > 0) advance(look, a);
+    };
+    look_up();
+    look_up();
+    // The half under way: tile n's K (even) or V (odd). Its rows' offsets stay for V.
+    long long v_off = 0;
+    uint32_t there = 0;
+    auto issue = [&](int h) {
+      if (h >= 2 * n_tiles) return;
+      const int n = h >> 1, slot = n % kSlots;
+      long long off;
+      if ((h & 1) == 0) {
+        const int page = page_of[0], sl = slot_of[0];
+        const bool held = sl >= 0;
+        const bool ok = held && static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages);
+        if (held && !ok) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+        off = ok ? page * a.k_strides[0] + sl * a.k_strides[1] + head_of[0] * a.k_strides[2] : 0;
+        v_off = ok ? page * a.v_strides[0] + sl * a.v_strides[1] + head_of[0] * a.v_strides[2] : 0;
+        there = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0) s_keys[(n % L::kMasks) * 4 + w] = there;
+        look_up();
+      } else {
+        off = v_off;
+      }
+      const unsigned char* base = (h & 1 ? a.v : a.k) + c16 * 16;
+      const uint32_t to = F8 ? sbase + L::offRaw + (h % kAhead) * L::kRaw + w * (L::kRaw / 4) + lane * 16
+                             : sbase + (h & 1 ? L::offV : L::offK) + slot * L::kTile;
+#pragma unroll
+      for (int i = 0; i < 32 / kRows; ++i) {
+        const int r = i * kRows + r_lane;
+        const unsigned char* p = base + __shfl_sync(0xffffffffu, off, r);
+        const uint32_t dst = F8 ? to + i * 512
+                                : to + (c16 >> 3) * L::kAtom + sw128_offset(32 * w + r, c16 & 7);
+        cp_async16(dst, p, (there >> r) & 1);
+      }
+    };
+    // an item's query rows: row x is token x / G, head x % G of the group; zeros behind
+    auto load_q = [&](const Cursor& c) {
+      constexpr int kChunks = D / 8;  // 16 bytes of a row each
+      constexpr int kPer = kTreeRows * kChunks / 128;  // of a thread
+      const int l = tid - 32 * kWarpLoad;
+      const int rows = min(kTreeRows, c.s.n * a.group - c.qt * kTreeRows);
+      float* s_qs = reinterpret_cast<float*>(smem + L::offQs);
+#pragma unroll
+      for (int x0 = 0; x0 < kPer; x0 += 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int id = (x0 + i) * 128 + l, row = id / kChunks, ch = id % kChunks;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (row < rows) {
+            const int at = c.qt * kTreeRows + row, token = at / a.group, g = at - token * a.group;
+            x[i] = *reinterpret_cast<const uint4*>(a.q + (c.s.c0 + token) * a.q_token +
+                                                   (static_cast<long long>(c.hh) * a.group + g) * a.q_head + ch * 8);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int id = (x0 + i) * 128 + l, row = id / kChunks, ch = id % kChunks;
+          uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          if constexpr (F8) {
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float u = fabsf(bf16lo_f32(y[e])), v = fabsf(bf16hi_f32(y[e]));
+              top = fmaxf(top, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
+            }
+#pragma unroll
+            for (int m = kChunks / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+            // 2^e brings the row's largest element into [2^13, 2^14) (see decode.cuh)
+            const int floor_log2 = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            const int e2 = top > 0.f ? min(13 - floor_log2, 126) : 0;
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+            if (ch == 0) s_qs[row] = fminf(a.scale_log2 * (a.cache.k_scale * down), FLT_MAX);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = pack_f16(bf16lo_f32(y[e]) * up, bf16hi_f32(y[e]) * up);
+          }
+          st_shared_v4(sbase + L::offQ + (ch >> 3) * L::kAtom + sw128_offset(row, ch & 7), y[0], y[1], y[2], y[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+    };
+
+    Cursor c = s_first;
+    int item = 0;
+    bool ok = true;
+    // bf16: the slots of the first kAhead halves are free
+    for (int h = 0; h < kAhead; ++h) {
+      issue(h);
+      cp_async_commit();
+    }
+#pragma unroll 1
+    for (int h = 0; h < 2 * n_tiles && ok; ++h) {
+      const int n = h >> 1, slot = n % kSlots;
+      const bool keys = (h & 1) == 0;
+      if (keys && (c.t == 0 || n == 0)) {
+        // the query's buffer is free once the previous item's last product has read it
+        if (item > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (item - 1) & 1, abort_flag, st)))) break;
+        load_q(c);
+      }
+      cp_async_wait<kAhead - 1>();
+      const uint32_t full = keys ? k_full(slot) : v_full(slot);
+      if constexpr (F8) {
+        // widen this lane's own bytes
+        const uint32_t empty = keys ? k_empty(slot) : v_empty(slot);
+        if (n >= kSlots &&
+            !(ok = __all_sync(0xffffffffu, mbar_wait(empty, ((n / kSlots) - 1) & 1, abort_flag, st))))
+          break;
+        const uint32_t from = sbase + L::offRaw + (h % kAhead) * L::kRaw + w * (L::kRaw / 4) + lane * 16;
+        const uint32_t to = sbase + (keys ? L::offK : L::offV) + slot * L::kTile;
+#pragma unroll
+        for (int i = 0; i < 32 / kRows; ++i) {
+          const uint4 x = ld_shared_v4(from + i * 512);
+          const int row = 32 * w + i * kRows + r_lane;
+          const uint32_t at = to + (c16 >> 2) * L::kAtom;
+          const int ch = (c16 & 3) * 2;
+          st_shared_v4(at + sw128_offset(row, ch), e4m3x2_f16x2(x.x), e4m3x2_f16x2(x.x >> 16),
+                       e4m3x2_f16x2(x.y), e4m3x2_f16x2(x.y >> 16));
+          st_shared_v4(at + sw128_offset(row, ch + 1), e4m3x2_f16x2(x.z), e4m3x2_f16x2(x.z >> 16),
+                       e4m3x2_f16x2(x.w), e4m3x2_f16x2(x.w >> 16));
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(full);
+      if (!keys) {
+        if (c.t + 1 == c.nt) ++item;
+        if (n + 1 < n_tiles) advance(c, a);
+      }
+      // the next half: bf16 waits for its slot
+      const int h2 = h + kAhead, n2 = h2 >> 1;
+      if (!F8 && h2 < 2 * n_tiles && n2 >= kSlots) {
+        const uint32_t empty = h2 & 1 ? v_empty(n2 % kSlots) : k_empty(n2 % kSlots);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(empty, ((n2 / kSlots) - 1) & 1, abort_flag, st)))) break;
+      }
+      issue(h2);
+      cp_async_commit();
+    }
+    cp_async_wait<0>();
+  } else {
+    regs_increase<kRegsSoftmax>();
+    // ---- softmax: warpgroup t takes the run's tiles t, t + 2, ... ----
+    const int t = warp >> 2, sub = warp & 3;
+    const int row = sub * 32 + lane;  // of the item == lane of tensor memory
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+    const uint32_t tS = lane_base + L::cS + t * kTreeKeys, tO = lane_base + L::cO + t * D;
+    const uint32_t* s_keys = reinterpret_cast<const uint32_t*>(smem + L::offKeys);
+    float2* s_ml = reinterpret_cast<float2*>(smem + L::offMl);  // [warpgroup][row]
+    // A wait that gives up ends all waits; the warps still meet at every barrier, and
+    // what they write is undefined.
+    bool live = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (live) live = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, st));
+    };
+    Cursor c = s_first;
+    int n = 0, item = 0;
+    while (n < n_tiles) {
+      // ---- an item: its tiles [c.t, c.t + count) are the run's [n, n + count) ----
+      const int t_begin = c.t, count = min(c.nt - c.t, n_tiles - n);
+      const bool ends = c.t + count == c.nt;
+      const int at = c.qt * kTreeRows + row;  // of the sequence's rows
+      const bool has = at < c.s.n * a.group;
+      const bool some = __any_sync(0xffffffffu, has);
+      const int token = has ? at / a.group : 0, ctx = c.s.len - c.s.n;
+      const long long* mask = a.mask ? a.mask + (c.s.c0 + token) * a.mask_stride : nullptr;
+      int place = ctx + token;
+      if (mask) {
+        int ones = 0;
+        for (int x = 0; x < 2 * a.words; ++x)
+          ones += __popc(mask_bits(mask, a.words, 32 * x) & bits(0, c.s.n - 32 * x));
+        place = ctx + max(ones, 1) - 1;
+      }
+      // the context keys that this row sees begin at `near`, and with a chain also the others
+      const int near = a.window == 0 ? 0 : place - a.window + 1;
+      float m_used = -INFINITY, l_sum = 0.f;
+      float qs = a.scale_log2;
+      int mine = 0;  // tiles of this warpgroup
+      if (F8 && count == 1 && (n & 1) != t) mbar_arrive(q_empty);
+      for (int x = 0; x < count; ++x) {
+        const int nn = n + x;
+        if ((nn & 1) != t) continue;
+        const int tile = t_begin + x, k0 = c.k.from(tile);
+        wait(s_full(t), (nn >> 1) & 1);
+        tc_fence_after();
+        if (F8 && mine == 0) {
+          qs = reinterpret_cast<const float*>(smem + L::offQs)[row];
+          mbar_arrive(q_empty);
+        }
+        ++mine;
+        if (!some) {  // no row of this warp: its part of P is not looked at
+          tc_fence_before();
+          mbar_arrive(p_full(t));
+          continue;
+        }
+        // the keys that this row sees
+        uint32_t see[4];
+        bool all = true;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int k1 = k0 + 32 * y;
+          uint32_t u;
+          if (mask) {
+            u = bits(near - k1, ctx - k1) | bits(0, min(a.sinks, ctx) - k1);
+            if (k1 + 32 > ctx) u |= mask_bits(mask, a.words, k1 - ctx) & bits(ctx - k1, c.s.len - k1);
+          } else {
+            u = bits(near - k1, place + 1 - k1) | bits(0, min(a.sinks, place + 1) - k1);
+          }
+          see[y] = u & s_keys[(nn % L::kMasks) * 4 + y];
+          all &= see[y] == ~0u;
+        }
+        all = __all_sync(0xffffffffu, all);
+        auto hide = [&](uint32_t (&x)[32], uint32_t word) {
+          if (all) return;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((word >> i) & 1)) x[i] = 0xff800000u;  // -inf
+        };
+        // Two passes over the row, 32 scores at a time: they stay in tensor memory in between.
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t sc[2][32];
+        tmem_ld32(tS, sc[0]);
+        tmem_wait_ld();
+        reg_pin(sc[0]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t(&r)[32] = sc[y & 1];
+          if (y < 3) tmem_ld32(tS + 32 * (y + 1), sc[(y + 1) & 1]);
+          hide(r, see[y]);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              m4[u] = fmax3(m4[u], __uint_as_float(r[i + u]), __uint_as_float(r[i + 4 + u]));
+          if (y < 3) {
+            tmem_wait_ld();
+            reg_pin(sc[(y + 1) & 1]);
+          }
+        }
+        tmem_ld32(tS, sc[0]);
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qs;
+        const float m_old = m_used;
+        const bool bump = mx > m_used + kSlack;
+        if (bump) m_used = mx;
+        // (a row that has seen no key yet has no maximum)
+        const float ref = (m_used == -INFINITY ? 0.f : m_used) - (F8 ? kF16Shift : 0.f);
+        const float2 qs2 = make_float2(qs, qs), neg = make_float2(-ref, -ref);
+        float2 sum = make_float2(0.f, 0.f);
+        tmem_wait_ld();
+        reg_pin(sc[0]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t(&r)[32] = sc[y & 1];
+          if (y < 3) tmem_ld32(tS + 32 * (y + 1), sc[(y + 1) & 1]);
+          hide(r, see[y]);
+          // P of 32 keys, two steps of a product: bf16 in the place of their scores, 8 columns
+          // of the first terms and 8 of the second for each step; fp16 8 columns a step
+          uint32_t w[F8 ? 16 : 32];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 z = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), qs2, neg);
+            const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+            sum = add2(sum, p);
+            if constexpr (F8) {
+              w[i] = pack_f16(p.x, p.y);
+            } else {
+              const uint32_t h0 = below(p.x), h1 = below(p.y);
+              w[(i >> 3) * 16 + (i & 7)] = __byte_perm(h0, h1, 0x7632);
+              w[(i >> 3) * 16 + 8 + (i & 7)] =
+                  pack_bf16(p.x - __uint_as_float(h0), p.y - __uint_as_float(h1));
+            }
+          }
+          if (y < 3) {
+            tmem_wait_ld();
+            reg_pin(sc[(y + 1) & 1]);
+          }
+          if constexpr (F8)
+            tmem_st16(tS + 16 * y, w);
+          else
+            tmem_st32(tS + 32 * y, w);
+        }
+        // (the previous product into O_t was done before this tile's scores were computed)
+        if (mine > 1 && __any_sync(0xffffffffu, bump)) {
+          const float alpha = bump ? ex2_approx(m_old - m_used) : 1.f;
+          l_sum *= alpha;
+#pragma unroll
+          for (int y = 0; y < D / 32; ++y) {
+            uint32_t ov[32];
+            tmem_ld32(tO + 32 * y, ov);
+            tmem_wait_ld();
+            reg_pin(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(tO + 32 * y, ov);
+          }
+        }
+        l_sum += sum.x + sum.y;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_full(t));
+      }
+
+      // ---- the item's end, or the run's: join the two accumulators ----
+      {
+        const int last = n + count - 1;  // the warpgroup's last tile is it or the one before
+        const int mine_last = (last & 1) == t ? last : last - 1;
+        if (mine > 0) wait(o_done(t), (mine_last >> 1) & 1);
+        const float ref = m_used == -INFINITY ? -INFINITY : m_used - (F8 ? kF16Shift : 0.f);
+        s_ml[t * kTreeRows + row] = make_float2(ref, l_sum);
+        tc_fence_before();
+        named_bar_sync(1, kSoftmax);
+        tc_fence_after();
+        const float2 ml0 = s_ml[row], ml1 = s_ml[kTreeRows + row];
+        named_bar_sync(1, kSoftmax);  // the next item's are written behind this
+        const float M = fmaxf(ml0.x, ml1.x);
+        const float f0 = ml0.x == -INFINITY ? 0.f : ex2_approx(ml0.x - M);
+        const float f1 = ml1.x == -INFINITY ? 0.f : ex2_approx(ml1.x - M);
+        const float l = ml0.y * f0 + ml1.y * f1;
+        const bool whole = t_begin == 0 && ends;
+        const float mul = !whole ? 1.f : M == -INFINITY ? 0.f : a.o_scale / l;
+        const long long out = (static_cast<long long>(c.s.c0) + token) * a.H + c.hh * a.group + at % a.group;
+        const long long slot = 2 * cta + (item == 0 ? 0 : 1);
+        if (has && t == 0) {
+          if (whole)
+            a.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+          else
+            a.part_ml[slot * kTreeRows + row] = make_float2(M, l);
+        }
+        if (some) {
+#pragma unroll
+          for (int y = 0; y < D / 64; ++y) {
+            const int col = t * (D / 2) + 32 * y;
+            float x[32];
+            uint32_t u[32];
+            tmem_ld32(lane_base + L::cO + col, u);
+            tmem_wait_ld();
+            reg_pin(u);
+            // (an accumulator without a weight may hold anything)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = f0 > 0.f ? __uint_as_float(u[i]) * f0 : 0.f;
+            tmem_ld32(lane_base + L::cO + D + col, u);
+            tmem_wait_ld();
+            reg_pin(u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = (x[i] + (f1 > 0.f ? __uint_as_float(u[i]) * f1 : 0.f)) * mul;
+            if (!has) continue;
+            if (whole) {
+              uint4* to = reinterpret_cast<uint4*>(a.o + out * D + col);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                to[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                   pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+            } else {
+              float4* to = reinterpret_cast<float4*>(a.part_o + (slot * kTreeRows + row) * D + col);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                to[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(o_free);  // the next item's first products may overwrite the accumulators
+      }
+      n += count;
+      if (n == n_tiles && a.cut && tid == 0) {
+        // an item that begins in this run and goes on in the next ones
+        int parts = 0;
+        if (!ends && t_begin == 0) parts = run_of(r1 + c.nt - count - 1, tiles, G) - cta + 1;
+        a.cut[cta] = make_int2(item == 0 ? 0 : 1, parts);
+        a.item[cta] = make_int4(c.b, c.hh, c.qt, 0);
+      }
+      ++item;
+      if (n < n_tiles) {
+        c.t += count - 1;
+        advance(c, a);
+      }
+    }
+    if (n_tiles == 0 && a.cut && tid == 0) a.cut[cta] = make_int2(0, 0);
+  }
+
+  // ---- teardown ----
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpIssue) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Items cut between CTAs: their parts, in the order of the keys. blockIdx.x: the run that
+// the item begins in, y: 8 of its rows. Few parts: a warp a row; many: all warps a row,
+// one after the other.
+constexpr int kJoinWarps = 8, kDeep = 4, kFewParts = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kVec = D / 32;
+  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps];
+  const int c0 = blockIdx.x;
+  const int2 cut = a.cut[c0];
+  const int parts = cut.y;
+  if (parts == 0) return;
+  const int4 it = a.item[c0];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Seq s = sequence(a, it.x);
+  const int rows = min(kTreeRows, s.n * a.group - it.z * kTreeRows);
+  const bool few = parts <= kFewParts;
+  for (int i = 0; i < (few ? 1 : kJoinWarps); ++i) {
+    const int row = blockIdx.y * kJoinWarps + (few ? warp : i);
+    if (row >= rows) return;  // (many: all warps alike)
+    float M = -INFINITY, l = 0.f, o[kVec] = {};
+    const int step = few ? 1 : kJoinWarps;
+    for (int p0 = few ? 0 : warp; p0 < parts; p0 += step * kDeep) {
+      float2 ml[kDeep];
+      float v[kDeep][kVec];
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        const int p = p0 + u * step;
+        if (p >= parts) {
+          ml[u] = make_float2(-INFINITY, 0.f);
+          continue;
+        }
+        const long long at = (2 * (c0 + p) + (p == 0 ? cut.x : 0)) * static_cast<long long>(kTreeRows) + row;
+        ml[u] = a.part_ml[at];
+        const float* from = a.part_o + at * D + lane * kVec;
+#pragma unroll
+        for (int x = 0; x < kVec; x += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(from + x);
+          v[u][x] = y.x, v[u][x + 1] = y.y;
+        }
+      }
+      float to = M;
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) to = fmaxf(to, ml[u].x);
+      if (to == -INFINITY) continue;  // no weight so far
+      const float f = M == -INFINITY ? 0.f : ex2_approx(M - to);
+      M = to;
+      l *= f;
+#pragma unroll
+      for (int x = 0; x < kVec; ++x) o[x] *= f;
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        if (ml[u].x == -INFINITY) continue;
+        const float w = ex2_approx(ml[u].x - to);
+        l += ml[u].y * w;
+#pragma unroll
+        for (int x = 0; x < kVec; ++x) o[x] += v[u][x] * w;
+      }
+    }
+    const int at = it.z * kTreeRows + row, token = at / a.group;
+    const long long out = (static_cast<long long>(s.c0) + token) * a.H + it.y * a.group + at % a.group;
+    if (few) {
+      const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+#pragma unroll
+      for (int x = 0; x < kVec; x += 2)
+        *reinterpret_cast<uint32_t*>(a.o + out * D + lane * kVec + x) = pack_bf16(o[x] * f, o[x + 1] * f);
+      if (lane == 0) a.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+      continue;
+    }
+    if (lane == 0) s_ml[warp] = make_float2(M, l);
+#pragma unroll
+    for (int x = 0; x < kVec; ++x) s_o[warp][lane * kVec + x] = o[x];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      M = -INFINITY;
+      l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_ml[w].x);
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        if (s_ml[w].x == -INFINITY) continue;
+        const float f = ex2_approx(s_ml[w].x - M);
+        l += s_ml[w].y * f;
+        v += s_o[w][threadIdx.x] * f;
+      }
+      const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+      a.o[out * D + threadIdx.x] = __float2bfloat16_rn(v * f);
+      if (threadIdx.x == 0) a.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+    }
+    __syncthreads();
+  }
+}
+
+template <int D, bool F8>
+cudaError_t launch_tree_t(const TreeArgs& a, int ctas, bool join, cudaStream_t stream) {
+  using L = Layout<D, F8>;
+  auto kern = tree_kernel<D, F8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  // The warpgroups' register shares must fit the launch allocation, or an increase would
+  // wait forever: refuse to launch otherwise.
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs < kRegsAtLaunch) return cudaErrorInvalidConfiguration;
+  e = launch_pdl(kern, dim3(ctas), dim3(kBlock), L::kAlloc, stream, a);
+  if (e != cudaSuccess || !join) return e;
+  const int rows = std::min(kTreeRows, a.T * a.group);
+  return launch_pdl(tree_join_kernel<D>, dim3(ctas, (rows + kJoinWarps - 1) / kJoinWarps),
+                    dim3(32 * kJoinWarps), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tree(const TreeArgs& a, int ctas, bool join, cudaStream_t stream) {
+  const bool f8 = a.cache.type == ATTN_CACHE_E4M3;
+  if (a.cache.d == 64)
+    return f8 ? launch_tree_t<64, true>(a, ctas, join, stream) : launch_tree_t<64, false>(a, ctas, join, stream);
+  return f8 ? launch_tree_t<128, true>(a, ctas, join, stream) : launch_tree_t<128, false>(a, ctas, join, stream);
+}
+
+}  // namespace eba

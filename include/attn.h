@@ -460,6 +460,42 @@ int attn_decode_window(const attn_cache_t* cache, const void* q, const long long
                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * attn_decode_tree - attention of several drafted tokens per sequence over its cached
+ * keys, as a step of speculative decoding verifies them (or the next tokens of a prompt).
+ *   q [T, H, d] bf16, strides (token, head) as for attn_decode. cu_q: device int32
+ *   [B + 1], the tokens of sequence b are rows [cu_q[b], cu_q[b + 1]); NULL: one each
+ *   (T = B). seq_lens count them, the last ones of their sequences: they are in the cache.
+ *   The n tokens of a sequence with c = seq_lens[b] - n keys before them see
+ *   - mask NULL: token i, at the place p = c + i, the keys up to p, and of these with a
+ *     window those after p - window and the first `sinks`;
+ *   - mask: device int64 [T, mask_words] with rows mask_stride apart: token i sees the
+ *     drafted key c + x if bit x % 64 of its word x / 64 is set (bits of n and above do
+ *     not count; a token usually has its ancestors' bits and its own). Its place is
+ *     p = c - 1 + the number of its bits (of none: c), and of the keys before c it sees
+ *     all, or with a window those after p - window and the first `sinks`. mask_words <=
+ *     ATTN_MAX_MASK_WORDS.
+ *   window 0: none. With one, pages that lie wholly between the sinks and the window of
+ *   a sequence's first token (at the place c) are not looked up.
+ *   o [T, H, d] bf16, lse [T, H] fp32. A token that sees no key gives O = 0, lse = -inf,
+ *   and so do the tokens of a sequence of length 0 (an empty slot). Rows outside
+ *   [cu_q[0], cu_q[B]) are left as they were. Lengths and offsets out of range count as the
+ *   nearest in range, a length below the number of its tokens as 0, and both are recorded
+ *   as ATTN_ERR_PAGE.
+ *   workspace: attn_decode_tree_workspace_size(...) bytes, as for attn_decode.
+ * Deterministic as attn_decode, and of its precision (e4m3 caches: weights as fp16 to
+ * 2^-12). A NaN or infinite element of a drafted token's k or v may reach other tokens of
+ * its sequence.
+ */
+#define ATTN_MAX_MASK_WORDS 16
+size_t attn_decode_tree_workspace_size(int T, int B, int H, int H_kv, int d);
+int attn_decode_tree(const attn_cache_t* cache, const void* q, const long long* q_strides,
+                     const int* page_table, long long table_stride, int max_pages,
+                     const int* seq_lens, int B, const int* cu_q, int T, int H,
+                     const long long* mask, long long mask_stride, int mask_words, int window,
+                     int sinks, float scale, void* o, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
  * The pages of a cache whose page tables the GPU keeps: sequences share pages, take
  * free ones and give them back without the host knowing which.
  *
