@@ -1310,6 +1310,11 @@ int attn_decode_tree(const attn_cache_t* cache, const void* q, const long long* 
   a.mask = mask;
   a.mask_stride = mask_stride;
   a.words = mask_words;
+  // n / d for n < 2^31 as n * ceil(2^(31 + l) / d) >> 31 + l with 2^l >= d (Granlund, Montgomery)
+  int l = 0;
+  while ((1ll << l) < cache->page_size) ++l;
+  a.page_shift = 31 + l;
+  a.page_mul = static_cast<unsigned>(((1ull << a.page_shift) + cache->page_size - 1) / cache->page_size);
   a.max_len = static_cast<int>(max_len);
   a.T = T;
   a.B = B;

@@ -23,8 +23,8 @@
 //  - Two softmax warpgroups take the tiles in turn, each with its own maximum, sums and
 //    accumulator in tensor memory; a thread owns a row. At an item's end each thread
 //    joins one half of a row's columns of both. S_t and P_t share 128 columns:
-//    P is two bf16 terms (P = hi + lo to 2^-15, as in decode.cuh), or with an e4m3
-//    cache fp16 (2^-12, and q scaled per row by a power of two into fp16's range).
+//    P is bf16 as in the forward pass (fwd.cuh), or with an e4m3 cache fp16 (and q
+//    scaled per row by a power of two into fp16's range).
 //  - The QK and the two PV products are issued by threads of three warps (see fwd.cuh
 //    for why one is not enough).
 // Tensor memory: S_0 [0,128) S_1 [128,256) O_0 [256,256+d) O_1 [256+d,256+2d); P_t at S_t.
@@ -41,12 +41,13 @@ namespace eba {
 namespace {
 
 constexpr int kSoftmax = 256;  // threads: two warpgroups
-constexpr int kWarpLoad = 8, kWarpIssue = 12;  // first warps of the loaders and the issuers
-constexpr int kBlock = 512;
+constexpr int kWarpLoad = 8, kWarpIssue = 16;  // first warps of the loaders (of K, of V) and the issuers
+constexpr int kBlock = 640;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kRegsSoftmax = 184, kRegsLoad = 88, kRegsIssue = 56;
-constexpr int kRegsAtLaunch = (256 * kRegsSoftmax + 128 * kRegsLoad + 128 * kRegsIssue) / kBlock;
-static_assert(kRegsAtLaunch == 128, "register split must add up to the launch allocation");
+constexpr uint32_t kRegsSoftmax = 128, kRegsLoad = 80, kRegsIssue = 64;
+constexpr int kRegsAtLaunch = (256 * kRegsSoftmax + 256 * kRegsLoad + 128 * kRegsIssue) / kBlock;
+static_assert(kRegsAtLaunch == 96 && kRegsAtLaunch * kBlock == 256 * kRegsSoftmax + 256 * kRegsLoad + 128 * kRegsIssue,
+              "register split must add up to the launch allocation");
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 8.f;     // scores may pass the reference by a factor 2^8
 constexpr float kF16Shift = 7.f;  // e4m3 caches: P's largest value is 2^(8 + 7)
@@ -57,21 +58,22 @@ struct Layout {
   static constexpr int kTile = kTreeKeys * D * 2;      // of 16-bit elements, for the products
   static constexpr int kAtom = kTreeKeys * 128;        // 64 elements wide
   static constexpr int kSlots = F8 ? 2 : 3;            // of K, and of V
-  static constexpr int kAhead = 4;                     // halves (K or V tiles) on their way
+  static constexpr int kAhead = 2;                     // tiles on their way
   static constexpr int kRaw = F8 ? kTreeKeys * kRow : 0;  // a stage of stored bytes
   static constexpr int kMasks = 8;                     // tiles whose key masks are kept
   static constexpr int offQ = 0;
   static constexpr int offK = offQ + kTreeRows * D * 2;
   static constexpr int offV = offK + kSlots * kTile;
   static constexpr int offRaw = offV + kSlots * kTile;
-  static constexpr int offMl = offRaw + kAhead * kRaw;     // [2][128] a warpgroup's reference and sum
-  static constexpr int offQs = offMl + 2 * kTreeRows * 8;  // [128] score factors (e4m3)
+  static constexpr int offMl = offRaw + 2 * kAhead * kRaw;     // [2][128] a warpgroup's reference and sum
+  static constexpr int offFix = offMl + 2 * kTreeRows * 8;  // [2][128] fp16 (bf16 caches)
+  static constexpr int offQs = offFix + (F8 ? 0 : 2 * kTreeRows * 2);  // [128] score factors (e4m3)
   static constexpr int offKeys = offQs + (F8 ? kTreeRows * 4 : 0);  // [kMasks][4]: keys that are there
   static constexpr int nBar = 4 * kSlots + 2 + 6 + 1 + 3;
   static constexpr int offBar = offKeys + kMasks * 16;
   static constexpr int offMisc = offBar + nBar * 8;          // tensor memory's address, abort flag
-  static constexpr int offScan = offMisc + 8;                // [16]
-  static constexpr int offFirst = offScan + 64;
+  static constexpr int offScan = offMisc + 8;                // [kBlock / 32]
+  static constexpr int offFirst = offScan + kBlock / 32 * 4;
   static constexpr int kBytes = offFirst + 64;
   // d = 128 fills shared memory to within a few hundred bytes of the limit, leaving no room
   // to realign the base: the kernel checks instead that it lies on a 1024-byte boundary.
@@ -100,10 +102,6 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
-}
-// The largest bf16 strictly below p > 0 (0 for 0), as fp32 bits (see decode.cuh).
-__device__ __forceinline__ uint32_t below(float p) {
-  return (max(__float_as_uint(p), 1u) - 1u) & 0xFFFF0000u;
 }
 // Instruction descriptor of fp16 operands: idesc_bf16 without the type bits.
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn, bool f16) {
@@ -141,17 +139,20 @@ __device__ __forceinline__ bool faulty(const TreeArgs& a, int b) {
   return raw < 0 || raw > a.max_len || c0 < 0 || c1 < c0 || c1 > a.T || (raw > 0 && raw < c1 - c0);
 }
 
-// Keys that any row of an item sees: the sinks [0, sunk), then [low, high).
+// Keys that any row of an item sees: the sinks [0, sunk), then [low, high), whose tiles
+// begin at the 16 keys that hold low.
+constexpr int kBox = 16;
 struct Keys {
   int sunk, low, high;
   __device__ __forceinline__ int sink_tiles() const { return (sunk + kTreeKeys - 1) / kTreeKeys; }
   __device__ __forceinline__ int tiles() const {
-    return sink_tiles() + (high - low + kTreeKeys - 1) / kTreeKeys;
+    return sink_tiles() + (high - (low & -kBox) + kTreeKeys - 1) / kTreeKeys;
   }
-  // first key of tile t, and the end of those that count
+  // first key of tile t, and the range of those that count
   __device__ __forceinline__ int from(int t) const {
-    return t < sink_tiles() ? t * kTreeKeys : low + (t - sink_tiles()) * kTreeKeys;
+    return t < sink_tiles() ? t * kTreeKeys : (low & -kBox) + (t - sink_tiles()) * kTreeKeys;
   }
+  __device__ __forceinline__ int begin(int t) const { return t < sink_tiles() ? 0 : low; }
   __device__ __forceinline__ int end(int t) const { return t < sink_tiles() ? sunk : high; }
 };
 __device__ __forceinline__ Keys item_keys(const TreeArgs& a, const Seq& s, int qt) {
@@ -190,7 +191,7 @@ __device__ __forceinline__ void next_item(Cursor& c, const TreeArgs& a) {
   set_item(c, a);
 }
 __device__ __forceinline__ void advance(Cursor& c, const TreeArgs& a) {
-  if (++c.t == c.nt) next_item(c, a);
+  if (__builtin_expect(++c.t == c.nt, 0)) next_item(c, a);
 }
 // Tiles of one of a sequence's heads.
 __device__ __forceinline__ int head_tiles(const TreeArgs& a, const Seq& s) {
@@ -227,7 +228,8 @@ __device__ __forceinline__ uint32_t mask_bits(const long long* m, int words, int
   return __funnelshift_r(lo, hi, sh);
 }
 
-template <int D, bool F8>
+// WHOLE: the page size is a multiple of 16 keys.
+template <int D, bool F8, bool WHOLE>
 __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
   using L = Layout<D, F8>;
   constexpr int kSlots = L::kSlots, kAhead = L::kAhead;
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
           // P_t of this accumulator's previous tile has been used
           if (n > 1 && !(ok = mbar_wait(o_done(t), ((n >> 1) - 1) & 1, abort_flag, st))) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * L::kAtom + (kk & 3) * 32) >> 4;
             mma_ss(tmem + L::cS + t * kTreeKeys, sdesc_join(q_lo + off, hi),
@@ -395,12 +397,11 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
           if (first && item > 0 && !(ok = mbar_wait(o_free, (item - 1) & 1, abort_flag, st))) break;
           own = item;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < kTreeKeys / 16; ++kk) {
             const uint64_t b = sdesc_join(v_lo + slot * (L::kTile >> 4) + kk * (2048 >> 4), hi);
-            const uint32_t p = tmem + L::cS + t * kTreeKeys + kk * (F8 ? 8 : 16), o = tmem + L::cO + t * D;
+            const uint32_t p = tmem + L::cS + t * kTreeKeys + kk * 8, o = tmem + L::cO + t * D;
             mma_ts(o, p, b, id_pv, !first || kk > 0);
-            if constexpr (!F8) mma_ts(o, p + 8, b, id_pv, 1u);
           }
           mma_commit(v_empty(slot));
           mma_commit(o_done(t));
@@ -414,86 +415,119 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
     }
   } else if (warp >= kWarpLoad) {
     regs_decrease<kRegsLoad>();
-    const int w = warp - kWarpLoad;           // rows 32 w .. 32 w + 31 of each tile
+    const int w = (warp - kWarpLoad) & 3;     // rows 32 w .. 32 w + 31 of each tile
+    const bool keys = warp < kWarpLoad + 4;   // K's loaders, or V's
     constexpr int kLanes = L::kRow / 16;      // of a row: 16 bytes each
     constexpr int kRows = 32 / kLanes;        // of an instruction
     const int c16 = lane % kLanes, r_lane = lane / kLanes;
+    const unsigned char* base = (keys ? a.k : a.v) + c16 * 16;
+    const long long st_page = keys ? a.k_strides[0] : a.v_strides[0];
+    const long long st_slot = keys ? a.k_strides[1] : a.v_strides[1];
+    const long long st_head = keys ? a.k_strides[2] : a.v_strides[2];
+    const uint32_t tile_base = sbase + (keys ? L::offK : L::offV);
+    const uint32_t raw = sbase + L::offRaw + (keys ? 0 : kAhead * L::kRaw) + w * (L::kRaw / 4) + lane * 16;
     uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + L::offKeys);
-    // look-ups, two tiles ahead of the loads
+    auto full = [&](int s) { return keys ? k_full(s) : v_full(s); };
+    auto empty = [&](int s) { return keys ? k_empty(s) : v_empty(s); };
+    // Look-ups, two tiles ahead of the loads. WHOLE: each 16 keys lie in one page, and lanes
+    // 0 and 1 look up the warp's two sixteens; else a lane looks up its row.
     Cursor look = s_first;
     int look_left = n_tiles;
     int page_of[2] = {}, slot_of[2] = {-1, -1};  // slot -1: no such key
-    long long head_of[2] = {};                   // K/V head
+    int head_of[2] = {};                         // K/V head
+    uint32_t span_of[2] = {};                    // keys of the 32 that count
     auto look_up = [&]() {
-      page_of[0] = page_of[1], slot_of[0] = slot_of[1], head_of[0] = head_of[1];
+      page_of[0] = page_of[1], slot_of[0] = slot_of[1], head_of[0] = head_of[1], span_of[0] = span_of[1];
       page_of[1] = 0, slot_of[1] = -1;
       if (look_left <= 0) return;
-      const int key = look.k.from(look.t) + 32 * w + lane;
+      const int first = look.k.from(look.t) + 32 * w;
+      span_of[1] = bits(look.k.begin(look.t) - first, look.k.end(look.t) - first);
       head_of[1] = look.hh;
-      if (key < look.k.end(look.t)) {
-        const int entry = key / a.cache.page_size;
+      const uint32_t mine = WHOLE ? (lane < 2 ? span_of[1] >> (kBox * lane) & 0xffffu : 0u) : span_of[1] >> lane & 1u;
+      if (mine) {
+        const int key = first + (WHOLE ? kBox * lane : lane);
+        const int entry = static_cast<int>(static_cast<uint64_t>(key) * a.page_mul >> a.page_shift);
         slot_of[1] = key - entry * a.cache.page_size;
         page_of[1] = a.table[look.b * a.table_stride + entry];
       }
       if (--look_left > 0) advance(look, a);
     };
-    look_up();
-    look_up();
-    // The half under way: tile n's K (even) or V (odd). Its rows' offsets stay for V.
-    long long v_off = 0;
-    uint32_t there = 0;
-    auto issue = [&](int h) {
-      if (h >= 2 * n_tiles) return;
-      const int n = h >> 1, slot = n % kSlots;
-      long long off;
-      if ((h & 1) == 0) {
-        const int page = page_of[0], sl = slot_of[0];
-        const bool held = sl >= 0;
-        const bool ok = held && static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages);
-        if (held && !ok) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-        off = ok ? page * a.k_strides[0] + sl * a.k_strides[1] + head_of[0] * a.k_strides[2] : 0;
-        v_off = ok ? page * a.v_strides[0] + sl * a.v_strides[1] + head_of[0] * a.v_strides[2] : 0;
-        there = __ballot_sync(0xffffffffu, ok);
-        if (lane == 0) s_keys[(n % L::kMasks) * 4 + w] = there;
-        look_up();
-      } else {
-        off = v_off;
-      }
-      const unsigned char* base = (h & 1 ? a.v : a.k) + c16 * 16;
-      const uint32_t to = F8 ? sbase + L::offRaw + (h % kAhead) * L::kRaw + w * (L::kRaw / 4) + lane * 16
-                             : sbase + (h & 1 ? L::offV : L::offK) + slot * L::kTile;
+    // where this lane's 16 bytes of a row go: rows repeat the swizzle after kPats of them
+    constexpr int kPats = F8 ? 1 : 8 / kRows;
+    uint32_t pat[kPats];
 #pragma unroll
-      for (int i = 0; i < 32 / kRows; ++i) {
-        const int r = i * kRows + r_lane;
-        const unsigned char* p = base + __shfl_sync(0xffffffffu, off, r);
-        const uint32_t dst = F8 ? to + i * 512
-                                : to + (c16 >> 3) * L::kAtom + sw128_offset(32 * w + r, c16 & 7);
-        cp_async16(dst, p, (there >> r) & 1);
+    for (int i = 0; i < kPats; ++i)
+      pat[i] = F8 ? 0u : (c16 >> 3) * L::kAtom + 32 * w * 128 + sw128_offset(i * kRows + r_lane, c16 & 7);
+    // and, widened, of an e4m3 cache
+    constexpr int kWides = F8 ? 8 / kRows : 1;
+    uint32_t wide[kWides];
+#pragma unroll
+    for (int i = 0; i < kWides; ++i)
+      wide[i] = (c16 >> 2) * L::kAtom + 32 * w * 128 + sw128_offset(i * kRows + r_lane, (c16 & 3) * 2);
+    // one tile's copies
+    auto issue = [&](int n) {
+      const int page = page_of[0], sl = slot_of[0];
+      const bool held = sl >= 0;
+      const bool ok = held && static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages);
+      if (held && !ok) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+      const long long off = ok ? page * st_page + sl * st_slot + head_of[0] * st_head : 0;
+      const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+      const uint32_t there = WHOLE ? span_of[0] & ((oks & 1 ? 0xffffu : 0u) | (oks & 2 ? 0xffff0000u : 0u)) : oks;
+      if (keys && lane == 0) s_keys[(n % L::kMasks) * 4 + w] = there;
+      const uint32_t to = F8 ? raw + (n % kAhead) * L::kRaw : tile_base + (n % kSlots) * L::kTile;
+      constexpr int kPer = kBox / kRows;  // instructions of 16 keys
+      auto dst = [&](int i) { return F8 ? to + i * 512 : to + pat[i % kPats] + i / kPats * 1024; };
+      if constexpr (WHOLE) {
+        const uint32_t mine = there >> r_lane;
+#pragma unroll 1
+        for (int box = 0; box < 2; ++box) {
+          const unsigned char* p = base + __shfl_sync(0xffffffffu, off, box) + r_lane * st_slot;
+          const uint32_t valid = mine >> (box * kBox);
+          const uint32_t at = box * kPer * (F8 ? 512 : 1024 / kPats);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i, p += kRows * st_slot) cp_async16(at + dst(i), p, valid >> (i * kRows) & 1);
+        }
+      } else {
+        // (addresses of several rows first: one after the other they wait for each shuffle)
+#pragma unroll
+        for (int i0 = 0; i0 < 2 * kPer; i0 += kPer) {
+          const unsigned char* p[kPer];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) p[i] = base + __shfl_sync(0xffffffffu, off, (i0 + i) * kRows + r_lane);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            cp_async16(dst(i0 + i), p[i], there >> ((i0 + i) * kRows + r_lane) & 1);
+        }
       }
     };
-    // an item's query rows: row x is token x / G, head x % G of the group; zeros behind
+    // an item's query rows (V's loaders): row x is token x / G, head x % G of the group; zeros
+    // behind the last
     auto load_q = [&](const Cursor& c) {
       constexpr int kChunks = D / 8;  // 16 bytes of a row each
       constexpr int kPer = kTreeRows * kChunks / 128;  // of a thread
-      const int l = tid - 32 * kWarpLoad;
+      constexpr int kStep = 128 / kChunks;             // rows between them
+      const int l = tid - 32 * (kWarpLoad + 4), ch = l % kChunks;
       const int rows = min(kTreeRows, c.s.n * a.group - c.qt * kTreeRows);
+      const int at = c.qt * kTreeRows + l / kChunks;
+      int token = at / a.group, g = at - token * a.group;
+      const int step_t = kStep / a.group, step_g = kStep - step_t * a.group;
+      const __nv_bfloat16* q = a.q + static_cast<long long>(c.hh) * a.group * a.q_head + ch * 8;
       float* s_qs = reinterpret_cast<float*>(smem + L::offQs);
-#pragma unroll
+#pragma unroll 1
       for (int x0 = 0; x0 < kPer; x0 += 8) {
         uint4 x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int id = (x0 + i) * 128 + l, row = id / kChunks, ch = id % kChunks;
           x[i] = make_uint4(0, 0, 0, 0);
-          if (row < rows) {
-            const int at = c.qt * kTreeRows + row, token = at / a.group, g = at - token * a.group;
-            x[i] = *reinterpret_cast<const uint4*>(a.q + (c.s.c0 + token) * a.q_token +
-                                                   (static_cast<long long>(c.hh) * a.group + g) * a.q_head + ch * 8);
-          }
+          if ((x0 + i) * kStep + l / kChunks < rows)
+            x[i] = *reinterpret_cast<const uint4*>(q + (c.s.c0 + token) * a.q_token + g * a.q_head);
+          token += step_t;
+          g += step_g;
+          if (g >= a.group) g -= a.group, ++token;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int id = (x0 + i) * 128 + l, row = id / kChunks, ch = id % kChunks;
+          const int row = (x0 + i) * kStep + l / kChunks;
           uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           if constexpr (F8) {
             float top = 0.f;
@@ -523,56 +557,52 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
     Cursor c = s_first;
     int item = 0;
     bool ok = true;
-    // bf16: the slots of the first kAhead halves are free
-    for (int h = 0; h < kAhead; ++h) {
-      issue(h);
-      cp_async_commit();
-    }
+    // Step n: tile n is handed over, tile n + kAhead fetched, and the one two further looked
+    // up. (One loop, also for the first tiles: every copy of this code costs instruction
+    // fetches, which bound this kernel next to its loads.)
 #pragma unroll 1
-    for (int h = 0; h < 2 * n_tiles && ok; ++h) {
-      const int n = h >> 1, slot = n % kSlots;
-      const bool keys = (h & 1) == 0;
-      if (keys && (c.t == 0 || n == 0)) {
-        // the query's buffer is free once the previous item's last product has read it
-        if (item > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (item - 1) & 1, abort_flag, st)))) break;
-        load_q(c);
-      }
-      cp_async_wait<kAhead - 1>();
-      const uint32_t full = keys ? k_full(slot) : v_full(slot);
-      if constexpr (F8) {
-        // widen this lane's own bytes
-        const uint32_t empty = keys ? k_empty(slot) : v_empty(slot);
-        if (n >= kSlots &&
-            !(ok = __all_sync(0xffffffffu, mbar_wait(empty, ((n / kSlots) - 1) & 1, abort_flag, st))))
-          break;
-        const uint32_t from = sbase + L::offRaw + (h % kAhead) * L::kRaw + w * (L::kRaw / 4) + lane * 16;
-        const uint32_t to = sbase + (keys ? L::offK : L::offV) + slot * L::kTile;
-#pragma unroll
-        for (int i = 0; i < 32 / kRows; ++i) {
-          const uint4 x = ld_shared_v4(from + i * 512);
-          const int row = 32 * w + i * kRows + r_lane;
-          const uint32_t at = to + (c16 >> 2) * L::kAtom;
-          const int ch = (c16 & 3) * 2;
-          st_shared_v4(at + sw128_offset(row, ch), e4m3x2_f16x2(x.x), e4m3x2_f16x2(x.x >> 16),
-                       e4m3x2_f16x2(x.y), e4m3x2_f16x2(x.y >> 16));
-          st_shared_v4(at + sw128_offset(row, ch + 1), e4m3x2_f16x2(x.z), e4m3x2_f16x2(x.z >> 16),
-                       e4m3x2_f16x2(x.w), e4m3x2_f16x2(x.w >> 16));
+    for (int n = -kAhead - 2; n < n_tiles; ++n) {
+      const int n2 = n + kAhead;
+      if (n >= 0) {
+        const int slot = n % kSlots;
+        if (!keys) {
+          if (c.t == 0 || n == 0) {
+            // the query's buffer is free once the previous item's last product has read it
+            if (item > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (item - 1) & 1, abort_flag, st)))) break;
+            load_q(c);
+          }
+          if (c.t + 1 == c.nt) ++item;
+          if (n + 1 < n_tiles) advance(c, a);
         }
+        cp_async_wait<kAhead - 1>();
+        if constexpr (F8) {
+          // widen this lane's own bytes
+          if (n >= kSlots &&
+              !(ok = __all_sync(0xffffffffu, mbar_wait(empty(slot), ((n / kSlots) - 1) & 1, abort_flag, st))))
+            break;
+          uint4 got[32 / kRows];
+#pragma unroll
+          for (int i = 0; i < 32 / kRows; ++i) got[i] = ld_shared_v4(raw + (n % kAhead) * L::kRaw + i * 512);
+#pragma unroll
+          for (int i = 0; i < 32 / kRows; ++i) {
+            const uint4 x = got[i];
+            // (the swizzle repeats after 8 rows, and the second chunk is the first's neighbour)
+            const uint32_t at = tile_base + slot * L::kTile + wide[i % kWides] + i / kWides * 1024;
+            st_shared_v4(at, e4m3x2_f16x2(x.x), e4m3x2_f16x2(x.x >> 16), e4m3x2_f16x2(x.y), e4m3x2_f16x2(x.y >> 16));
+            st_shared_v4(at ^ 16u, e4m3x2_f16x2(x.z), e4m3x2_f16x2(x.z >> 16), e4m3x2_f16x2(x.w),
+                         e4m3x2_f16x2(x.w >> 16));
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(full(slot));
+        // bf16: the next tile waits for its slot
+        if (!F8 && n2 < n_tiles && n2 >= kSlots &&
+            !(ok = __all_sync(0xffffffffu, mbar_wait(empty(n2 % kSlots), ((n2 / kSlots) - 1) & 1, abort_flag, st))))
+          break;
       }
-      fence_proxy_async_smem();
-      mbar_arrive(full);
-      if (!keys) {
-        if (c.t + 1 == c.nt) ++item;
-        if (n + 1 < n_tiles) advance(c, a);
-      }
-      // the next half: bf16 waits for its slot
-      const int h2 = h + kAhead, n2 = h2 >> 1;
-      if (!F8 && h2 < 2 * n_tiles && n2 >= kSlots) {
-        const uint32_t empty = h2 & 1 ? v_empty(n2 % kSlots) : k_empty(n2 % kSlots);
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(empty, ((n2 / kSlots) - 1) & 1, abort_flag, st)))) break;
-      }
-      issue(h2);
+      if (n2 >= 0 && n2 < n_tiles) issue(n2);
       cp_async_commit();
+      look_up();
     }
     cp_async_wait<0>();
   } else {
@@ -584,6 +614,7 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
     const uint32_t tS = lane_base + L::cS + t * kTreeKeys, tO = lane_base + L::cO + t * D;
     const uint32_t* s_keys = reinterpret_cast<const uint32_t*>(smem + L::offKeys);
     float2* s_ml = reinterpret_cast<float2*>(smem + L::offMl);  // [warpgroup][row]
+    __half* s_fix = reinterpret_cast<__half*>(smem + L::offFix);
     // A wait that gives up ends all waits; the warps still meet at every barrier, and
     // what they write is undefined.
     bool live = true;
@@ -610,14 +641,16 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
       }
       // the context keys that this row sees begin at `near`, and with a chain also the others
       const int near = a.window == 0 ? 0 : place - a.window + 1;
-      float m_used = -INFINITY, l_sum = 0.f;
+      const int near_most = __reduce_max_sync(0xffffffffu, near);
+      float m_used = -INFINITY;
+      float l_sum = 0.f, l_fix = 0.f;  // the weights' sum, and what their rounding adds to it
       float qs = a.scale_log2;
       int mine = 0;  // tiles of this warpgroup
       if (F8 && count == 1 && (n & 1) != t) mbar_arrive(q_empty);
-      for (int x = 0; x < count; ++x) {
-        const int nn = n + x;
+      for (int step = 0; step < count; ++step) {
+        const int nn = n + step;
         if ((nn & 1) != t) continue;
-        const int tile = t_begin + x, k0 = c.k.from(tile);
+        const int k0 = c.k.from(t_begin + step);
         wait(s_full(t), (nn >> 1) & 1);
         tc_fence_after();
         if (F8 && mine == 0) {
@@ -630,51 +663,53 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
           mbar_arrive(p_full(t));
           continue;
         }
-        // the keys that this row sees
-        uint32_t see[4];
-        bool all = true;
+        // Two passes over the row's scores, 32 at a time, in loops that are not unrolled:
+        // in between the scores stay in tensor memory. (With a row's 128 scores in registers
+        // and the loops unrolled, the roles' code pushed each other out of the instruction
+        // cache.)
+        const uint4 there = ld_shared_v4(sbase + L::offKeys + (nn % L::kMasks) * 16);
+        // in most tiles all keys are there, and all rows see them
+        const bool plain = (there.x & there.y & there.z & there.w) == ~0u && k0 >= near_most && k0 + kTreeKeys <= ctx;
+        uint32_t see[4] = {there.x, there.y, there.z, there.w};
+        if (__builtin_expect(!plain, 0)) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int k1 = k0 + 32 * y;
-          uint32_t u;
-          if (mask) {
-            u = bits(near - k1, ctx - k1) | bits(0, min(a.sinks, ctx) - k1);
-            if (k1 + 32 > ctx) u |= mask_bits(mask, a.words, k1 - ctx) & bits(ctx - k1, c.s.len - k1);
-          } else {
-            u = bits(near - k1, place + 1 - k1) | bits(0, min(a.sinks, place + 1) - k1);
+          for (int y = 0; y < 4; ++y) {
+            const int k1 = k0 + 32 * y;
+            uint32_t u;
+            if (mask) {
+              u = bits(near - k1, ctx - k1) | bits(0, min(a.sinks, ctx) - k1);
+              if (k1 + 32 > ctx) u |= mask_bits(mask, a.words, k1 - ctx) & bits(ctx - k1, c.s.len - k1);
+            } else {
+              u = bits(near - k1, place + 1 - k1) | bits(0, min(a.sinks, place + 1) - k1);
+            }
+            see[y] &= u;
           }
-          see[y] = u & s_keys[(nn % L::kMasks) * 4 + y];
-          all &= see[y] == ~0u;
         }
-        all = __all_sync(0xffffffffu, all);
-        auto hide = [&](uint32_t (&x)[32], uint32_t word) {
-          if (all) return;
+        uint32_t x[32];
+        // the next 32 scores, those that the row does not see as -inf
+        auto read = [&](int y) {
+          tmem_ld32(tS + 32 * y, x);
+          tmem_wait_ld();
+          reg_pin(x);
+          if (__builtin_expect(!plain, 0)) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((word >> i) & 1)) x[i] = 0xff800000u;  // -inf
+            for (int i = 0; i < 32; ++i)
+              if (!((see[0] >> i) & 1)) x[i] = 0xff800000u;
+            const uint32_t first = see[0];
+            see[0] = see[1], see[1] = see[2], see[2] = see[3], see[3] = first;
+          }
         };
-        // Two passes over the row, 32 scores at a time: they stay in tensor memory in between.
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        uint32_t sc[2][32];
-        tmem_ld32(tS, sc[0]);
-        tmem_wait_ld();
-        reg_pin(sc[0]);
-#pragma unroll
+#pragma unroll 1
         for (int y = 0; y < 4; ++y) {
-          uint32_t(&r)[32] = sc[y & 1];
-          if (y < 3) tmem_ld32(tS + 32 * (y + 1), sc[(y + 1) & 1]);
-          hide(r, see[y]);
+          read(y);
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
+          for (int i = 0; i < 32; i += 8) {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              m4[u] = fmax3(m4[u], __uint_as_float(r[i + u]), __uint_as_float(r[i + 4 + u]));
-          if (y < 3) {
-            tmem_wait_ld();
-            reg_pin(sc[(y + 1) & 1]);
+              m4[u] = fmax3(m4[u], __uint_as_float(x[i + u]), __uint_as_float(x[i + 4 + u]));
           }
         }
-        tmem_ld32(tS, sc[0]);
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qs;
         const float m_old = m_used;
         const bool bump = mx > m_used + kSlack;
@@ -682,45 +717,29 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
         // (a row that has seen no key yet has no maximum)
         const float ref = (m_used == -INFINITY ? 0.f : m_used) - (F8 ? kF16Shift : 0.f);
         const float2 qs2 = make_float2(qs, qs), neg = make_float2(-ref, -ref);
-        float2 sum = make_float2(0.f, 0.f);
-        tmem_wait_ld();
-        reg_pin(sc[0]);
-#pragma unroll
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
         for (int y = 0; y < 4; ++y) {
-          uint32_t(&r)[32] = sc[y & 1];
-          if (y < 3) tmem_ld32(tS + 32 * (y + 1), sc[(y + 1) & 1]);
-          hide(r, see[y]);
-          // P of 32 keys, two steps of a product: bf16 in the place of their scores, 8 columns
-          // of the first terms and 8 of the second for each step; fp16 8 columns a step
-          uint32_t w[F8 ? 16 : 32];
+          read(y);
+          uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 z = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), qs2, neg);
+            const float2 z = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), qs2, neg);
             const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-            sum = add2(sum, p);
-            if constexpr (F8) {
-              w[i] = pack_f16(p.x, p.y);
-            } else {
-              const uint32_t h0 = below(p.x), h1 = below(p.y);
-              w[(i >> 3) * 16 + (i & 7)] = __byte_perm(h0, h1, 0x7632);
-              w[(i >> 3) * 16 + 8 + (i & 7)] =
-                  pack_bf16(p.x - __uint_as_float(h0), p.y - __uint_as_float(h1));
-            }
+            w[i] = F8 ? pack_f16(p.x, p.y) : pack_bf16(p.x, p.y);
+            sum[i & 1] = add2(sum[i & 1], p);
           }
-          if (y < 3) {
-            tmem_wait_ld();
-            reg_pin(sc[(y + 1) & 1]);
-          }
-          if constexpr (F8)
-            tmem_st16(tS + 16 * y, w);
-          else
-            tmem_st32(tS + 32 * y, w);
+          tmem_st16(tS + 16 * y, w);
         }
+        // bf16: the rounding of the tile's largest weight (see fwd.cuh: the others' even out)
+        const float top = F8 ? 0.f : ex2_approx(mx - ref);
+        const float top_err = bf16lo_f32(pack_bf16(top, 0.f)) - top;
         // (the previous product into O_t was done before this tile's scores were computed)
-        if (mine > 1 && __any_sync(0xffffffffu, bump)) {
+        if (__builtin_expect(mine > 1 && __any_sync(0xffffffffu, bump), 0)) {
           const float alpha = bump ? ex2_approx(m_old - m_used) : 1.f;
           l_sum *= alpha;
-#pragma unroll
+          l_fix *= alpha;
+#pragma unroll 1
           for (int y = 0; y < D / 32; ++y) {
             uint32_t ov[32];
             tmem_ld32(tO + 32 * y, ov);
@@ -731,7 +750,8 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
             tmem_st32(tO + 32 * y, ov);
           }
         }
-        l_sum += sum.x + sum.y;
+        l_sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        l_fix += top_err;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(p_full(t));
@@ -744,15 +764,19 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
         if (mine > 0) wait(o_done(t), (mine_last >> 1) & 1);
         const float ref = m_used == -INFINITY ? -INFINITY : m_used - (F8 ? kF16Shift : 0.f);
         s_ml[t * kTreeRows + row] = make_float2(ref, l_sum);
+        // what O is too large by, as its weights are the rounded ones
+        if (!F8) s_fix[t * kTreeRows + row] = __float2half_rn(l_sum > 0.f ? -l_fix / (l_sum + l_fix) : 0.f);
         tc_fence_before();
         named_bar_sync(1, kSoftmax);
         tc_fence_after();
         const float2 ml0 = s_ml[row], ml1 = s_ml[kTreeRows + row];
+        const float fix0 = F8 ? 0.f : __half2float(s_fix[row]), fix1 = F8 ? 0.f : __half2float(s_fix[kTreeRows + row]);
         named_bar_sync(1, kSoftmax);  // the next item's are written behind this
         const float M = fmaxf(ml0.x, ml1.x);
         const float f0 = ml0.x == -INFINITY ? 0.f : ex2_approx(ml0.x - M);
         const float f1 = ml1.x == -INFINITY ? 0.f : ex2_approx(ml1.x - M);
         const float l = ml0.y * f0 + ml1.y * f1;
+        const float g0 = fmaf(f0, fix0, f0), g1 = fmaf(f1, fix1, f1);
         const bool whole = t_begin == 0 && ends;
         const float mul = !whole ? 1.f : M == -INFINITY ? 0.f : a.o_scale / l;
         const long long out = (static_cast<long long>(c.s.c0) + token) * a.H + c.hh * a.group + at % a.group;
@@ -764,7 +788,7 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
             a.part_ml[slot * kTreeRows + row] = make_float2(M, l);
         }
         if (some) {
-#pragma unroll
+#pragma unroll 1
           for (int y = 0; y < D / 64; ++y) {
             const int col = t * (D / 2) + 32 * y;
             float x[32];
@@ -774,12 +798,12 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
             reg_pin(u);
             // (an accumulator without a weight may hold anything)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = f0 > 0.f ? __uint_as_float(u[i]) * f0 : 0.f;
+            for (int i = 0; i < 32; ++i) x[i] = f0 > 0.f ? __uint_as_float(u[i]) * g0 : 0.f;
             tmem_ld32(lane_base + L::cO + D + col, u);
             tmem_wait_ld();
             reg_pin(u);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = (x[i] + (f1 > 0.f ? __uint_as_float(u[i]) * f1 : 0.f)) * mul;
+            for (int i = 0; i < 32; ++i) x[i] = (x[i] + (f1 > 0.f ? __uint_as_float(u[i]) * g1 : 0.f)) * mul;
             if (!has) continue;
             if (whole) {
               uint4* to = reinterpret_cast<uint4*>(a.o + out * D + col);
@@ -925,7 +949,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
 template <int D, bool F8>
 cudaError_t launch_tree_t(const TreeArgs& a, int ctas, bool join, cudaStream_t stream) {
   using L = Layout<D, F8>;
-  auto kern = tree_kernel<D, F8>;
+  auto kern = a.cache.page_size % kBox == 0 ? tree_kernel<D, F8, true> : tree_kernel<D, F8, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   // The warpgroups' register shares must fit the launch allocation, or an increase would

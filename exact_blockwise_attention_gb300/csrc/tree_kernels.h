@@ -27,6 +27,8 @@ struct TreeArgs {
   const long long* mask;  // null: each token sees those before it
   long long mask_stride;
   int words;              // of a token's mask
+  unsigned page_mul;      // key / page_size = key * page_mul >> page_shift, for every int >= 0
+  int page_shift;
   int max_len;            // keys a table row can hold
   int T, B, H, group;
   int window, sinks;      // window 0: none

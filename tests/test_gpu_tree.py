@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import oracle
-from cache_util import Paged, bf16, decode_tolerances, np64
+from cache_util import Paged, bf16, np64
 from oracle import tree
 
 pytestmark = pytest.mark.gpu
@@ -32,6 +32,31 @@ def status_is_clean(eba):
     eba.poll_device_status()
     yield
     assert eba.poll_device_status() == 0
+
+
+def tolerances(q, keys, values, scale, o, lse, e4m3):
+    """Bounds of |O - exact| [T, H, d] and |lse - exact| [T, H] by arithmetic, token t over
+    keys[t], values[t].
+
+    Scores: d products added in fp32, off by at most d 2^-24 sum |q k| scale, and as much
+    again for the scaling, the base-2 reference and the exponential's own 2^-20. The weights
+    enter the product with V as bf16 (half a step, 2^-8) or, with an e4m3 cache, fp16
+    (2^-11), which moves O by at most that of P |v|, and once more through the sum they are
+    divided by; so do the scores' error and the fp32 sums over n keys (n / 16 + 64
+    roundings). The bf16 output is off by half a step of its own."""
+    q = np64(q)
+    to, tl = np.zeros_like(o), np.zeros_like(lse)
+    for t in range(len(keys)):
+        n, hk = keys[t].shape[:2]
+        for h in range(q.shape[1] if n else 0):
+            g = h // (q.shape[1] // hk)
+            big = (np.abs(keys[t][:, g]) @ np.abs(q[t, h])).max() * scale
+            score = 2 * q.shape[2] * 2.0 ** -24 * big + 2.0 ** -20
+            weight = score + (2.0 ** -11 if e4m3 else 2.0 ** -8) + (n / 16 + 64) * 2.0 ** -24
+            p, _ = oracle.softmax_weights(q[t, h][None], keys[t][:, g], scale)
+            to[t, h] = 2.0 ** -8 * np.abs(o[t, h]) + 2 * weight * (p @ np.abs(values[t][:, g]))[0]
+            tl[t, h] = score + (n / 16 + 64) * 2.0 ** -24 + 2.0 ** -22 * abs(lse[t, h])
+    return to, tl
 
 
 def random_masks(r, news):
@@ -102,13 +127,16 @@ def check(eba, p, news, H, masks=None, words=1, window=None, sinks=0, scale=None
     vs = [values[b][s] for b in range(len(news)) for s in sets[b]]
     mine = q[before:before + T]
     ro, rl = oracle.decode(mine, ks, vs, scale)
-    to, tl = decode_tolerances(mine, ks, vs, scale, ro, rl, p.k.dtype != torch.bfloat16)
+    to, tl = tolerances(mine, ks, vs, scale, ro, rl, p.k.dtype != torch.bfloat16)
     o, lse = np64(o)[before:before + T], np64(lse)[before:before + T]
     assert np.isfinite(o).all()
     blind = np.isneginf(rl)
     assert (np.isneginf(lse) == blind).all() and (o[blind] == 0).all()
     assert (np.abs(o - ro) <= to).all(), np.max(np.abs(o - ro) - to)
     assert (np.abs(lse[~blind] - rl[~blind]) <= tl[~blind]).all()
+    # as a whole: two independent roundings to bf16 at most, each of rms 2^-8 / sqrt(3)
+    if ro.size > 4000:
+        assert np.linalg.norm(o - ro) <= 2.0 ** -8 * np.linalg.norm(ro)
 
 
 # lengths, drafted tokens, H, H_kv, d, page size, e4m3, heads first
@@ -256,7 +284,7 @@ def test_faults_are_reported(eba):
     o, lse = eba.decode_tree(cache, q.cuda(), p.gtable, p.glens, cu)
     sets = [[j for j in tree.seen(300, 3, i) if not 112 <= j < 128] for i in range(3)]
     ro, rl = oracle.decode(q[:3], [keys[0][s] for s in sets], [values[0][s] for s in sets], 0.125)
-    to, tl = decode_tolerances(q[:3], [keys[0][s] for s in sets], [values[0][s] for s in sets], 0.125, ro, rl, False)
+    to, tl = tolerances(q[:3], [keys[0][s] for s in sets], [values[0][s] for s in sets], 0.125, ro, rl, False)
     assert (np.abs(np64(o)[:3] - ro) <= to).all() and (np.abs(np64(lse)[:3] - rl) <= tl).all()
     assert eba.poll_device_status() == 7
     # lengths and offsets out of range
@@ -299,7 +327,7 @@ def test_captured_call_follows_its_batch(eba):
         sets = [(b, tree.seen(n[b], news[b], i, masks[b][i])) for b in range(2) for i in range(news[b])]
         ks, vs = [keys[b][s] for b, s in sets], [values[b][s] for b, s in sets]
         ro, rl = oracle.decode(q[:T], ks, vs, 1 / math.sqrt(128))
-        to, tl = decode_tolerances(q[:T], ks, vs, 1 / math.sqrt(128), ro, rl, False)
+        to, tl = tolerances(q[:T], ks, vs, 1 / math.sqrt(128), ro, rl, False)
         assert (np.abs(np64(o)[:T] - ro) <= to).all() and (np.abs(np64(lse)[:T] - rl) <= tl).all()
 
 
@@ -344,12 +372,12 @@ def test_a_step_of_speculative_decoding(eba):
     q1 = bf16(g, B, H, d)
     o1, l1 = eba.decode(cache, q1.cuda(), table, now)
     ro, rl = oracle.decode(q1, ks, vs, 0.125)
-    to, tl = decode_tolerances(q1, ks, vs, 0.125, ro, rl, False)
+    to, tl = tolerances(q1, ks, vs, 0.125, ro, rl, False)
     assert (np.abs(np64(o1) - ro) <= to).all() and (np.abs(np64(l1) - rl) <= tl).all()
     # what the path's last token saw is that sequence
     last = [at[b] + paths[b][-1] for b in range(B)]
     ro, rl = oracle.decode(q[last], ks, vs, 0.125)
-    to, tl = decode_tolerances(q[last], ks, vs, 0.125, ro, rl, False)
+    to, tl = tolerances(q[last], ks, vs, 0.125, ro, rl, False)
     assert (np.abs(np64(o)[last] - ro) <= to).all() and (np.abs(np64(lse)[last] - rl) <= tl).all()
     held = [-(-(c + len(x)) // size) for c, x in zip(ctx, paths)]
     assert (table.cpu() >= 0).sum(1).tolist() == held and int(pool.refs.sum()) == sum(held)
