@@ -444,6 +444,26 @@ DecodePlan decode_plan(int B, int H, int H_kv, int d, long long capacity, int ty
   return p;
 }
 
+// A cache's pages for the tree decode's loads (see launch_tree). False: no such map.
+bool make_cache_map(CUtensorMap* m, const void* ptr, const long long* strides, const attn_cache_t& c,
+                    int box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const bool f8 = c.type == ATTN_CACHE_E4M3;
+  const cuuint64_t esz = f8 ? 1 : 2, row = c.d * esz;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.H_kv),
+                        static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.n_pages)};
+  cuuint64_t st[3];
+  for (int i = 0; i < 3; ++i)  // (a dimension of size 1 may have any stride)
+    st[i] = dims[i + 1] == 1 ? row : static_cast<cuuint64_t>(strides[2 - i]) * esz;
+  cuuint32_t boxes[4] = {f8 ? static_cast<cuuint32_t>(c.d) : 64u, 1, static_cast<cuuint32_t>(box), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr),
+            dims, st, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The workspace of a tree decode: see TreeArgs.
 size_t tree_bytes(int d) {
   constexpr size_t kParts = 2 * eba::kTreeCtas * static_cast<size_t>(eba::kTreeRows);
@@ -1334,7 +1354,13 @@ int attn_decode_tree(const attn_cache_t* cache, const void* q, const long long* 
   if (!a.status) return ATTN_ERR_CUDA;
   a.limit_ns = g_wait_limit_ns.load();
   const int ctas = static_cast<int>(std::min<double>(eba::kTreeCtas, std::ceil(items * item_tiles)));
-  cudaError_t e = eba::launch_tree(a, ctas, max_len > eba::kTreeKeys || (window > 0 && sinks > 0),
+  // TMA where a page holds whole boxes and the strides are within a tensor map's limits
+  CUtensorMap tk{}, tv{};
+  a.box = cache->page_size % 32 == 0 ? 32 : cache->page_size % 16 == 0 ? 16 : 0;
+  if (a.box && !(make_cache_map(&tk, cache->k, cache->k_strides, *cache, a.box) &&
+                 make_cache_map(&tv, cache->v, cache->v_strides, *cache, a.box)))
+    a.box = 0;
+  cudaError_t e = eba::launch_tree(tk, tv, a, ctas, max_len > eba::kTreeKeys || (window > 0 && sinks > 0),
                                    static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }

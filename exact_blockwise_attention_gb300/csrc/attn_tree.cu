@@ -42,6 +42,7 @@ namespace {
 
 constexpr int kSoftmax = 256;  // threads: two warpgroups
 constexpr int kWarpLoad = 8, kWarpIssue = 16;  // first warps of the loaders (of K, of V) and the issuers
+constexpr int kWarpTma = 19;  // the producer of TMA loads
 constexpr int kBlock = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kRegsSoftmax = 128, kRegsLoad = 80, kRegsIssue = 64;
@@ -69,11 +70,12 @@ struct Layout {
   static constexpr int offFix = offMl + 2 * kTreeRows * 8;  // [2][128] fp16 (bf16 caches)
   static constexpr int offQs = offFix + (F8 ? 0 : 2 * kTreeRows * 2);  // [128] score factors (e4m3)
   static constexpr int offKeys = offQs + (F8 ? kTreeRows * 4 : 0);  // [kMasks][4]: keys that are there
-  static constexpr int nBar = 4 * kSlots + 2 + 6 + 1 + 3;
-  static constexpr int offBar = offKeys + kMasks * 16;
+  static constexpr int offFlag = offKeys + kMasks * 16;  // [kMasks] bytes
+  static constexpr int nBar = 4 * kSlots + 2 + 6 + 1 + 3 + (F8 ? 4 * kAhead : 0);
+  static constexpr int offBar = offFlag + kMasks;
   static constexpr int offMisc = offBar + nBar * 8;          // tensor memory's address, abort flag
-  static constexpr int offScan = offMisc + 8;                // [kBlock / 32]
-  static constexpr int offFirst = offScan + kBlock / 32 * 4;
+  static constexpr int offScan = offMl;                      // [kBlock / 32], before the items
+  static constexpr int offFirst = offMisc + 8;
   static constexpr int kBytes = offFirst + 64;
   // d = 128 fills shared memory to within a few hundred bytes of the limit, leaving no room
   // to realign the base: the kernel checks instead that it lies on a 1024-byte boundary.
@@ -140,17 +142,16 @@ __device__ __forceinline__ bool faulty(const TreeArgs& a, int b) {
 }
 
 // Keys that any row of an item sees: the sinks [0, sunk), then [low, high), whose tiles
-// begin at the 16 keys that hold low.
-constexpr int kBox = 16;
+// begin at the 32 keys that hold low.
 struct Keys {
   int sunk, low, high;
   __device__ __forceinline__ int sink_tiles() const { return (sunk + kTreeKeys - 1) / kTreeKeys; }
   __device__ __forceinline__ int tiles() const {
-    return sink_tiles() + (high - (low & -kBox) + kTreeKeys - 1) / kTreeKeys;
+    return sink_tiles() + (high - (low & -32) + kTreeKeys - 1) / kTreeKeys;
   }
   // first key of tile t, and the range of those that count
   __device__ __forceinline__ int from(int t) const {
-    return t < sink_tiles() ? t * kTreeKeys : (low & -kBox) + (t - sink_tiles()) * kTreeKeys;
+    return t < sink_tiles() ? t * kTreeKeys : (low & -32) + (t - sink_tiles()) * kTreeKeys;
   }
   __device__ __forceinline__ int begin(int t) const { return t < sink_tiles() ? 0 : low; }
   __device__ __forceinline__ int end(int t) const { return t < sink_tiles() ? sunk : high; }
@@ -228,9 +229,25 @@ __device__ __forceinline__ uint32_t mask_bits(const long long* m, int words, int
   return __funnelshift_r(lo, hi, sh);
 }
 
-// WHOLE: the page size is a multiple of 16 keys.
-template <int D, bool F8, bool WHOLE>
-__global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
+// What the roles need to know of a tile besides its keys.
+enum : uint8_t { kFirst = 0x80, kLast = 0x40, kItem = 0x3f };  // of its item in this run; the item's number
+
+// 4-D tiled load: box at coordinates (x, y, z, w) -> shared memory, counted on `bar`. x must
+// be a multiple of 16 bytes.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                            int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// TMA: the page size is a multiple of 16 keys (a.box of 16 or 32 of them to a load).
+template <int D, bool F8, bool TMA>
+__global__ void __launch_bounds__(kBlock, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ TreeArgs a) {
   using L = Layout<D, F8>;
   constexpr int kSlots = L::kSlots, kAhead = L::kAhead;
   extern __shared__ uint8_t smem_raw[];
@@ -257,6 +274,9 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
   auto o_done = [&](int t) { return b1 + 48 + 8u * t; };
   const uint32_t o_free = b1 + 64;  // the item's end has read both accumulators
   auto mma_done = [&](int i) { return b1 + 72 + 8u * i; };
+  // stages of stored bytes: K's, then V's
+  auto raw_full = [&](int s) { return b1 + 96 + 8u * s; };
+  auto raw_empty = [&](int s) { return b1 + 96 + 8u * (2 * kAhead + s); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
   int* s_scan = reinterpret_cast<int*>(smem + L::offScan);
@@ -266,12 +286,17 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
 
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(k_full(s), 128);
+      // (TMA: the producer's expectation, and its own copies done)
+      mbar_init(k_full(s), TMA && !F8 ? 2 : 128);
       mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), 128);
+      mbar_init(v_full(s), TMA && !F8 ? 2 : 128);
       mbar_init(v_empty(s), 1);
     }
-    mbar_init(q_full, 128);
+    for (int s = 0; F8 && s < 2 * kAhead; ++s) {
+      mbar_init(raw_full(s), 2);
+      mbar_init(raw_empty(s), 128);
+    }
+    mbar_init(q_full, 256);
     mbar_init(q_empty, F8 ? 1 + kSoftmax : 1);  // the item's last product; its factors are read
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full(t), 2);  // the product's commit, and the issuing thread
@@ -286,6 +311,10 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
   if (warp == kWarpIssue) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
+  }
+  if (TMA && warp == kWarpTma && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
   pdl_wait();
 
@@ -364,19 +393,16 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
       constexpr uint32_t id_pv = idesc(kTreeRows, D, true, F8);
       const uint32_t q_lo = sdesc_lo(sbase + L::offQ, 16), k_lo = sdesc_lo(sbase + L::offK, 16);
       const uint32_t v_lo = sdesc_lo(sbase + L::offV, L::kAtom);
+      const volatile uint8_t* s_flag = smem + L::offFlag;
       bool ok = true;
-      Cursor c = s_first;
-      int item = 0;   // running index in this CTA
-      int own = -1;   // PV: the item of this thread's last tile
-      for (int n = 0; n < n_tiles && ok; ++n) {
+      int own = -1;  // PV: the item of this thread's last tile
+      for (int n = role == 0 ? 0 : role - 1; n < n_tiles && ok; n += role == 0 ? 1 : 2) {
         const int slot = n % kSlots, t = n & 1;
         const uint32_t sp = (n / kSlots) & 1;
-        const bool last = c.t + 1 == c.nt;
         if (role == 0) {
-          if (c.t == 0 || n == 0) {
-            if (!(ok = mbar_wait(q_full, item & 1, abort_flag, st))) break;
-          }
           if (!(ok = mbar_wait(k_full(slot), sp, abort_flag, st))) break;
+          const int f = s_flag[n % L::kMasks];
+          if ((f & kFirst) && !(ok = mbar_wait(q_full, f & 1, abort_flag, st))) break;
           // P_t of this accumulator's previous tile has been used
           if (n > 1 && !(ok = mbar_wait(o_done(t), ((n >> 1) - 1) & 1, abort_flag, st))) break;
           tc_fence_after();
@@ -387,14 +413,16 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
                    sdesc_join(k_lo + slot * (L::kTile >> 4) + off, hi), id_qk, kk > 0);
           }
           mma_commit(k_empty(slot));
-          if (last) mma_commit(q_empty);
+          if (f & kLast) mma_commit(q_empty);
           mma_commit(s_full(t));
           mbar_arrive(s_full(t));  // what the loaders wrote for the softmax is visible behind this
-        } else if (t == role - 1) {
-          const bool first = own != item;  // this accumulator's first tile of the item
+        } else {
           if (!(ok = mbar_wait(p_full(t), (n >> 1) & 1, abort_flag, st))) break;
           if (!(ok = mbar_wait(v_full(slot), sp, abort_flag, st))) break;
-          if (first && item > 0 && !(ok = mbar_wait(o_free, (item - 1) & 1, abort_flag, st))) break;
+          const int item = s_flag[n % L::kMasks] & kItem;
+          const bool first = own != item;  // this accumulator's first tile of the item
+          // the item before has been read out
+          if (first && (item != 0 || n > 1) && !(ok = mbar_wait(o_free, (item - 1) & 1, abort_flag, st))) break;
           own = item;
           tc_fence_after();
 #pragma unroll 2
@@ -406,205 +434,329 @@ __global__ void __launch_bounds__(kBlock, 1) tree_kernel(const __grid_constant__
           mma_commit(v_empty(slot));
           mma_commit(o_done(t));
         }
-        if (last) ++item;
-        if (n + 1 < n_tiles) advance(c, a);
       }
       // Every MMA this thread issued must be finished before tensor memory is released.
       mma_commit(mma_done(role));
       mbar_wait_drain(mma_done(role), 0, st);
     }
+    if (TMA && warp == kWarpTma) {
+      // ---- TMA producer: lane i has box i / kAtoms of each tile (and half i % kAtoms of its rows) ----
+      constexpr int kAtoms = F8 ? 1 : D / 64;
+      constexpr int kLanes = L::kRow / 16, kRows = 32 / kLanes;
+      const int box = a.box, bx = lane / kAtoms, atom = lane % kAtoms;
+      const bool mine = bx * box < kTreeKeys;
+      const uint32_t whole = box == 32 ? ~0u : 0xffffu;
+      const uint32_t box_bytes = box * (F8 ? L::kRow : 128);
+      uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + L::offKeys);
+      uint8_t* s_flag = smem + L::offFlag;
+      Cursor look = s_first;
+      int item = -1, left = n_tiles;
+      // looked up two tiles ahead
+      int page_of[2] = {}, slot_of[2] = {}, head_of[2] = {}, flag_of[2] = {};
+      uint32_t part_of[2] = {};  // the box's keys that count
+      int n = -2, halves = 0;  // started
+      // tile n's keys (half 0) or values; false when a wait gave up
+      auto fetch = [&](int half, uint32_t keys) {
+        const int slot = F8 ? half * kAhead + n % kAhead : n % kSlots;
+        const uint32_t full = F8 ? raw_full(slot) : half ? v_full(slot) : k_full(slot);
+        const uint32_t empty = F8 ? raw_empty(slot) : half ? v_empty(slot) : k_empty(slot);
+        constexpr int kTurns = F8 ? kAhead : kSlots;
+        if (n >= kTurns && !__all_sync(0xffffffffu, mbar_wait(empty, ((n / kTurns) - 1) & 1, abort_flag, st)))
+          return false;
+        const uint32_t to = sbase + (F8 ? L::offRaw + slot * L::kRaw : (half ? L::offV : L::offK) + slot * L::kTile);
+        const bool load = mine && keys == whole;
+        const uint32_t loads = __ballot_sync(0xffffffffu, load);
+        if (lane == 0) mbar_arrive_expect_tx(full, __popc(loads) * box_bytes);
+        __syncwarp();
+        if (load)
+          tma_load_4d(to + (F8 ? 0 : atom * L::kAtom) + bx * box_bytes, half ? &tm_v : &tm_k, full, atom * 64,
+                      head_of[0], slot_of[0], page_of[0]);
+        // Boxes that are cut off or not there: row by row, zeros for the keys that do not count.
+        uint32_t rest = __ballot_sync(0xffffffffu, mine && atom == 0 && !load);
+        if (__builtin_expect(rest != 0, 0)) {
+          const long long st_page = half ? a.v_strides[0] : a.k_strides[0];
+          const long long st_slot = half ? a.v_strides[1] : a.k_strides[1];
+          const long long st_head = half ? a.v_strides[2] : a.k_strides[2];
+          const long long off = keys ? page_of[0] * st_page + slot_of[0] * st_slot + head_of[0] * st_head : 0;
+          const int c16 = lane % kLanes, r_lane = lane / kLanes;
+#pragma unroll 1
+          while (rest) {
+            const int from = __ffs(rest) - 1;
+            rest &= rest - 1;
+            const uint32_t count = __shfl_sync(0xffffffffu, keys, from);
+            const unsigned char* p = (half ? a.v : a.k) + __shfl_sync(0xffffffffu, off, from) + c16 * 16;
+#pragma unroll 1
+            for (int r = r_lane; r < box; r += kRows) {
+              const int row = from / kAtoms * box + r;
+              const uint32_t at = F8 ? row * L::kRow + c16 * 16 : (c16 >> 3) * L::kAtom + sw128_offset(row, c16 & 7);
+              cp_async16(to + at, p + (count >> r & 1 ? r * st_slot : 0), count >> r & 1);
+            }
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(full);
+        ++halves;
+        return true;
+      };
+#pragma unroll 1
+      for (; n < n_tiles; ++n) {
+        if (n >= 0) {
+          const bool held = part_of[0] != 0;
+          const bool there = held && static_cast<unsigned>(page_of[0]) < static_cast<unsigned>(a.cache.n_pages);
+          if (held && !there) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+          const uint32_t keys = there ? part_of[0] : 0u;
+          // the tile's keys that are there, 32 to a word
+          const uint32_t lo = __shfl_sync(0xffffffffu, keys, (box == 32 ? lane : 2 * lane) * kAtoms & 31);
+          const uint32_t up = __shfl_sync(0xffffffffu, keys, (2 * lane + 1) * kAtoms & 31);
+          if (lane < 4) s_keys[(n % L::kMasks) * 4 + lane] = box == 32 ? lo : lo | up << 16;
+          if (lane == 0) s_flag[n % L::kMasks] = static_cast<uint8_t>(flag_of[0]);
+          __syncwarp();
+          if (!fetch(0, keys) || !fetch(1, keys)) break;
+        }
+        page_of[0] = page_of[1], slot_of[0] = slot_of[1], head_of[0] = head_of[1];
+        flag_of[0] = flag_of[1], part_of[0] = part_of[1];
+        part_of[1] = 0;
+        if (left > 0) {
+          const bool first = look.t == 0 || left == n_tiles;
+          item += first;
+          flag_of[1] = (first ? kFirst : 0) | (look.t + 1 == look.nt ? kLast : 0) | (item & kItem);
+          head_of[1] = look.hh;
+          const int key = look.k.from(look.t) + bx * box;
+          const uint32_t part = mine ? bits(look.k.begin(look.t) - key, look.k.end(look.t) - key) & whole : 0u;
+          if (part) {
+            const int entry = static_cast<int>(static_cast<uint64_t>(key) * a.page_mul >> a.page_shift);
+            slot_of[1] = key - entry * a.cache.page_size;
+            page_of[1] = a.table[look.b * a.table_stride + entry];
+            part_of[1] = part;
+          }
+          if (--left > 0) advance(look, a);
+        }
+      }
+      // Every copy started here must land before the CTA may exit.
+      constexpr int kTurns = F8 ? kAhead : kSlots;
+      for (int h = max(0, halves - 2 * kTurns); h < halves; ++h) {
+        const int slot = F8 ? (h & 1) * kAhead + (h >> 1) % kAhead : (h >> 1) % kSlots;
+        mbar_wait_drain(F8 ? raw_full(slot) : h & 1 ? v_full(slot) : k_full(slot), ((h >> 1) / kTurns) & 1, st);
+      }
+    }
   } else if (warp >= kWarpLoad) {
     regs_decrease<kRegsLoad>();
-    const int w = (warp - kWarpLoad) & 3;     // rows 32 w .. 32 w + 31 of each tile
-    const bool keys = warp < kWarpLoad + 4;   // K's loaders, or V's
-    constexpr int kLanes = L::kRow / 16;      // of a row: 16 bytes each
-    constexpr int kRows = 32 / kLanes;        // of an instruction
-    const int c16 = lane % kLanes, r_lane = lane / kLanes;
-    const unsigned char* base = (keys ? a.k : a.v) + c16 * 16;
-    const long long st_page = keys ? a.k_strides[0] : a.v_strides[0];
-    const long long st_slot = keys ? a.k_strides[1] : a.v_strides[1];
-    const long long st_head = keys ? a.k_strides[2] : a.v_strides[2];
-    const uint32_t tile_base = sbase + (keys ? L::offK : L::offV);
-    const uint32_t raw = sbase + L::offRaw + (keys ? 0 : kAhead * L::kRaw) + w * (L::kRaw / 4) + lane * 16;
-    uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + L::offKeys);
-    auto full = [&](int s) { return keys ? k_full(s) : v_full(s); };
-    auto empty = [&](int s) { return keys ? k_empty(s) : v_empty(s); };
-    // Look-ups, two tiles ahead of the loads. WHOLE: each 16 keys lie in one page, and lanes
-    // 0 and 1 look up the warp's two sixteens; else a lane looks up its row.
-    Cursor look = s_first;
-    int look_left = n_tiles;
-    int page_of[2] = {}, slot_of[2] = {-1, -1};  // slot -1: no such key
-    int head_of[2] = {};                         // K/V head
-    uint32_t span_of[2] = {};                    // keys of the 32 that count
-    auto look_up = [&]() {
-      page_of[0] = page_of[1], slot_of[0] = slot_of[1], head_of[0] = head_of[1], span_of[0] = span_of[1];
-      page_of[1] = 0, slot_of[1] = -1;
-      if (look_left <= 0) return;
-      const int first = look.k.from(look.t) + 32 * w;
-      span_of[1] = bits(look.k.begin(look.t) - first, look.k.end(look.t) - first);
-      head_of[1] = look.hh;
-      const uint32_t mine = WHOLE ? (lane < 2 ? span_of[1] >> (kBox * lane) & 0xffffu : 0u) : span_of[1] >> lane & 1u;
-      if (mine) {
-        const int key = first + (WHOLE ? kBox * lane : lane);
-        const int entry = static_cast<int>(static_cast<uint64_t>(key) * a.page_mul >> a.page_shift);
-        slot_of[1] = key - entry * a.cache.page_size;
-        page_of[1] = a.table[look.b * a.table_stride + entry];
-      }
-      if (--look_left > 0) advance(look, a);
-    };
-    // where this lane's 16 bytes of a row go: rows repeat the swizzle after kPats of them
-    constexpr int kPats = F8 ? 1 : 8 / kRows;
-    uint32_t pat[kPats];
-#pragma unroll
-    for (int i = 0; i < kPats; ++i)
-      pat[i] = F8 ? 0u : (c16 >> 3) * L::kAtom + 32 * w * 128 + sw128_offset(i * kRows + r_lane, c16 & 7);
-    // and, widened, of an e4m3 cache
-    constexpr int kWides = F8 ? 8 / kRows : 1;
-    uint32_t wide[kWides];
-#pragma unroll
-    for (int i = 0; i < kWides; ++i)
-      wide[i] = (c16 >> 2) * L::kAtom + 32 * w * 128 + sw128_offset(i * kRows + r_lane, (c16 & 3) * 2);
-    // one tile's copies
-    auto issue = [&](int n) {
-      const int page = page_of[0], sl = slot_of[0];
-      const bool held = sl >= 0;
-      const bool ok = held && static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages);
-      if (held && !ok) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-      const long long off = ok ? page * st_page + sl * st_slot + head_of[0] * st_head : 0;
-      const uint32_t oks = __ballot_sync(0xffffffffu, ok);
-      const uint32_t there = WHOLE ? span_of[0] & ((oks & 1 ? 0xffffu : 0u) | (oks & 2 ? 0xffff0000u : 0u)) : oks;
-      if (keys && lane == 0) s_keys[(n % L::kMasks) * 4 + w] = there;
-      const uint32_t to = F8 ? raw + (n % kAhead) * L::kRaw : tile_base + (n % kSlots) * L::kTile;
-      constexpr int kPer = kBox / kRows;  // instructions of 16 keys
-      auto dst = [&](int i) { return F8 ? to + i * 512 : to + pat[i % kPats] + i / kPats * 1024; };
-      if constexpr (WHOLE) {
-        const uint32_t mine = there >> r_lane;
-#pragma unroll 1
-        for (int box = 0; box < 2; ++box) {
-          const unsigned char* p = base + __shfl_sync(0xffffffffu, off, box) + r_lane * st_slot;
-          const uint32_t valid = mine >> (box * kBox);
-          const uint32_t at = box * kPer * (F8 ? 512 : 1024 / kPats);
-#pragma unroll
-          for (int i = 0; i < kPer; ++i, p += kRows * st_slot) cp_async16(at + dst(i), p, valid >> (i * kRows) & 1);
-        }
-      } else {
-        // (addresses of several rows first: one after the other they wait for each shuffle)
-#pragma unroll
-        for (int i0 = 0; i0 < 2 * kPer; i0 += kPer) {
-          const unsigned char* p[kPer];
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) p[i] = base + __shfl_sync(0xffffffffu, off, (i0 + i) * kRows + r_lane);
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            cp_async16(dst(i0 + i), p[i], there >> ((i0 + i) * kRows + r_lane) & 1);
-        }
-      }
-    };
-    // an item's query rows (V's loaders): row x is token x / G, head x % G of the group; zeros
-    // behind the last
-    auto load_q = [&](const Cursor& c) {
-      constexpr int kChunks = D / 8;  // 16 bytes of a row each
-      constexpr int kPer = kTreeRows * kChunks / 128;  // of a thread
-      constexpr int kStep = 128 / kChunks;             // rows between them
-      const int l = tid - 32 * (kWarpLoad + 4), ch = l % kChunks;
+    // An item's query rows, by all of these warps: row x is token x / G, head x % G of the
+    // group; zeros behind the last.
+    constexpr int kChunks = D / 8;           // 16 bytes of a row each
+    constexpr int kStep = 256 / kChunks;     // rows between a thread's
+    constexpr int kPer = kTreeRows / kStep;  // of a thread
+    const int l = tid - 32 * kWarpLoad, ch = l % kChunks;
+    auto fetch_q = [&](const Cursor& c, uint4 (&x)[kPer]) {
       const int rows = min(kTreeRows, c.s.n * a.group - c.qt * kTreeRows);
       const int at = c.qt * kTreeRows + l / kChunks;
       int token = at / a.group, g = at - token * a.group;
       const int step_t = kStep / a.group, step_g = kStep - step_t * a.group;
       const __nv_bfloat16* q = a.q + static_cast<long long>(c.hh) * a.group * a.q_head + ch * 8;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (i * kStep + l / kChunks < rows)
+          x[i] = *reinterpret_cast<const uint4*>(q + (c.s.c0 + token) * a.q_token + g * a.q_head);
+        token += step_t;
+        g += step_g;
+        if (g >= a.group) g -= a.group, ++token;
+      }
+    };
+    auto store_q = [&](const uint4 (&x)[kPer]) {
       float* s_qs = reinterpret_cast<float*>(smem + L::offQs);
-#pragma unroll 1
-      for (int x0 = 0; x0 < kPer; x0 += 8) {
-        uint4 x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = make_uint4(0, 0, 0, 0);
-          if ((x0 + i) * kStep + l / kChunks < rows)
-            x[i] = *reinterpret_cast<const uint4*>(q + (c.s.c0 + token) * a.q_token + g * a.q_head);
-          token += step_t;
-          g += step_g;
-          if (g >= a.group) g -= a.group, ++token;
-        }
+      for (int i = 0; i < kPer; ++i) {
+        const int row = i * kStep + l / kChunks;
+        uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        if constexpr (F8) {
+          float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = (x0 + i) * kStep + l / kChunks;
-          uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          if constexpr (F8) {
-            float top = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float u = fabsf(bf16lo_f32(y[e])), v = fabsf(bf16hi_f32(y[e]));
-              top = fmaxf(top, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
-            }
-#pragma unroll
-            for (int m = kChunks / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-            // 2^e brings the row's largest element into [2^13, 2^14) (see decode.cuh)
-            const int floor_log2 = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-            const int e2 = top > 0.f ? min(13 - floor_log2, 126) : 0;
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-            if (ch == 0) s_qs[row] = fminf(a.scale_log2 * (a.cache.k_scale * down), FLT_MAX);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = pack_f16(bf16lo_f32(y[e]) * up, bf16hi_f32(y[e]) * up);
+          for (int e = 0; e < 4; ++e) {
+            const float u = fabsf(bf16lo_f32(y[e])), v = fabsf(bf16hi_f32(y[e]));
+            top = fmaxf(top, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
           }
-          st_shared_v4(sbase + L::offQ + (ch >> 3) * L::kAtom + sw128_offset(row, ch & 7), y[0], y[1], y[2], y[3]);
+#pragma unroll
+          for (int m = kChunks / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+          // 2^e brings the row's largest element into [2^13, 2^14) (see decode.cuh)
+          const int floor_log2 = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+          const int e2 = top > 0.f ? min(13 - floor_log2, 126) : 0;
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+          if (ch == 0) s_qs[row] = fminf(a.scale_log2 * (a.cache.k_scale * down), FLT_MAX);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = pack_f16(bf16lo_f32(y[e]) * up, bf16hi_f32(y[e]) * up);
         }
+        st_shared_v4(sbase + L::offQ + (ch >> 3) * L::kAtom + sw128_offset(row, ch & 7), y[0], y[1], y[2], y[3]);
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     };
-
+    int item = 0;  // running index in this CTA
+    // The query's buffer is free once the previous item's last product has read it.
+    auto q_free = [&]() {
+      return item == 0 || __all_sync(0xffffffffu, mbar_wait(q_empty, (item - 1) & 1, abort_flag, st));
+    };
     Cursor c = s_first;
-    int item = 0;
-    bool ok = true;
-    // Step n: tile n is handed over, tile n + kAhead fetched, and the one two further looked
-    // up. (One loop, also for the first tiles: every copy of this code costs instruction
-    // fetches, which bound this kernel next to its loads.)
-#pragma unroll 1
-    for (int n = -kAhead - 2; n < n_tiles; ++n) {
-      const int n2 = n + kAhead;
-      if (n >= 0) {
-        const int slot = n % kSlots;
-        if (!keys) {
-          if (c.t == 0 || n == 0) {
-            // the query's buffer is free once the previous item's last product has read it
-            if (item > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (item - 1) & 1, abort_flag, st)))) break;
-            load_q(c);
-          }
-          if (c.t + 1 == c.nt) ++item;
-          if (n + 1 < n_tiles) advance(c, a);
-        }
-        cp_async_wait<kAhead - 1>();
-        if constexpr (F8) {
-          // widen this lane's own bytes
-          if (n >= kSlots &&
-              !(ok = __all_sync(0xffffffffu, mbar_wait(empty(slot), ((n / kSlots) - 1) & 1, abort_flag, st))))
-            break;
-          uint4 got[32 / kRows];
-#pragma unroll
-          for (int i = 0; i < 32 / kRows; ++i) got[i] = ld_shared_v4(raw + (n % kAhead) * L::kRaw + i * 512);
-#pragma unroll
-          for (int i = 0; i < 32 / kRows; ++i) {
-            const uint4 x = got[i];
-            // (the swizzle repeats after 8 rows, and the second chunk is the first's neighbour)
-            const uint32_t at = tile_base + slot * L::kTile + wide[i % kWides] + i / kWides * 1024;
-            st_shared_v4(at, e4m3x2_f16x2(x.x), e4m3x2_f16x2(x.x >> 16), e4m3x2_f16x2(x.y), e4m3x2_f16x2(x.y >> 16));
-            st_shared_v4(at ^ 16u, e4m3x2_f16x2(x.z), e4m3x2_f16x2(x.z >> 16), e4m3x2_f16x2(x.w),
-                         e4m3x2_f16x2(x.w >> 16));
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(full(slot));
-        // bf16: the next tile waits for its slot
-        if (!F8 && n2 < n_tiles && n2 >= kSlots &&
-            !(ok = __all_sync(0xffffffffu, mbar_wait(empty(n2 % kSlots), ((n2 / kSlots) - 1) & 1, abort_flag, st))))
-          break;
+    if constexpr (TMA && !F8) {
+      // ---- the queries alone: the next item's wait in registers ----
+      for (int left = n_tiles; left > 0;) {
+        uint4 x[kPer];
+        fetch_q(c, x);
+        if (!q_free()) break;
+        store_q(x);
+        ++item;
+        left -= c.nt - c.t;
+        if (left > 0) next_item(c, a);
       }
-      if (n2 >= 0 && n2 < n_tiles) issue(n2);
-      cp_async_commit();
-      look_up();
+    } else {
+      // ---- warps 0 to 3: keys, 4 to 7: values; rows 32 w .. 32 w + 31 of each tile ----
+      const int w = (warp - kWarpLoad) & 3;
+      const bool keys = warp < kWarpLoad + 4;
+      constexpr int kLanes = L::kRow / 16;  // of a row: 16 bytes each
+      constexpr int kRows = 32 / kLanes;    // of an instruction
+      constexpr int kLoads = 32 / kRows;    // instructions of 32 rows
+      const int c16 = lane % kLanes, r_lane = lane / kLanes;
+      const uint32_t tile_base = sbase + (keys ? L::offK : L::offV);
+      const uint32_t raw = sbase + L::offRaw + (keys ? 0 : kAhead * L::kRaw) + w * (L::kRaw / 4) + lane * 16;
+      uint8_t* s_flag = smem + L::offFlag;
+      auto full = [&](int s) { return keys ? k_full(s) : v_full(s); };
+      auto empty = [&](int s) { return keys ? k_empty(s) : v_empty(s); };
+      // e4m3: where this lane's 16 bytes go, widened (the swizzle repeats after 8 rows)
+      constexpr int kWides = F8 ? 8 / kRows : 1;
+      uint32_t wide[kWides];
+#pragma unroll
+      for (int i = 0; i < kWides; ++i)
+        wide[i] = (c16 >> 2) * L::kAtom + 32 * w * 128 + sw128_offset(i * kRows + r_lane, (c16 & 3) * 2);
+      auto widen = [&](int n) {
+        uint4 got[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) got[i] = ld_shared_v4(raw + (n % kAhead) * L::kRaw + i * 512);
+        const uint32_t to = tile_base + (n % kSlots) * L::kTile;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const uint4 x = got[i];
+          const uint32_t at = to + wide[i % kWides] + i / kWides * 1024;
+          st_shared_v4(at, e4m3x2_f16x2(x.x), e4m3x2_f16x2(x.x >> 16), e4m3x2_f16x2(x.y), e4m3x2_f16x2(x.y >> 16));
+          // (the row's next chunk: its neighbour)
+          st_shared_v4(at ^ 16u, e4m3x2_f16x2(x.z), e4m3x2_f16x2(x.z >> 16), e4m3x2_f16x2(x.w),
+                       e4m3x2_f16x2(x.w >> 16));
+        }
+      };
+      auto slot_free = [&](int n) {
+        return n < kSlots ||
+               __all_sync(0xffffffffu, mbar_wait(empty(n % kSlots), ((n / kSlots) - 1) & 1, abort_flag, st));
+      };
+      if constexpr (TMA) {
+        // e4m3 by TMA: widen only
+#pragma unroll 1
+        for (int n = 0; n < n_tiles; ++n) {
+          const int stage = (keys ? 0 : kAhead) + n % kAhead;
+          if (!__all_sync(0xffffffffu, mbar_wait(raw_full(stage), (n / kAhead) & 1, abort_flag, st))) break;
+          if (s_flag[n % L::kMasks] & kFirst) {
+            if (n > 0) next_item(c, a);
+            uint4 x[kPer];
+            fetch_q(c, x);
+            if (!q_free()) break;
+            store_q(x);
+            ++item;
+          }
+          if (!slot_free(n)) break;
+          widen(n);
+          mbar_arrive(raw_empty(stage));
+          fence_proxy_async_smem();
+          mbar_arrive(full(n % kSlots));
+        }
+      } else {
+        const unsigned char* base = (keys ? a.k : a.v) + c16 * 16;
+        const long long st_page = keys ? a.k_strides[0] : a.v_strides[0];
+        const long long st_slot = keys ? a.k_strides[1] : a.v_strides[1];
+        const long long st_head = keys ? a.k_strides[2] : a.v_strides[2];
+        uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + L::offKeys);
+        // each lane looks its row up, two tiles ahead of the load
+        Cursor look = s_first;
+        int left = n_tiles, look_item = -1;
+        int page_of[2] = {}, slot_of[2] = {-1, -1};  // slot -1: no such key
+        int head_of[2] = {}, flag_of[2] = {};
+        auto look_up = [&]() {
+          page_of[0] = page_of[1], slot_of[0] = slot_of[1], head_of[0] = head_of[1], flag_of[0] = flag_of[1];
+          page_of[1] = 0, slot_of[1] = -1;
+          if (left <= 0) return;
+          const bool first = look.t == 0 || left == n_tiles;
+          look_item += first;
+          flag_of[1] = (first ? kFirst : 0) | (look.t + 1 == look.nt ? kLast : 0) | (look_item & kItem);
+          head_of[1] = look.hh;
+          const int key = look.k.from(look.t) + 32 * w + lane;
+          if (key >= look.k.begin(look.t) && key < look.k.end(look.t)) {
+            const int entry = static_cast<int>(static_cast<uint64_t>(key) * a.page_mul >> a.page_shift);
+            slot_of[1] = key - entry * a.cache.page_size;
+            page_of[1] = a.table[look.b * a.table_stride + entry];
+          }
+          if (--left > 0) advance(look, a);
+        };
+        // bf16: where this lane's 16 bytes go (the swizzle repeats after 8 rows)
+        constexpr int kPats = F8 ? 1 : 8 / kRows;
+        uint32_t pat[kPats];
+#pragma unroll
+        for (int i = 0; i < kPats; ++i)
+          pat[i] = F8 ? 0u : (c16 >> 3) * L::kAtom + 32 * w * 128 + sw128_offset(i * kRows + r_lane, c16 & 7);
+        auto issue = [&](int n) {
+          const int page = page_of[0], sl = slot_of[0];
+          const bool held = sl >= 0;
+          const bool there = held && static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages);
+          if (held && !there) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+          const long long off = there ? page * st_page + sl * st_slot + head_of[0] * st_head : 0;
+          const uint32_t rows = __ballot_sync(0xffffffffu, there);
+          if (keys && lane == 0) s_keys[(n % L::kMasks) * 4 + w] = rows;
+          if (keys && w == 0 && lane == 0) s_flag[n % L::kMasks] = static_cast<uint8_t>(flag_of[0]);
+          const uint32_t to = F8 ? raw + (n % kAhead) * L::kRaw : tile_base + (n % kSlots) * L::kTile;
+          // (addresses of several rows first: one after the other they wait for each shuffle)
+          constexpr int kSet = kLoads < 8 ? kLoads : 8;
+#pragma unroll
+          for (int i0 = 0; i0 < kLoads; i0 += kSet) {
+            const unsigned char* p[kSet];
+#pragma unroll
+            for (int i = 0; i < kSet; ++i) p[i] = base + __shfl_sync(0xffffffffu, off, (i0 + i) * kRows + r_lane);
+#pragma unroll
+            for (int i = 0; i < kSet; ++i)
+              cp_async16(F8 ? to + (i0 + i) * 512 : to + pat[(i0 + i) % kPats] + (i0 + i) / kPats * 1024, p[i],
+                         rows >> ((i0 + i) * kRows + r_lane) & 1);
+          }
+        };
+        // Step n: tile n is handed over, tile n + kAhead fetched, and the one two further looked
+        // up. (One loop, also for the first tiles: every copy of this code costs instruction
+        // fetches.)
+#pragma unroll 1
+        for (int n = -kAhead - 2; n < n_tiles; ++n) {
+          if (n >= 0) {
+            if (c.t == 0 || n == 0) {
+              uint4 x[kPer];
+              fetch_q(c, x);
+              if (!q_free()) break;
+              store_q(x);
+              ++item;
+            }
+            if (n + 1 < n_tiles) advance(c, a);
+            cp_async_wait<kAhead - 1>();
+            if constexpr (F8) {
+              if (!slot_free(n)) break;
+              widen(n);  // this lane's own bytes
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(full(n % kSlots));
+            // bf16: the next tile waits for its slot
+            if (!F8 && n + kAhead < n_tiles && !slot_free(n + kAhead)) break;
+          }
+          if (n + kAhead >= 0 && n + kAhead < n_tiles) issue(n + kAhead);
+          cp_async_commit();
+          look_up();
+        }
+        cp_async_wait<0>();
+      }
     }
-    cp_async_wait<0>();
   } else {
     regs_increase<kRegsSoftmax>();
     // ---- softmax: warpgroup t takes the run's tiles t, t + 2, ... ----
@@ -946,10 +1098,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
   }
 }
 
-template <int D, bool F8>
-cudaError_t launch_tree_t(const TreeArgs& a, int ctas, bool join, cudaStream_t stream) {
+template <int D, bool F8, bool TMA>
+cudaError_t launch_tree_t(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, bool join,
+                          cudaStream_t stream) {
   using L = Layout<D, F8>;
-  auto kern = a.cache.page_size % kBox == 0 ? tree_kernel<D, F8, true> : tree_kernel<D, F8, false>;
+  auto kern = tree_kernel<D, F8, TMA>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   // The warpgroups' register shares must fit the launch allocation, or an increase would
@@ -958,20 +1111,30 @@ cudaError_t launch_tree_t(const TreeArgs& a, int ctas, bool join, cudaStream_t s
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
   if (fa.numRegs < kRegsAtLaunch) return cudaErrorInvalidConfiguration;
-  e = launch_pdl(kern, dim3(ctas), dim3(kBlock), L::kAlloc, stream, a);
+  e = launch_pdl(kern, dim3(ctas), dim3(kBlock), L::kAlloc, stream, tk, tv, a);
   if (e != cudaSuccess || !join) return e;
   const int rows = std::min(kTreeRows, a.T * a.group);
   return launch_pdl(tree_join_kernel<D>, dim3(ctas, (rows + kJoinWarps - 1) / kJoinWarps),
                     dim3(32 * kJoinWarps), 0, stream, a);
 }
 
+template <int D, bool F8>
+cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, bool join,
+                          cudaStream_t stream) {
+  return a.box ? launch_tree_t<D, F8, true>(tk, tv, a, ctas, join, stream)
+               : launch_tree_t<D, F8, false>(tk, tv, a, ctas, join, stream);
+}
+
 }  // namespace
 
-cudaError_t launch_tree(const TreeArgs& a, int ctas, bool join, cudaStream_t stream) {
+cudaError_t launch_tree(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, bool join,
+                        cudaStream_t stream) {
   const bool f8 = a.cache.type == ATTN_CACHE_E4M3;
   if (a.cache.d == 64)
-    return f8 ? launch_tree_t<64, true>(a, ctas, join, stream) : launch_tree_t<64, false>(a, ctas, join, stream);
-  return f8 ? launch_tree_t<128, true>(a, ctas, join, stream) : launch_tree_t<128, false>(a, ctas, join, stream);
+    return f8 ? launch_tree_d<64, true>(tk, tv, a, ctas, join, stream)
+              : launch_tree_d<64, false>(tk, tv, a, ctas, join, stream);
+  return f8 ? launch_tree_d<128, true>(tk, tv, a, ctas, join, stream)
+            : launch_tree_d<128, false>(tk, tv, a, ctas, join, stream);
 }
 
 }  // namespace eba

@@ -2,6 +2,7 @@
 // over the paged cache.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,6 +30,7 @@ struct TreeArgs {
   int words;              // of a token's mask
   unsigned page_mul;      // key / page_size = key * page_mul >> page_shift, for every int >= 0
   int page_shift;
+  int box;                // keys of a TMA load: 32 or 16, a divisor of page_size; 0: no TMA
   int max_len;            // keys a table row can hold
   int T, B, H, group;
   int window, sinks;      // window 0: none
@@ -45,7 +47,9 @@ struct TreeArgs {
   int* status;
   unsigned long long limit_ns;
 };
-// ctas: the grid. join: items may be cut between CTAs.
-cudaError_t launch_tree(const TreeArgs& a, int ctas, bool join, cudaStream_t stream);
+// tk, tv: 4-D views (d, H_kv, page_size, n_pages) of the pages, with boxes of a.box rows of 64
+// bf16 elements (128-byte swizzle) or of a whole e4m3 row; unused without a.box. ctas: the
+// grid. join: items may be cut between CTAs.
+cudaError_t launch_tree(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, bool join, cudaStream_t stream);
 
 }  // namespace eba
