@@ -501,6 +501,46 @@ def _sides(left, right, sinks):
     return out
 
 
+_WINDOW_LAYOUTS = None  # _Layouts, below
+
+
+def _window_layout(q, k, v, left, right, sinks):
+    """A windowed call's sizes and window as the C ABI takes them, and the bytes of the
+    backward's workspace; its checks are made once for each form of tensors."""
+    try:
+        key = (_form(q), _form(k), _form(v), left, right, sinks, type(left), type(right), type(sinks))
+        lay = _WINDOW_LAYOUTS.get(key)
+    except AttributeError:
+        lay = key = None
+    if lay is None:
+        sizes = _qkv(q, k, v, gqa=True)
+        window = _sides(left, right, sinks)
+        lay = (*sizes, *window), int(lib().attn_bwd_window_workspace_size(*sizes, *window))
+        _WINDOW_LAYOUTS.add(key, lay)
+    return lay
+
+
+def _fwd_window(q, k, v, sizes, scale):
+    o = torch.empty_like(q)
+    lse = torch.empty(sizes[0:2] + sizes[3:4], device=q.device, dtype=torch.float32)
+    _launch(q.device, lib().attn_fwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), *sizes, _scale(scale, sizes[5]))
+    return o, lse
+
+
+def _bwd_window(q, k, v, o, do, lse, sizes, need, scale, workspace):
+    if workspace is None:
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+    elif workspace.numel() * workspace.element_size() < need or workspace.device != q.device or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {q.device}")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    _launch(q.device, lib().attn_bwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+            do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes,
+            _scale(scale, sizes[5]), workspace.data_ptr(), need)
+    return dq, dk, dv
+
+
 def fwd_window(q, k, v, left, right=0, sinks=0, scale=None):
     """Attention within a sliding window and to the first tokens: (o bf16 [B,H,Lq,d],
     lse fp32 [B,H,Lq]).
@@ -509,13 +549,7 @@ def fwd_window(q, k, v, left, right=0, sinks=0, scale=None):
     sees the keys p - left to p + right and, up to p + right, the first ``sinks``. left
     or right None: no end to that side (left=None is plain causal attention). A query
     that sees no key gives o = 0 and lse = -inf. k, v may have H_kv < H heads."""
-    B, H, Hkv, Lq, Lk, d = _qkv(q, k, v, gqa=True)
-    left, right, sinks = _sides(left, right, sinks)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Lq), device=q.device, dtype=torch.float32)
-    _launch(q.device, lib().attn_fwd_window, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv,
-            Lq, Lk, d, left, right, sinks, _scale(scale, d))
-    return o, lse
+    return _fwd_window(q, k, v, _window_layout(q, k, v, left, right, sinks)[0], scale)
 
 
 def bwd_window_workspace_size(B, H, H_kv, Lq, Lk, d, left, right=0, sinks=0) -> int:
@@ -525,27 +559,18 @@ def bwd_window_workspace_size(B, H, H_kv, Lq, Lk, d, left, right=0, sinks=0) -> 
 def bwd_window(q, k, v, o, do, lse, left, right=0, sinks=0, scale=None, workspace=None):
     """Gradients (dq, dk, dv) of sum(o * do) for fwd_window; P is recomputed from lse.
     Keys that no query sees, and queries that see no key, have zero gradients."""
-    B, H, Hkv, Lq, Lk, d = _bwd_inputs(q, k, v, o, do, lse, gqa=True)
-    left, right, sinks = _sides(left, right, sinks)
-    need = int(lib().attn_bwd_window_workspace_size(B, H, Hkv, Lq, Lk, d, left, right, sinks))
-    if workspace is None:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-    elif workspace.numel() * workspace.element_size() < need or workspace.device != q.device or \
-            not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {q.device}")
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    _launch(q.device, lib().attn_bwd_window, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse),
-            _ptr(dq), _ptr(dk), _ptr(dv), B, H, Hkv, Lq, Lk, d, left, right, sinks, _scale(scale, d),
-            _ptr(workspace), need)
-    return dq, dk, dv
+    sizes, need = _window_layout(q, k, v, left, right, sinks)
+    _bwd_inputs(q, k, v, o, do, lse, gqa=True)
+    return _bwd_window(q, k, v, o, do, lse, sizes, need, scale, workspace)
 
 
 class _AttentionWindow(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, left, right, sinks, scale):
-        o, lse = fwd_window(q, k, v, left, right, sinks, scale)
+        sizes, need = _window_layout(q, k, v, left, right, sinks)
+        o, lse = _fwd_window(q, k, v, sizes, scale)
         ctx.save_for_backward(q, k, v, o, lse)
-        ctx.window = (left, right, sinks, scale)
+        ctx.call = sizes, need, scale
         return o
 
     @staticmethod
@@ -555,9 +580,10 @@ class _AttentionWindow(torch.autograd.Function):
         do = do.contiguous()
         if do.data_ptr() & 15:  # autograd also hands over views
             do = do.clone()
-        grads = bwd_window(q, k, v, o, do, lse, *ctx.window)
-        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None,
-                None)
+        grads = _bwd_window(q, k, v, o, do, lse, *ctx.call, None)
+        need = ctx.needs_input_grad
+        return (grads[0] if need[0] else None, grads[1] if need[1] else None, grads[2] if need[2] else None,
+                None, None, None, None)
 
 
 def attention_window(q, k, v, left, right=0, sinks=0, scale=None):
@@ -715,6 +741,7 @@ def _off_boundary(name):
 
 
 _ROPE_LAYOUTS = _Layouts()
+_WINDOW_LAYOUTS = _Layouts()
 
 
 def _rope_layout(q, k, positions, plan):
@@ -1013,6 +1040,7 @@ def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None
     the first ``sinks``; pages that hold none of these need not be there."""
     try:
         key = (_form(q), _form(page_table), _form(seq_lens), _form(positions), cache._key, window, sinks,
+               type(window), type(sinks),
                None if rope is None else (rope.n_axes, rope.n_pairs))
         lay = _DECODE_LAYOUTS.get(key)
     except AttributeError:
@@ -1104,7 +1132,7 @@ def decode_tree(cache, q, page_table, seq_lens, cu_q=None, mask=None, window=Non
     masks and tables, so a captured call follows their contents."""
     try:
         key = (_form(q), _form(page_table), _form(seq_lens), _form(cu_q), _form(mask), cache._key, window,
-               sinks)
+               sinks, type(window), type(sinks))
         lay = _TREE_LAYOUTS.get(key)
     except AttributeError:
         lay = key = None
