@@ -156,19 +156,22 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(32 * kPoolWa
     const long long items = static_cast<long long>(a.n) * parts;
     for (long long x = worker; x < items; x += kPoolWorkers) {
       const int i = static_cast<int>(x / parts), part = static_cast<int>(x - static_cast<long long>(i) * parts);
+      const int s = a.src[i], d = a.dst[i];
       if (__ldcg(a.to + i) == kPairBad) continue;
-      const int s = a.src[i], d = a.dst[i], len = a.lens[s], whole = len / size;
       const int* in = a.table + s * a.table_stride;
       int* out = a.table + d * a.table_stride;
       int page[kPoolDeep];
+      const int len = a.lens[s];
 #pragma unroll
       for (int u = 0; u < kPoolDeep; ++u) {
         const int e = part * kRun + 32 * u + lane;
-        page[u] = e < whole ? in[e] : -1;
+        page[u] = e < a.max_pages ? in[e] : -1;
       }
+      const int whole = len / size;
 #pragma unroll
       for (int u = 0; u < kPoolDeep; ++u) {
         const int e = part * kRun + 32 * u + lane;
+        if (e >= whole) page[u] = -1;
         if (page[u] >= a.pool.n_pages) {
           bad_page(a.status);
           page[u] = -1;

@@ -43,6 +43,7 @@ namespace {
 constexpr int kSoftmax = 256;  // threads: two warpgroups
 constexpr int kWarpLoad = 8, kWarpIssue = 16;  // first warps of the loaders (of K, of V) and the issuers
 constexpr int kWarpTma = 19;  // the producer of TMA loads
+constexpr int kWarpTmaV = 12;  // bf16: and of the values'
 constexpr int kBlock = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kRegsSoftmax = 128, kRegsLoad = 80, kRegsIssue = 64;
@@ -62,6 +63,7 @@ struct Layout {
   static constexpr int kAhead = 2;                     // tiles on their way
   static constexpr int kRaw = F8 ? kTreeKeys * kRow : 0;  // a stage of stored bytes
   static constexpr int kMasks = 8;                     // tiles whose key masks are kept
+  static constexpr int kQThreads(bool tma) { return tma && !F8 ? 128 : 256; }  // that fetch queries
   static constexpr int offQ = 0;
   static constexpr int offK = offQ + kTreeRows * D * 2;
   static constexpr int offV = offK + kSlots * kTile;
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kBlock, 1)
       mbar_init(raw_full(s), 2);
       mbar_init(raw_empty(s), 128);
     }
-    mbar_init(q_full, 256);
+    mbar_init(q_full, L::kQThreads(TMA));
     mbar_init(q_empty, F8 ? 1 + kSoftmax : 1);  // the item's last product; its factors are read
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full(t), 2);  // the product's commit, and the issuing thread
@@ -384,6 +386,115 @@ __global__ void __launch_bounds__(kBlock, 1)
   __syncthreads();
   const int n_tiles = r1 - r0;
 
+  // TMA producer of keys, values or both: lane i has box i / kAtoms of each tile, and half
+  // i % kAtoms of its rows.
+  auto produce = [&](bool k_too, bool v_too) {
+    constexpr int kAtoms = F8 ? 1 : D / 64;
+    constexpr int kLanes = L::kRow / 16, kRows = 32 / kLanes;
+    const int box = a.box, bx = lane / kAtoms, atom = lane % kAtoms;
+    const bool mine = bx * box < kTreeKeys;
+    const uint32_t whole = box == 32 ? ~0u : 0xffffu;
+    const uint32_t box_bytes = box * (F8 ? L::kRow : 128);
+    uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + L::offKeys);
+    uint8_t* s_flag = smem + L::offFlag;
+    Cursor look = s_first;
+    int item = -1, left = n_tiles;
+    // looked up two tiles ahead
+    int page_of[2] = {}, slot_of[2] = {}, head_of[2] = {}, flag_of[2] = {};
+    uint32_t part_of[2] = {};  // the box's keys that count
+    int n = -2, halves = 0;  // started
+    // tile n's keys (half 0) or values; false when a wait gave up
+    auto fetch = [&](int half, uint32_t keys) {
+      const int slot = F8 ? half * kAhead + n % kAhead : n % kSlots;
+      const uint32_t full = F8 ? raw_full(slot) : half ? v_full(slot) : k_full(slot);
+      const uint32_t empty = F8 ? raw_empty(slot) : half ? v_empty(slot) : k_empty(slot);
+      constexpr int kTurns = F8 ? kAhead : kSlots;
+      if (n >= kTurns && !__all_sync(0xffffffffu, mbar_wait(empty, ((n / kTurns) - 1) & 1, abort_flag, st)))
+        return false;
+      const uint32_t to = sbase + (F8 ? L::offRaw + slot * L::kRaw : (half ? L::offV : L::offK) + slot * L::kTile);
+      const bool load = mine && keys == whole;
+      const uint32_t loads = __ballot_sync(0xffffffffu, load);
+      if (lane == 0) mbar_arrive_expect_tx(full, __popc(loads) * box_bytes);
+      __syncwarp();
+      if (load)
+        tma_load_4d(to + (F8 ? 0 : atom * L::kAtom) + bx * box_bytes, half ? &tm_v : &tm_k, full, atom * 64,
+                    head_of[0], slot_of[0], page_of[0]);
+      // Boxes that are cut off or not there: row by row, zeros for the keys that do not count.
+      uint32_t rest = __ballot_sync(0xffffffffu, mine && atom == 0 && !load);
+      if (__builtin_expect(rest != 0, 0)) {
+        const long long st_page = half ? a.v_strides[0] : a.k_strides[0];
+        const long long st_slot = half ? a.v_strides[1] : a.k_strides[1];
+        const long long st_head = half ? a.v_strides[2] : a.k_strides[2];
+        const long long off = keys ? page_of[0] * st_page + slot_of[0] * st_slot + head_of[0] * st_head : 0;
+        const int c16 = lane % kLanes, r_lane = lane / kLanes;
+#pragma unroll 1
+        while (rest) {
+          const int from = __ffs(rest) - 1;
+          rest &= rest - 1;
+          const uint32_t count = __shfl_sync(0xffffffffu, keys, from);
+          const unsigned char* p = (half ? a.v : a.k) + __shfl_sync(0xffffffffu, off, from) + c16 * 16;
+#pragma unroll 1
+          for (int r = r_lane; r < box; r += kRows) {
+            const int row = from / kAtoms * box + r;
+            const uint32_t at = F8 ? row * L::kRow + c16 * 16 : (c16 >> 3) * L::kAtom + sw128_offset(row, c16 & 7);
+            cp_async16(to + at, p + (count >> r & 1 ? r * st_slot : 0), count >> r & 1);
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(full);
+      ++halves;
+      return true;
+    };
+#pragma unroll 1
+    for (; n < n_tiles; ++n) {
+      if (n >= 0) {
+        const bool held = part_of[0] != 0;
+        const bool there = held && static_cast<unsigned>(page_of[0]) < static_cast<unsigned>(a.cache.n_pages);
+        if (held && !there) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+        const uint32_t keys = there ? part_of[0] : 0u;
+        // the tile's keys that are there, 32 to a word
+        const uint32_t lo = __shfl_sync(0xffffffffu, keys, (box == 32 ? lane : 2 * lane) * kAtoms & 31);
+        const uint32_t up = __shfl_sync(0xffffffffu, keys, (2 * lane + 1) * kAtoms & 31);
+        if (k_too && lane < 4) s_keys[(n % L::kMasks) * 4 + lane] = box == 32 ? lo : lo | up << 16;
+        if (k_too && lane == 0) s_flag[n % L::kMasks] = static_cast<uint8_t>(flag_of[0]);
+        __syncwarp();
+        if (k_too && !fetch(0, keys)) break;
+        if (v_too && !fetch(1, keys)) break;
+      }
+      page_of[0] = page_of[1], slot_of[0] = slot_of[1], head_of[0] = head_of[1];
+      flag_of[0] = flag_of[1], part_of[0] = part_of[1];
+      part_of[1] = 0;
+      if (left > 0) {
+        const bool first = look.t == 0 || left == n_tiles;
+        item += first;
+        flag_of[1] = (first ? kFirst : 0) | (look.t + 1 == look.nt ? kLast : 0) | (item & kItem);
+        head_of[1] = look.hh;
+        const int key = look.k.from(look.t) + bx * box;
+        const uint32_t part = mine ? bits(look.k.begin(look.t) - key, look.k.end(look.t) - key) & whole : 0u;
+        if (part) {
+          const int entry = static_cast<int>(static_cast<uint64_t>(key) * a.page_mul >> a.page_shift);
+          slot_of[1] = key - entry * a.cache.page_size;
+          page_of[1] = a.table[look.b * a.table_stride + entry];
+          part_of[1] = part;
+        }
+        if (--left > 0) advance(look, a);
+      }
+    }
+    // Every copy started here must land before the CTA may exit.
+    constexpr int kTurns = F8 ? kAhead : kSlots;
+    const int both = k_too && v_too ? 2 : 1;
+    for (int h = max(0, halves - both * kTurns); h < halves; ++h) {
+      const int i = h / both;
+      const bool value = both == 2 ? h & 1 : v_too;
+      const int slot = F8 ? (value ? kAhead : 0) + i % kAhead : i % kSlots;
+      mbar_wait_drain(F8 ? raw_full(slot) : value ? v_full(slot) : k_full(slot), (i / kTurns) & 1, st);
+    }
+  };
+
   if (warp >= kWarpIssue) {
     regs_decrease<kRegsIssue>();
     const int role = warp - kWarpIssue;  // 0: QK, 1 / 2: PV of the even / odd tiles
@@ -439,115 +550,14 @@ __global__ void __launch_bounds__(kBlock, 1)
       mma_commit(mma_done(role));
       mbar_wait_drain(mma_done(role), 0, st);
     }
-    if (TMA && warp == kWarpTma) {
-      // ---- TMA producer: lane i has box i / kAtoms of each tile (and half i % kAtoms of its rows) ----
-      constexpr int kAtoms = F8 ? 1 : D / 64;
-      constexpr int kLanes = L::kRow / 16, kRows = 32 / kLanes;
-      const int box = a.box, bx = lane / kAtoms, atom = lane % kAtoms;
-      const bool mine = bx * box < kTreeKeys;
-      const uint32_t whole = box == 32 ? ~0u : 0xffffu;
-      const uint32_t box_bytes = box * (F8 ? L::kRow : 128);
-      uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + L::offKeys);
-      uint8_t* s_flag = smem + L::offFlag;
-      Cursor look = s_first;
-      int item = -1, left = n_tiles;
-      // looked up two tiles ahead
-      int page_of[2] = {}, slot_of[2] = {}, head_of[2] = {}, flag_of[2] = {};
-      uint32_t part_of[2] = {};  // the box's keys that count
-      int n = -2, halves = 0;  // started
-      // tile n's keys (half 0) or values; false when a wait gave up
-      auto fetch = [&](int half, uint32_t keys) {
-        const int slot = F8 ? half * kAhead + n % kAhead : n % kSlots;
-        const uint32_t full = F8 ? raw_full(slot) : half ? v_full(slot) : k_full(slot);
-        const uint32_t empty = F8 ? raw_empty(slot) : half ? v_empty(slot) : k_empty(slot);
-        constexpr int kTurns = F8 ? kAhead : kSlots;
-        if (n >= kTurns && !__all_sync(0xffffffffu, mbar_wait(empty, ((n / kTurns) - 1) & 1, abort_flag, st)))
-          return false;
-        const uint32_t to = sbase + (F8 ? L::offRaw + slot * L::kRaw : (half ? L::offV : L::offK) + slot * L::kTile);
-        const bool load = mine && keys == whole;
-        const uint32_t loads = __ballot_sync(0xffffffffu, load);
-        if (lane == 0) mbar_arrive_expect_tx(full, __popc(loads) * box_bytes);
-        __syncwarp();
-        if (load)
-          tma_load_4d(to + (F8 ? 0 : atom * L::kAtom) + bx * box_bytes, half ? &tm_v : &tm_k, full, atom * 64,
-                      head_of[0], slot_of[0], page_of[0]);
-        // Boxes that are cut off or not there: row by row, zeros for the keys that do not count.
-        uint32_t rest = __ballot_sync(0xffffffffu, mine && atom == 0 && !load);
-        if (__builtin_expect(rest != 0, 0)) {
-          const long long st_page = half ? a.v_strides[0] : a.k_strides[0];
-          const long long st_slot = half ? a.v_strides[1] : a.k_strides[1];
-          const long long st_head = half ? a.v_strides[2] : a.k_strides[2];
-          const long long off = keys ? page_of[0] * st_page + slot_of[0] * st_slot + head_of[0] * st_head : 0;
-          const int c16 = lane % kLanes, r_lane = lane / kLanes;
-#pragma unroll 1
-          while (rest) {
-            const int from = __ffs(rest) - 1;
-            rest &= rest - 1;
-            const uint32_t count = __shfl_sync(0xffffffffu, keys, from);
-            const unsigned char* p = (half ? a.v : a.k) + __shfl_sync(0xffffffffu, off, from) + c16 * 16;
-#pragma unroll 1
-            for (int r = r_lane; r < box; r += kRows) {
-              const int row = from / kAtoms * box + r;
-              const uint32_t at = F8 ? row * L::kRow + c16 * 16 : (c16 >> 3) * L::kAtom + sw128_offset(row, c16 & 7);
-              cp_async16(to + at, p + (count >> r & 1 ? r * st_slot : 0), count >> r & 1);
-            }
-          }
-          cp_async_commit();
-          cp_async_wait<0>();
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (lane == 0) mbar_arrive(full);
-        ++halves;
-        return true;
-      };
-#pragma unroll 1
-      for (; n < n_tiles; ++n) {
-        if (n >= 0) {
-          const bool held = part_of[0] != 0;
-          const bool there = held && static_cast<unsigned>(page_of[0]) < static_cast<unsigned>(a.cache.n_pages);
-          if (held && !there) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-          const uint32_t keys = there ? part_of[0] : 0u;
-          // the tile's keys that are there, 32 to a word
-          const uint32_t lo = __shfl_sync(0xffffffffu, keys, (box == 32 ? lane : 2 * lane) * kAtoms & 31);
-          const uint32_t up = __shfl_sync(0xffffffffu, keys, (2 * lane + 1) * kAtoms & 31);
-          if (lane < 4) s_keys[(n % L::kMasks) * 4 + lane] = box == 32 ? lo : lo | up << 16;
-          if (lane == 0) s_flag[n % L::kMasks] = static_cast<uint8_t>(flag_of[0]);
-          __syncwarp();
-          if (!fetch(0, keys) || !fetch(1, keys)) break;
-        }
-        page_of[0] = page_of[1], slot_of[0] = slot_of[1], head_of[0] = head_of[1];
-        flag_of[0] = flag_of[1], part_of[0] = part_of[1];
-        part_of[1] = 0;
-        if (left > 0) {
-          const bool first = look.t == 0 || left == n_tiles;
-          item += first;
-          flag_of[1] = (first ? kFirst : 0) | (look.t + 1 == look.nt ? kLast : 0) | (item & kItem);
-          head_of[1] = look.hh;
-          const int key = look.k.from(look.t) + bx * box;
-          const uint32_t part = mine ? bits(look.k.begin(look.t) - key, look.k.end(look.t) - key) & whole : 0u;
-          if (part) {
-            const int entry = static_cast<int>(static_cast<uint64_t>(key) * a.page_mul >> a.page_shift);
-            slot_of[1] = key - entry * a.cache.page_size;
-            page_of[1] = a.table[look.b * a.table_stride + entry];
-            part_of[1] = part;
-          }
-          if (--left > 0) advance(look, a);
-        }
-      }
-      // Every copy started here must land before the CTA may exit.
-      constexpr int kTurns = F8 ? kAhead : kSlots;
-      for (int h = max(0, halves - 2 * kTurns); h < halves; ++h) {
-        const int slot = F8 ? (h & 1) * kAhead + (h >> 1) % kAhead : (h >> 1) % kSlots;
-        mbar_wait_drain(F8 ? raw_full(slot) : h & 1 ? v_full(slot) : k_full(slot), ((h >> 1) / kTurns) & 1, st);
-      }
-    }
+    if constexpr (TMA)
+      if (warp == kWarpTma) produce(true, F8);
   } else if (warp >= kWarpLoad) {
     regs_decrease<kRegsLoad>();
     // An item's query rows, by all of these warps: row x is token x / G, head x % G of the
     // group; zeros behind the last.
     constexpr int kChunks = D / 8;           // 16 bytes of a row each
-    constexpr int kStep = 256 / kChunks;     // rows between a thread's
+    constexpr int kStep = L::kQThreads(TMA) / kChunks;  // rows between a thread's
     constexpr int kPer = kTreeRows / kStep;  // of a thread
     const int l = tid - 32 * kWarpLoad, ch = l % kChunks;
     auto fetch_q = [&](const Cursor& c, uint4 (&x)[kPer]) {
@@ -602,8 +612,9 @@ __global__ void __launch_bounds__(kBlock, 1)
     };
     Cursor c = s_first;
     if constexpr (TMA && !F8) {
-      // ---- the queries alone: the next item's wait in registers ----
-      for (int left = n_tiles; left > 0;) {
+      // ---- the values' loads; the queries, the next item's waiting in registers ----
+      if (warp == kWarpTmaV) produce(false, true);
+      for (int left = warp < kWarpTmaV ? n_tiles : 0; left > 0;) {
         uint4 x[kPer];
         fetch_q(c, x);
         if (!q_free()) break;
@@ -799,9 +810,8 @@ __global__ void __launch_bounds__(kBlock, 1)
       float qs = a.scale_log2;
       int mine = 0;  // tiles of this warpgroup
       if (F8 && count == 1 && (n & 1) != t) mbar_arrive(q_empty);
-      for (int step = 0; step < count; ++step) {
+      for (int step = (n ^ t) & 1; step < count; step += 2) {
         const int nn = n + step;
-        if ((nn & 1) != t) continue;
         const int k0 = c.k.from(t_begin + step);
         wait(s_full(t), (nn >> 1) & 1);
         tc_fence_after();
