@@ -43,10 +43,10 @@ namespace {
 constexpr int kSoftmax = 256;  // threads: two warpgroups
 constexpr int kWarpLoad = 8, kWarpIssue = 16;  // first warps of the loaders (of K, of V) and the issuers
 constexpr int kWarpTma = 19;  // the producer of TMA loads
-constexpr int kWarpTmaV = 12;  // bf16: and of the values'
+constexpr int kWarpTmaV = 18;  // bf16: and of the values'
 constexpr int kBlock = 640;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kRegsSoftmax = 128, kRegsLoad = 80, kRegsIssue = 64;
+constexpr uint32_t kRegsSoftmax = 136, kRegsLoad = 72, kRegsIssue = 64;
 constexpr int kRegsAtLaunch = (256 * kRegsSoftmax + 256 * kRegsLoad + 128 * kRegsIssue) / kBlock;
 static_assert(kRegsAtLaunch == 96 && kRegsAtLaunch * kBlock == 256 * kRegsSoftmax + 256 * kRegsLoad + 128 * kRegsIssue,
               "register split must add up to the launch allocation");
@@ -63,18 +63,17 @@ struct Layout {
   static constexpr int kAhead = 2;                     // tiles on their way
   static constexpr int kRaw = F8 ? kTreeKeys * kRow : 0;  // a stage of stored bytes
   static constexpr int kMasks = 8;                     // tiles whose key masks are kept
-  static constexpr int kQThreads(bool tma) { return tma && !F8 ? 128 : 256; }  // that fetch queries
   static constexpr int offQ = 0;
   static constexpr int offK = offQ + kTreeRows * D * 2;
   static constexpr int offV = offK + kSlots * kTile;
   static constexpr int offRaw = offV + kSlots * kTile;
-  static constexpr int offMl = offRaw + 2 * kAhead * kRaw;     // [2][128] a warpgroup's reference and sum
-  static constexpr int offFix = offMl + 2 * kTreeRows * 8;  // [2][128] fp16 (bf16 caches)
-  static constexpr int offQs = offFix + (F8 ? 0 : 2 * kTreeRows * 2);  // [128] score factors (e4m3)
+  static constexpr int offMl = offRaw + 2 * kAhead * kRaw;  // [2][128]: what the warpgroups exchange
+  static constexpr int offQs = offMl + 2 * kTreeRows * 8;  // [128] score factors (e4m3)
   static constexpr int offKeys = offQs + (F8 ? kTreeRows * 4 : 0);  // [kMasks][4]: keys that are there
-  static constexpr int offFlag = offKeys + kMasks * 16;  // [kMasks] bytes
-  static constexpr int nBar = 4 * kSlots + 2 + 6 + 1 + 3 + (F8 ? 4 * kAhead : 0);
-  static constexpr int offBar = offFlag + kMasks;
+  static constexpr int kFlags = 16;                    // and their flags (read later)
+  static constexpr int offFlag = offKeys + kMasks * 16;  // [kFlags] bytes
+  static constexpr int nBar = 4 * kSlots + 2 + 8 + 1 + 2 + (F8 ? 4 * kAhead : 0);
+  static constexpr int offBar = offFlag + kFlags;
   static constexpr int offMisc = offBar + nBar * 8;          // tensor memory's address, abort flag
   static constexpr int offScan = offMl;                      // [kBlock / 32], before the items
   static constexpr int offFirst = offMisc + 8;
@@ -84,7 +83,7 @@ struct Layout {
   static constexpr bool kAlignSlack = D == 64;
   static constexpr int kAlloc = kBytes + (kAlignSlack ? 1024 : 0);
   static_assert(kAlloc <= 232448, "shared memory over the limit");
-  static constexpr uint32_t cS = 0, cO = 256;
+  static constexpr uint32_t cS = 0, cO = 256, cP = 384;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -119,6 +118,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// Whether `mine` holds for any thread of a named barrier, at which all of them meet.
+__device__ __forceinline__ bool vote_any(int id, int threads, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return any != 0;
 }
 
 // ---- the list of tiles -----------------------------------------------------------------
@@ -271,14 +283,16 @@ __global__ void __launch_bounds__(kBlock, 1)
   auto v_empty = [&](int s) { return bar0 + 8u * (3 * kSlots + s); };
   const uint32_t b1 = bar0 + 8u * (4 * kSlots);
   const uint32_t q_full = b1, q_empty = b1 + 8;
-  auto s_full = [&](int t) { return b1 + 16 + 8u * t; };
-  auto p_full = [&](int t) { return b1 + 32 + 8u * t; };
-  auto o_done = [&](int t) { return b1 + 48 + 8u * t; };
-  const uint32_t o_free = b1 + 64;  // the item's end has read both accumulators
-  auto mma_done = [&](int i) { return b1 + 72 + 8u * i; };
+  // S of a tile is computed; read by the softmax; P is written; O += P V is done
+  auto s_full = [&](int i) { return b1 + 16 + 8u * i; };
+  auto s_free = [&](int i) { return b1 + 32 + 8u * i; };
+  auto p_full = [&](int i) { return b1 + 48 + 8u * i; };
+  auto pv_done = [&](int i) { return b1 + 64 + 8u * i; };
+  const uint32_t o_free = b1 + 80;  // the item's end has read O
+  auto mma_done = [&](int i) { return b1 + 88 + 8u * i; };
   // stages of stored bytes: K's, then V's
-  auto raw_full = [&](int s) { return b1 + 96 + 8u * s; };
-  auto raw_empty = [&](int s) { return b1 + 96 + 8u * (2 * kAhead + s); };
+  auto raw_full = [&](int s) { return b1 + 104 + 8u * s; };
+  auto raw_empty = [&](int s) { return b1 + 104 + 8u * (2 * kAhead + s); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
   int* s_scan = reinterpret_cast<int*>(smem + L::offScan);
@@ -298,15 +312,16 @@ __global__ void __launch_bounds__(kBlock, 1)
       mbar_init(raw_full(s), 2);
       mbar_init(raw_empty(s), 128);
     }
-    mbar_init(q_full, L::kQThreads(TMA));
+    mbar_init(q_full, 256);
     mbar_init(q_empty, F8 ? 1 + kSoftmax : 1);  // the item's last product; its factors are read
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(s_full(t), 2);  // the product's commit, and the issuing thread
-      mbar_init(p_full(t), 128);
-      mbar_init(o_done(t), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full(i), 2);  // the product's commit, and the issuing thread
+      mbar_init(s_free(i), kSoftmax);
+      mbar_init(p_full(i), kSoftmax);
+      mbar_init(pv_done(i), 1);
+      mbar_init(mma_done(i), 1);
     }
     mbar_init(o_free, kSoftmax);
-    for (int i = 0; i < 3; ++i) mbar_init(mma_done(i), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -460,7 +475,7 @@ __global__ void __launch_bounds__(kBlock, 1)
         const uint32_t lo = __shfl_sync(0xffffffffu, keys, (box == 32 ? lane : 2 * lane) * kAtoms & 31);
         const uint32_t up = __shfl_sync(0xffffffffu, keys, (2 * lane + 1) * kAtoms & 31);
         if (k_too && lane < 4) s_keys[(n % L::kMasks) * 4 + lane] = box == 32 ? lo : lo | up << 16;
-        if (k_too && lane == 0) s_flag[n % L::kMasks] = static_cast<uint8_t>(flag_of[0]);
+        if (k_too && lane == 0) s_flag[n % L::kFlags] = static_cast<uint8_t>(flag_of[0]);
         __syncwarp();
         if (k_too && !fetch(0, keys)) break;
         if (v_too && !fetch(1, keys)) break;
@@ -497,8 +512,8 @@ __global__ void __launch_bounds__(kBlock, 1)
 
   if (warp >= kWarpIssue) {
     regs_decrease<kRegsIssue>();
-    const int role = warp - kWarpIssue;  // 0: QK, 1 / 2: PV of the even / odd tiles
-    if (role < 3 && lane == 0) {
+    const int role = warp - kWarpIssue;  // 0: S = Q K^T, 1: O += P V
+    if (role < 2 && lane == 0) {
       constexpr uint32_t hi = sdesc_hi(1024);
       constexpr uint32_t id_qk = idesc(kTreeRows, kTreeKeys, false, F8);
       constexpr uint32_t id_pv = idesc(kTreeRows, D, true, F8);
@@ -506,44 +521,38 @@ __global__ void __launch_bounds__(kBlock, 1)
       const uint32_t v_lo = sdesc_lo(sbase + L::offV, L::kAtom);
       const volatile uint8_t* s_flag = smem + L::offFlag;
       bool ok = true;
-      int own = -1;  // PV: the item of this thread's last tile
-      for (int n = role == 0 ? 0 : role - 1; n < n_tiles && ok; n += role == 0 ? 1 : 2) {
-        const int slot = n % kSlots, t = n & 1;
-        const uint32_t sp = (n / kSlots) & 1;
+      for (int n = 0; n < n_tiles && ok; ++n) {
+        const int slot = n % kSlots, i = n & 1;
+        const uint32_t sp = (n / kSlots) & 1, before = ((n >> 1) - 1) & 1;
         if (role == 0) {
           if (!(ok = mbar_wait(k_full(slot), sp, abort_flag, st))) break;
-          const int f = s_flag[n % L::kMasks];
+          const int f = s_flag[n % L::kFlags];
           if ((f & kFirst) && !(ok = mbar_wait(q_full, f & 1, abort_flag, st))) break;
-          // P_t of this accumulator's previous tile has been used
-          if (n > 1 && !(ok = mbar_wait(o_done(t), ((n >> 1) - 1) & 1, abort_flag, st))) break;
+          if (n > 1 && !(ok = mbar_wait(s_free(i), before, abort_flag, st))) break;
           tc_fence_after();
 #pragma unroll 2
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * L::kAtom + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + L::cS + t * kTreeKeys, sdesc_join(q_lo + off, hi),
+            mma_ss(tmem + L::cS + i * kTreeKeys, sdesc_join(q_lo + off, hi),
                    sdesc_join(k_lo + slot * (L::kTile >> 4) + off, hi), id_qk, kk > 0);
           }
           mma_commit(k_empty(slot));
           if (f & kLast) mma_commit(q_empty);
-          mma_commit(s_full(t));
-          mbar_arrive(s_full(t));  // what the loaders wrote for the softmax is visible behind this
+          mma_commit(s_full(i));
+          mbar_arrive(s_full(i));  // what the loaders wrote for the softmax is visible behind this
         } else {
-          if (!(ok = mbar_wait(p_full(t), (n >> 1) & 1, abort_flag, st))) break;
+          if (!(ok = mbar_wait(p_full(i), (n >> 1) & 1, abort_flag, st))) break;
           if (!(ok = mbar_wait(v_full(slot), sp, abort_flag, st))) break;
-          const int item = s_flag[n % L::kMasks] & kItem;
-          const bool first = own != item;  // this accumulator's first tile of the item
-          // the item before has been read out
-          if (first && (item != 0 || n > 1) && !(ok = mbar_wait(o_free, (item - 1) & 1, abort_flag, st))) break;
-          own = item;
+          const int f = s_flag[n % L::kFlags];
+          const bool first = f & kFirst;  // overwrites O, once the item before has been read out
+          if (first && n > 0 && !(ok = mbar_wait(o_free, ((f & kItem) - 1) & 1, abort_flag, st))) break;
           tc_fence_after();
 #pragma unroll 2
-          for (int kk = 0; kk < kTreeKeys / 16; ++kk) {
-            const uint64_t b = sdesc_join(v_lo + slot * (L::kTile >> 4) + kk * (2048 >> 4), hi);
-            const uint32_t p = tmem + L::cS + t * kTreeKeys + kk * 8, o = tmem + L::cO + t * D;
-            mma_ts(o, p, b, id_pv, !first || kk > 0);
-          }
+          for (int kk = 0; kk < kTreeKeys / 16; ++kk)
+            mma_ts(tmem + L::cO, tmem + L::cP + i * (kTreeKeys / 2) + kk * 8,
+                   sdesc_join(v_lo + slot * (L::kTile >> 4) + kk * (2048 >> 4), hi), id_pv, !first || kk > 0);
           mma_commit(v_empty(slot));
-          mma_commit(o_done(t));
+          mma_commit(pv_done(i));
         }
       }
       // Every MMA this thread issued must be finished before tensor memory is released.
@@ -551,13 +560,13 @@ __global__ void __launch_bounds__(kBlock, 1)
       mbar_wait_drain(mma_done(role), 0, st);
     }
     if constexpr (TMA)
-      if (warp == kWarpTma) produce(true, F8);
+      if (warp == kWarpTma || (!F8 && warp == kWarpTmaV)) produce(warp == kWarpTma, F8 || warp == kWarpTmaV);
   } else if (warp >= kWarpLoad) {
     regs_decrease<kRegsLoad>();
     // An item's query rows, by all of these warps: row x is token x / G, head x % G of the
     // group; zeros behind the last.
     constexpr int kChunks = D / 8;           // 16 bytes of a row each
-    constexpr int kStep = L::kQThreads(TMA) / kChunks;  // rows between a thread's
+    constexpr int kStep = 256 / kChunks;     // rows between a thread's
     constexpr int kPer = kTreeRows / kStep;  // of a thread
     const int l = tid - 32 * kWarpLoad, ch = l % kChunks;
     auto fetch_q = [&](const Cursor& c, uint4 (&x)[kPer]) {
@@ -612,9 +621,8 @@ __global__ void __launch_bounds__(kBlock, 1)
     };
     Cursor c = s_first;
     if constexpr (TMA && !F8) {
-      // ---- the values' loads; the queries, the next item's waiting in registers ----
-      if (warp == kWarpTmaV) produce(false, true);
-      for (int left = warp < kWarpTmaV ? n_tiles : 0; left > 0;) {
+      // ---- the queries alone: the next item's wait in registers ----
+      for (int left = n_tiles; left > 0;) {
         uint4 x[kPer];
         fetch_q(c, x);
         if (!q_free()) break;
@@ -667,7 +675,7 @@ __global__ void __launch_bounds__(kBlock, 1)
         for (int n = 0; n < n_tiles; ++n) {
           const int stage = (keys ? 0 : kAhead) + n % kAhead;
           if (!__all_sync(0xffffffffu, mbar_wait(raw_full(stage), (n / kAhead) & 1, abort_flag, st))) break;
-          if (s_flag[n % L::kMasks] & kFirst) {
+          if (s_flag[n % L::kFlags] & kFirst) {
             if (n > 0) next_item(c, a);
             uint4 x[kPer];
             fetch_q(c, x);
@@ -722,7 +730,7 @@ __global__ void __launch_bounds__(kBlock, 1)
           const long long off = there ? page * st_page + sl * st_slot + head_of[0] * st_head : 0;
           const uint32_t rows = __ballot_sync(0xffffffffu, there);
           if (keys && lane == 0) s_keys[(n % L::kMasks) * 4 + w] = rows;
-          if (keys && w == 0 && lane == 0) s_flag[n % L::kMasks] = static_cast<uint8_t>(flag_of[0]);
+          if (keys && w == 0 && lane == 0) s_flag[n % L::kFlags] = static_cast<uint8_t>(flag_of[0]);
           const uint32_t to = F8 ? raw + (n % kAhead) * L::kRaw : tile_base + (n % kSlots) * L::kTile;
           // (addresses of several rows first: one after the other they wait for each shuffle)
           constexpr int kSet = kLoads < 8 ? kLoads : 8;
@@ -770,14 +778,13 @@ __global__ void __launch_bounds__(kBlock, 1)
     }
   } else {
     regs_increase<kRegsSoftmax>();
-    // ---- softmax: warpgroup t takes the run's tiles t, t + 2, ... ----
-    const int t = warp >> 2, sub = warp & 3;
+    // ---- softmax: warpgroup g has keys 64 g .. 64 g + 63 of every tile, a thread one row ----
+    const int g = warp >> 2, sub = warp & 3;
     const int row = sub * 32 + lane;  // of the item == lane of tensor memory
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
-    const uint32_t tS = lane_base + L::cS + t * kTreeKeys, tO = lane_base + L::cO + t * D;
-    const uint32_t* s_keys = reinterpret_cast<const uint32_t*>(smem + L::offKeys);
-    float2* s_ml = reinterpret_cast<float2*>(smem + L::offMl);  // [warpgroup][row]
-    __half* s_fix = reinterpret_cast<__half*>(smem + L::offFix);
+    const uint32_t tO = lane_base + L::cO + g * (D / 2);  // the columns that it rescales and writes out
+    float* s_max = reinterpret_cast<float*>(smem + L::offMl);   // [warpgroup][row]
+    float2* s_sum = reinterpret_cast<float2*>(smem + L::offMl);  // at an item's end
     // A wait that gives up ends all waits; the warps still meet at every barrier, and
     // what they write is undefined.
     bool live = true;
@@ -808,142 +815,131 @@ __global__ void __launch_bounds__(kBlock, 1)
       float m_used = -INFINITY;
       float l_sum = 0.f, l_fix = 0.f;  // the weights' sum, and what their rounding adds to it
       float qs = a.scale_log2;
-      int mine = 0;  // tiles of this warpgroup
-      if (F8 && count == 1 && (n & 1) != t) mbar_arrive(q_empty);
-      for (int step = (n ^ t) & 1; step < count; step += 2) {
-        const int nn = n + step;
-        const int k0 = c.k.from(t_begin + step);
-        wait(s_full(t), (nn >> 1) & 1);
+#pragma unroll 1
+      for (int step = 0; step < count; ++step) {
+        const int nn = n + step, i = nn & 1;
+        const int k1 = c.k.from(t_begin + step) + 64 * g;
+        wait(s_full(i), (nn >> 1) & 1);
         tc_fence_after();
-        if (F8 && mine == 0) {
+        if (F8 && step == 0) {
           qs = reinterpret_cast<const float*>(smem + L::offQs)[row];
           mbar_arrive(q_empty);
         }
-        ++mine;
-        if (!some) {  // no row of this warp: its part of P is not looked at
-          tc_fence_before();
-          mbar_arrive(p_full(t));
-          continue;
+        uint32_t x[64];  // this row's scores
+        if (some) {
+          tmem_ld32(lane_base + L::cS + i * kTreeKeys + 64 * g, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld32(lane_base + L::cS + i * kTreeKeys + 64 * g + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
         }
-        // Two passes over the row's scores, 32 at a time, in loops that are not unrolled:
-        // in between the scores stay in tensor memory. (With a row's 128 scores in registers
-        // and the loops unrolled, the roles' code pushed each other out of the instruction
-        // cache.)
-        const uint4 there = ld_shared_v4(sbase + L::offKeys + (nn % L::kMasks) * 16);
-        // in most tiles all keys are there, and all rows see them
-        const bool plain = (there.x & there.y & there.z & there.w) == ~0u && k0 >= near_most && k0 + kTreeKeys <= ctx;
-        uint32_t see[4] = {there.x, there.y, there.z, there.w};
-        if (__builtin_expect(!plain, 0)) {
+        // the keys that are there; in most tiles all, and all rows see them
+        const uint2 there = *reinterpret_cast<const uint2*>(smem + L::offKeys + (nn % L::kMasks) * 16 + 8 * g);
+        if (some) {
+          tmem_wait_ld();
+          reg_pin(*reinterpret_cast<uint32_t(*)[32]>(x));
+          reg_pin(*reinterpret_cast<uint32_t(*)[32]>(x + 32));
+        }
+        tc_fence_before();
+        mbar_arrive(s_free(i));  // the tile after the next may be computed
+        if (__builtin_expect((there.x & there.y) != ~0u || k1 < near_most || k1 + 64 > ctx, 0)) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int k1 = k0 + 32 * y;
+          for (int y = 0; y < 2; ++y) {
+            const int k2 = k1 + 32 * y;
             uint32_t u;
             if (mask) {
-              u = bits(near - k1, ctx - k1) | bits(0, min(a.sinks, ctx) - k1);
-              if (k1 + 32 > ctx) u |= mask_bits(mask, a.words, k1 - ctx) & bits(ctx - k1, c.s.len - k1);
+              u = bits(near - k2, ctx - k2) | bits(0, min(a.sinks, ctx) - k2);
+              if (k2 + 32 > ctx) u |= mask_bits(mask, a.words, k2 - ctx) & bits(ctx - k2, c.s.len - k2);
             } else {
-              u = bits(near - k1, place + 1 - k1) | bits(0, min(a.sinks, place + 1) - k1);
+              u = bits(near - k2, place + 1 - k2) | bits(0, min(a.sinks, place + 1) - k2);
             }
-            see[y] &= u;
+            u &= y ? there.y : there.x;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((u >> e) & 1)) x[32 * y + e] = 0xff800000u;  // -inf
           }
         }
-        uint32_t x[32];
-        // the next 32 scores, those that the row does not see as -inf
-        auto read = [&](int y) {
-          tmem_ld32(tS + 32 * y, x);
-          tmem_wait_ld();
-          reg_pin(x);
-          if (__builtin_expect(!plain, 0)) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((see[0] >> i) & 1)) x[i] = 0xff800000u;
-            const uint32_t first = see[0];
-            see[0] = see[1], see[1] = see[2], see[2] = see[3], see[3] = first;
-          }
-        };
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 64; e += 8) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) m4[u] = fmax3(m4[u], __uint_as_float(x[e + u]), __uint_as_float(x[e + 4 + u]));
+        }
+        const float mine = some ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qs : -INFINITY;
+        // The reference moves when either warpgroup's part of the row passes it by more than
+        // kSlack: a vote of both each tile, and an exchange in the few where it does.
+        if (__builtin_expect(vote_any(1, kSoftmax, mine > m_used + kSlack), 0)) {
+          s_max[g * kTreeRows + row] = mine;
+          named_bar_sync(1, kSoftmax);
+          const float both = fmaxf(mine, s_max[(1 - g) * kTreeRows + row]);
+          const bool bump = both > m_used + kSlack;
+          const float alpha = bump ? ex2_approx(m_used - both) : 1.f;
+          if (bump) m_used = both;
+          l_sum *= alpha;
+          l_fix *= alpha;
+          if (step > 0) {
+            // O holds the products up to the tile before, once that is done
+            wait(pv_done(1 - i), ((nn - 1) >> 1) & 1);
+            tc_fence_after();
+            if (__any_sync(0xffffffffu, bump)) {
 #pragma unroll 1
-        for (int y = 0; y < 4; ++y) {
-          read(y);
+              for (int y = 0; y < D / 64; ++y) {
+                uint32_t ov[32];
+                tmem_ld32(tO + 32 * y, ov);
+                tmem_wait_ld();
+                reg_pin(ov);
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              m4[u] = fmax3(m4[u], __uint_as_float(x[i + u]), __uint_as_float(x[i + 4 + u]));
+                for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                tmem_st32(tO + 32 * y, ov);
+              }
+            }
           }
         }
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qs;
-        const float m_old = m_used;
-        const bool bump = mx > m_used + kSlack;
-        if (bump) m_used = mx;
         // (a row that has seen no key yet has no maximum)
         const float ref = (m_used == -INFINITY ? 0.f : m_used) - (F8 ? kF16Shift : 0.f);
         const float2 qs2 = make_float2(qs, qs), neg = make_float2(-ref, -ref);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-        for (int y = 0; y < 4; ++y) {
-          read(y);
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 z = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), qs2, neg);
-            const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-            w[i] = F8 ? pack_f16(p.x, p.y) : pack_bf16(p.x, p.y);
-            sum[i & 1] = add2(sum[i & 1], p);
-          }
-          tmem_st16(tS + 16 * y, w);
+        if (nn > 1) {
+          wait(pv_done(i), ((nn >> 1) - 1) & 1);  // P of the tile before the last has been used
+          tc_fence_after();
         }
-        // bf16: the rounding of the tile's largest weight (see fwd.cuh: the others' even out)
-        const float top = F8 ? 0.f : ex2_approx(mx - ref);
-        const float top_err = bf16lo_f32(pack_bf16(top, 0.f)) - top;
-        // (the previous product into O_t was done before this tile's scores were computed)
-        if (__builtin_expect(mine > 1 && __any_sync(0xffffffffu, bump), 0)) {
-          const float alpha = bump ? ex2_approx(m_old - m_used) : 1.f;
-          l_sum *= alpha;
-          l_fix *= alpha;
-#pragma unroll 1
-          for (int y = 0; y < D / 32; ++y) {
-            uint32_t ov[32];
-            tmem_ld32(tO + 32 * y, ov);
-            tmem_wait_ld();
-            reg_pin(ov);
+        if (some) {
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-            tmem_st32(tO + 32 * y, ov);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t* y = x + 32 * half + 2 * e;
+              const float2 z = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), qs2, neg);
+              const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+              w[e] = F8 ? pack_f16(p.x, p.y) : pack_bf16(p.x, p.y);
+              sum[e & 1] = add2(sum[e & 1], p);
+            }
+            tmem_st16(lane_base + L::cP + i * (kTreeKeys / 2) + 32 * g + 16 * half, w);
           }
+          l_sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          // bf16: the rounding of the largest weight (see fwd.cuh: the others' even out)
+          const float top = F8 ? 0.f : ex2_approx(mine - ref);
+          l_fix += bf16lo_f32(pack_bf16(top, 0.f)) - top;
+          tmem_st_wait();
         }
-        l_sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        l_fix += top_err;
-        tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(p_full(t));
+        mbar_arrive(p_full(i));
       }
 
-      // ---- the item's end, or the run's: join the two accumulators ----
+      // ---- the item's end, or the run's: the row's sums of both warpgroups, and half of O ----
       {
-        const int last = n + count - 1;  // the warpgroup's last tile is it or the one before
-        const int mine_last = (last & 1) == t ? last : last - 1;
-        if (mine > 0) wait(o_done(t), (mine_last >> 1) & 1);
-        const float ref = m_used == -INFINITY ? -INFINITY : m_used - (F8 ? kF16Shift : 0.f);
-        s_ml[t * kTreeRows + row] = make_float2(ref, l_sum);
-        // what O is too large by, as its weights are the rounded ones
-        if (!F8) s_fix[t * kTreeRows + row] = __float2half_rn(l_sum > 0.f ? -l_fix / (l_sum + l_fix) : 0.f);
-        tc_fence_before();
-        named_bar_sync(1, kSoftmax);
+        const int last = n + count - 1;
+        wait(pv_done(last & 1), (last >> 1) & 1);
         tc_fence_after();
-        const float2 ml0 = s_ml[row], ml1 = s_ml[kTreeRows + row];
-        const float fix0 = F8 ? 0.f : __half2float(s_fix[row]), fix1 = F8 ? 0.f : __half2float(s_fix[kTreeRows + row]);
-        named_bar_sync(1, kSoftmax);  // the next item's are written behind this
-        const float M = fmaxf(ml0.x, ml1.x);
-        const float f0 = ml0.x == -INFINITY ? 0.f : ex2_approx(ml0.x - M);
-        const float f1 = ml1.x == -INFINITY ? 0.f : ex2_approx(ml1.x - M);
-        const float l = ml0.y * f0 + ml1.y * f1;
-        const float g0 = fmaf(f0, fix0, f0), g1 = fmaf(f1, fix1, f1);
+        s_sum[g * kTreeRows + row] = make_float2(l_sum, l_fix);
+        named_bar_sync(1, kSoftmax);
+        const float2 other = s_sum[(1 - g) * kTreeRows + row];
+        const float l = l_sum + other.x, rounded = l + (l_fix + other.y);
+        const float M = m_used == -INFINITY ? -INFINITY : m_used - (F8 ? kF16Shift : 0.f);
         const bool whole = t_begin == 0 && ends;
-        const float mul = !whole ? 1.f : M == -INFINITY ? 0.f : a.o_scale / l;
+        // a part: O as its weights' sum l would have it
+        const float mul = M == -INFINITY ? 0.f : whole ? a.o_scale / rounded : l / rounded;
         const long long out = (static_cast<long long>(c.s.c0) + token) * a.H + c.hh * a.group + at % a.group;
         const long long slot = 2 * cta + (item == 0 ? 0 : 1);
-        if (has && t == 0) {
+        if (has && g == 0) {
           if (whole)
             a.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
           else
@@ -952,37 +948,31 @@ __global__ void __launch_bounds__(kBlock, 1)
         if (some) {
 #pragma unroll 1
           for (int y = 0; y < D / 64; ++y) {
-            const int col = t * (D / 2) + 32 * y;
-            float x[32];
+            const int col = g * (D / 2) + 32 * y;
             uint32_t u[32];
-            tmem_ld32(lane_base + L::cO + col, u);
+            tmem_ld32(tO + 32 * y, u);
             tmem_wait_ld();
             reg_pin(u);
-            // (an accumulator without a weight may hold anything)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = f0 > 0.f ? __uint_as_float(u[i]) * g0 : 0.f;
-            tmem_ld32(lane_base + L::cO + D + col, u);
-            tmem_wait_ld();
-            reg_pin(u);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = (x[i] + (f1 > 0.f ? __uint_as_float(u[i]) * g1 : 0.f)) * mul;
             if (!has) continue;
+            float v[32];
+            // (a row without a weight: whatever was added)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = mul > 0.f ? __uint_as_float(u[e]) * mul : 0.f;
             if (whole) {
               uint4* to = reinterpret_cast<uint4*>(a.o + out * D + col);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                to[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                                   pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+              for (int e = 0; e < 4; ++e)
+                to[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                                   pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
             } else {
               float4* to = reinterpret_cast<float4*>(a.part_o + (slot * kTreeRows + row) * D + col);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                to[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
             }
           }
         }
         tc_fence_before();
-        mbar_arrive(o_free);  // the next item's first products may overwrite the accumulators
+        mbar_arrive(o_free);  // the next item's first product may overwrite O
       }
       n += count;
       if (n == n_tiles && a.cut && tid == 0) {
