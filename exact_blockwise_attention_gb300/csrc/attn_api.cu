@@ -460,7 +460,11 @@ bool make_cache_map(CUtensorMap* m, const void* ptr, const long long* strides, c
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr),
             dims, st, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            // (no more than a row: what lies beside it is another head's, read at another time)
+            row == 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+            : row == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                         : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

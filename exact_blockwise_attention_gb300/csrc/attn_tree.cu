@@ -42,8 +42,7 @@ namespace {
 
 constexpr int kSoftmax = 256;  // threads: two warpgroups
 constexpr int kWarpLoad = 8, kWarpIssue = 16;  // first warps of the loaders (of K, of V) and the issuers
-constexpr int kWarpTma = 19;  // the producer of TMA loads
-constexpr int kWarpTmaV = 18;  // bf16: and of the values'
+constexpr int kWarpTmaK = 18, kWarpTmaV = 19;  // the producers of TMA loads
 constexpr int kBlock = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kRegsSoftmax = 136, kRegsLoad = 72, kRegsIssue = 64;
@@ -329,10 +328,8 @@ __global__ void __launch_bounds__(kBlock, 1)
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  if (TMA && warp == kWarpTma && lane == 0) {
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-  }
+  if (TMA && warp == kWarpTmaK && lane == 0) tma_prefetch_desc(&tm_k);
+  if (TMA && warp == kWarpTmaV && lane == 0) tma_prefetch_desc(&tm_v);
   pdl_wait();
 
   // ---- this CTA's run: each thread counts a run of sequences ----
@@ -401,84 +398,86 @@ __global__ void __launch_bounds__(kBlock, 1)
   __syncthreads();
   const int n_tiles = r1 - r0;
 
-  // TMA producer of keys, values or both: lane i has box i / kAtoms of each tile, and half
+  // TMA producer of the keys or the values: lane i has box i / kAtoms of each tile, and half
   // i % kAtoms of its rows.
-  auto produce = [&](bool k_too, bool v_too) {
+  auto produce = [&](bool values) {
     constexpr int kAtoms = F8 ? 1 : D / 64;
     constexpr int kLanes = L::kRow / 16, kRows = 32 / kLanes;
+    constexpr int kTurns = F8 ? kAhead : kSlots;
     const int box = a.box, bx = lane / kAtoms, atom = lane % kAtoms;
     const bool mine = bx * box < kTreeKeys;
     const uint32_t whole = box == 32 ? ~0u : 0xffffu;
     const uint32_t box_bytes = box * (F8 ? L::kRow : 128);
+    const CUtensorMap* map = values ? &tm_v : &tm_k;
     uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + L::offKeys);
     uint8_t* s_flag = smem + L::offFlag;
+    auto full = [&](int i) {
+      return F8 ? raw_full((values ? kAhead : 0) + i % kAhead) : values ? v_full(i % kSlots) : k_full(i % kSlots);
+    };
     Cursor look = s_first;
     int item = -1, left = n_tiles;
     // looked up two tiles ahead
     int page_of[2] = {}, slot_of[2] = {}, head_of[2] = {}, flag_of[2] = {};
     uint32_t part_of[2] = {};  // the box's keys that count
-    int n = -2, halves = 0;  // started
-    // tile n's keys (half 0) or values; false when a wait gave up
-    auto fetch = [&](int half, uint32_t keys) {
-      const int slot = F8 ? half * kAhead + n % kAhead : n % kSlots;
-      const uint32_t full = F8 ? raw_full(slot) : half ? v_full(slot) : k_full(slot);
-      const uint32_t empty = F8 ? raw_empty(slot) : half ? v_empty(slot) : k_empty(slot);
-      constexpr int kTurns = F8 ? kAhead : kSlots;
-      if (n >= kTurns && !__all_sync(0xffffffffu, mbar_wait(empty, ((n / kTurns) - 1) & 1, abort_flag, st)))
-        return false;
-      const uint32_t to = sbase + (F8 ? L::offRaw + slot * L::kRaw : (half ? L::offV : L::offK) + slot * L::kTile);
-      const bool load = mine && keys == whole;
-      const uint32_t loads = __ballot_sync(0xffffffffu, load);
-      if (lane == 0) mbar_arrive_expect_tx(full, __popc(loads) * box_bytes);
-      __syncwarp();
-      if (load)
-        tma_load_4d(to + (F8 ? 0 : atom * L::kAtom) + bx * box_bytes, half ? &tm_v : &tm_k, full, atom * 64,
-                    head_of[0], slot_of[0], page_of[0]);
-      // Boxes that are cut off or not there: row by row, zeros for the keys that do not count.
-      uint32_t rest = __ballot_sync(0xffffffffu, mine && atom == 0 && !load);
-      if (__builtin_expect(rest != 0, 0)) {
-        const long long st_page = half ? a.v_strides[0] : a.k_strides[0];
-        const long long st_slot = half ? a.v_strides[1] : a.k_strides[1];
-        const long long st_head = half ? a.v_strides[2] : a.k_strides[2];
-        const long long off = keys ? page_of[0] * st_page + slot_of[0] * st_slot + head_of[0] * st_head : 0;
-        const int c16 = lane % kLanes, r_lane = lane / kLanes;
-#pragma unroll 1
-        while (rest) {
-          const int from = __ffs(rest) - 1;
-          rest &= rest - 1;
-          const uint32_t count = __shfl_sync(0xffffffffu, keys, from);
-          const unsigned char* p = (half ? a.v : a.k) + __shfl_sync(0xffffffffu, off, from) + c16 * 16;
-#pragma unroll 1
-          for (int r = r_lane; r < box; r += kRows) {
-            const int row = from / kAtoms * box + r;
-            const uint32_t at = F8 ? row * L::kRow + c16 * 16 : (c16 >> 3) * L::kAtom + sw128_offset(row, c16 & 7);
-            cp_async16(to + at, p + (count >> r & 1 ? r * st_slot : 0), count >> r & 1);
-          }
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (lane == 0) mbar_arrive(full);
-      ++halves;
-      return true;
-    };
+    int n = -2;
 #pragma unroll 1
     for (; n < n_tiles; ++n) {
       if (n >= 0) {
-        const bool held = part_of[0] != 0;
-        const bool there = held && static_cast<unsigned>(page_of[0]) < static_cast<unsigned>(a.cache.n_pages);
-        if (held && !there) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+        const int slot = F8 ? (values ? kAhead : 0) + n % kAhead : n % kSlots;
+        const uint32_t empty = F8 ? raw_empty(slot) : values ? v_empty(slot) : k_empty(slot);
+        if (n >= kTurns && !__all_sync(0xffffffffu, mbar_wait(empty, ((n / kTurns) - 1) & 1, abort_flag, st))) break;
+        const bool there = static_cast<unsigned>(page_of[0]) < static_cast<unsigned>(a.cache.n_pages);
+        if (part_of[0] && !there) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
         const uint32_t keys = there ? part_of[0] : 0u;
-        // the tile's keys that are there, 32 to a word
-        const uint32_t lo = __shfl_sync(0xffffffffu, keys, (box == 32 ? lane : 2 * lane) * kAtoms & 31);
-        const uint32_t up = __shfl_sync(0xffffffffu, keys, (2 * lane + 1) * kAtoms & 31);
-        if (k_too && lane < 4) s_keys[(n % L::kMasks) * 4 + lane] = box == 32 ? lo : lo | up << 16;
-        if (k_too && lane == 0) s_flag[n % L::kFlags] = static_cast<uint8_t>(flag_of[0]);
+        const bool load = mine && keys == whole;
+        const uint32_t loads = __ballot_sync(0xffffffffu, load), boxes = __ballot_sync(0xffffffffu, mine);
+        const uint32_t to =
+            sbase + (F8 ? L::offRaw + slot * L::kRaw : (values ? L::offV : L::offK) + slot * L::kTile);
+        if (lane == 0) mbar_arrive_expect_tx(full(n), __popc(loads) * box_bytes);
         __syncwarp();
-        if (k_too && !fetch(0, keys)) break;
-        if (v_too && !fetch(1, keys)) break;
+        if (load)
+          tma_load_4d(to + (F8 ? 0 : atom * L::kAtom) + bx * box_bytes, map, full(n), atom * 64, head_of[0],
+                      slot_of[0], page_of[0]);
+        if (!values) {
+          // the tile's keys that are there, 32 to a word
+          uint32_t word = ~0u;
+          if (loads != boxes) {
+            const uint32_t lo = __shfl_sync(0xffffffffu, keys, (box == 32 ? lane : 2 * lane) * kAtoms & 31);
+            const uint32_t up = __shfl_sync(0xffffffffu, keys, (2 * lane + 1) * kAtoms & 31);
+            word = box == 32 ? lo : lo | up << 16;
+          }
+          if (lane < 4) s_keys[(n % L::kMasks) * 4 + lane] = word;
+          __syncwarp();
+        }
+        // (both producers, the same: either may be ahead, and its readers go by it)
+        if (lane == 0) s_flag[n % L::kFlags] = static_cast<uint8_t>(flag_of[0]);
+        if (__builtin_expect(loads != boxes, 0)) {
+          // Boxes that are cut off or not there: row by row, zeros for the keys that do not count.
+          uint32_t rest = __ballot_sync(0xffffffffu, mine && atom == 0 && !load);
+          const long long st_page = values ? a.v_strides[0] : a.k_strides[0];
+          const long long st_slot = values ? a.v_strides[1] : a.k_strides[1];
+          const long long st_head = values ? a.v_strides[2] : a.k_strides[2];
+          const long long off = keys ? page_of[0] * st_page + slot_of[0] * st_slot + head_of[0] * st_head : 0;
+          const int c16 = lane % kLanes, r_lane = lane / kLanes;
+#pragma unroll 1
+          while (rest) {
+            const int from = __ffs(rest) - 1;
+            rest &= rest - 1;
+            const uint32_t count = __shfl_sync(0xffffffffu, keys, from);
+            const unsigned char* p = (values ? a.v : a.k) + __shfl_sync(0xffffffffu, off, from) + c16 * 16;
+#pragma unroll 1
+            for (int r = r_lane; r < box; r += kRows) {
+              const int row = from / kAtoms * box + r;
+              const uint32_t at = F8 ? row * L::kRow + c16 * 16 : (c16 >> 3) * L::kAtom + sw128_offset(row, c16 & 7);
+              cp_async16(to + at, p + (count >> r & 1 ? r * st_slot : 0), count >> r & 1);
+            }
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(full(n));
       }
       page_of[0] = page_of[1], slot_of[0] = slot_of[1], head_of[0] = head_of[1];
       flag_of[0] = flag_of[1], part_of[0] = part_of[1];
@@ -499,15 +498,9 @@ __global__ void __launch_bounds__(kBlock, 1)
         if (--left > 0) advance(look, a);
       }
     }
-    // Every copy started here must land before the CTA may exit.
-    constexpr int kTurns = F8 ? kAhead : kSlots;
-    const int both = k_too && v_too ? 2 : 1;
-    for (int h = max(0, halves - both * kTurns); h < halves; ++h) {
-      const int i = h / both;
-      const bool value = both == 2 ? h & 1 : v_too;
-      const int slot = F8 ? (value ? kAhead : 0) + i % kAhead : i % kSlots;
-      mbar_wait_drain(F8 ? raw_full(slot) : value ? v_full(slot) : k_full(slot), (i / kTurns) & 1, st);
-    }
+    // Every copy started here must land before the CTA may exit. (n: tiles started, also where a
+    // wait gave up.)
+    for (int i = max(0, n - kTurns); i < n; ++i) mbar_wait_drain(full(i), (i / kTurns) & 1, st);
   };
 
   if (warp >= kWarpIssue) {
@@ -560,7 +553,7 @@ __global__ void __launch_bounds__(kBlock, 1)
       mbar_wait_drain(mma_done(role), 0, st);
     }
     if constexpr (TMA)
-      if (warp == kWarpTma || (!F8 && warp == kWarpTmaV)) produce(warp == kWarpTma, F8 || warp == kWarpTmaV);
+      if (warp >= kWarpTmaK) produce(warp == kWarpTmaV);
   } else if (warp >= kWarpLoad) {
     regs_decrease<kRegsLoad>();
     // An item's query rows, by all of these warps: row x is token x / G, head x % G of the
