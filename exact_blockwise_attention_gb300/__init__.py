@@ -1013,15 +1013,12 @@ def decode_workspace_size(cache, B, H, max_pages, window=None, sinks=0) -> int:
 
 
 def _window(window, sinks):
-    """Checks the window and sinks of a cache call: ints, (None, 0) for no window."""
-    if window is None:
-        if sinks:
-            raise ValueError("sinks are used with a window only")
-        return None, 0
+    """Checks the window and sinks of a cache call: ints; (None, 0) without a window,
+    where the sinks are seen as all other keys are."""
     for name, x, least in (("window", window, 1), ("sinks", sinks, 0)):
-        if not isinstance(x, int) or not least <= x < 1 << 31:
+        if (name == "sinks" or x is not None) and (not isinstance(x, int) or not least <= x < 1 << 31):
             raise ValueError(f"{name} must be an int of at least {least}, got {x!r}")
-    return window, sinks
+    return window, 0 if window is None else sinks
 
 
 def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None, workspace=None,
@@ -1037,7 +1034,8 @@ def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None
     them, so a captured call follows their contents.
 
     With a ``window`` the token sees the last that many of its sequence's keys and
-    the first ``sinks``; pages that hold none of these need not be there."""
+    the first ``sinks``; pages that hold none of these need not be there. Without one
+    ``sinks`` is of no effect: all keys are seen."""
     try:
         key = (_form(q), _form(page_table), _form(seq_lens), _form(positions), cache._key, window, sinks,
                type(window), type(sinks),
@@ -1123,7 +1121,7 @@ def decode_tree(cache, q, page_table, seq_lens, cu_q=None, mask=None, window=Non
     With a ``window`` a token at place p sees of the keys before the drafts (without a
     mask: of all) those after p - window and the first ``sinks``; its place is that
     of the drafts' first key plus its place in the chain, or plus the number of its
-    mask's bits less one. Pages between the sinks and the window of a token at the
+    mask's bits less one (without one ``sinks`` is of no effect). Pages between the sinks and the window of a token at the
     drafts' first key need not be there. q is taken as it is: rotate it with rope_fwd, the new keys
     in cache_append.
 

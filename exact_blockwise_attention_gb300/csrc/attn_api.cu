@@ -1345,7 +1345,7 @@ int attn_decode_tree(const attn_cache_t* cache, const void* q, const long long* 
   a.H = H;
   a.group = group;
   a.window = window;
-  a.sinks = sinks;
+  a.sinks = window > 0 ? sinks : 0;  // without a window they are seen as all keys are
   a.scale_log2 = scale * kLog2e;
   a.o_scale = cache->v_scale;
   a.o = static_cast<__nv_bfloat16*>(o);

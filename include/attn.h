@@ -474,7 +474,7 @@ int attn_decode_window(const attn_cache_t* cache, const void* q, const long long
  *     p = c - 1 + the number of its bits (of none: c), and of the keys before c it sees
  *     all, or with a window those after p - window and the first `sinks`. mask_words <=
  *     ATTN_MAX_MASK_WORDS.
- *   window 0: none. With one, pages that lie wholly between the sinks and the window of
+ *   window 0: none, and sinks is of no effect. With one, pages that lie wholly between the sinks and the window of
  *   a sequence's first token (at the place c) are not looked up.
  *   o [T, H, d] bf16, lse [T, H] fp32. A token that sees no key gives O = 0, lse = -inf,
  *   and so do the tokens of a sequence of length 0 (an empty slot). Rows outside

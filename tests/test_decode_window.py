@@ -19,10 +19,10 @@ def test_binding_refuses(eba):
     kv = torch.zeros(2, 5, 16, 2, 64, dtype=torch.bfloat16)
     cache = eba.PagedCache(kv[0], kv[1])
     # (sizes are checked before devices: nothing of this needs a GPU)
-    for window, sinks in ((0, 0), (-3, 0), (1.5, 0), ("8", 0), (8, -1), (8, 1.0), (1 << 31, 0), (8, 1 << 31), (None, 2)):
+    for window, sinks in ((0, 0), (-3, 0), (1.5, 0), ("8", 0), (8, -1), (8, 1.0), (1 << 31, 0), (8, 1 << 31), (None, -1), (None, 2.0)):
         with pytest.raises(ValueError, match="window|sinks"):
             eba._window(window, sinks)
-    assert eba._window(None, 0) == (None, 0) and eba._window(8, 4) == (8, 4)
+    assert eba._window(None, 0) == eba._window(None, 7) == (None, 0) and eba._window(8, 4) == (8, 4)
     with pytest.raises(ValueError):
         eba.decode(cache, torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 2, dtype=torch.int32),
                    torch.zeros(1, dtype=torch.int32), window=0)

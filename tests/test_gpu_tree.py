@@ -234,7 +234,7 @@ def test_one_token_each_is_decode(eba):
     p = Paged([900, 333, 0, 64], 16, 2, 128, seed=6)
     cache = p.on_gpu(eba)
     q = bf16(torch.Generator().manual_seed(5), 4, 8, 128).cuda()
-    for window, sinks in ((None, 0), (100, 4)):
+    for window, sinks in ((None, 0), (None, 6), (100, 4)):
         a = eba.decode(cache, q, p.gtable, p.glens, window=window, sinks=sinks)
         b = eba.decode_tree(cache, q, p.gtable, p.glens, window=window, sinks=sinks)
         assert (a[0].float() - b[0].float()).abs().max() <= 2.0 ** -7

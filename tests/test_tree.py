@@ -49,7 +49,7 @@ def test_binding_refuses(eba):
     for bad in (dict(cache=kv), dict(q=q[:, :3]), dict(q=q[:0]), dict(q=torch.zeros(5, 4, 128)), dict(cu=i32(0, 5)),
                 dict(cu=None), dict(cu=cu.long()), dict(mask=mask.int()), dict(mask=mask[:4]), dict(mask=mask[:, :0]),
                 dict(mask=torch.zeros(5, 17, dtype=torch.int64)), dict(mask=mask.t().contiguous().t()), dict(mask=[1] * 5),
-                dict(window=0), dict(window=-2), dict(sinks=3), dict(window=4, sinks=-1), dict(lens=lens[:1]),
+                dict(window=0), dict(window=-2), dict(sinks=-3), dict(window=4, sinks=-1), dict(lens=lens[:1]),
                 dict(table=table[:1])):
         with pytest.raises(ValueError):
             layout(**bad)
