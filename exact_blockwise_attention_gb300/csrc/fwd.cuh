@@ -74,6 +74,11 @@ struct FwdCfg {
   static constexpr int kAtomCols = 128 / kEsz;   // elements per atom row
   static constexpr int kQBufs = (D == 64 || FP8) ? 2 : 1;  // Q tile pairs in flight across items
   static constexpr int kSlots = FP8 ? 6 : (D == 64) ? 8 : 3;
+  // Barriers that say a slot's load has landed. Each reader waits for the K loads or for
+  // the V loads only, so a slot of an odd ring, which holds the two in turn, has a barrier
+  // for each: with one, the phase after the next has the parity of the last one, and a
+  // reader that ran ahead of the load between them took it for its own.
+  static constexpr int kFulls = kSlots % 2 ? 2 * kSlots : kSlots;
   static constexpr int kP = kPTmem ? 0 : kBM * kBN * kEsz;
   static constexpr int kPAtoms = kBN * kEsz / 128;  // atoms of a P tile row
   static constexpr int offQ = 0;
@@ -89,10 +94,10 @@ struct FwdCfg {
   // fills for the other roles.
   static constexpr int kItemRing = 4;
   static constexpr int kItemBytes = 64;
-  // q_full[2], q_empty[2], kv_full[kSlots], kv_empty[kSlots], s_full[2],
+  // q_full[2], q_empty[2], kv_full[kFulls], kv_empty[kSlots], s_full[2],
   // p_full[2], o_done[2], mma_done[3], s_free[2], exp_turn[2], item_full[R],
   // item_empty[R]
-  static constexpr int nBar = 4 + 2 * kSlots + 13 + 2 * kItemRing;
+  static constexpr int nBar = 4 + kFulls + kSlots + 13 + 2 * kItemRing;
   static constexpr int offMisc = offBar + nBar * 8;
   static constexpr int offItems = (offMisc + 16 + 15) & ~15;
   static constexpr int kBytes = offItems + kItemRing * kItemBytes;
@@ -283,23 +288,25 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
   const uint32_t bar0 = sbase + L::offBar;
   auto q_full = [&](int b) { return bar0 + 8u * b; };
   auto q_empty = [&](int b) { return bar0 + 8u * (2 + b); };
-  auto kv_full = [&](int s) { return bar0 + 8u * (4 + s); };
-  auto kv_empty = [&](int s) { return bar0 + 8u * (4 + L::kSlots + s); };
-  auto s_full = [&](int t) { return bar0 + 8u * (4 + 2 * L::kSlots + t); };
-  auto p_full = [&](int t) { return bar0 + 8u * (6 + 2 * L::kSlots + t); };
-  auto o_done = [&](int t) { return bar0 + 8u * (8 + 2 * L::kSlots + t); };
-  auto mma_done = [&](int i) { return bar0 + 8u * (10 + 2 * L::kSlots + i); };
+  // kv_full(i): ring position i has landed; its phases run by kv_phase(i).
+  auto kv_full = [&](int i) { return bar0 + 8u * (4 + i % L::kFulls); };
+  auto kv_phase = [&](int i) { return static_cast<uint32_t>(i / L::kFulls) & 1; };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (4 + L::kFulls + s); };
+  auto s_full = [&](int t) { return bar0 + 8u * (4 + L::kFulls + L::kSlots + t); };
+  auto p_full = [&](int t) { return bar0 + 8u * (6 + L::kFulls + L::kSlots + t); };
+  auto o_done = [&](int t) { return bar0 + 8u * (8 + L::kFulls + L::kSlots + t); };
+  auto mma_done = [&](int i) { return bar0 + 8u * (10 + L::kFulls + L::kSlots + i); };
   // s_free(t): the softmax of tile t has loaded S_t into registers, so the next
   // S_t may be computed while it works on this one.
-  auto s_free = [&](int t) { return bar0 + 8u * (13 + 2 * L::kSlots + t); };
+  auto s_free = [&](int t) { return bar0 + 8u * (13 + L::kFulls + L::kSlots + t); };
   // exp_turn(t): the other softmax warpgroup has finished its exponentials of
   // the round, so warpgroup t may start its own (the two take turns).
-  auto exp_turn = [&](int t) { return bar0 + 8u * (15 + 2 * L::kSlots + t); };
+  auto exp_turn = [&](int t) { return bar0 + 8u * (15 + L::kFulls + L::kSlots + t); };
   // item_full(i): descriptor slot i is written; item_empty(i): every reader
   // has its copy (packed sequences only). Readers: the three MMA issuer
   // threads and the 256 softmax threads.
-  auto item_full = [&](int i) { return bar0 + 8u * (17 + 2 * L::kSlots + i); };
-  auto item_empty = [&](int i) { return bar0 + 8u * (17 + 2 * L::kSlots + L::kItemRing + i); };
+  auto item_full = [&](int i) { return bar0 + 8u * (17 + L::kFulls + L::kSlots + i); };
+  auto item_empty = [&](int i) { return bar0 + 8u * (17 + L::kFulls + L::kSlots + L::kItemRing + i); };
   constexpr int kItemReaders = 3 + 256;
   const uint32_t sItems = sbase + L::offItems;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
@@ -311,8 +318,8 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
       mbar_init(q_full(b), 1);
       mbar_init(q_empty(b), 1);
     }
+    for (int i = 0; i < L::kFulls; ++i) mbar_init(kv_full(i), 1);
     for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(kv_full(s), 1);
       // With per-tile PV issuers a V slot is released by both tile issuers
       // (one of them only hands it on when its tile is absent) and a K slot
       // by two commits of the QK issuer, so every slot takes two arrivals
@@ -418,14 +425,14 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(kv_full(slot), L::kTile);
+            mbar_arrive_expect_tx(kv_full(idx), L::kTile);
             const CUtensorMap* m = w ? &tm_v : &tm_k;
             if (FP8 && w) {
               // V^T: the d rows of 128 consecutive keys (one atom)
-              tma_load_3d(sKV + slot * L::kTile, &tm_v, kv_full(slot), key_row<VT>(it, j), 0, it.kvh);
+              tma_load_3d(sKV + slot * L::kTile, &tm_v, kv_full(idx), key_row<VT>(it, j), 0, it.kvh);
             } else {
               for (int a = 0; a < L::kAtoms; ++a)
-                load_rows(sKV + slot * L::kTile + a * L::kAtom, m, kv_full(slot),
+                load_rows(sKV + slot * L::kTile + a * L::kAtom, m, kv_full(idx),
                           a * L::kAtomCols, key_row<VT>(it, j), it.kvh);
             }
             ++idx;
@@ -436,7 +443,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
       for (int i = max(0, nq - L::kQBufs); i < nq; ++i)
         mbar_wait_drain(q_full(i % L::kQBufs), (i / L::kQBufs) & 1, st);
       for (int i = max(0, idx - L::kSlots); i < idx; ++i)
-        mbar_wait_drain(kv_full(i % L::kSlots), (i / L::kSlots) & 1, st);
+        mbar_wait_drain(kv_full(i), kv_phase(i), st);
     }
    } else {
     // ---------------- MMA issuers ----------------
@@ -521,7 +528,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
           // Round j issues S_t = Q_t K_j^T for both tiles.
           for (int j = 0; j < it.n_kv && ok; ++j) {
             const int ik = kvbase + 2 * j;
-            if (!(ok = mbar_wait(kv_full(ik % L::kSlots), (ik / L::kSlots) & 1, abort_flag, st)))
+            if (!(ok = mbar_wait(kv_full(ik), kv_phase(ik), abort_flag, st)))
               break;
             tc_fence_after();
             for (int t = 0; t < it.n_tiles && ok; ++t) {
@@ -551,7 +558,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
               if (!(ok = mbar_wait(p_full(t), uses[t] & 1, abort_flag, st))) break;
               ++uses[t];
             }
-            if (!(ok = mbar_wait(kv_full(iv % L::kSlots), (iv / L::kSlots) & 1, abort_flag, st)))
+            if (!(ok = mbar_wait(kv_full(iv), kv_phase(iv), abort_flag, st)))
               break;
             if (t < it.n_tiles) {
               tc_fence_after();
