@@ -18,7 +18,7 @@ Entry points (same names as the C ABI):
   fwd_varlen(q, k, v, cu_q, cu_k, scale=None)   -> (o, lse)      packed sequences
   fwd_fp8(q8, k8, vt8, q_scale, k_scale, v_scale, scale=None) -> (o, lse)   e4m3, d = 128
   bwd_varlen(q, k, v, o, do, lse, cu_q, cu_k, scale=None) -> (dq, dk, dv)
-  fwd_window(q, k, v, left, right=0, sinks=0, scale=None) -> (o, lse)   a sliding window and first tokens
+  fwd_window(q, k, v, left, right=0, sinks=0, scale=None, rest=False) -> (o, lse)   a sliding window and first tokens
   bwd_window(q, k, v, o, do, lse, left, right=0, sinks=0, scale=None) -> (dq, dk, dv)
   attention_window(q, k, v, left, right=0, sinks=0, scale=None) -> o   (autograd-aware)
   rope_fwd(q, k, positions, plan), rope_bwd(dq, dk, positions, plan) -> (q, k)   rotary positions
@@ -127,11 +127,11 @@ def _declare(L):
     L.attn_fwd_fp8.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, f, f, f, vp]
     L.attn_bwd_gqa.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, vp, sz,
                                vp]
-    L.attn_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f, vp]
+    L.attn_fwd_window.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f, vp]
     L.attn_fwd_window.restype = ctypes.c_int
     L.attn_bwd_window_workspace_size.argtypes = [i, i, i, i, i, i, i, i, i]
     L.attn_bwd_window_workspace_size.restype = sz
-    L.attn_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f, vp,
+    L.attn_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f, vp,
                                   sz, vp]
     L.attn_bwd_window.restype = ctypes.c_int
     ip = ctypes.POINTER(i)
@@ -505,8 +505,9 @@ _WINDOW_LAYOUTS = None  # _Layouts, below
 
 
 def _window_layout(q, k, v, left, right, sinks):
-    """A windowed call's sizes and window as the C ABI takes them, and the bytes of the
-    backward's workspace; its checks are made once for each form of tensors."""
+    """A windowed call's sizes and window as the C ABI takes them, the bytes of the
+    backward's workspace, and whether a training step keeps what rounding took from o;
+    its checks are made once for each form of tensors."""
     try:
         key = (_form(q), _form(k), _form(v), left, right, sinks, type(left), type(right), type(sinks))
         lay = _WINDOW_LAYOUTS.get(key)
@@ -515,20 +516,26 @@ def _window_layout(q, k, v, left, right, sinks):
     if lay is None:
         sizes = _qkv(q, k, v, gqa=True)
         window = _sides(left, right, sinks)
-        lay = (*sizes, *window), int(lib().attn_bwd_window_workspace_size(*sizes, *window))
+        # Kept where no row sees more than 512 keys: the error of dq and dk goes from 0.0038
+        # to 0.0025 with 2 keys a row, 0.0027 to 0.0024 with 8, 0.00243 to 0.00238 with 61,
+        # and a step of 12544 tokens that see 1568 each would take 838 us instead of 808.
+        left, right = (x if x >= 0 else sizes[4] for x in window[:2])
+        lay = ((*sizes, *window), int(lib().attn_bwd_window_workspace_size(*sizes, *window)),
+               min(sizes[4], left + right + 1) <= 512)
         _WINDOW_LAYOUTS.add(key, lay)
     return lay
 
 
-def _fwd_window(q, k, v, sizes, scale):
+def _fwd_window(q, k, v, sizes, scale, rest):
     o = torch.empty_like(q)
+    rest = torch.empty_like(q) if rest else None
     lse = torch.empty(sizes[0:2] + sizes[3:4], device=q.device, dtype=torch.float32)
     _launch(q.device, lib().attn_fwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-            lse.data_ptr(), *sizes, _scale(scale, sizes[5]))
-    return o, lse
+            None if rest is None else rest.data_ptr(), lse.data_ptr(), *sizes, _scale(scale, sizes[5]))
+    return o, lse, rest
 
 
-def _bwd_window(q, k, v, o, do, lse, sizes, need, scale, workspace):
+def _bwd_window(q, k, v, o, do, lse, sizes, need, scale, workspace, rest):
     if workspace is None:
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
     elif workspace.numel() * workspace.element_size() < need or workspace.device != q.device or \
@@ -536,58 +543,66 @@ def _bwd_window(q, k, v, o, do, lse, sizes, need, scale, workspace):
         raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {q.device}")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     _launch(q.device, lib().attn_bwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-            do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes,
-            _scale(scale, sizes[5]), workspace.data_ptr(), need)
+            None if rest is None else rest.data_ptr(), do.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), *sizes, _scale(scale, sizes[5]), workspace.data_ptr(), need)
     return dq, dk, dv
 
 
-def fwd_window(q, k, v, left, right=0, sinks=0, scale=None):
+def fwd_window(q, k, v, left, right=0, sinks=0, scale=None, rest=False):
     """Attention within a sliding window and to the first tokens: (o bf16 [B,H,Lq,d],
     lse fp32 [B,H,Lq]).
 
     Query i stands at the place p = i + Lk - Lq, the last query at the last key, and
     sees the keys p - left to p + right and, up to p + right, the first ``sinks``. left
     or right None: no end to that side (left=None is plain causal attention). A query
-    that sees no key gives o = 0 and lse = -inf. k, v may have H_kv < H heads."""
-    return _fwd_window(q, k, v, _window_layout(q, k, v, left, right, sinks)[0], scale)
+    that sees no key gives o = 0 and lse = -inf. k, v may have H_kv < H heads.
+
+    With ``rest`` a third tensor, of o's shape and type: what rounding took from o, for
+    bwd_window."""
+    out = _fwd_window(q, k, v, _window_layout(q, k, v, left, right, sinks)[0], scale, rest)
+    return out if rest else out[:2]
 
 
 def bwd_window_workspace_size(B, H, H_kv, Lq, Lk, d, left, right=0, sinks=0) -> int:
     return int(lib().attn_bwd_window_workspace_size(B, H, H_kv, Lq, Lk, d, *_sides(left, right, sinks)))
 
 
-def bwd_window(q, k, v, o, do, lse, left, right=0, sinks=0, scale=None, workspace=None):
+def bwd_window(q, k, v, o, do, lse, left, right=0, sinks=0, scale=None, workspace=None, rest=None):
     """Gradients (dq, dk, dv) of sum(o * do) for fwd_window; P is recomputed from lse.
-    Keys that no query sees, and queries that see no key, have zero gradients."""
-    sizes, need = _window_layout(q, k, v, left, right, sinks)
+    Keys that no query sees, and queries that see no key, have zero gradients. With
+    fwd_window's ``rest`` dq and dk are more exact where rows see few keys."""
+    sizes, need, _ = _window_layout(q, k, v, left, right, sinks)
     _bwd_inputs(q, k, v, o, do, lse, gqa=True)
-    return _bwd_window(q, k, v, o, do, lse, sizes, need, scale, workspace)
+    if rest is not None:
+        _bwd_inputs(q, k, v, rest, do, lse, gqa=True)
+    return _bwd_window(q, k, v, o, do, lse, sizes, need, scale, workspace, rest)
 
 
 class _AttentionWindow(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, left, right, sinks, scale):
-        sizes, need = _window_layout(q, k, v, left, right, sinks)
-        o, lse = _fwd_window(q, k, v, sizes, scale)
-        ctx.save_for_backward(q, k, v, o, lse)
+        sizes, need, few = _window_layout(q, k, v, left, right, sinks)
+        o, lse, rest = _fwd_window(q, k, v, sizes, scale, few and any(ctx.needs_input_grad[:2]))
+        ctx.save_for_backward(q, k, v, o, lse, rest)
         ctx.call = sizes, need, scale
         return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, do):
-        q, k, v, o, lse = ctx.saved_tensors
+        q, k, v, o, lse, rest = ctx.saved_tensors
         do = do.contiguous()
         if do.data_ptr() & 15:  # autograd also hands over views
             do = do.clone()
-        grads = _bwd_window(q, k, v, o, do, lse, *ctx.call, None)
+        grads = _bwd_window(q, k, v, o, do, lse, *ctx.call, None, rest)
         need = ctx.needs_input_grad
         return (grads[0] if need[0] else None, grads[1] if need[1] else None, grads[2] if need[2] else None,
                 None, None, None, None)
 
 
 def attention_window(q, k, v, left, right=0, sinks=0, scale=None):
-    """Autograd-aware fwd_window; only o and lse are saved for backward."""
+    """Autograd-aware fwd_window; only o and lse are saved for backward, and with narrow
+    windows (of up to 512 keys) what rounding took from o."""
     return _AttentionWindow.apply(q, k, v, left, right, sinks, scale)
 
 

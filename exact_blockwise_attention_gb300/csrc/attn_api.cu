@@ -897,9 +897,9 @@ int attn_bwd_gqa(const void* q, const void* k, const void* v, const void* o, con
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
-int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
-                    int H_kv, int Lq, int Lk, int d, int left, int right, int sinks, float scale,
-                    void* stream) {
+int attn_fwd_window(const void* q, const void* k, const void* v, void* o, void* o_rest, float* lse,
+                    int B, int H, int H_kv, int Lq, int Lk, int d, int left, int right, int sinks,
+                    float scale, void* stream) {
   int s = check_sizes(B, H, Lq, Lk, d, scale);
   if (s != ATTN_OK) return s;
   if (H_kv < 1 || H % H_kv != 0) return ATTN_ERR_INVALID_ARG;
@@ -907,6 +907,7 @@ int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float*
   eba::WindowTiles w;
   if (!window_tiles(Lq, Lk, left, right, sinks, BHkv, &w)) return ATTN_ERR_INVALID_ARG;
   if ((s = check_ptrs({q, k, v, o, lse})) != ATTN_OK) return s;
+  if (!aligned16(o_rest)) return ATTN_ERR_MISALIGNED;
   eba::FwdArgs a{};
   a.B = B;
   a.H = H;
@@ -919,6 +920,7 @@ int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float*
   a.scale_log2 = scale * kLog2e;
   a.bounds[1] = Lk;
   a.o = o;
+  a.rest = o_rest;
   a.lse = lse;
   if (static_cast<long long>(a.n_pairs) * BH >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
   a.status = status_word_ptr();
@@ -940,8 +942,8 @@ size_t attn_bwd_window_workspace_size(int B, int H, int H_kv, int Lq, int Lk, in
   return attn_bwd_workspace_size(B, H, Lq, Lk, d) + window_part_bytes(w, heads, d);
 }
 
-int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO,
-                    const float* lse, void* dq, void* dk, void* dv, int B, int H, int H_kv, int Lq,
+int attn_bwd_window(const void* q, const void* k, const void* v, const void* o,
+                    const void* o_rest, const void* dO, const float* lse, void* dq, void* dk, void* dv, int B, int H, int H_kv, int Lq,
                     int Lk, int d, int left, int right, int sinks, float scale, void* workspace,
                     size_t workspace_bytes, void* stream) {
   int s = check_sizes(B, H, Lq, Lk, d, scale);
@@ -951,6 +953,7 @@ int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, 
   eba::WindowTiles w;
   if (!window_tiles(Lq, Lk, left, right, sinks, BHkv, &w)) return ATTN_ERR_INVALID_ARG;
   if ((s = check_ptrs({q, k, v, o, dO, lse, dq, dk, dv})) != ATTN_OK) return s;
+  if (!aligned16(o_rest)) return ATTN_ERR_MISALIGNED;
   const size_t plain = attn_bwd_workspace_size(B, H, Lq, Lk, d);
   if (!workspace || workspace_bytes < plain + window_part_bytes(w, BHkv, d)) return ATTN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
@@ -968,6 +971,7 @@ int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, 
   a.scale = scale;
   a.scale_log2 = scale * kLog2e;
   a.o = o;
+  a.rest = o_rest;
   a.dO = dO;
   a.lse = lse;
   a.dq_acc = ws;

@@ -227,6 +227,22 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, const WindowTiles&
   return it;
 }
 
+// What rounding took from 32 elements of a row of O.
+__device__ __forceinline__ void store_rest(__nv_bfloat16* to, const uint32_t* x, float mul) {
+  uint4* dst = reinterpret_cast<uint4*>(to);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float a = __uint_as_float(x[8 * v + 2 * u]) * mul, b = __uint_as_float(x[8 * v + 2 * u + 1]) * mul;
+      const uint32_t p = pack_bf16(a, b);
+      w[u] = pack_bf16(a - bf16lo_f32(p), b - bf16hi_f32(p));
+    }
+    dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // First key row of round j.
 template <typename VT>
 __device__ __forceinline__ int key_row(const FwdItem& it, int j) {
@@ -662,6 +678,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
                 pack_bf16(__uint_as_float(w[4]) * inv_l, __uint_as_float(w[5]) * inv_l),
                 pack_bf16(__uint_as_float(w[6]) * inv_l, __uint_as_float(w[7]) * inv_l));
           }
+          if (WINDOW && args.rest) store_rest(static_cast<__nv_bfloat16*>(args.rest) + po_off + 32 * c, oc, inv_l);
         }
       }
       float* lse_p = args.lse + static_cast<size_t>(pchunk) * args.lse_chunk_stride;
@@ -725,6 +742,10 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
           } else if (VARLEN || WINDOW) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.o) + o_off);
             for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
+            if (WINDOW && args.rest) {
+              dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.rest) + o_off);
+              for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
           lse_out[orow] = -INFINITY;
         }
@@ -983,6 +1004,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
                   pack_bf16(__uint_as_float(w[4]) * inv_l, __uint_as_float(w[5]) * inv_l),
                   pack_bf16(__uint_as_float(w[6]) * inv_l, __uint_as_float(w[7]) * inv_l));
             }
+            if (WINDOW && args.rest) store_rest(static_cast<__nv_bfloat16*>(args.rest) + o_off + 32 * c, ov, inv_l);
           }
         }
       }

@@ -54,6 +54,7 @@ struct FwdArgs {
   float o_scale;     // FP8: the V dequantisation scale (O multiplier); otherwise unused
   int bounds[ATTN_MAX_CHUNKS + 1];
   void* o;     // bf16 [B,H,Lq,d] (full forward) or fp32 [C,B,H,Lq,d] (partials)
+  void* rest;  // windowed: bf16 [B,H,Lq,d], what rounding took from o; or nullptr
   float* lse;  // [C,B,H,Lq]
   long long o_chunk_stride;    // elements between consecutive chunks of o
   long long lse_chunk_stride;  // elements between consecutive chunks of lse
@@ -71,6 +72,7 @@ struct BwdArgs {
   float scale;
   float scale_log2;
   const void* o;    // bf16 [B,H,Lq,d]
+  const void* rest; // windowed: bf16 [B,H,Lq,d], added to o for D; or nullptr
   const void* dO;   // bf16 [B,H,Lq,d]
   const float* lse; // [B,H,Lq]
   float* dq_acc;    // fp32 [B,H,Lq,d] workspace

@@ -239,17 +239,20 @@ int attn_merge(const float* o_parts, const float* lse_parts, int n_chunks, void*
  * are neither read nor computed; within the others a masked weight is exactly 0, which
  * keeps out every finite value (a NaN or infinite element of q, k, v or dO may reach
  * the rows of the tiles that it is in).
+ *   o_rest: bf16, of O's shape, or NULL: what rounding took from O, for the backward. Where
+ *   rows see few keys their gradients are more exact with it (dQ, dK of windows of 2 keys:
+ *   2^-8.7 instead of 2^-8 off, as a whole); with many keys it makes no difference.
  *   workspace: attn_bwd_window_workspace_size(...) bytes. dQ is accumulated with atomic
  *   adds as in attn_bwd (its low bits may vary from run to run; dK, dV do not).
  */
-int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
-                    int H_kv, int Lq, int Lk, int d, int left, int right, int sinks, float scale,
-                    void* stream);
+int attn_fwd_window(const void* q, const void* k, const void* v, void* o, void* o_rest, float* lse,
+                    int B, int H, int H_kv, int Lq, int Lk, int d, int left, int right, int sinks,
+                    float scale, void* stream);
 size_t attn_bwd_window_workspace_size(int B, int H, int H_kv, int Lq, int Lk, int d, int left,
                                       int right, int sinks);
-int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO,
-                    const float* lse, void* dq, void* dk, void* dv, int B, int H, int H_kv, int Lq,
-                    int Lk, int d, int left, int right, int sinks, float scale, void* workspace,
+int attn_bwd_window(const void* q, const void* k, const void* v, const void* o,
+                    const void* o_rest, const void* dO, const float* lse, void* dq, void* dk,
+                    void* dv, int B, int H, int H_kv, int Lq, int Lk, int d, int left, int right, int sinks, float scale, void* workspace,
                     size_t workspace_bytes, void* stream);
 
 /*

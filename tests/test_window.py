@@ -84,18 +84,18 @@ def test_abi_refuses(eba):
     one = ctypes.c_void_p(4096)
     off = ctypes.c_void_p(4100)
 
-    def fwd(B=1, H=4, Hkv=2, Lq=9, Lk=9, d=64, left=3, right=0, sinks=0, scale=0.1, q=one):
-        return L.attn_fwd_window(q, one, one, one, one, B, H, Hkv, Lq, Lk, d, left, right, sinks, scale, None)
+    def fwd(B=1, H=4, Hkv=2, Lq=9, Lk=9, d=64, left=3, right=0, sinks=0, scale=0.1, q=one, rest=None):
+        return L.attn_fwd_window(q, one, one, one, rest, one, B, H, Hkv, Lq, Lk, d, left, right, sinks, scale, None)
 
-    def bwd(B=1, H=4, Hkv=2, Lq=9, Lk=9, d=64, left=3, right=0, sinks=0, scale=0.1, q=one, ws=one, n=1 << 40):
-        return L.attn_bwd_window(q, one, one, one, one, one, one, one, one, B, H, Hkv, Lq, Lk, d, left, right, sinks, scale, ws, n, None)
+    def bwd(B=1, H=4, Hkv=2, Lq=9, Lk=9, d=64, left=3, right=0, sinks=0, scale=0.1, q=one, ws=one, n=1 << 40, rest=None):
+        return L.attn_bwd_window(q, one, one, one, rest, one, one, one, one, one, B, H, Hkv, Lq, Lk, d, left, right, sinks, scale, ws, n, None)
 
     for f in (fwd, bwd):
         for bad in (dict(B=0), dict(H=0), dict(Lq=0), dict(Lk=0), dict(Hkv=3), dict(Hkv=0), dict(left=-2), dict(right=-2),
                     dict(sinks=-1), dict(scale=0.0), dict(scale=float("inf")), dict(q=None), dict(Lq=(1 << 29) + 1),
                     dict(Lk=(1 << 29) + 1)):
             assert f(**bad) == 1, bad
-        assert f(d=96) == 2 and f(q=off) == 3
+        assert f(d=96) == 2 and f(q=off) == 3 and f(rest=off) == 3
     assert bwd(ws=None) == 6 and bwd(n=100) == 6 and bwd(ws=off) == 3
 
 
