@@ -642,7 +642,7 @@ int fwd_common(const void* q, const void* k, const void* v, void* o, float* lse,
 // The window of a call: what its sizes make of left, right (-1: no end) and sinks.
 // False: out of range.
 bool window_tiles(int Lq, int Lk, int left, int right, int sinks, long long heads,
-                  eba::WindowTiles* w) {
+                  int d, eba::WindowTiles* w) {
   constexpr int kMost = 1 << 29;  // places and their sums stay within an int
   if (Lq > kMost || Lk > kMost || left < -1 || right < -1 || sinks < 0) return false;
   const int all = Lq + Lk;  // beyond every distance
@@ -653,6 +653,9 @@ bool window_tiles(int Lq, int Lk, int left, int right, int sinks, long long head
   w->off = Lk - Lq;
   const bool left_end = w->left < all, right_end = w->right < all;
   w->by_cost = left_end == right_end ? 0 : right_end ? 1 : -1;
+  // (the order by cost walks the heads side by side: only while L2 holds them)
+  if (left_end && right_end && heads * Lk * d * 4 <= 64ll << 20)
+    w->by_cost = w->right <= w->left / 2 ? 1 : w->left <= w->right / 2 ? -1 : 2;
   constexpr int R = eba::kTileRows;
   const int n_qtiles = (Lq + R - 1) / R;
   w->run_tiles = left_end && right_end ? std::min(n_qtiles, (w->left + w->right + R - 1) / R + 2) : n_qtiles;
@@ -905,7 +908,7 @@ int attn_fwd_window(const void* q, const void* k, const void* v, void* o, void* 
   if (H_kv < 1 || H % H_kv != 0) return ATTN_ERR_INVALID_ARG;
   const long long BH = static_cast<long long>(B) * H, BHkv = static_cast<long long>(B) * H_kv;
   eba::WindowTiles w;
-  if (!window_tiles(Lq, Lk, left, right, sinks, BHkv, &w)) return ATTN_ERR_INVALID_ARG;
+  if (!window_tiles(Lq, Lk, left, right, sinks, BHkv, d, &w)) return ATTN_ERR_INVALID_ARG;
   if ((s = check_ptrs({q, k, v, o, lse})) != ATTN_OK) return s;
   if (!aligned16(o_rest)) return ATTN_ERR_MISALIGNED;
   eba::FwdArgs a{};
@@ -938,7 +941,7 @@ size_t attn_bwd_window_workspace_size(int B, int H, int H_kv, int Lq, int Lk, in
   if (check_sizes(B, H, Lq, Lk, d, 1.0f) != ATTN_OK || H_kv < 1 || H % H_kv != 0) return 0;
   const long long heads = static_cast<long long>(B) * H_kv;
   eba::WindowTiles w;
-  if (!window_tiles(Lq, Lk, left, right, sinks, heads, &w)) return 0;
+  if (!window_tiles(Lq, Lk, left, right, sinks, heads, d, &w)) return 0;
   return attn_bwd_workspace_size(B, H, Lq, Lk, d) + window_part_bytes(w, heads, d);
 }
 
@@ -951,7 +954,7 @@ int attn_bwd_window(const void* q, const void* k, const void* v, const void* o,
   if (H_kv < 1 || H % H_kv != 0) return ATTN_ERR_INVALID_ARG;
   const long long BH = static_cast<long long>(B) * H, BHkv = static_cast<long long>(B) * H_kv;
   eba::WindowTiles w;
-  if (!window_tiles(Lq, Lk, left, right, sinks, BHkv, &w)) return ATTN_ERR_INVALID_ARG;
+  if (!window_tiles(Lq, Lk, left, right, sinks, BHkv, d, &w)) return ATTN_ERR_INVALID_ARG;
   if ((s = check_ptrs({q, k, v, o, dO, lse, dq, dk, dv})) != ATTN_OK) return s;
   if (!aligned16(o_rest)) return ATTN_ERR_MISALIGNED;
   const size_t plain = attn_bwd_workspace_size(B, H, Lq, Lk, d);

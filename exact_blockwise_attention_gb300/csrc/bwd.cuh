@@ -243,7 +243,7 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, const WindowTiles&
     if (wt.by_cost) {
       it.kvh = w % heads;
       t = w / heads;
-      if (wt.by_cost < 0) t = rest - 1 - t;
+      t = wt.by_cost == 2 ? from_middle(t, rest) : wt.by_cost < 0 ? rest - 1 - t : t;
     } else {
       it.kvh = w / rest;
       t = w - it.kvh * rest;

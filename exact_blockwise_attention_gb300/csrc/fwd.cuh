@@ -204,7 +204,7 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, const WindowTiles&
   if (wt.by_cost) {
     it.bh = item % BH;
     const int rank = item / BH;
-    it.pair = wt.by_cost > 0 ? a.n_pairs - 1 - rank : rank;
+    it.pair = wt.by_cost == 2 ? from_middle(rank, a.n_pairs) : wt.by_cost > 0 ? a.n_pairs - 1 - rank : rank;
   } else {
     it.pair = item % a.n_pairs;
     it.bh = item / a.n_pairs;

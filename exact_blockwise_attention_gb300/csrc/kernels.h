@@ -160,12 +160,18 @@ struct PackedTiles {
   int Lq, Lk;  // per sequence
 };
 
+// The rank-th of n, from the middle outwards.
+__host__ __device__ constexpr int from_middle(int rank, int n) {
+  return rank & 1 ? n / 2 - (rank + 1) / 2 : n / 2 + rank / 2;
+}
+
 // A sliding window and first tokens ("sinks"): query i stands at place p = i + off and
 // sees the keys p - left to p + right and, up to p + right, the first `sinks`.
 //
-// by_cost: one side has no end, so items differ: 1 (no left end, the last queries see
-// and the first keys are seen most), -1 (no right end: the other way round), 0 (equal).
-// Items then run through the heads, the largest first.
+// by_cost: items differ, those near an end of the sequence are smaller: 1 (no left end, or
+// mainly a left side: the last queries see and the first keys are seen most), -1 (the other
+// way round), 2 (the middle ones most), 0 (taken as equal). Items then run through the
+// heads, the largest first, so that the last ones on the SMs are small.
 // Backward: the first cut_tiles key tiles hold sinks, which all later queries see. Each
 // is cut in `pieces` of `piece` query tiles, which leave fp32 parts that a last kernel
 // adds up: else one such item is as long as the whole sequence and the others wait.
