@@ -11,23 +11,37 @@
 // which the warp matrix instruction of the single-token kernel cannot keep up with and
 // tcgen05 can: of a tile of 128 keys of 128 elements, 64 KB and 1.4 us of an SM's share
 // of the HBM rate, the products take 0.75 us. So the kernel is built to keep loads on
-// their way:
+// their way and every step of a tile short:
 //  - The list of all 128-key tiles of all (sequence, K/V head, 128 rows) items is cut
 //    into equal runs, one per CTA, as in decode.cuh: lengths need not be known to the
 //    host. Items cut between CTAs leave fp32 parts that the join kernel adds up in order.
-//  - Four warps load. bf16: cp.async, 16 bytes a lane, straight into the swizzled tiles,
-//    three K and three V tiles, four halves ahead. e4m3: into 16 KB stages, each lane's
-//    own, from which it widens its bytes to fp16 (exact) into two K and two V tiles.
-//    A lane looks its row's page up two tiles ahead. Keys that no row of the item sees
-//    are not read: their rows are zeros.
-//  - Two softmax warpgroups take the tiles in turn, each with its own maximum, sums and
-//    accumulator in tensor memory; a thread owns a row. At an item's end each thread
-//    joins one half of a row's columns of both. S_t and P_t share 128 columns:
-//    P is bf16 as in the forward pass (fwd.cuh), or with an e4m3 cache fp16 (and q
-//    scaled per row by a power of two into fp16's range).
-//  - The QK and the two PV products are issued by threads of three warps (see fwd.cuh
-//    for why one is not enough).
-// Tensor memory: S_0 [0,128) S_1 [128,256) O_0 [256,256+d) O_1 [256+d,256+2d); P_t at S_t.
+//  - Pages of a multiple of 16 keys are loaded by TMA, a box of 32 or 16 keys by 64
+//    elements to a lane of a warp for the keys and of one for the values, which look
+//    their pages up two tiles ahead; boxes that are cut off are loaded row by row, with
+//    zeros for the keys that no row of the item sees. Other page sizes: eight warps with
+//    cp.async. (Eight warps of cp.async for all: the e4m3 chains below 250 us, by TMA 190.)
+//    bf16: three K and three V tiles. e4m3: two of each, and two stages of stored bytes,
+//    which the eight warps widen to fp16 (exact).
+//  - Both softmax warpgroups share each tile, 64 keys each, a thread a row: one maximum,
+//    one accumulator, no joining at an item's end. A row's reference moves when one of
+//    its halves passes it by more than 2^8: a vote each tile, an exchange in the few where
+//    it does. (The warpgroups in turn, with an accumulator each: the bf16 batch below 141 us,
+//    so 131; the rows of 64 elements 112 and 94 us.)
+//  - P in columns of its own, bf16 as in the forward pass (fwd.cuh; the row's largest
+//    weight's rounding is added to the sum), or with an e4m3 cache fp16 (and q scaled per
+//    row by a power of two into fp16's range).
+//  - The QK and the PV products are issued by threads of two warps (see fwd.cuh), and
+//    loops are rolled: while the roles' code was larger than the instruction cache, its
+//    misses took more time than anything else (this, P as one bf16 term instead of two,
+//    and eight loading warps instead of four: 293 -> 148 us).
+// Measured (one GB300; bytes of the caches at the time of the call): 32 sequences of up to
+// 8191 keys, 32 drafts, 8 heads of 128 for 32: 133 us, 5.2 TB/s, 77 % of a copy; 8 of up
+// to 131071 e4m3 keys, 12 drafts, 4 heads of 128 for 32: 180 us, 3.4 TB/s; 16 of up to 6007
+// keys, 24 drafts, 16 heads of 64: 89 us, 3.2 TB/s. A tile takes 2000 cycles of the softmax
+// (scores and maximum 720, exponentials 885, vote and waits the rest) however short its
+// rows: that bounds rows of 64 elements or bytes; rows of 256 bytes: HBM, unequal SMs at
+// the end, the join.
+// Tensor memory: S_0 [0,128) S_1 [128,256) O [256,256+d) P_0 [384,448) P_1 [448,512).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -994,10 +1008,11 @@ __global__ void __launch_bounds__(kBlock, 1)
   }
 }
 
-// Items cut between CTAs: their parts, in the order of the keys. blockIdx.x: the run that
-// the item begins in, y: 8 of its rows. Few parts: a warp a row; many: all warps a row,
-// one after the other.
-constexpr int kJoinWarps = 8, kDeep = 4, kFewParts = 8;
+// Items cut between CTAs: their parts, in the order of the keys. blockIdx.x: a run, y: 8 rows.
+// Few parts: the blocks of the run that the item begins in, a warp a row. More than 8: those
+// of its first 8 runs, a row each, all warps: with the first run's blocks alone, row after
+// row, 1501 keys of 8 heads (12 parts each) took 25.0 us in all, so 18.6.
+constexpr int kJoinWarps = 8, kDeep = 4, kFewParts = kJoinWarps;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ TreeArgs a) {
   pdl_launch_dependents();
@@ -1005,89 +1020,90 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
   constexpr int kVec = D / 32;
   __shared__ float s_o[kJoinWarps][D];
   __shared__ float2 s_ml[kJoinWarps];
-  const int c0 = blockIdx.x;
-  const int2 cut = a.cut[c0];
-  const int parts = cut.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int run = blockIdx.x;
+  int2 cut = lane < kJoinWarps && run >= lane ? a.cut[run - lane] : make_int2(0, 0);
+  // (no run is among the first 8 of two such items, or of one and begins another)
+  const uint32_t longs = __ballot_sync(0xffffffffu, cut.y > kFewParts);
+  const bool few = longs == 0;
+  const int behind = few ? 0 : __ffs(longs) - 1, c0 = run - behind;
+  cut.x = __shfl_sync(0xffffffffu, cut.x, behind);
+  const int parts = __shfl_sync(0xffffffffu, cut.y, behind);
   if (parts == 0) return;
   const int4 it = a.item[c0];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Seq s = sequence(a, it.x);
   const int rows = min(kTreeRows, s.n * a.group - it.z * kTreeRows);
-  const bool few = parts <= kFewParts;
-  for (int i = 0; i < (few ? 1 : kJoinWarps); ++i) {
-    const int row = blockIdx.y * kJoinWarps + (few ? warp : i);
-    if (row >= rows) return;  // (many: all warps alike)
-    float M = -INFINITY, l = 0.f, o[kVec] = {};
-    const int step = few ? 1 : kJoinWarps;
-    for (int p0 = few ? 0 : warp; p0 < parts; p0 += step * kDeep) {
-      float2 ml[kDeep];
-      float v[kDeep][kVec];
+  const int row = blockIdx.y * kJoinWarps + (few ? warp : behind);
+  if (row >= rows) return;  // (many: all warps alike)
+  float M = -INFINITY, l = 0.f, o[kVec] = {};
+  const int step = few ? 1 : kJoinWarps;
+  for (int p0 = few ? 0 : warp; p0 < parts; p0 += step * kDeep) {
+    float2 ml[kDeep];
+    float v[kDeep][kVec];
 #pragma unroll
-      for (int u = 0; u < kDeep; ++u) {
-        const int p = p0 + u * step;
-        if (p >= parts) {
-          ml[u] = make_float2(-INFINITY, 0.f);
-          continue;
-        }
-        const long long at = (2 * (c0 + p) + (p == 0 ? cut.x : 0)) * static_cast<long long>(kTreeRows) + row;
-        ml[u] = a.part_ml[at];
-        const float* from = a.part_o + at * D + lane * kVec;
-#pragma unroll
-        for (int x = 0; x < kVec; x += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(from + x);
-          v[u][x] = y.x, v[u][x + 1] = y.y;
-        }
+    for (int u = 0; u < kDeep; ++u) {
+      const int p = p0 + u * step;
+      if (p >= parts) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+        continue;
       }
-      float to = M;
+      const long long at = (2 * (c0 + p) + (p == 0 ? cut.x : 0)) * static_cast<long long>(kTreeRows) + row;
+      ml[u] = a.part_ml[at];
+      const float* from = a.part_o + at * D + lane * kVec;
 #pragma unroll
-      for (int u = 0; u < kDeep; ++u) to = fmaxf(to, ml[u].x);
-      if (to == -INFINITY) continue;  // no weight so far
-      const float f = M == -INFINITY ? 0.f : ex2_approx(M - to);
-      M = to;
-      l *= f;
-#pragma unroll
-      for (int x = 0; x < kVec; ++x) o[x] *= f;
-#pragma unroll
-      for (int u = 0; u < kDeep; ++u) {
-        if (ml[u].x == -INFINITY) continue;
-        const float w = ex2_approx(ml[u].x - to);
-        l += ml[u].y * w;
-#pragma unroll
-        for (int x = 0; x < kVec; ++x) o[x] += v[u][x] * w;
+      for (int x = 0; x < kVec; x += 2) {
+        const float2 y = *reinterpret_cast<const float2*>(from + x);
+        v[u][x] = y.x, v[u][x + 1] = y.y;
       }
     }
-    const int at = it.z * kTreeRows + row, token = at / a.group;
-    const long long out = (static_cast<long long>(s.c0) + token) * a.H + it.y * a.group + at % a.group;
-    if (few) {
-      const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+    float to = M;
 #pragma unroll
-      for (int x = 0; x < kVec; x += 2)
-        *reinterpret_cast<uint32_t*>(a.o + out * D + lane * kVec + x) = pack_bf16(o[x] * f, o[x + 1] * f);
-      if (lane == 0) a.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
-      continue;
+    for (int u = 0; u < kDeep; ++u) to = fmaxf(to, ml[u].x);
+    if (to == -INFINITY) continue;  // no weight so far
+    const float f = M == -INFINITY ? 0.f : ex2_approx(M - to);
+    M = to;
+    l *= f;
+#pragma unroll
+    for (int x = 0; x < kVec; ++x) o[x] *= f;
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      if (ml[u].x == -INFINITY) continue;
+      const float w = ex2_approx(ml[u].x - to);
+      l += ml[u].y * w;
+#pragma unroll
+      for (int x = 0; x < kVec; ++x) o[x] += v[u][x] * w;
     }
-    if (lane == 0) s_ml[warp] = make_float2(M, l);
+  }
+  const int at = it.z * kTreeRows + row, token = at / a.group;
+  const long long out = (static_cast<long long>(s.c0) + token) * a.H + it.y * a.group + at % a.group;
+  if (few) {
+    const float f = M == -INFINITY ? 0.f : a.o_scale / l;
 #pragma unroll
-    for (int x = 0; x < kVec; ++x) s_o[warp][lane * kVec + x] = o[x];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      M = -INFINITY;
-      l = 0.f;
+    for (int x = 0; x < kVec; x += 2)
+      *reinterpret_cast<uint32_t*>(a.o + out * D + lane * kVec + x) = pack_bf16(o[x] * f, o[x + 1] * f);
+    if (lane == 0) a.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+    return;
+  }
+  if (lane == 0) s_ml[warp] = make_float2(M, l);
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_ml[w].x);
-      float v = 0.f;
+  for (int x = 0; x < kVec; ++x) s_o[warp][lane * kVec + x] = o[x];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    M = -INFINITY;
+    l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) {
-        if (s_ml[w].x == -INFINITY) continue;
-        const float f = ex2_approx(s_ml[w].x - M);
-        l += s_ml[w].y * f;
-        v += s_o[w][threadIdx.x] * f;
-      }
-      const float f = M == -INFINITY ? 0.f : a.o_scale / l;
-      a.o[out * D + threadIdx.x] = __float2bfloat16_rn(v * f);
-      if (threadIdx.x == 0) a.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_ml[w].x);
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (s_ml[w].x == -INFINITY) continue;
+      const float f = ex2_approx(s_ml[w].x - M);
+      l += s_ml[w].y * f;
+      v += s_o[w][threadIdx.x] * f;
     }
-    __syncthreads();
+    const float f = M == -INFINITY ? 0.f : a.o_scale / l;
+    a.o[out * D + threadIdx.x] = __float2bfloat16_rn(v * f);
+    if (threadIdx.x == 0) a.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
   }
 }
 

@@ -485,8 +485,8 @@ int attn_decode_window(const attn_cache_t* cache, const void* q, const long long
  *   nearest in range, a length below the number of its tokens as 0, and both are recorded
  *   as ATTN_ERR_PAGE.
  *   workspace: attn_decode_tree_workspace_size(...) bytes, as for attn_decode.
- * Deterministic as attn_decode, and of its precision (e4m3 caches: weights as fp16 to
- * 2^-12). A NaN or infinite element of a drafted token's k or v may reach other tokens of
+ * Deterministic as attn_decode. Weights enter the products as bf16, as in attn_fwd (e4m3
+ * caches: as fp16, to 2^-12); their sums are fp32. A NaN or infinite element of a drafted token's k or v may reach other tokens of
  * its sequence.
  */
 #define ATTN_MAX_MASK_WORDS 16
