@@ -1317,7 +1317,7 @@ int attn_decode_tree(const attn_cache_t* cache, const void* q, const long long* 
   // items of 128 rows, tiles of 128 keys (the sinks' and the window's may each be partly filled)
   const long long rows = static_cast<long long>(T) * group;
   const double items = (static_cast<double>(rows) / eba::kTreeRows + std::min(T, B)) * cache->H_kv;
-  const double item_tiles = static_cast<double>(max_len) / eba::kTreeKeys + 2;
+  const double item_tiles = static_cast<double>(max_len) / eba::kTreeKeys + 2 + eba::kTreeEnd;
   if (static_cast<long long>(T) * H >= (1ll << 31) - eba::kTreeRows || items * item_tiles >= 2147483647.0)
     return ATTN_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < tree_bytes(cache->d)) return ATTN_ERR_WORKSPACE;

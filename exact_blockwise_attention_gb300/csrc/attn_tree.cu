@@ -13,8 +13,8 @@
 // of the HBM rate, the products take 0.75 us. So the kernel is built to keep loads on
 // their way and every step of a tile short:
 //  - The list of all 128-key tiles of all (sequence, K/V head, 128 rows) items is cut
-//    into equal runs, one per CTA, as in decode.cuh: lengths need not be known to the
-//    host. Items cut between CTAs leave fp32 parts that the join kernel adds up in order.
+//    into runs of equal cost, one per CTA, as in decode.cuh: lengths need not be known to
+//    the host. Items cut between CTAs leave fp32 parts that the join kernel adds up in order.
 //  - Pages of a multiple of 16 keys are loaded by TMA, a box of 32 or 16 keys by 64
 //    elements to a lane of a warp for the keys and of one for the values, which look
 //    their pages up two tiles ahead; boxes that are cut off are loaded row by row, with
@@ -35,12 +35,13 @@
 //    misses took more time than anything else (this, P as one bf16 term instead of two,
 //    and eight loading warps instead of four: 293 -> 148 us).
 // Measured (one GB300; bytes of the caches at the time of the call): 32 sequences of up to
-// 8191 keys, 32 drafts, 8 heads of 128 for 32: 133 us, 5.2 TB/s, 77 % of a copy; 8 of up
+// 8191 keys, 32 drafts, 8 heads of 128 for 32: 131 us, 5.3 TB/s, 79 % of a copy; 8 of up
 // to 131071 e4m3 keys, 12 drafts, 4 heads of 128 for 32: 180 us, 3.4 TB/s; 16 of up to 6007
-// keys, 24 drafts, 16 heads of 64: 89 us, 3.2 TB/s. A tile takes 2000 cycles of the softmax
+// keys, 24 drafts, 16 heads of 64: 76 us, 3.7 TB/s. A tile takes 2000 cycles of the softmax
 // (scores and maximum 720, exponentials 885, vote and waits the rest) however short its
-// rows: that bounds rows of 64 elements or bytes; rows of 256 bytes: HBM, unequal SMs at
-// the end, the join.
+// rows, a producer 1750: these bound rows of 128 bytes (more slots, two producers for each
+// operand, or copies of few rows that share a tile's keys among more warps: no gain); rows
+// of 256 bytes: HBM, unequal SMs at the end, the join.
 // Tensor memory: S_0 [0,128) S_1 [128,256) O [256,256+d) P_0 [384,448) P_1 [448,512).
 #include <cuda_fp16.h>
 
@@ -228,13 +229,15 @@ __device__ __forceinline__ int head_tiles(const TreeArgs& a, const Seq& s) {
   return n;
 }
 
-__device__ __forceinline__ int first_tile(int i, int tiles, int ctas) {
-  return static_cast<int>(static_cast<long long>(i) * tiles / ctas);
+// The list is cut in units: each tile is one, and each item's end kTreeEnd more (0 in short
+// runs). A run begins at a unit's tile, or, at the unit of an end, at the next item.
+__device__ __forceinline__ int first_unit(int i, int units, int ctas) {
+  return static_cast<int>(static_cast<long long>(i) * units / ctas);
 }
-// The run that tile t is in.
-__device__ __forceinline__ int run_of(int t, int tiles, int ctas) {
-  int i = static_cast<int>(static_cast<long long>(t) * ctas / tiles);
-  while (i + 1 < ctas && first_tile(i + 1, tiles, ctas) <= t) ++i;
+// The run that unit u is in.
+__device__ __forceinline__ int run_of(int u, int units, int ctas) {
+  int i = static_cast<int>(static_cast<long long>(u) * ctas / units);
+  while (i + 1 < ctas && first_unit(i + 1, units, ctas) <= u) ++i;
   return i;
 }
 
@@ -308,9 +311,10 @@ __global__ void __launch_bounds__(kBlock, 1)
   auto raw_empty = [&](int s) { return b1 + 104 + 8u * (2 * kAhead + s); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
-  int* s_scan = reinterpret_cast<int*>(smem + L::offScan);
+  int2* s_scan = reinterpret_cast<int2*>(smem + L::offScan);
   Cursor& s_first = *reinterpret_cast<Cursor*>(smem + L::offFirst);
-  static_assert(sizeof(Cursor) <= 64, "");
+  int* s_cut = reinterpret_cast<int*>(smem + L::offFirst + sizeof(Cursor));  // tiles before the run, and its end
+  static_assert(sizeof(Cursor) + 8 <= 64, "");
   const DeviceStatus st{a.status, a.limit_ns};
 
   if (tid == 0) {
@@ -350,53 +354,69 @@ __global__ void __launch_bounds__(kBlock, 1)
   const int cta = blockIdx.x;
   const int per = (a.B + kBlock - 1) / kBlock;
   const int b0 = min(tid * per, a.B), b_end = min(b0 + per, a.B);
-  int mine = 0;
+  int2 mine = make_int2(0, 0);  // tiles, items
   for (int b = b0; b < b_end; ++b) {
     if (cta == 0 && faulty(a, b)) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
-    mine += head_tiles(a, sequence(a, b)) * a.cache.H_kv;
+    const Seq s = sequence(a, b);
+    mine.x += head_tiles(a, s) * a.cache.H_kv;
+    mine.y += s.items * a.cache.H_kv;
   }
-  int incl = mine;
+  int2 incl = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, m);
-    if (lane >= m) incl += o;
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, m), y = __shfl_up_sync(0xffffffffu, incl.y, m);
+    if (lane >= m) incl.x += x, incl.y += y;
   }
   if (lane == 31) s_scan[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int before = 0, tiles = 0;
+  int2 before = make_int2(0, 0), all = make_int2(0, 0);
 #pragma unroll
   for (int w = 0; w < kBlock / 32; ++w) {
-    before += w < warp ? s_scan[w] : 0;
-    tiles += s_scan[w];
+    const int2 x = s_scan[w];
+    if (w < warp) before.x += x.x, before.y += x.y;
+    all.x += x.x, all.y += x.y;
   }
+  const int tiles = all.x;
   const int G = max(1, min(static_cast<int>(gridDim.x), tiles));  // no run is empty
-  const int r0 = cta < G ? first_tile(cta, tiles, G) : tiles;
-  const int r1 = cta < G ? first_tile(cta + 1, tiles, G) : tiles;
-  {
-    int at = before + incl - mine;
-    if (r0 < r1 && r0 >= at && r0 < at + mine) {
+  const int end_units = tiles / G >= 4 * kTreeEnd ? kTreeEnd : 0;
+  const int units = tiles + end_units * all.y;
+  const int u1 = first_unit(cta + 1, units, G);
+  if (cta < G) {
+    const int at0 = before.x + incl.x - mine.x, items0 = before.y + incl.y - mine.y;
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      const int u = e ? u1 : first_unit(cta, units, G);
+      int at = at0, unit = at0 + end_units * items0;
+      if (e && cta + 1 == G && tid == 0) s_cut[1] = tiles;
+      if (u < unit || u >= unit + mine.x + end_units * mine.y) continue;
       for (int b = b0; b < b_end; ++b) {
         Cursor c;
         c.s = sequence(a, b);
-        const int ht = head_tiles(a, c.s);
-        if (r0 < at + ht * a.cache.H_kv) {
-          int in = r0 - at;
-          c.b = b;
-          c.hh = in / ht;
-          in -= c.hh * ht;
-          for (c.qt = 0;; ++c.qt) {
-            set_item(c, a);
-            if (in < c.nt) break;
-            in -= c.nt;
-          }
-          c.t = in;
-          s_first = c;
-          break;
+        const int ht = head_tiles(a, c.s), hu = ht + end_units * c.s.items;
+        if (u >= unit + hu * a.cache.H_kv) {
+          unit += hu * a.cache.H_kv;
+          at += ht * a.cache.H_kv;
+          continue;
         }
-        at += ht * a.cache.H_kv;
+        int in = u - unit;
+        c.b = b;
+        c.hh = in / hu;
+        in -= c.hh * hu;
+        at += c.hh * ht;
+        for (c.qt = 0;; ++c.qt) {
+          set_item(c, a);
+          if (in < c.nt + end_units) break;
+          in -= c.nt + end_units;
+          at += c.nt;
+        }
+        c.t = min(in, c.nt);
+        s_cut[e] = at + c.t;
+        if (c.t == c.nt) next_item(c, a);
+        if (e == 0) s_first = c;
+        break;
       }
     }
   }
@@ -410,7 +430,7 @@ __global__ void __launch_bounds__(kBlock, 1)
     for (long long x = tid; x < rows; x += kBlock) a.lse[row0 + x] = -INFINITY;
   }
   __syncthreads();
-  const int n_tiles = r1 - r0;
+  const int n_tiles = cta < G && tiles > 0 ? s_cut[1] - s_cut[0] : 0;
 
   // TMA producer of the keys or the values: lane i has box i / kAtoms of each tile, and half
   // i % kAtoms of its rows.
@@ -985,7 +1005,7 @@ __global__ void __launch_bounds__(kBlock, 1)
       if (n == n_tiles && a.cut && tid == 0) {
         // an item that begins in this run and goes on in the next ones
         int parts = 0;
-        if (!ends && t_begin == 0) parts = run_of(r1 + c.nt - count - 1, tiles, G) - cta + 1;
+        if (!ends && t_begin == 0) parts = run_of(u1 + c.nt - count - 1, units, G) - cta + 1;
         a.cut[cta] = make_int2(item == 0 ? 0 : 1, parts);
         a.item[cta] = make_int4(c.b, c.hh, c.qt, 0);
       }

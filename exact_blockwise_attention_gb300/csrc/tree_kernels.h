@@ -14,6 +14,10 @@ namespace eba {
 constexpr int kTreeCtas = 152;
 constexpr int kTreeKeys = 128;  // keys of a tile
 constexpr int kTreeRows = 128;  // (token, head) rows of an item
+// Tiles that an item's end takes as long as, in the split of the list between CTAs. (16 times
+// up to 6007 keys, 16 heads of 64: 0 / 1 / 2 / 3 / 5 tiles 90 / 84 / 78 / 76 / 78 us; 32 times up
+// to 8191 keys, 8 heads of 128: 136 / 134 / 134 / 132 / 133 us)
+constexpr int kTreeEnd = 3;
 struct TreeArgs {
   const __nv_bfloat16* q;  // [T, H, d], strides below
   long long q_token, q_head;

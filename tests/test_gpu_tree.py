@@ -201,6 +201,19 @@ def test_prompt_of_many_tokens(eba):
         check(eba, Paged([1500, 700], 16, 1, 64, seed=3), [1100, 700], 2, None, window=window, sinks=5 if window else 0)
 
 
+@pytest.mark.parametrize("seed,window", [(0, None), (1, None), (2, 300), (3, None)])
+def test_long_runs_over_many_ends(eba, seed, window):
+    """So many tiles that an item's end counts in the split of the list: runs that begin at
+    ends, of items of one tile and of many, and items cut in several."""
+    r = np.random.default_rng(seed + 40)
+    lens = [int(n) for n in r.choice([1, 2, 127, 128, 129, 700, 3000, 6100], 48)] + [9000]
+    if window:
+        lens = [min(3 * n, 700) for n in lens] * 4
+    news = [int(r.integers(1, min(n, 3) + 1)) for n in lens]
+    assert window or sum(-(-n // 128) for n in lens) * 8 >= 12 * 152
+    check(eba, Paged(lens, 16, 8, 64, seed=seed), news, 8, random_masks(r, news), window=window, sinks=3 if window else 0)
+
+
 def test_rows_of_no_sequence_stay(eba):
     r = np.random.default_rng(6)
     news = [3, 0, 5]
