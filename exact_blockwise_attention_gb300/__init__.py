@@ -1136,9 +1136,9 @@ def decode_tree(cache, q, page_table, seq_lens, cu_q=None, mask=None, window=Non
     With a ``window`` a token at place p sees of the keys before the drafts (without a
     mask: of all) those after p - window and the first ``sinks``; its place is that
     of the drafts' first key plus its place in the chain, or plus the number of its
-    mask's bits less one (without one ``sinks`` is of no effect). Pages between the sinks and the window of a token at the
-    drafts' first key need not be there. q is taken as it is: rotate it with rope_fwd, the new keys
-    in cache_append.
+    mask's bits less one. Pages between the sinks and the window of a token at the
+    drafts' first key need not be there. Without a window ``sinks`` is of no effect.
+    q is taken as it is: rotate it with rope_fwd, the new keys in cache_append.
 
     A token that sees nothing, or whose sequence has length 0, gives o = 0 and
     lse = -inf; rows of no sequence are not written. The GPU reads lengths, offsets,
@@ -1232,11 +1232,17 @@ class PagePool:
             raise ValueError("page_size must be positive")
         self.refs, self.page_size, self.n_pages, self.device = refs, page_size, refs.numel(), refs.device
         self._scratch = torch.empty_like(refs)
+        self._stream = self._here() if refs.is_cuda else None
         self._struct = _PoolStruct(0, self._scratch.data_ptr(), self.n_pages, page_size)
+
+    def _here(self):
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def _at(self):
         if self.device.type != "cuda":
             raise ValueError("the pool must be on a CUDA device")
+        if self._here() != self._stream:  # a pool that goes leaves its scratch to that stream's work
+            self._scratch.record_stream(torch.cuda.current_stream(self.device))
         self._struct.refs = self.refs.data_ptr()
         return self._struct
 

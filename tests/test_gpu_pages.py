@@ -289,3 +289,22 @@ def test_pages_behind_2_to_the_31_elements(eba):
     eba.cache_gather(cache, gpu([[n - 1, n - 5]]), gpu([3, 9]), gpu([0, 2]), to_table=gpu([[n - 7]]), to_start=gpu([5]))
     assert (k[n - 7, 5:7] == 3).all() and (v[n - 7, 5:7] == 4).all()
     assert (k[n - 7, :5] == 0).all() and (k[n - 7, 7:] == 0).all()
+
+
+def test_a_pool_that_goes_leaves_its_scratch_to_its_stream(eba):
+    """Memory of a pool used on another stream is not handed out while that one may run."""
+    batch = Batch(eba, 8, 40, 16, 4096, 3)
+    pool = eba.PagePool(batch.grefs, 16)
+    at, side = pool._scratch.data_ptr(), torch.cuda.Stream()
+    more = np.minimum(batch.lens + 50, 640)
+    gmore = gpu(more)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        eba.pages_reserve(pool, batch.gtable, batch.glens, gmore)
+    del pool
+    held = [torch.empty(4096, dtype=torch.int32, device="cuda") for _ in range(64)]
+    assert not side.query() and all(x.data_ptr() != at for x in held)
+    side.synchronize()
+    pages.reserve(batch.refs, batch.table, 16, batch.lens, more)
+    batch.check()

@@ -394,3 +394,27 @@ def test_a_step_of_speculative_decoding(eba):
     assert (np.abs(np64(o)[last] - ro) <= to).all() and (np.abs(np64(lse)[last] - rl) <= tl).all()
     held = [-(-(c + len(x)) // size) for c, x in zip(ctx, paths)]
     assert (table.cpu() >= 0).sum(1).tolist() == held and int(pool.refs.sum()) == sum(held)
+
+
+def test_two_calls_at_once(eba):
+    """Calls on streams of their own, at the same time and behind one another."""
+    r = np.random.default_rng(12)
+    calls = []
+    for seed, (d, e4m3) in enumerate(((64, False), (128, True), (128, False))):
+        news = [int(n) for n in r.integers(1, 20, 9)]
+        p = Paged([int(n) + 20 for n in r.integers(1, 4000, 9)], 32, 4, d, e4m3=e4m3, seed=seed)
+        q = bf16(torch.Generator().manual_seed(seed), sum(news), 8, d).cuda()
+        cu = torch.tensor([0, *np.cumsum(news)], dtype=torch.int32).cuda()
+        mask = words_of(random_masks(r, news), 1)[:, 0].cuda()
+        calls.append((p.on_gpu(eba), q, p.gtable, p.glens, cu, mask))
+    alone = [eba.decode_tree(*c) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[] for _ in calls]
+    for _ in range(20):
+        for c, s, out in zip(calls, streams, got):
+            with torch.cuda.stream(s):
+                out.append(eba.decode_tree(*c))
+    torch.cuda.synchronize()
+    for (o, lse), outs in zip(alone, got):
+        assert all(torch.equal(o, x) and torch.equal(lse, y) for x, y in outs)

@@ -292,3 +292,32 @@ def test_refusals(eba):
         eba.bwd_window(q, k, v, o, do, lse, 5, rest=o.float())
     with pytest.raises(ValueError):
         eba.bwd_window(q, k, v, o, do, lse, 5, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+def test_two_steps_at_once(eba):
+    """Training steps on streams of their own, at the same time."""
+    steps = []
+    for seed, (L, d, left, right) in enumerate(((823, 128, 100, 5), (1500, 64, 40, 0), (640, 128, 600, None))):
+        q, k, v, do = (x.cuda() for x in inputs(seed, 1, 8, 4, L, L, d))
+        for x in (q, k, v):
+            x.requires_grad_(True)
+        steps.append(((q, k, v), do, (left, right, 2)))
+
+    def step(args, do, window):
+        o = eba.attention_window(*args, *window)
+        return (o.detach(), *torch.autograd.grad(o, args, do))
+
+    alone = [step(*s) for s in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    got = [[] for _ in steps]
+    for _ in range(10):
+        for s, stream, out in zip(steps, streams, got):
+            with torch.cuda.stream(stream):
+                out.append(step(*s))
+    torch.cuda.synchronize()
+    for want, outs in zip(alone, got):
+        for x in outs:
+            # (dq is added up in any order: see test_captured_training_step)
+            assert all(torch.equal(want[i], x[i]) for i in (0, 2, 3))
+            assert (want[1].float() - x[1].float()).norm() <= 2 * U / 16 * want[1].float().norm()
