@@ -17,12 +17,14 @@
 //                    dK, dV accumulate in tensor memory, dQ tiles are added
 //                    into the fp32 accumulator atomically
 //   bwd_dq_kernel    dQ = bf16(scale * accumulator)
-// Work items come in four kinds (template arguments): dense [B*H, L, d]
+// Work items come in five kinds (template arguments): dense [B*H, L, d]
 // heads; grouped-query heads (an item walks the query tiles of every head of
 // its group); packed variable-length sequences ([T, H, d], per-sequence
 // bounds); short sequences packed several to a tile (block-diagonal; each
 // query row gets all of its dQ from one tile, so dQ is stored directly and
-// the accumulator, its zeroing and bwd_dq_kernel are skipped).
+// the accumulator, its zeroing and bwd_dq_kernel are skipped); a sliding window and first
+// tokens (an item walks the query tiles that see any of its keys; the first tokens' are cut
+// in pieces, whose dK, dV bwd_pieces_kernel adds up).
 //
 // bwd_kernel roles (512 threads):
 //   warps 0-7    two "compute" warpgroups; warpgroup w handles query columns

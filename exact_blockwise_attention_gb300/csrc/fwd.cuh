@@ -13,7 +13,8 @@
 // its key range streams past them. Item kinds (template arguments): dense
 // [B*H, L, d] heads (query head bh reads K/V head bh / group), packed
 // variable-length sequences ([T, H, d]), short sequences packed several to a
-// tile (block-diagonal), and an FP8 (e4m3) form of the dense one. Roles:
+// tile (block-diagonal), a sliding window and first tokens (tiles without a visible pair are
+// left out), and an FP8 (e4m3) form of the dense one. Roles:
 //   TMA producer warp   Q tiles once, then K_j / V_j into a ring of slots
 //   MMA issuer warps    S_t = Q_t K_j^T and O_t += P_t V_j, each issued by a
 //                       single elected thread
