@@ -1,8 +1,8 @@
 // Launch of the forward kernel within a sliding window (see fwd.cuh, WindowTiles): tiles
 // without a visible pair are left out, the others computed whole, as tensor cores want them.
-// What is computed beyond the visible pairs is half a tile at each end of a row's window, and
+// What is computed beyond the visible pairs is half a tile at each end of a tile's window, and
 // what bounds it is what bounds the dense kernel, at items of fewer rounds: 12544 tokens, 1568
-// keys each, 16 heads on 4 of 128: 183 us, 831 TFLOP/s of visible pairs (dense: 1277);
+// keys each, 16 heads on 4 of 128: 181 us, 840 TFLOP/s of visible pairs (dense: 1277);
 // 2 x 6273 tokens, 784 keys to both sides, 16 heads of 64: 142 us, 534 TFLOP/s.
 #include "fwd.cuh"
 
