@@ -294,6 +294,21 @@ def test_refusals(eba):
         eba.bwd_window(q, k, v, o, do, lse, 5, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
 
 
+@pytest.mark.parametrize("left,right,sinks", [(100, 50, 0), (130, 0, 3), (0, 200, 0)])
+def test_heads_beyond_l2(eba, left, right, sinks):
+    """More heads than are walked side by side: the same bits as each batch alone."""
+    q, k, v, do = (x.cuda() for x in inputs(31, 4, 128, 128, 300, 300, 128))
+    o, lse = eba.fwd_window(q, k, v, left, right, sinks)
+    dq, dk, dv = eba.bwd_window(q, k, v, o, do, lse, left, right, sinks)
+    for b in range(4):
+        one = [x[b:b + 1] for x in (q, k, v)]
+        o1, lse1 = eba.fwd_window(*one, left, right, sinks)
+        dq1, dk1, dv1 = eba.bwd_window(*one, o1, do[b:b + 1], lse1, left, right, sinks)
+        for x, y in ((o, o1), (lse, lse1), (dk, dk1), (dv, dv1)):
+            assert torch.equal(x[b:b + 1], y)
+        assert (dq[b:b + 1].float() - dq1.float()).norm() <= 2 * U / 16 * dq1.float().norm()
+
+
 def test_two_steps_at_once(eba):
     """Training steps on streams of their own, at the same time."""
     steps = []
