@@ -41,10 +41,11 @@ __global__ void __launch_bounds__(kReleaseThreads)
   pdl_launch_dependents();
   pdl_wait();
   for (int b = blockIdx.y; b < a.n_seqs; b += gridDim.y) {
-    const int e0 = pages_of(max(a.first[b], 0), a.pool.page_size);
+    // (both bounds within the table before any entry's index is formed from them)
+    const int e0 = min(pages_of(max(a.first[b], 0), a.pool.page_size), a.max_pages);
     const int e1 = min(a.last[b] / a.pool.page_size, a.max_pages);
     int* row = a.table + b * a.table_stride;
-    for (int e = e0 + blockIdx.x * kReleaseThreads + threadIdx.x; e < e1;
+    for (long long e = e0 + static_cast<long long>(blockIdx.x) * kReleaseThreads + threadIdx.x; e < e1;
          e += gridDim.x * kReleaseThreads) {
       const int page = row[e];
       if (page < 0) continue;
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kCopyThreads) gather_kernel(const __grid_const
 
 cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t stream) {
   // few blocks a sequence: most calls give back a few pages of each
-  const int x = std::min((a.max_pages + kReleaseThreads - 1) / kReleaseThreads, 8);
+  const int x = std::min((a.max_pages - 1) / kReleaseThreads + 1, 8);
   return launch_pdl(release_kernel, dim3(x, std::min(a.n_seqs, 65535)), dim3(kReleaseThreads), 0, stream, a);
 }
 

@@ -1,0 +1,56 @@
+"""The pages' bookkeeping at the ends of its arguments' ranges, against plain loops."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import pages
+from test_gpu_pages import PAGE_FAULT, Batch, gpu, same
+
+pytestmark = pytest.mark.gpu
+TOP = 2**31 - 1
+
+
+@pytest.fixture(scope="module")
+def eba():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from exact_blockwise_attention_gb300 import _build
+
+    _build.build()
+    import exact_blockwise_attention_gb300 as m
+
+    return m
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean(eba):
+    eba.poll_device_status()
+    yield
+    assert eba.poll_device_status() == 0
+
+
+@pytest.mark.parametrize("size", [1, 2, 16])
+def test_release_of_bounds_beyond_the_table(eba, size):
+    """Bounds outside the table count as its ends: from the largest number on there is nothing
+    to give back."""
+    s = Batch(eba, 5, 700, size, 5000, seed=7)
+    first = np.array([TOP, TOP - 1, TOP - 300, 700 * size, 3])
+    for last in (np.full(5, TOP), np.full(5, -TOP - 1), np.array([TOP, 0, TOP, TOP, TOP])):
+        assert pages.release(s.refs, s.table, size, first, last) == 0
+        eba.pages_release(s.pool, s.gtable, gpu(first), gpu(last))
+        s.check()
+    assert (s.table[4, 3:] == -1).all() and (s.table[:4] >= 0).any()
+
+
+def test_release_at_the_end_of_the_widest_table(eba):
+    """One sequence with 2^31 - 1 entries, the last few of which hold pages."""
+    row = torch.full((1, TOP), -1, dtype=torch.int32, device="cuda")
+    row[0, -5:] = gpu([3, 1, 4, 0, 2])
+    refs = gpu([1, 1, 1, 1, 1])
+    pool = eba.PagePool(refs, 1)
+    eba.pages_release(pool, row, gpu([TOP - 3]), gpu([TOP]))
+    same(row[0, -5:], [3, 1, -1, -1, -1])
+    same(refs, [0, 1, 0, 1, 0])
+    eba.pages_release(pool, row, gpu([TOP - 4000]), gpu([TOP - 4]))
+    same(row[0, -5:], [-1, 1, -1, -1, -1])
+    same(refs, [0, 1, 0, 0, 0])
