@@ -91,10 +91,11 @@ __device__ __forceinline__ int warp_sum(int x) {
   return x;
 }
 
-// A sequence's entries [e0, e1) that may want a page (those that hold none do).
+// A sequence's entries [e0, e1), within its row, that may want a page (those that hold
+// none do).
 __device__ __forceinline__ bool wanted_range(const PoolArgs& a, int b, int& e0, int& e1) {
   const int len = a.lens[b], more = a.new_lens[b];
-  if (len < 0 || more > static_cast<long long>(a.max_pages) * a.pool.page_size) {
+  if (len < 0 || max(len, more) > static_cast<long long>(a.max_pages) * a.pool.page_size) {
     if ((threadIdx.x & 31) == 0) bad_page(a.status);
     return false;
   }
@@ -188,7 +189,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(32 * kPoolWa
       int e0, e1;
       if (!wanted_range(a, b, e0, e1)) continue;
       const int* row = a.table + b * a.table_stride;
-      for (int e = e0 + lane; e < e1; e += 32) want += row[e] < 0;
+      for (long long e = static_cast<long long>(e0) + lane; e < e1; e += 32) want += row[e] < 0;
     }
     want = warp_sum(want);
   }
@@ -277,7 +278,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(32 * kPoolWa
       int e0, e1;
       if (!wanted_range(a, b, e0, e1)) continue;
       int* row = a.table + b * a.table_stride;
-      for (int e = e0; e < e1; e += 32) {
+      for (long long e = e0; e < e1; e += 32) {
         const bool mine = e + lane < e1 && row[e + lane] < 0;
         const uint32_t wants = __ballot_sync(0xffffffffu, mine);
         if (mine) row[e + lane] = take(before_want + __popc(wants & ((1u << lane) - 1u)));

@@ -78,7 +78,7 @@ def reserve(refs, table, size, lens, new_lens) -> int:
     faults, free = 0, 0
     room = table.shape[1] * size
     for b in range(len(table)):
-        if lens[b] < 0 or new_lens[b] > room:
+        if lens[b] < 0 or lens[b] > room or new_lens[b] > room:
             faults += 1
             continue
         for e in range(-(-lens[b] // size), -(-new_lens[b] // size)):

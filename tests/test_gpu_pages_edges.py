@@ -54,3 +54,29 @@ def test_release_at_the_end_of_the_widest_table(eba):
     eba.pages_release(pool, row, gpu([TOP - 4000]), gpu([TOP - 4]))
     same(row[0, -5:], [-1, 1, -1, -1, -1])
     same(refs, [0, 1, 0, 0, 0])
+
+
+@pytest.mark.parametrize("size", [1, 2, 16])
+def test_reserve_of_lengths_beyond_the_table(eba, size):
+    """A length beyond the table is out of range also where nothing is wanted: the sequence
+    gets no page and the status says so."""
+    s = Batch(eba, 6, 30, size, 400, seed=8, fill=0.3)
+    more = np.minimum(s.lens + 3 * size, 30 * size)
+    s.lens[:3] = TOP, TOP - 40, 30 * size + 1
+    s.glens.copy_(gpu(s.lens))
+    for grow in (more, np.full(6, -5), np.where(np.arange(6) < 3, TOP, 0)):
+        assert pages.reserve(s.refs, s.table, size, s.lens, grow) == 3
+        eba.pages_reserve(s.pool, s.gtable, s.glens, gpu(grow))
+        s.check()
+        assert eba.poll_device_status() == PAGE_FAULT
+
+
+def test_reserve_at_the_end_of_the_widest_table(eba):
+    """One sequence with 2^31 - 1 entries grows to its last ones."""
+    row = torch.full((1, TOP), -1, dtype=torch.int32, device="cuda")
+    row[0, -2] = 7
+    refs = gpu([0, 1, 0, 0, 1, 0, 0, 1])
+    pool = eba.PagePool(refs, 1)
+    eba.pages_reserve(pool, row, gpu([TOP - 4]), gpu([TOP]))
+    same(row[0, -5:], [-1, 0, 2, 7, 3])
+    same(refs, [1, 1, 1, 1, 1, 0, 0, 1])
