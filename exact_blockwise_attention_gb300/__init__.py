@@ -1141,7 +1141,7 @@ def decode_tree(cache, q, page_table, seq_lens, cu_q=None, mask=None, window=Non
     q is taken as it is: rotate it with rope_fwd, the new keys in cache_append.
 
     A token that sees nothing, or whose sequence has length 0, gives o = 0 and
-    lse = -inf; rows of no sequence are not written. The GPU reads lengths, offsets,
+    lse = -inf, and so do all where offsets fall; rows of no sequence are not written. The GPU reads lengths, offsets,
     masks and tables, so a captured call follows their contents."""
     try:
         key = (_form(q), _form(page_table), _form(seq_lens), _form(cu_q), _form(mask), cache._key, window,

@@ -355,12 +355,18 @@ __global__ void __launch_bounds__(kBlock, 1)
   const int per = (a.B + kBlock - 1) / kBlock;
   const int b0 = min(tid * per, a.B), b_end = min(b0 + per, a.B);
   int2 mine = make_int2(0, 0);  // tiles, items
+  bool falls = false;
   for (int b = b0; b < b_end; ++b) {
     if (cta == 0 && faulty(a, b)) atomicCAS(a.status, 0, ATTN_ERR_PAGE);
+    falls |= a.cu && a.cu[b + 1] < a.cu[b];
     const Seq s = sequence(a, b);
     mine.x += head_tiles(a, s) * a.cache.H_kv;
     mine.y += s.items * a.cache.H_kv;
   }
+  // Where offsets fall, rows may belong to many sequences, and the sums below need not fit an
+  // int: such a call computes nothing.
+  falls = __syncthreads_or(falls);
+  if (falls) mine = make_int2(0, 0);
   int2 incl = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -420,14 +426,20 @@ __global__ void __launch_bounds__(kBlock, 1)
       }
     }
   }
-  // Sequences without keys: O = 0, lse = -inf.
-  for (int b = cta; b < a.B; b += gridDim.x) {
-    const Seq s = sequence(a, b);
-    if (s.items > 0) continue;
-    const long long row0 = static_cast<long long>(s.c0) * a.H, rows = static_cast<long long>(s.n) * a.H;
-    for (long long x = tid; x < rows * (D / 8); x += kBlock)
+  // Sequences without keys, and all rows where offsets fall: O = 0, lse = -inf.
+  auto blank = [&](long long token0, long long tokens, int first, int step) {
+    const long long row0 = token0 * a.H, rows = tokens * a.H;
+    for (long long x = first; x < rows * (D / 8); x += step)
       *reinterpret_cast<uint4*>(a.o + row0 * D + x * 8) = make_uint4(0, 0, 0, 0);
-    for (long long x = tid; x < rows; x += kBlock) a.lse[row0 + x] = -INFINITY;
+    for (long long x = first; x < rows; x += step) a.lse[row0 + x] = -INFINITY;
+  };
+  if (falls) {
+    blank(0, a.T, cta * kBlock + tid, gridDim.x * kBlock);
+  } else {
+    for (int b = cta; b < a.B; b += gridDim.x) {
+      const Seq s = sequence(a, b);
+      if (s.items == 0) blank(s.c0, s.n, tid, kBlock);
+    }
   }
   __syncthreads();
   const int n_tiles = cta < G && tiles > 0 ? s_cut[1] - s_cut[0] : 0;

@@ -483,7 +483,8 @@ int attn_decode_window(const attn_cache_t* cache, const void* q, const long long
  *   and so do the tokens of a sequence of length 0 (an empty slot). Rows outside
  *   [cu_q[0], cu_q[B]) are left as they were. Lengths and offsets out of range count as the
  *   nearest in range, a length below the number of its tokens as 0, and both are recorded
- *   as ATTN_ERR_PAGE.
+ *   as ATTN_ERR_PAGE. So are offsets that fall (cu_q[b + 1] < cu_q[b] for any b): then all T
+ *   tokens give O = 0, lse = -inf.
  *   workspace: attn_decode_tree_workspace_size(...) bytes, as for attn_decode.
  * Deterministic as attn_decode. Weights enter the products as bf16, as in attn_fwd (e4m3
  * caches: as fp16, to 2^-12); their sums are fp32. A NaN or infinite element of a drafted token's k or v may reach other tokens of
