@@ -972,15 +972,18 @@ __global__ void __launch_bounds__(kBlock, 1)
         named_bar_sync(1, kSoftmax);
         const float2 other = s_sum[(1 - g) * kTreeRows + row];
         const float l = l_sum + other.x, rounded = l + (l_fix + other.y);
-        const float M = m_used == -INFINITY ? -INFINITY : m_used - (F8 ? kF16Shift : 0.f);
+        // No weight: nothing seen, or only scores of -inf. (A NaN score leaves the maximum as it
+        // was, but not the sum: such a row is NaN, its part's reference any finite one.)
+        const bool none = m_used == -INFINITY && l == 0.f;
+        const float M = none ? -INFINITY : (m_used == -INFINITY ? 0.f : m_used) - (F8 ? kF16Shift : 0.f);
         const bool whole = t_begin == 0 && ends;
         // a part: O as its weights' sum l would have it
-        const float mul = M == -INFINITY ? 0.f : whole ? a.o_scale / rounded : l / rounded;
+        const float mul = none ? 0.f : whole ? a.o_scale / rounded : l / rounded;
         const long long out = (static_cast<long long>(c.s.c0) + token) * a.H + c.hh * a.group + at % a.group;
         const long long slot = 2 * cta + (item == 0 ? 0 : 1);
         if (has && g == 0) {
           if (whole)
-            a.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2_approx(l)) * kLn2;
+            a.lse[out] = none ? -INFINITY : (M + lg2_approx(l)) * kLn2;
           else
             a.part_ml[slot * kTreeRows + row] = make_float2(M, l);
         }
@@ -996,7 +999,7 @@ __global__ void __launch_bounds__(kBlock, 1)
             float v[32];
             // (a row without a weight: whatever was added)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = mul > 0.f ? __uint_as_float(u[e]) * mul : 0.f;
+            for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : __uint_as_float(u[e]) * mul;
             if (whole) {
               uint4* to = reinterpret_cast<uint4*>(a.o + out * D + col);
 #pragma unroll

@@ -487,8 +487,10 @@ int attn_decode_window(const attn_cache_t* cache, const void* q, const long long
  *   tokens give O = 0, lse = -inf.
  *   workspace: attn_decode_tree_workspace_size(...) bytes, as for attn_decode.
  * Deterministic as attn_decode. Weights enter the products as bf16, as in attn_fwd (e4m3
- * caches: as fp16, to 2^-12); their sums are fp32. A NaN or infinite element of a drafted token's k or v may reach other tokens of
- * its sequence.
+ * caches: as fp16, to 2^-12), in attn_decode as two bf16 terms: O is 0.0023 off as a whole,
+ * attn_decode's 0.0017; their sums are fp32. A NaN or a score of +inf that a token sees makes
+ * its row NaN. A NaN or infinite element of v may reach other tokens of its sequence that do
+ * not see it (a drafted token's, or of a key that a window hides from some of them); of k, none.
  */
 #define ATTN_MAX_MASK_WORDS 16
 size_t attn_decode_tree_workspace_size(int T, int B, int H, int H_kv, int d);
