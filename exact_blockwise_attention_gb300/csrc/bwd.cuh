@@ -1115,7 +1115,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // D_i = sum_k dO_ik O_ik and -lse2_i = -lse_i * log2(e) (stored negated, the
 // addend of the exponent) for rows < Lq; padding rows up to the 128-row tile
 // boundary get D = 0 and -lse2 = -inf (so their
-// recomputed P is exactly 0). Also zeroes the fp32 dQ accumulator.
+// recomputed P is exactly 0), and rows without a weight (lse = -inf: no key, or only
+// scores of -inf) -lse2 = -inf too. Also zeroes the fp32 dQ accumulator.
 // VarlenTable: each sequence's rows are padded to whole tiles (padded row p
 // of a head is row p - 128 cu_qt[s] of the sequence s owning tile p / 128).
 // PackedTiles: padded row p is row p % 128 of tile p / 128, which holds the
@@ -1196,7 +1197,8 @@ __global__ void __launch_bounds__(256)
   for (int m = kLanesPerRow / 2; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
   if (in_range && seg == 0) {
     a.delta[prow] = valid ? dot : 0.f;
-    a.nlse2[prow] = valid ? -(a.lse[bh * a.Lq + r] * kLog2e) : -INFINITY;
+    const float lse = valid ? a.lse[bh * a.Lq + r] : -INFINITY;
+    a.nlse2[prow] = lse == -INFINITY ? -INFINITY : -(lse * kLog2e);
   }
 }
 

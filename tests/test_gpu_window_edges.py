@@ -1,0 +1,51 @@
+"""Windowed attention where its masks leave nothing or hide something: rows without a weight,
+hidden values of any finite size, NaN where no pair of a tile is visible."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from cache_util import np64
+from test_gpu_window import U, compare, exact_and_bounds, inputs, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def eba():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from exact_blockwise_attention_gb300 import _build
+
+    _build.build()
+    import exact_blockwise_attention_gb300 as m
+
+    return m
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean(eba):
+    eba.poll_device_status()
+    yield
+    assert eba.poll_device_status() == 0
+
+
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (4, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_row_without_a_weight_has_no_gradients(eba, d, H, Hkv):
+    """All that row 7 sees has the score -inf: its weights are 0, so it gets no gradient and adds
+    none, as if its dO were 0."""
+    q, k, v, do = inputs(5, 1, H, Hkv, 300, 300, d)
+    k[:, :, 3:8] = -1
+    q[:, :, 7], do7 = 0, do[:, :, 7].clone()
+    do[:, :, 7] = 0
+    want = exact_and_bounds(q, k, v, do, 4, 0, 0, 1 / math.sqrt(d))
+    q[:, :, 7], do[:, :, 7] = 3e38, do7
+    for with_rest in (True, False):
+        got = run(eba, q, k, v, do, 4, 0, 0, with_rest=with_rest)
+        assert (got["o"][:, :, 7] == 0).all() and torch.isneginf(got["lse"][:, :, 7]).all()
+        assert (got["dq"][:, :, 7] == 0).all()
+        others = [i for i in range(300) if i != 7]
+        rows = {n: got[n] if n in ("dk", "dv") else got[n][:, :, others] for n in got}
+        compare(rows, {n: want[n] if n in ("dk", "dv") else tuple(x[:, :, others] for x in want[n]) for n in want})
