@@ -292,6 +292,20 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, const VarlenTable&
   return it;
 }
 
+// Windowed: zeros in the columns outside [lo, hi] of row r of a warpgroup's half of dS^T.
+__device__ __noinline__ void hide_row(uint32_t drow, int r, int lo, int hi) {
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 8) {
+    if (c >= lo && c + 7 <= hi) continue;
+    const uint32_t at = drow + sw128_offset(r, c >> 3);
+    uint4 x = ld_shared_v4(at);
+    auto keep = [&](int c2) {
+      return (c2 >= lo && c2 <= hi ? 0xffffu : 0u) | (c2 + 1 >= lo && c2 + 1 <= hi ? 0xffff0000u : 0u);
+    };
+    st_shared_v4(at, x.x & keep(c), x.y & keep(c + 2), x.z & keep(c + 4), x.w & keep(c + 6));
+  }
+}
+
 // Row r of an item's unscaled dV (which = 0) or dK, where its key tile is cut in pieces.
 template <int D>
 __device__ __forceinline__ float* bwd_part(const BwdArgs& a, int part, int which, int r) {
@@ -937,6 +951,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rounded to bf16 and packed (the A operand of dV).
         uint32_t pp[32];
         float pf[64];
+        // windowed: the columns that see this key, [lo, hi]; all: every lane's are all 64
+        int lo = 0, hi = 63;
+        bool all = true;
         {
           // Staged so that each step has 32-64 independent operations: -lse2 of
           // the 64 columns, S^T from TMEM, x = s * scale * log2e - lse2, 2^x, pack.
@@ -971,9 +988,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The queries that see this key: places key - right to key + left, or all from
             // the former on; of this warpgroup's columns [lo, hi].
             const int p0 = qc.row(it) + 64 * wg + vt.off;
-            const int lo = key - vt.right - p0;
-            const int hi = !key_ok || it.blind ? -1 : key < vt.sinks ? 63 : key + vt.left - p0;
-            if (__all_sync(0xffffffffu, lo <= 0 && hi >= 63)) {
+            lo = key - vt.right - p0;
+            hi = !key_ok || it.blind ? -1 : key < vt.sinks ? 63 : key + vt.left - p0;
+            all = __all_sync(0xffffffffu, lo <= 0 && hi >= 63);
+            if (all) {
 #pragma unroll
               for (int j = 0; j < 64; ++j) pf[j] = ex2_approx(pf[j]);
             } else {
@@ -1039,6 +1057,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ch = 0; ch < 8; ++ch)
           st_shared_v4(drow + sw128_offset(r, ch), dsp[4 * ch], dsp[4 * ch + 1], dsp[4 * ch + 2],
                        dsp[4 * ch + 3]);
+        // A hidden pair's dS is 0 whatever dP and D are. Its P is, so that only a dP or D that is
+        // no finite number asks for more than the product above: an exponent of ones, here in
+        // the OR of the row's (also where values of 2 and more meet others). hide_row is a
+        // function of its own: 2 x 6273 tokens, 784 keys to both sides, 16 heads of 64 take 510 us
+        // forward and backward, 501 without this, 522 with its code in line, and 554 or, in
+        // registers, 624 with dS masked in every tile that hides a pair.
+        uint32_t any = 0u;
+        if (WINDOW && !all) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) any |= dsp[j];
+        }
+        if (WINDOW && !all && ((any & 0x7f80u) == 0x7f80u || (any & 0x7f800000u) == 0x7f800000u))
+          hide_row(drow, r, lo, hi);
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(pds_full);

@@ -49,3 +49,22 @@ def test_a_row_without_a_weight_has_no_gradients(eba, d, H, Hkv):
         others = [i for i in range(300) if i != 7]
         rows = {n: got[n] if n in ("dk", "dv") else got[n][:, :, others] for n in got}
         compare(rows, {n: want[n] if n in ("dk", "dv") else tuple(x[:, :, others] for x in want[n]) for n in want})
+
+
+@pytest.mark.parametrize("size", [1e30, 3e38])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (4, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_hidden_values_do_not_reach_gradients(eba, d, H, Hkv, size):
+    """Keys and values from 300 on of any finite size: rows that do not see them, and keys that
+    only such rows see, keep their gradients (dQ but for the order in which it is added up)."""
+    q, k, v, do = inputs(4, 1, H, Hkv, 600, 600, d)
+    a = run(eba, q, k, v, do, 100, 0, 2)
+    k2, v2 = k.clone(), v.clone()
+    k2[:, :, 300:], v2[:, :, 300:] = size, -size
+    b = run(eba, q, k2, v2, do, 100, 0, 2)
+    for n in ("o", "lse"):
+        assert torch.equal(a[n][:, :, :300], b[n][:, :, :300])
+    for n in ("dk", "dv"):  # (keys 0 and 1 are seen by all rows)
+        assert torch.equal(a[n][:, :, 2:200], b[n][:, :, 2:200]), n
+    x, y = np64(a["dq"][:, :, :300]), np64(b["dq"][:, :, :300])
+    assert np.isfinite(y).all() and np.linalg.norm(x - y) <= 2 * U / 16 * np.linalg.norm(x)
