@@ -659,17 +659,22 @@ bool window_tiles(int Lq, int Lk, int left, int right, int sinks, long long head
   constexpr int R = eba::kTileRows;
   const int n_qtiles = (Lq + R - 1) / R;
   w->run_tiles = left_end && right_end ? std::min(n_qtiles, (w->left + w->right + R - 1) / R + 2) : n_qtiles;
+  // Key tiles behind the sinks and wholly before the first query's window.
+  const int sink_tiles = (w->sinks + R - 1) / R;
+  w->blind0 = sink_tiles;
+  w->blind_tiles = std::max(0, std::max(0, w->off - w->left) / R - sink_tiles);
   if (!left_end || w->sinks == 0) return true;
   // Pieces as long as an ordinary item, at least 8 query tiles (each leaves 2 x 128 x d
   // floats). Many sinks' key tiles keep all SMs busy by themselves and stay whole.
-  const int sink_tiles = (w->sinks + R - 1) / R;
-  const int piece = std::max(w->run_tiles, 8);
   if (sink_tiles * heads > 4 * 152) {
     w->by_cost = 1;
     return true;
   }
-  w->piece = piece;
-  w->pieces = (n_qtiles + piece - 1) / piece;
+  const int most = std::max(w->run_tiles, 8);
+  // (no more of them than query tiles that see any of the last sinks)
+  const int seen = n_qtiles - std::max(0, (sink_tiles - 1) * R - w->right - w->off) / R;
+  w->pieces = std::min((n_qtiles + most - 1) / most, seen);
+  w->piece = seen / w->pieces;
   if (w->pieces > 1) w->cut_tiles = sink_tiles; else w->pieces = w->piece = 0;
   return true;
 }
@@ -984,7 +989,8 @@ int attn_bwd_window(const void* q, const void* k, const void* v, const void* o,
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  const long long items = (a.n_ktiles + static_cast<long long>(w.cut_tiles) * (w.pieces - 1)) * BHkv;
+  const long long items =
+      (a.n_ktiles - w.blind_tiles + static_cast<long long>(w.cut_tiles) * (w.pieces - 1)) * BHkv;
   if (items >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
   a.status = status_word_ptr();
   if (!a.status) return ATTN_ERR_CUDA;
@@ -994,6 +1000,20 @@ int attn_bwd_window(const void* q, const void* k, const void* v, const void* o,
       !make_map(&tv, v, BHkv, Lk, d) || !make_map(&tdo, dO, BH, Lq, d) ||
       !make_map_f32(&tdqa, ws, BH, Lq, d))
     return ATTN_ERR_CUDA;
+  if (w.blind_tiles > 0) {
+    const size_t row = d * 2, pitch = Lk * row, bytes = static_cast<size_t>(w.blind_tiles) * eba::kTileRows * row;
+    for (void* x : {dk, dv}) {
+      char* to = static_cast<char*>(x) + static_cast<size_t>(w.blind0) * eba::kTileRows * row;
+      const cudaStream_t st = static_cast<cudaStream_t>(stream);
+      cudaError_t e = cudaSuccess;
+      if (pitch < (1ull << 31)) {
+        e = cudaMemset2DAsync(to, pitch, 0, bytes, BHkv, st);
+      } else {  // (a pitch has 31 bits)
+        for (long long h = 0; h < BHkv && e == cudaSuccess; ++h) e = cudaMemsetAsync(to + h * pitch, 0, bytes, st);
+      }
+      if (e != cudaSuccess) return cuda_fail(e);
+    }
+  }
   cudaError_t e =
       eba::launch_bwd_window(tq, tk, tv, tdo, tdqa, a, w, d, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);

@@ -156,10 +156,7 @@ struct BwdSmem {
 struct BwdItem {
   int kvh, qh0, ktile, nq1, nq, kbeg, kend, qbeg;
   size_t vbase;  // -lse2 / D offset of query head qh0's first tile
-  // windowed: which part of its key tile's gradients this item leaves (-1: they are whole);
-  // no query sees the keys (the one tile is walked for its zeros)
-  int part;
-  bool blind;
+  int part;  // windowed: which part of its key tile's gradients this item leaves (-1: they are whole)
 };
 
 __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, const NoVarlen&, int w) {
@@ -240,7 +237,7 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, const WindowTiles&
     piece = x - it.ktile * wt.pieces;
   } else {
     w -= heads * cut;
-    const int rest = a.n_ktiles - wt.cut_tiles;
+    const int rest = a.n_ktiles - wt.cut_tiles - wt.blind_tiles;
     int t;
     if (wt.by_cost) {
       it.kvh = w % heads;
@@ -251,6 +248,7 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, const WindowTiles&
       t = w - it.kvh * rest;
     }
     it.ktile = wt.cut_tiles + t;
+    if (it.ktile >= wt.blind0) it.ktile += wt.blind_tiles;
   }
   it.qh0 = it.kvh * a.group;
   it.kbeg = 0;
@@ -258,15 +256,15 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, const WindowTiles&
   const int k0 = it.ktile * kBM, k1 = min(a.Lk, k0 + kBM);
   const int first = max(0, k0 - wt.right - wt.off);
   const int last = k0 < wt.sinks ? a.Lq - 1 : min(a.Lq - 1, k1 - 1 + wt.left - wt.off);
-  int t0 = first / kBN, t1 = last >= first ? last / kBN + 1 : 0;
+  int t0 = first / kBN, t1 = last / kBN + 1;
   it.part = -1;
   if (piece >= 0) {
-    t0 = max(t0, piece * wt.piece);
-    t1 = min(t1, (piece + 1) * wt.piece);
+    // (at least wt.piece of the run's tiles for each; the first ones take one more)
+    const int more = t1 - t0 - wt.pieces * wt.piece;
+    if (piece + 1 < wt.pieces) t1 = t0 + (piece + 1) * wt.piece + min(piece + 1, more);
+    t0 += piece * wt.piece + min(piece, more);
     it.part = (it.kvh * wt.cut_tiles + it.ktile) * wt.pieces + piece;
   }
-  it.blind = t1 <= t0;
-  if (it.blind) t0 = 0, t1 = 1;
   it.nq1 = t1 - t0;
   it.nq = a.group * it.nq1;
   it.qbeg = t0 * kBN;
@@ -368,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   else if constexpr (PACKED)
     n_items = (vt.n_seqs + vt.pack - 1) / vt.pack;
   else if constexpr (WINDOW)
-    n_items = args.B * H_kv * (args.n_ktiles + vt.cut_tiles * (vt.pieces - 1));
+    n_items = args.B * H_kv * (args.n_ktiles - vt.blind_tiles + vt.cut_tiles * (vt.pieces - 1));
   else
     n_items = args.B * H_kv * args.n_ktiles;
   // 128-row box (or 32-column fp32 box for the dQ reduce) whose first row is
@@ -989,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the former on; of this warpgroup's columns [lo, hi].
             const int p0 = qc.row(it) + 64 * wg + vt.off;
             lo = key - vt.right - p0;
-            hi = !key_ok || it.blind ? -1 : key < vt.sinks ? 63 : key + vt.left - p0;
+            hi = !key_ok ? -1 : key < vt.sinks ? 63 : key + vt.left - p0;
             all = __all_sync(0xffffffffu, lo <= 0 && hi >= 63);
             if (all) {
 #pragma unroll

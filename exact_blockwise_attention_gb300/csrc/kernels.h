@@ -173,12 +173,15 @@ __host__ __device__ constexpr int from_middle(int rank, int n) {
 // way round), 2 (the middle ones most), 0 (taken as equal). Items then run through the
 // heads, the largest first, so that the last ones on the SMs are small.
 // Backward: the first cut_tiles key tiles hold sinks, which all later queries see. Each
-// is cut in `pieces` of `piece` query tiles, which leave fp32 parts that a last kernel
-// adds up: else one such item is as long as the whole sequence and the others wait.
+// is cut in `pieces` of `piece` query tiles or one more, which leave fp32 parts that a last kernel
+// adds up: else one such item is as long as the whole sequence and the others wait. The
+// blind_tiles key tiles from blind0 on no query sees: they are no items, and their dK, dV are
+// set to zero beforehand.
 struct WindowTiles {
   int left, right, sinks, off;
   int by_cost;
   int cut_tiles, pieces, piece;
+  int blind0, blind_tiles;
   int run_tiles;  // query tiles of an ordinary backward item
 };
 

@@ -68,3 +68,39 @@ def test_hidden_values_do_not_reach_gradients(eba, d, H, Hkv, size):
         assert torch.equal(a[n][:, :, 2:200], b[n][:, :, 2:200]), n
     x, y = np64(a["dq"][:, :, :300]), np64(b["dq"][:, :, :300])
     assert np.isfinite(y).all() and np.linalg.norm(x - y) <= 2 * U / 16 * np.linalg.norm(x)
+
+
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (4, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_that_no_query_sees(eba, d, H, Hkv):
+    """Key tiles without a visible pair: NaN there reaches nothing, and their gradients are 0
+    whatever the queries are."""
+    q, k, v, do = inputs(11, 1, H, Hkv, 300, 1200, d)  # places 900 to 1199: tiles from 896 on
+    a = run(eba, q, k, v, do, 3, 0, 0)
+    k[:, :, :896], v[:, :, :896] = math.nan, math.nan
+    b = run(eba, q, k, v, do, 3, 0, 0)
+    for n in ("o", "lse", "dk", "dv"):
+        assert torch.equal(a[n], b[n]), n
+    assert (b["dk"][:, :, :896] == 0).all() and (b["dv"][:, :, :896] == 0).all()
+    x, y = np64(a["dq"]), np64(b["dq"])
+    assert np.isfinite(y).all() and np.linalg.norm(x - y) <= 2 * U / 16 * np.linalg.norm(x)
+    q[:, :, 5], do[:, :, 5] = math.nan, math.nan
+    c = run(eba, q, k, v, do, 3, 0, 0)
+    assert (c["dk"][:, :, :896] == 0).all() and (c["dv"][:, :, :896] == 0).all()
+
+
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (4, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Lq,Lk,nan", [(700, 100, 512), (2600, 300, 2176)])
+def test_queries_that_see_no_key(eba, Lq, Lk, nan, d, H, Hkv):
+    """Query tiles before the first key: NaN there reaches no gradient. (The second case: also
+    where the first tokens' gradients are cut in pieces.)"""
+    q, k, v, do = inputs(12, 1, H, Hkv, Lq, Lk, d)
+    a = run(eba, q, k, v, do, 64, 0, 4)
+    q[:, :, :nan], do[:, :, :nan] = math.nan, math.nan
+    b = run(eba, q, k, v, do, 64, 0, 4)
+    for n in ("o", "lse", "dk", "dv"):
+        assert torch.equal(a[n], b[n]), n
+    x, y = np64(a["dq"]), np64(b["dq"])
+    assert (y[:, :, :Lq - Lk] == 0).all()
+    assert np.isfinite(y).all() and np.linalg.norm(x - y) <= 2 * U / 16 * np.linalg.norm(x)
