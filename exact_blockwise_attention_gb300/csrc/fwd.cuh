@@ -244,6 +244,16 @@ __device__ __forceinline__ void store_rest(__nv_bfloat16* to, const uint32_t* x,
   }
 }
 
+// Zeros for a row of O, and of what rounding took from it, that has no weight.
+template <int D>
+__device__ __forceinline__ void zero_row(const FwdArgs& a, size_t off) {
+#pragma unroll 1
+  for (int i = 0; i < D; i += 8) {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + off + i) = make_uint4(0u, 0u, 0u, 0u);
+    if (a.rest) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.rest) + off + i) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 // First key row of round j.
 template <typename VT>
 __device__ __forceinline__ int key_row(const FwdItem& it, int j) {
@@ -704,6 +714,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
       }
       float* lse_p = args.lse + static_cast<size_t>(pchunk) * args.lse_chunk_stride;
       lse_p[porow] = (pm + lg2_approx(pls)) * kLn2;
+      if (WINDOW && plo == 0.f) zero_row<D>(args, po_off);  // (0 times a hidden NaN)
     };
     auto read_o = [&](uint32_t (&ov)[D]) {
 #pragma unroll
@@ -760,13 +771,11 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
                 static_cast<float*>(args.o) + static_cast<size_t>(it.chunk) * args.o_chunk_stride +
                 orow * D);
             for (int v = 0; v < D / 4; ++v) dst[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-          } else if (VARLEN || WINDOW) {
+          } else if (VARLEN) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.o) + o_off);
             for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
-            if (WINDOW && args.rest) {
-              dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.rest) + o_off);
-              for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
-            }
+          } else if (WINDOW) {
+            zero_row<D>(args, o_off);
           }
           lse_out[orow] = -INFINITY;
         }
@@ -1039,6 +1048,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::kThreads, 1)
         }
       }
       if (row_ok) lse_out[orow] = (m_used + lg2_approx(ls)) * kLn2;
+      if (WINDOW && row_ok && lo == 0.f) zero_row<D>(args, o_off);  // (0 times a hidden NaN)
       // The next item's first P_t V overwrites O_t only after this warpgroup
       // arrives on p_full again, i.e. after these loads.
       tc_fence_before();

@@ -104,3 +104,33 @@ def test_queries_that_see_no_key(eba, Lq, Lk, nan, d, H, Hkv):
     x, y = np64(a["dq"]), np64(b["dq"])
     assert (y[:, :, :Lq - Lk] == 0).all()
     assert np.isfinite(y).all() and np.linalg.norm(x - y) <= 2 * U / 16 * np.linalg.norm(x)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Lq,Lk", [(300, 172), (200, 100), (556, 300)])
+def test_rows_that_see_nothing_are_zero_beside_nan(eba, Lq, Lk, d):
+    """Rows without a key give O = 0 also where others of their tiles see a NaN value."""
+    q, k, v, do = inputs(13, 3, 4, 2, Lq, Lk, d)
+    v[:, :, 0] = math.nan
+    o, lse, rest = eba.fwd_window(*(x.cuda() for x in (q, k, v)), 20, 0, 0, rest=True)
+    blind = Lq - Lk
+    assert (o[:, :, :blind] == 0).all() and (rest[:, :, :blind] == 0).all()
+    assert torch.isneginf(lse[:, :, :blind]).all()
+    assert torch.isnan(o[:, :, blind:blind + 21]).all() and torch.isfinite(lse[:, :, blind:]).all()
+    got = run(eba, q, k, v, do, 20, 0, 0)
+    assert (got["dq"][:, :, :blind] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_that_is_seen_shows(eba, d):
+    """A NaN query or a NaN key makes the rows that see it NaN, o and lse."""
+    q, k, v, _ = inputs(14, 1, 2, 2, 400, 400, d)
+    q[:, 0, 30] = math.nan
+    k[:, 1, 50] = math.nan
+    o, lse, rest = eba.fwd_window(*(x.cuda() for x in (q, k, v)), 10, 0, 0, rest=True)
+    assert torch.isnan(o[:, 0, 30]).all() and torch.isnan(lse[:, 0, 30]).all()
+    assert torch.isnan(o[:, 1, 50:61]).all() and torch.isnan(lse[:, 1, 50:61]).all()
+    others = [i for i in range(400) if i != 30]
+    assert torch.isfinite(o[:, 0, others]).all() and torch.isfinite(lse[:, 0, others]).all()
+    rest_of = [i for i in range(400) if not 50 <= i <= 60]
+    assert torch.isfinite(o[:, 1, rest_of]).all() and torch.isfinite(lse[:, 1, rest_of]).all()
