@@ -126,6 +126,7 @@ __device__ __forceinline__ int check_pair(const PoolArgs& a, int i, int lane) {
   const int whole = len / a.pool.page_size;
   if (len % a.pool.page_size == 0) return kPairWhole;
   const int page = a.table[s * a.table_stride + whole];
+  if (page >= a.pool.n_pages && lane == 0) bad_page(a.status);
   return page >= 0 && page < a.pool.n_pages ? kPairCopies : kPairWhole;
 }
 

@@ -64,6 +64,7 @@ def fork(refs, table, size, lens, src, dst):
         whole = lens[src[i]] // size
         part = table[src[i], whole]
         if not 0 <= part < len(refs):
+            faults += part >= len(refs)
             continue
         page, free = _take(refs, free)
         table[dst[i], whole] = page

@@ -80,3 +80,23 @@ def test_reserve_at_the_end_of_the_widest_table(eba):
     eba.pages_reserve(pool, row, gpu([TOP - 4]), gpu([TOP]))
     same(row[0, -5:], [-1, 0, 2, 7, 3])
     same(refs, [1, 1, 1, 1, 1, 0, 0, 1])
+
+
+def test_fork_records_a_last_page_out_of_range(eba):
+    """A source whose last, partly filled page has no page's number: the fork lacks its last
+    tokens, and the status says so."""
+    s = Batch(eba, 4, 6, 16, 100, seed=5)
+    s.lens[:] = 20, 33, 16, 7
+    s.table[:], s.refs[:] = -1, 0
+    s.table[0, :2], s.table[1, :3], s.table[2, 0], s.table[3, 0] = (4, 100), (5, 6, 2**31 - 1), 7, 8
+    s.refs[4:9] = 1
+    s.glens.copy_(gpu(s.lens))
+    s.gtable.copy_(gpu(s.table))
+    s.grefs.copy_(gpu(s.refs))
+    for src, dst in ((0, 2), (1, 3)):
+        want = pages.fork(s.refs, s.table, 16, s.lens, np.array([src]), np.array([dst]))
+        got = eba.pages_fork(s.pool, s.gtable, s.glens, gpu([src]), gpu([dst]))
+        same(got[0], want[0])
+        same(got[1], want[1])
+        s.check()
+        assert want[2] == 1 and eba.poll_device_status() == PAGE_FAULT
