@@ -104,6 +104,11 @@ __device__ __forceinline__ bool wanted_range(const PoolArgs& a, int b, int& e0, 
   return true;
 }
 
+// Whether a table's entry holds no page.
+__device__ __forceinline__ bool wants_page(const PoolArgs& a, int entry) {
+  return static_cast<unsigned>(entry) >= static_cast<unsigned>(a.pool.n_pages);
+}
+
 // What a fork's pair asks for, kept in a.to between the cluster's barriers.
 enum : int { kPairBad = -3, kPairWhole = -2, kPairCopies = -1 };
 
@@ -190,7 +195,10 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(32 * kPoolWa
       int e0, e1;
       if (!wanted_range(a, b, e0, e1)) continue;
       const int* row = a.table + b * a.table_stride;
-      for (long long e = static_cast<long long>(e0) + lane; e < e1; e += 32) want += row[e] < 0;
+      for (long long e = static_cast<long long>(e0) + lane; e < e1; e += 32) {
+        want += wants_page(a, row[e]);
+        if (row[e] >= a.pool.n_pages) bad_page(a.status);
+      }
     }
     want = warp_sum(want);
   }
@@ -280,7 +288,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(32 * kPoolWa
       if (!wanted_range(a, b, e0, e1)) continue;
       int* row = a.table + b * a.table_stride;
       for (long long e = e0; e < e1; e += 32) {
-        const bool mine = e + lane < e1 && row[e + lane] < 0;
+        const bool mine = e + lane < e1 && wants_page(a, row[e + lane]);
         const uint32_t wants = __ballot_sync(0xffffffffu, mine);
         if (mine) row[e + lane] = take(before_want + __popc(wants & ((1u << lane) - 1u)));
         before_want += __popc(wants);

@@ -549,8 +549,9 @@ int attn_pages_fork(const attn_pool_t* pool, int* page_table, long long table_st
 /*
  * attn_pages_reserve - room for each sequence to grow from seq_lens[b] to
  * new_lens[b] keys: those of its entries behind its last key's that hold no page
- * get a free one. Where none is left the entry stays -1 and ATTN_ERR_PAGE is
- * recorded. A sequence whose lengths are out of range gets none and is recorded.
+ * (also by a number of n_pages or more, which is recorded) get a free one. Where none
+ * is left the entry is -1 and ATTN_ERR_PAGE recorded. A sequence with seq_lens[b] below
+ * 0, or either length beyond its row, gets none and is recorded.
  */
 int attn_pages_reserve(const attn_pool_t* pool, int* page_table, long long table_stride,
                        int max_pages, const int* seq_lens, const int* new_lens, int n_seqs,

@@ -83,7 +83,8 @@ def reserve(refs, table, size, lens, new_lens) -> int:
             faults += 1
             continue
         for e in range(-(-lens[b] // size), -(-new_lens[b] // size)):
-            if table[b, e] < 0:
+            if not 0 <= table[b, e] < len(refs):
+                faults += table[b, e] >= len(refs)
                 table[b, e], free = _take(refs, free)
                 faults += table[b, e] < 0
     return faults

@@ -100,3 +100,21 @@ def test_fork_records_a_last_page_out_of_range(eba):
         same(got[1], want[1])
         s.check()
         assert want[2] == 1 and eba.poll_device_status() == PAGE_FAULT
+
+
+def test_reserve_replaces_pages_out_of_range(eba):
+    """An entry with no page's number holds none: it gets one, and the status says so."""
+    s = Batch(eba, 3, 6, 4, 40, seed=6)
+    s.lens[:] = 5, 0, 3
+    s.table[:], s.refs[:] = -1, 0
+    s.table[0, :4], s.table[2, 0] = (0, 1, 40, 2), 3
+    s.refs[:4] = 1
+    s.glens.copy_(gpu(s.lens))
+    s.gtable.copy_(gpu(s.table))
+    s.grefs.copy_(gpu(s.refs))
+    more = np.array([20, 3, 3])
+    assert pages.reserve(s.refs, s.table, 4, s.lens, more) == 1
+    eba.pages_reserve(s.pool, s.gtable, s.glens, gpu(more))
+    s.check()
+    assert eba.poll_device_status() == PAGE_FAULT
+    assert (s.table[0, :5] == [0, 1, 4, 2, 5]).all() and s.table[1, 0] == 6
