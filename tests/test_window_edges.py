@@ -1,0 +1,23 @@
+"""Windowed attention's host side without a GPU: what a training step keeps, and the bytes of
+the backward's workspace."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def eba():
+    from exact_blockwise_attention_gb300 import _build
+
+    _build.build()
+    import exact_blockwise_attention_gb300 as m
+
+    return m
+
+
+@pytest.mark.parametrize("Lk,left,right,sinks,few", [
+    (9000, 511, 0, 0, True), (9000, 512, 0, 0, False), (9000, 255, 256, 0, True), (9000, 256, 256, 0, False),
+    (9000, 96, 0, 415, True), (9000, 96, 0, 416, False), (9000, 100, 0, 4000, False), (9000, 0, 0, 511, True),
+    (512, -1, -1, 0, True), (513, -1, 0, 0, False), (400, -1, 0, 4000, True), (513, 0, -1, 0, False),
+    (300, 2**31 - 1, 2**31 - 1, 2**31 - 1, True)])
+def test_few_keys_counts_the_sinks(eba, Lk, left, right, sinks, few):
+    """What rounding took from o is kept where no row sees more than 512 keys."""
+    assert eba._few_keys(Lk, left, right, sinks) == few
