@@ -665,8 +665,12 @@ bool window_tiles(int Lq, int Lk, int left, int right, int sinks, long long head
   w->blind_tiles = std::max(0, std::max(0, w->off - w->left) / R - sink_tiles);
   if (!left_end || w->sinks == 0) return true;
   // Pieces as long as an ordinary item, at least 8 query tiles (each leaves 2 x 128 x d
-  // floats). Many sinks' key tiles keep all SMs busy by themselves and stay whole.
-  if (sink_tiles * heads > 4 * 152) {
+  // floats), and no more of them than give each of 152 SMs four: they leave at most 160 MB
+  // (8 heads of 128, 131072 tokens, 4096 sinks: 0.1 GB; pieces of 8 tiles left 4.3 and took
+  // 8.76 ms, not 7.40; 64 sinks 1.74 ms both ways). Many sinks' key tiles keep all SMs busy
+  // by themselves and stay whole.
+  const long long whole = sink_tiles * heads;
+  if (whole > 4 * 152) {
     w->by_cost = 1;
     return true;
   }
@@ -674,6 +678,7 @@ bool window_tiles(int Lq, int Lk, int left, int right, int sinks, long long head
   // (no more of them than query tiles that see any of the last sinks)
   const int seen = n_qtiles - std::max(0, (sink_tiles - 1) * R - w->right - w->off) / R;
   w->pieces = std::min((n_qtiles + most - 1) / most, seen);
+  w->pieces = static_cast<int>(std::min<long long>(w->pieces, (4 * 152 + whole - 1) / whole));
   w->piece = seen / w->pieces;
   if (w->pieces > 1) w->cut_tiles = sink_tiles; else w->pieces = w->piece = 0;
   return true;

@@ -242,7 +242,8 @@ int attn_merge(const float* o_parts, const float* lse_parts, int n_chunks, void*
  *   o_rest: bf16, of O's shape, or NULL: what rounding took from O, for the backward. Where
  *   rows see few keys their gradients are more exact with it (dQ, dK of windows of 2 keys:
  *   2^-8.7 instead of 2^-8 off, as a whole); with many keys it makes no difference.
- *   workspace: attn_bwd_window_workspace_size(...) bytes. dQ is accumulated with atomic
+ *   workspace: attn_bwd_window_workspace_size(...) bytes, attn_bwd's and up to 160 MB for
+ *   parts of the first tokens' gradients. dQ is accumulated with atomic
  *   adds as in attn_bwd (its low bits may vary from run to run; dK, dV do not).
  */
 int attn_fwd_window(const void* q, const void* k, const void* v, void* o, void* o_rest, float* lse,

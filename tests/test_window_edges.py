@@ -21,3 +21,16 @@ def eba():
 def test_few_keys_counts_the_sinks(eba, Lk, left, right, sinks, few):
     """What rounding took from o is kept where no row sees more than 512 keys."""
     assert eba._few_keys(Lk, left, right, sinks) == few
+
+
+@pytest.mark.parametrize("H,Hkv,L,left,sinks", [
+    (8, 8, 131072, 511, 64), (8, 8, 131072, 511, 4096), (8, 8, 131072, 511, 9000), (1, 1, 1 << 20, 100, 60000),
+    (1, 1, 1 << 20, 100, 77000), (600, 600, 60000, 100, 1), (304, 304, 60000, 100, 200), (64, 1, 1 << 22, 20, 4),
+    (1, 1, 1 << 22, 20, 70000)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_parts_are_bounded(eba, H, Hkv, L, left, sinks, d):
+    """The parts of the first tokens' gradients: at most 1216, dK and dV of 128 keys each, in
+    fp32."""
+    more = eba.bwd_window_workspace_size(1, H, Hkv, L, L, d, left, 0, sinks) - eba.bwd_workspace_size(1, H, L, L, d)
+    assert 0 <= more <= 2 * 4 * 152 * 2 * 128 * d * 4
+    assert more <= 160 * 10 ** 6
