@@ -134,3 +134,23 @@ def test_nan_that_is_seen_shows(eba, d):
     assert torch.isfinite(o[:, 0, others]).all() and torch.isfinite(lse[:, 0, others]).all()
     rest_of = [i for i in range(400) if not 50 <= i <= 60]
     assert torch.isfinite(o[:, 1, rest_of]).all() and torch.isfinite(lse[:, 1, rest_of]).all()
+
+
+@pytest.mark.parametrize("H,Hkv,sinks", [(160, 160, 4), (320, 160, 4), (80, 80, 200)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_sinks_of_many_heads_stay_whole(eba, d, H, Hkv, sinks):
+    """More than 608 key tiles of sinks together are no longer cut in pieces, as those of a batch
+    alone are: both against the oracle, for some heads of each batch."""
+    L, left = 1200, 60
+    q, k, v, do = inputs(15, 4, H, Hkv, L, L, d)
+    plain = [eba.bwd_workspace_size(B, H, L, L, d) for B in (1, 4)]
+    need = [eba.bwd_window_workspace_size(B, H, Hkv, L, L, d, left, 0, sinks) for B in (1, 4)]
+    assert need[0] > plain[0] and need[1] == plain[1]
+    together = run(eba, q, k, v, do, left, 0, sinks)
+    alone = run(eba, *(x[2:3] for x in (q, k, v, do)), left, 0, sinks)
+    for b, g in ((0, 0), (2, Hkv // 2), (3, Hkv - 1)):
+        heads = slice(g * H // Hkv, (g + 1) * H // Hkv)
+        want = exact_and_bounds(q[b:b + 1, heads], k[b:b + 1, g:g + 1], v[b:b + 1, g:g + 1], do[b:b + 1, heads], left, 0,
+                                sinks, 1 / math.sqrt(d))
+        for got, at in ((together, b), (alone, 0)) if b == 2 else ((together, b),):
+            compare({n: x[at:at + 1, g:g + 1] if n in ("dk", "dv") else x[at:at + 1, heads] for n, x in got.items()}, want)
