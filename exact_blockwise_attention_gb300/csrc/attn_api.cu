@@ -658,7 +658,9 @@ bool window_tiles(int Lq, int Lk, int left, int right, int sinks, long long head
     w->by_cost = w->right <= w->left / 2 ? 1 : w->left <= w->right / 2 ? -1 : 2;
   constexpr int R = eba::kTileRows;
   const int n_qtiles = (Lq + R - 1) / R;
-  w->run_tiles = left_end && right_end ? std::min(n_qtiles, (w->left + w->right + R - 1) / R + 2) : n_qtiles;
+  const long long both = static_cast<long long>(w->left) + w->right;
+  w->run_tiles = n_qtiles;
+  if (left_end && right_end) w->run_tiles = static_cast<int>(std::min<long long>(n_qtiles, (both + R - 1) / R + 2));
   // Key tiles behind the sinks and wholly before the first query's window.
   const int sink_tiles = (w->sinks + R - 1) / R;
   w->blind0 = sink_tiles;

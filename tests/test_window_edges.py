@@ -34,3 +34,13 @@ def test_parts_are_bounded(eba, H, Hkv, L, left, sinks, d):
     more = eba.bwd_window_workspace_size(1, H, Hkv, L, L, d, left, 0, sinks) - eba.bwd_workspace_size(1, H, L, L, d)
     assert 0 <= more <= 2 * 4 * 152 * 2 * 128 * d * 4
     assert more <= 160 * 10 ** 6
+
+
+def test_window_as_wide_as_the_longest_sequences(eba):
+    """Both sides together pass an int: every tile of queries sees every tile of keys, and
+    nothing is cut."""
+    L = 1 << 29
+    plain = eba.bwd_workspace_size(1, 1, L, L, 64)
+    assert plain > 0
+    for side in (L - 1, L, 2 * L - 2, 2 * L - 1):
+        assert eba.bwd_window_workspace_size(1, 1, 1, L, L, 64, side, side, 5) == plain
