@@ -559,8 +559,9 @@ def fwd_window(q, k, v, left, right=0, sinks=0, scale=None, rest=False):
 
     Query i stands at the place p = i + Lk - Lq, the last query at the last key, and
     sees the keys p - left to p + right and, up to p + right, the first ``sinks``. left
-    or right None: no end to that side (left=None is plain causal attention). A query
-    that sees no key gives o = 0 and lse = -inf. k, v may have H_kv < H heads.
+    or right None: no end to that side (left=None is plain causal attention). ``decode``'s
+    and ``decode_tree``'s window of W keys is left = W - 1. A query that sees no key gives
+    o = 0 and lse = -inf. k, v may have H_kv < H heads.
 
     With ``rest`` a third tensor, of o's shape and type: what rounding took from o, for
     bwd_window."""
@@ -1053,8 +1054,8 @@ def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None
     seq_lens - 1. page_table and seq_lens as for cache_append; the GPU reads
     them, so a captured call follows their contents.
 
-    With a ``window`` the token sees the last that many of its sequence's keys and
-    the first ``sinks``; pages that hold none of these need not be there. Without one
+    With a ``window`` the token sees the last that many of its sequence's keys (its own
+    among them: fwd_window's left is one less) and the first ``sinks``; pages that hold none of these need not be there. Without one
     ``sinks`` is of no effect: all keys are seen."""
     try:
         key = (_form(q), _form(page_table), _form(seq_lens), _form(positions), cache._key, window, sinks,
@@ -1141,8 +1142,10 @@ def decode_tree(cache, q, page_table, seq_lens, cu_q=None, mask=None, window=Non
     With a ``window`` a token at place p sees of the keys before the drafts (without a
     mask: of all) those after p - window and the first ``sinks``; its place is that
     of the drafts' first key plus its place in the chain, or plus the number of its
-    mask's bits less one. Pages between the sinks and the window of a token at the
-    drafts' first key need not be there. Without a window ``sinks`` is of no effect.
+    mask's bits less one. (The window cuts nothing off a mask: leave out the bits of
+    ancestors ``window`` or more places back for what ``decode`` would see.) Pages
+    between the sinks and the window of a token at the drafts' first key need not be
+    there. Without a window ``sinks`` is of no effect.
     q is taken as it is: rotate it with rope_fwd, the new keys in cache_append.
 
     A token that sees nothing, or whose sequence has length 0, gives o = 0 and

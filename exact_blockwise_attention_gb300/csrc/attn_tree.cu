@@ -37,11 +37,13 @@
 // Measured (one GB300; bytes of the caches at the time of the call): 32 sequences of up to
 // 8191 keys, 32 drafts, 8 heads of 128 for 32: 131 us, 5.3 TB/s, 79 % of a copy; 8 of up
 // to 131071 e4m3 keys, 12 drafts, 4 heads of 128 for 32: 180 us, 3.4 TB/s; 16 of up to 6007
-// keys, 24 drafts, 16 heads of 64: 76 us, 3.7 TB/s. A tile takes 2000 cycles of the softmax
-// (scores and maximum 720, exponentials 885, vote and waits the rest) however short its
-// rows, a producer 1750: these bound rows of 128 bytes (more slots, two producers for each
-// operand, or copies of few rows that share a tile's keys among more warps: no gain); rows
-// of 256 bytes: HBM, unequal SMs at the end, the join.
+// keys, 24 drafts, 16 heads of 64: 76 us, 3.7 TB/s. Rows of 256 bytes: HBM, unequal SMs at the
+// end, the join. Rows of 128 bytes: a tile takes about 2400 cycles (bf16) and 3000 (e4m3) for
+// 1540 of HBM's share. No role's own work is that long (the softmax 2000 of scores, maximum,
+// exponentials, vote and waits, however few its rows; a producer 1750; widening 960): the roles
+// wait on one another through rings of two and three tiles. Changing one alone gained nothing
+// (more slots, two producers for each operand, copies of few rows that share a tile's keys
+// among more warps).
 // Tensor memory: S_0 [0,128) S_1 [128,256) O [256,256+d) P_0 [384,448) P_1 [448,512).
 #include <cuda_fp16.h>
 

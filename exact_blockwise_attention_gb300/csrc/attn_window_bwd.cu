@@ -1,9 +1,9 @@
 // Launch of the backward kernels within a sliding window (see bwd.cuh, WindowTiles): as the
 // dense ones without the tiles that hold no visible pair, and with the first tokens' key
 // tiles, which all later queries see, cut in pieces. 12544 tokens, 1568 keys each, 16 heads on
-// 4 of 128: 592 us, 644 TFLOP/s of visible pairs (dense: 917; 368 whole items on 152 SMs
-// take three rounds of 2.4); 2 x 6273 tokens, 784 keys to both sides, 16 heads of 64: 348 us,
-// 543 TFLOP/s.
+// 4 of 128: 577 us, 661 TFLOP/s of visible pairs (dense: 917; 388 whole items and 28 pieces on
+// 152 SMs take three rounds of 2.4); 2 x 6273 tokens, 784 keys to both sides, 16 heads of 64:
+// 357 us, 529 TFLOP/s.
 #include "bwd.cuh"
 
 namespace eba {

@@ -1058,9 +1058,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A hidden pair's dS is 0 whatever dP and D are. Its P is, so that only a dP or D that is
         // no finite number asks for more than the product above: an exponent of ones, here in
         // the OR of the row's (also where values of 2 and more meet others). hide_row is a
-        // function of its own: 2 x 6273 tokens, 784 keys to both sides, 16 heads of 64 take 510 us
-        // forward and backward, 501 without this, 522 with its code in line, and 554 or, in
-        // registers, 624 with dS masked in every tile that hides a pair.
+        // function of its own: 2 x 6273 tokens, 784 keys to both sides, 16 heads of 64 take 508 us
+        // forward and backward, 495 without this, 522 with its code in line, and 554 or, in
+        // registers, 624 with dS masked in every tile that hides a pair: what counts is the size
+        // of the kernel's code, 66 to 70 KB (two 64-bit divisions in bwd_item: 77 KB, 556 us).
         uint32_t any = 0u;
         if (WINDOW && !all) {
 #pragma unroll

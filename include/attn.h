@@ -233,8 +233,10 @@ int attn_merge(const float* o_parts, const float* lse_parts, int n_chunks, void*
  * the place p = i + Lk - Lq (the last query at the last key) and sees key j if
  *   j <= p + right  and  (j >= p - left  or  j < sinks).
  * left, right >= 0, or -1: no end to that side (right = 0: causal; left = -1, right = 0:
- * plain causal attention); sinks >= 0. Lq, Lk <= 2^29. A query that sees no key (its
- * place lies before the first one) gives O = 0, lse = -inf and zero gradients; a key
+ * plain causal attention); sinks >= 0. A causal row sees left + 1 keys: what
+ * attn_decode_window and attn_decode_tree call a window of W keys is left = W - 1.
+ * Lq, Lk <= 2^29. A query that sees no key (its place lies before the first one), or only
+ * scores of -inf, gives O = 0, lse = -inf and zero gradients; a key
  * that no query sees gets zero dK, dV. Tiles of 128 x 128 pairs without a visible one
  * are neither read nor computed; within the others a masked weight is exactly 0, which
  * keeps out every finite value (a NaN or infinite element of q, k, v or dO may reach
@@ -476,10 +478,13 @@ int attn_decode_window(const attn_cache_t* cache, const void* q, const long long
  *     drafted key c + x if bit x % 64 of its word x / 64 is set (bits of n and above do
  *     not count; a token usually has its ancestors' bits and its own). Its place is
  *     p = c - 1 + the number of its bits (of none: c), and of the keys before c it sees
- *     all, or with a window those after p - window and the first `sinks`. mask_words <=
- *     ATTN_MAX_MASK_WORDS.
- *   window 0: none, and sinks is of no effect. With one, pages that lie wholly between the sinks and the window of
- *   a sequence's first token (at the place c) are not looked up.
+ *     all, or with a window those after p - window and the first `sinks`. The window cuts
+ *     nothing off the mask. For what attn_decode_window would see, leave out of a path
+ *     longer than the window the bits of the ancestors `window` or more places back: the
+ *     token then sees the last `window` of its path and, of the keys before c, the sinks.
+ *     mask_words <= ATTN_MAX_MASK_WORDS.
+ *   window 0: none, and sinks is of no effect. With one, pages that lie wholly between the
+ *   sinks and the window of a sequence's first token (at the place c) are not looked up.
  *   o [T, H, d] bf16, lse [T, H] fp32. A token that sees no key gives O = 0, lse = -inf,
  *   and so do the tokens of a sequence of length 0 (an empty slot). Rows outside
  *   [cu_q[0], cu_q[B]) are left as they were. Lengths and offsets out of range count as the
