@@ -1055,8 +1055,9 @@ def decode(cache, q, page_table, seq_lens, scale=None, rope=None, positions=None
     them, so a captured call follows their contents.
 
     With a ``window`` the token sees the last that many of its sequence's keys (its own
-    among them: fwd_window's left is one less) and the first ``sinks``; pages that hold none of these need not be there. Without one
-    ``sinks`` is of no effect: all keys are seen."""
+    among them: fwd_window's left is one less) and the first ``sinks``; pages that hold
+    none of these need not be there. Without one ``sinks`` is of no effect: all keys are
+    seen."""
     try:
         key = (_form(q), _form(page_table), _form(seq_lens), _form(positions), cache._key, window, sinks,
                type(window), type(sinks),
@@ -1149,7 +1150,7 @@ def decode_tree(cache, q, page_table, seq_lens, cu_q=None, mask=None, window=Non
     q is taken as it is: rotate it with rope_fwd, the new keys in cache_append.
 
     A token that sees nothing, or whose sequence has length 0, gives o = 0 and
-    lse = -inf, and so do all where offsets fall; rows of no sequence are not written. The GPU reads lengths, offsets,
+    lse = -inf; rows of no sequence are not written. The GPU reads lengths, offsets,
     masks and tables, so a captured call follows their contents."""
     try:
         key = (_form(q), _form(page_table), _form(seq_lens), _form(cu_q), _form(mask), cache._key, window,

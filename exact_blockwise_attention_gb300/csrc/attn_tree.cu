@@ -365,10 +365,23 @@ __global__ void __launch_bounds__(kBlock, 1)
     mine.x += head_tiles(a, s) * a.cache.H_kv;
     mine.y += s.items * a.cache.H_kv;
   }
-  // Where offsets fall, rows may belong to many sequences, and the sums below need not fit an
-  // int: such a call computes nothing.
-  falls = __syncthreads_or(falls);
-  if (falls) mine = make_int2(0, 0);
+  // Where offsets fall, rows may belong to many sequences, and the list need not fit an int, as
+  // it does with the host's checks otherwise: a list that does not is not walked.
+  bool too_long = false;
+  if (__builtin_expect(__syncthreads_or(falls), 0)) {
+    unsigned long long* all = reinterpret_cast<unsigned long long*>(smem + L::offFirst);
+    if (tid == 0) *all = 0;
+    __syncthreads();
+    unsigned long long sum = 0;
+    for (int b = b0; b < b_end; ++b) {
+      const Seq s = sequence(a, b);
+      sum += static_cast<unsigned long long>(head_tiles(a, s) + kTreeEnd * s.items) * a.cache.H_kv;
+    }
+    atomicAdd(all, sum);
+    __syncthreads();
+    too_long = *all > 0x7fffffffull;
+    if (too_long) mine = make_int2(0, 0);
+  }
   int2 incl = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -428,14 +441,14 @@ __global__ void __launch_bounds__(kBlock, 1)
       }
     }
   }
-  // Sequences without keys, and all rows where offsets fall: O = 0, lse = -inf.
+  // Sequences without keys, and all rows of a list that is too long: O = 0, lse = -inf.
   auto blank = [&](long long token0, long long tokens, int first, int step) {
     const long long row0 = token0 * a.H, rows = tokens * a.H;
     for (long long x = first; x < rows * (D / 8); x += step)
       *reinterpret_cast<uint4*>(a.o + row0 * D + x * 8) = make_uint4(0, 0, 0, 0);
     for (long long x = first; x < rows; x += step) a.lse[row0 + x] = -INFINITY;
   };
-  if (falls) {
+  if (too_long) {
     blank(0, a.T, cta * kBlock + tid, gridDim.x * kBlock);
   } else {
     for (int b = cta; b < a.B; b += gridDim.x) {

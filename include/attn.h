@@ -489,12 +489,13 @@ int attn_decode_window(const attn_cache_t* cache, const void* q, const long long
  *   and so do the tokens of a sequence of length 0 (an empty slot). Rows outside
  *   [cu_q[0], cu_q[B]) are left as they were. Lengths and offsets out of range count as the
  *   nearest in range, a length below the number of its tokens as 0, and both are recorded
- *   as ATTN_ERR_PAGE. So are offsets that fall (cu_q[b + 1] < cu_q[b] for any b): then all T
- *   tokens give O = 0, lse = -inf.
+ *   as ATTN_ERR_PAGE. So are offsets that fall: a row then belongs to any of the sequences
+ *   that name it, and where these together have too much to do (2^31 tiles of 128 keys and 128
+ *   rows) all T tokens give O = 0, lse = -inf.
  *   workspace: attn_decode_tree_workspace_size(...) bytes, as for attn_decode.
- * Deterministic as attn_decode. Weights enter the products as bf16, as in attn_fwd (e4m3
- * caches: as fp16, to 2^-12), in attn_decode as two bf16 terms: O is 0.0023 off as a whole,
- * attn_decode's 0.0017; their sums are fp32. A NaN or a score of +inf that a token sees makes
+ * Deterministic as attn_decode. Weights enter the products as bf16, as in attn_fwd, where
+ * attn_decode has two bf16 terms: O is 0.0023 off as a whole, attn_decode's 0.0017 (e4m3
+ * caches: as fp16, to 2^-12). Their sums are fp32. A NaN or a score of +inf that a token sees makes
  * its row NaN. A NaN or infinite element of v may reach other tokens of its sequence that do
  * not see it (a drafted token's, or of a key that a window hides from some of them); of k, none.
  */
