@@ -154,3 +154,31 @@ def test_sinks_of_many_heads_stay_whole(eba, d, H, Hkv, sinks):
                                 sinks, 1 / math.sqrt(d))
         for got, at in ((together, b), (alone, 0)) if b == 2 else ((together, b),):
             compare({n: x[at:at + 1, g:g + 1] if n in ("dk", "dv") else x[at:at + 1, heads] for n, x in got.items()}, want)
+
+
+def test_captured_step_with_unseen_keys(eba):
+    """The zeros of keys that no query sees are part of a captured call."""
+    q, k, v, do = (x.cuda() for x in inputs(16, 2, 4, 2, 300, 1200, 128))
+    args = [x.clone().requires_grad_(True) for x in (q, k, v)]
+
+    def step():
+        o = eba.attention_window(*args, 60, 0, 4)
+        return (o, *torch.autograd.grad(o, args, do))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(3):
+        for x in out[2:]:
+            x.detach().fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run(eba, *(x.cpu() for x in (q, k, v, do)), 60, 0, 4)
+        assert torch.equal(out[0], want["o"]) and torch.equal(out[2], want["dk"]) and torch.equal(out[3], want["dv"])
+        assert (out[2][:, :, 128:768] == 0).all()
