@@ -1060,8 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the OR of the row's (also where values of 2 and more meet others). hide_row is a
         // function of its own: 2 x 6273 tokens, 784 keys to both sides, 16 heads of 64 take 508 us
         // forward and backward, 495 without this, 522 with its code in line, and 554 or, in
-        // registers, 624 with dS masked in every tile that hides a pair: what counts is the size
-        // of the kernel's code, 66 to 70 KB (two 64-bit divisions in bwd_item: 77 KB, 556 us).
+        // registers, 624 with dS masked in every tile that hides a pair.
         uint32_t any = 0u;
         if (WINDOW && !all) {
 #pragma unroll
