@@ -243,6 +243,22 @@ __device__ __forceinline__ int run_of(int u, int units, int ctas) {
   return i;
 }
 
+// Whether the list has more units than an int can count; each thread sums up sequences
+// [b0, b1). `all` is shared memory. (In line, where it is hardly ever called, its code cost
+// the rows of 64 elements below 1 us of 81.)
+__device__ __noinline__ bool list_too_long(const TreeArgs& a, unsigned long long* all, int b0, int b1) {
+  if (threadIdx.x == 0) *all = 0;
+  __syncthreads();
+  unsigned long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = sequence(a, b);
+    sum += static_cast<unsigned long long>(head_tiles(a, s) + kTreeEnd * s.items) * a.cache.H_kv;
+  }
+  atomicAdd(all, sum);
+  __syncthreads();
+  return *all > 0x7fffffffull;
+}
+
 // ---- masks -------------------------------------------------------------------------------
 
 // Bits [lo, hi) of a 32-bit word.
@@ -367,21 +383,11 @@ __global__ void __launch_bounds__(kBlock, 1)
   }
   // Where offsets fall, rows may belong to many sequences, and the list need not fit an int, as
   // it does with the host's checks otherwise: a list that does not is not walked.
-  bool too_long = false;
-  if (__builtin_expect(__syncthreads_or(falls), 0)) {
-    unsigned long long* all = reinterpret_cast<unsigned long long*>(smem + L::offFirst);
-    if (tid == 0) *all = 0;
-    __syncthreads();
-    unsigned long long sum = 0;
-    for (int b = b0; b < b_end; ++b) {
-      const Seq s = sequence(a, b);
-      sum += static_cast<unsigned long long>(head_tiles(a, s) + kTreeEnd * s.items) * a.cache.H_kv;
-    }
-    atomicAdd(all, sum);
-    __syncthreads();
-    too_long = *all > 0x7fffffffull;
-    if (too_long) mine = make_int2(0, 0);
-  }
+  // Where offsets fall, rows may belong to many sequences, and the list need not fit an int, as
+  // it does with the host's checks otherwise: a list that does not is not walked.
+  const bool too_long = __syncthreads_or(falls) &&
+                        list_too_long(a, reinterpret_cast<unsigned long long*>(smem + L::offFirst), b0, b_end);
+  if (too_long) mine = make_int2(0, 0);
   int2 incl = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
