@@ -984,6 +984,9 @@ int attn_bwd_window(const void* q, const void* k, const void* v, const void* o,
   a.n_ktiles = (Lk + eba::kTileRows - 1) / eba::kTileRows;
   a.Lq_pad = a.n_qtiles * eba::kTileRows;
   a.scale = scale;
+  // Where no row sees more than one key, its weight is 1 whatever the score: dQ = dK = 0, not
+  // scale times what rounding leaves of dP - D.
+  if (Lk == 1 || (w.left == 0 && w.sinks == 0 && (w.right == 0 || Lq == 1))) a.scale = 0.f;
   a.scale_log2 = scale * kLog2e;
   a.o = o;
   a.rest = o_rest;

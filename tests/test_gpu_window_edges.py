@@ -182,3 +182,17 @@ def test_captured_step_with_unseen_keys(eba):
         want = run(eba, *(x.cpu() for x in (q, k, v, do)), 60, 0, 4)
         assert torch.equal(out[0], want["o"]) and torch.equal(out[2], want["dk"]) and torch.equal(out[3], want["dv"])
         assert (out[2][:, :, 128:768] == 0).all()
+
+
+@pytest.mark.parametrize("Lq,Lk,left,right,sinks", [(1, 1, None, 0, 1), (1, 1, 1, 0, 0), (300, 1, 10, 0, 0), (300, 1, None, 400, 5),
+                                                    (1, 700, 0, 0, 0), (1, 700, 0, 5, 0), (500, 500, 0, 0, 0), (260, 900, 0, 0, 0),
+                                                    (900, 260, 0, 0, 0)])
+@pytest.mark.parametrize("H,Hkv,d", [(4, 4, 64), (10, 2, 128)])
+def test_one_key_a_row_has_no_gradient_but_its_values(eba, Lq, Lk, left, right, sinks, H, Hkv, d):
+    """A softmax of one score is 1: dQ and dK are 0, not what rounding leaves."""
+    q, k, v, do = inputs(Lq + Lk, 2, H, Hkv, Lq, Lk, d)
+    got = run(eba, q, k, v, do, left, right, sinks)
+    assert (got["dq"] == 0).all() and (got["dk"] == 0).all()
+    want = exact_and_bounds(q, k, v, do, left, right, sinks, 1 / math.sqrt(d))
+    assert np.abs(want["dq"][0]).max() < 1e-12
+    compare({n: got[n] for n in ("o", "lse", "dv")}, want)
