@@ -29,8 +29,9 @@
 //    so 131; the rows of 64 elements 112 and 94 us.)
 //  - P in columns of its own, bf16 as in the forward pass (fwd.cuh; the row's largest
 //    weight's rounding is added to the sum), or with an e4m3 cache fp16 (and q scaled per
-//    row by a power of two into fp16's range). O is 2^-8.8 off as a whole (2^-9.2 is its own
-//    rounding). P as two bf16 terms, in one buffer: 2^-9.2, the bf16 batch below 163 us.
+//    row by a power of two into fp16's range). O is 2^-8.8 off as a whole, of the single-token
+//    decode, whose P is two bf16 terms, 2^-9.2. Two terms here, in one buffer: the bf16 batch
+//    below 163 us.
 //  - The QK and the PV products are issued by threads of two warps (see fwd.cuh), and
 //    loops are rolled: while the roles' code was larger than the instruction cache, its
 //    misses took more time than anything else (this, P as one bf16 term instead of two,
